@@ -77,7 +77,8 @@ typedef enum {
     WTCONV_ERR_INVALID_ARG = 1,        /* null pointer, overlap, bad dtype or
                                           layout, B < 0, C, H or W < 1 */
     WTCONV_ERR_UNSUPPORTED_SHAPE = 2,  /* even or unsupported k, L out of
-                                          range, or H*W above 2^30 */
+                                          range, H*W above 2^30, or 2^32 and
+                                          more dropout groups */
     WTCONV_ERR_WORKSPACE = 3,          /* ws too small or misaligned */
     WTCONV_ERR_LAUNCH = 4,             /* the HIP runtime rejected a launch */
     WTCONV_ERR_SCRATCH_LIMIT = 5       /* wtconv_bwd_weight_noalloc: the call needs
@@ -251,10 +252,116 @@ wtconv_status_t wtconv_naive_bwd_weight(const wtconv_desc_t *desc, const void *x
                                         float *dw_lvl, float *dscale, void *ws,
                                         size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Block operators: what a residual block needs around its WTConv mixer and
+ * its matrix products. All of them work on rows: a row is the C channels of
+ * one pixel (b, i, j), or of one token (H = 1, W tokens; or H = W = 1).
+ *
+ *   channel norm     z = (h - mean) / sqrt(var + eps)      WTCONV_NORM_LAYER
+ *                    z = h / sqrt(mean(h^2) + eps)         WTCONV_NORM_RMS
+ *                    y = z * weight[c] + bias[c]
+ *   block residual   out = x_scale[c] * x + gate * D(v), v = z * weight + bias
+ *                    of the block's output h, or v = h     WTCONV_NORM_NONE;
+ *                    gate[c] (a layer scale), gate[b][c], or none
+ *   counter dropout  y = D(x)
+ *
+ * mean and var (biased) are over the row's channels; weight, bias, gate and
+ * x_scale are fp32 and each may be NULL (1, 0, 1, 1); weight and bias need a
+ * norm. h and the residual stream (x, out; of the norm: y) each have their
+ * own type and memory order, so a norm reads the mixer's planar output and
+ * writes the channels-last rows that a linear layer takes, and the residual
+ * adds such rows to a planar x, without a copy in between. All arithmetic is
+ * fp32 (the variance from a second pass over the row on chip), rounded once
+ * at the store.
+ *
+ * D keeps an element with probability 1 - T / 65536, T = floor(65536 p + 1/2), and
+ * multiplies what it keeps by 65536 / (65536 - T); what it drops is zero,
+ * whatever it was (p = 1 drops everything). The mask is never stored: it is
+ * a function of the element's place and of rng, two 64-bit integers in
+ * device memory {seed, offset}, and of the caller's site number, so the
+ * backward pass makes the same mask again. A program gives each use in a
+ * step its own site (below 2^31) and changes the offset between steps; as
+ * rng is read on the device, a captured graph sees the new values. The bits
+ * are those of Philox4x32-10 with key (seed low, seed high) and counter
+ * (group, site, offset low, offset high), group = row * ceil(C/8) + c/8,
+ * row = (b * H + i) * W + j, for every memory order alike: element c is kept
+ * when its 16 bits (word (c%8)/2, low half for even c) are >= T. With
+ * WTCONV_DROP_SAMPLE (stochastic depth) whole samples b are kept or dropped,
+ * by the low half of word 0 of counter (b, site + 2^31, ...); a dropped
+ * sample's h does not influence any result.
+ *
+ * Pointers need the alignment of their element type only; outputs must not
+ * overlap inputs or each other. B = 0 writes nothing but zero parameter
+ * gradients. Gradients of parameters are summed in a fixed order (bitwise
+ * reproducible) in fp32. A channels-last side with one pixel per sample (or
+ * with one channel) has the same memory order as a planar one.
+ * ------------------------------------------------------------------------ */
+typedef enum { WTCONV_NORM_NONE = 0, WTCONV_NORM_LAYER = 1, WTCONV_NORM_RMS = 2 } wtconv_norm_t;
+typedef enum {
+    WTCONV_GATE_NONE = 0,      /* gate NULL */
+    WTCONV_GATE_CHANNEL = 1,   /* gate [C] */
+    WTCONV_GATE_SAMPLE = 2     /* gate [B][C] */
+} wtconv_gate_t;
+typedef enum { WTCONV_DROP_NONE = 0, WTCONV_DROP_ELEMENT = 1, WTCONV_DROP_SAMPLE = 2 } wtconv_drop_t;
+
+typedef struct {
+    int32_t B, C, H, W;
+    int32_t h_dtype, h_layout;   /* the norm's x; the block's output h; dropout's x and y */
+    int32_t y_dtype, y_layout;   /* the norm's y; the residual's x and out (dropout: ignored) */
+    int32_t norm;                /* wtconv_norm_t */
+    float eps;                   /* > 0 where there is a norm */
+    int32_t gate;                /* wtconv_gate_t (residual only) */
+    int32_t drop;                /* wtconv_drop_t (residual and dropout) */
+    double p;                    /* 0..1, read where drop is not NONE */
+    int32_t site;                /* 0..2^31-1, read where drop is not NONE */
+} wtconv_block_desc_t;
+
+/* Device workspace of wtconv_norm_bwd and wtconv_residual_bwd for `desc`
+   (256-byte aligned; enough for every choice of wanted outputs), or
+   (size_t)-1 if the descriptor is invalid. The other calls need none. */
+size_t wtconv_block_workspace_size(const wtconv_block_desc_t *desc);
+
+/* How the norm or residual of `desc` runs: WTCONV_ROUTE_FUSED (each row is
+   read once and held in registers) or WTCONV_ROUTE_GENERIC (rows wider than
+   that: read once per statistic). -1 if the descriptor is invalid. No device
+   call is made. */
+int32_t wtconv_block_route(const wtconv_block_desc_t *desc, int32_t backward);
+
+/* y = norm(x) * weight + bias. The descriptor has a norm, no gate, no drop. */
+wtconv_status_t wtconv_norm_fwd(const wtconv_block_desc_t *desc, const void *x, const float *weight,
+                                const float *bias, void *y, void *stream);
+
+/* Gradients of wtconv_norm_fwd: dx [type and order of x], dweight [C],
+   dbias [C]; the statistics are computed from x again. An output that is
+   NULL is not computed. */
+wtconv_status_t wtconv_norm_bwd(const wtconv_block_desc_t *desc, const void *x, const void *dy,
+                                const float *weight, void *dx, float *dweight, float *dbias, void *ws,
+                                size_t ws_bytes, void *stream);
+
+/* out = x_scale * x + gate * D(norm(h) * weight + bias). rng (two 64-bit
+   integers on the device, 8-byte aligned) may be NULL without a drop. */
+wtconv_status_t wtconv_residual_fwd(const wtconv_block_desc_t *desc, const void *x, const void *h,
+                                    const float *weight, const float *bias, const float *gate,
+                                    const float *x_scale, const uint64_t *rng, void *out, void *stream);
+
+/* Gradients of wtconv_residual_fwd: dx [type and order of x] (without an
+   x_scale it equals dout; NULL saves the copy), dh [type and order of h],
+   dweight [C], dbias [C], dgate [C] or [B][C], dx_scale [C]. An output that
+   is NULL is not computed; x is read for dx_scale only (else NULL). */
+wtconv_status_t wtconv_residual_bwd(const wtconv_block_desc_t *desc, const void *x, const void *h,
+                                    const void *dout, const float *weight, const float *bias,
+                                    const float *gate, const float *x_scale, const uint64_t *rng, void *dx,
+                                    void *dh, float *dweight, float *dbias, float *dgate, float *dx_scale,
+                                    void *ws, size_t ws_bytes, void *stream);
+
+/* y = D(x), and its gradient: dx = D(dy) by the same call. */
+wtconv_status_t wtconv_dropout(const wtconv_block_desc_t *desc, const void *x, const uint64_t *rng, void *y,
+                               void *stream);
+
 /* Static description of a status code. */
 const char *wtconv_status_string(wtconv_status_t status);
 
-/* Library version, e.g. "0.3.0". */
+/* Library version, e.g. "0.4.0". */
 const char *wtconv_version(void);
 
 /* Measurement probes (not operations of the layer). They measure on the

@@ -16,7 +16,17 @@ _BINDING_NAMES = (
 
 _MODULE_NAMES = ("WTConv2d", "WTConvFunction", "wtconv")
 
-__all__ = ["CONFIGS", "WorkloadConfig", "get_config", *_BINDING_NAMES, *_MODULE_NAMES]
+# the block operators around the layer: channel norm, block residual, counter dropout
+_BLOCK_BINDING_NAMES = (
+    "wtconv_norm_fwd", "wtconv_norm_bwd", "wtconv_residual_fwd", "wtconv_residual_bwd", "wtconv_dropout",
+    "wtconv_block_workspace_size", "wtconv_block_route",
+)
+
+_BLOCK_NAMES = ("ChannelNorm2d", "BlockResidual2d", "CounterDropout", "channel_norm", "block_residual",
+                "counter_dropout", "dropout_rng")
+
+__all__ = ["CONFIGS", "WorkloadConfig", "get_config", *_BINDING_NAMES, *_MODULE_NAMES, *_BLOCK_BINDING_NAMES,
+           *_BLOCK_NAMES]
 
 
 def __getattr__(name):
@@ -28,4 +38,10 @@ def __getattr__(name):
     if name in _MODULE_NAMES:
         from . import module
         return getattr(module, name)
+    if name in _BLOCK_BINDING_NAMES:
+        from . import block_binding
+        return getattr(block_binding, name)
+    if name in _BLOCK_NAMES:
+        from . import block
+        return getattr(block, name)
     raise AttributeError(name)

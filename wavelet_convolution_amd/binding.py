@@ -37,6 +37,14 @@ class WTConvDesc(ctypes.Structure):
                 ("k_level", ctypes.c_int32), ("dtype", ctypes.c_int32), ("layout", ctypes.c_int32)]
 
 
+class WTConvBlockDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("C", ctypes.c_int32), ("H", ctypes.c_int32), ("W", ctypes.c_int32),
+                ("h_dtype", ctypes.c_int32), ("h_layout", ctypes.c_int32), ("y_dtype", ctypes.c_int32),
+                ("y_layout", ctypes.c_int32), ("norm", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("gate", ctypes.c_int32), ("drop", ctypes.c_int32), ("p", ctypes.c_double),
+                ("site", ctypes.c_int32)]
+
+
 _V = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _P = ctypes.POINTER(WTConvDesc)
@@ -74,6 +82,19 @@ def load_library() -> ctypes.CDLL:
             lib.wtconv_peak_fma.restype = ctypes.c_int
             lib.wtconv_peak_copy.argtypes = [_V, _V, _SZ, _V]
             lib.wtconv_peak_copy.restype = ctypes.c_int
+            _PB = ctypes.POINTER(WTConvBlockDesc)
+            lib.wtconv_block_workspace_size.argtypes = [_PB]
+            lib.wtconv_block_workspace_size.restype = _SZ
+            lib.wtconv_block_route.argtypes = [_PB, ctypes.c_int32]
+            lib.wtconv_block_route.restype = ctypes.c_int32
+            for name, n in (("wtconv_norm_fwd", 5), ("wtconv_residual_fwd", 9), ("wtconv_dropout", 4)):
+                fn = getattr(lib, name)
+                fn.argtypes = [_PB] + [_V] * n
+                fn.restype = ctypes.c_int
+            for name, n in (("wtconv_norm_bwd", 7), ("wtconv_residual_bwd", 15)):
+                fn = getattr(lib, name)
+                fn.argtypes = [_PB] + [_V] * n + [_SZ, _V]
+                fn.restype = ctypes.c_int
             lib.wtconv_status_string.argtypes = [ctypes.c_int]
             lib.wtconv_status_string.restype = ctypes.c_char_p
             lib.wtconv_version.restype = ctypes.c_char_p

@@ -1,0 +1,298 @@
+"""Thin ctypes binding of the block operators (argument marshalling only).
+
+Channel norm, block residual and counter dropout, as defined in wtconv.h:
+every function takes [B, C, H, W] tensors on the GPU in planar or
+channels-last memory order (tokens: H = 1, W tokens, channels last), checks
+what the plain pointers of the C ABI cannot carry, and calls the C-ABI entry
+point of the same name on the current stream of the tensors' device (or on
+`stream`, on which outputs are then allocated too). There is no fallback.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import binding as _b
+
+_DTYPES = {torch.float32: _b.WTCONV_F32, torch.bfloat16: _b.WTCONV_BF16}
+_NORMS = {"none": 0, "layer": 1, "rms": 2}
+_DROPS = {"none": 0, "element": 1, "sample": 2}
+GRADS = ("dx", "dh", "dweight", "dbias", "dgate", "dx_scale")
+
+
+def _code(table: dict, value, what: str) -> int:
+    try:
+        return table[value]
+    except (KeyError, TypeError):
+        raise ValueError(f"{what} must be one of {', '.join(map(str, table))}; got {value!r}") from None
+
+
+def _act(name: str, t: torch.Tensor, like: torch.Tensor | None = None) -> tuple[int, int]:
+    """(dtype, layout) codes of an activation tensor."""
+    if t.dim() != 4 or (like is not None and t.shape != like.shape):
+        want = "[B, C, H, W]" if like is None else tuple(like.shape)
+        raise ValueError(f"{name} must have shape {want}; got {tuple(t.shape)}")
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{name} must be float32 or bfloat16; got {t.dtype}")
+    return dt, _b.layout_of(t)
+
+
+def _rng(rng, act: torch.Tensor) -> None:
+    if rng is None or rng.dtype != torch.int64 or rng.numel() != 2 or not rng.is_contiguous():
+        raise ValueError(f"a dropout needs rng, a contiguous int64 tensor {{seed, offset}} on {act.device}")
+
+
+def _gate_code(gate, act: torch.Tensor) -> int:
+    if gate is None:
+        return 0
+    B, C = act.shape[:2]
+    if gate.dim() == 1:
+        _b._check_f32("gate", gate, (C,), act)
+        return 1
+    _b._check_f32("gate", gate, (B, C), act)
+    return 2
+
+
+def _elsewhere(act: torch.Tensor, stream) -> bool:
+    """Whether the call has to enter another device or stream first."""
+    if stream is None:
+        return act.device.index != torch.cuda.current_device()
+    if stream.device != act.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {act.device}")
+    return stream != torch.cuda.current_stream(act.device)
+
+
+def _enter(fn, act, stream, tensors, *args, **kw):
+    """fn on act's device and on `stream`: outputs and workspace are allocated there, and the tensors that come
+    from another stream are marked as in use on it."""
+    if stream is None:
+        with torch.cuda.device(act.device):
+            return fn(*args, **kw)
+    for t in tensors:
+        for u in t if isinstance(t, (tuple, list)) else (t,):
+            if u is not None:
+                u.record_stream(stream)
+    with torch.cuda.stream(stream):
+        return fn(*args, **kw)
+
+
+def _desc(act, h_code, y_code, norm=0, eps=1e-6, gate=0, drop=0, p=0.0, site=0):
+    B, C, H, W = act.shape
+    if not 0 <= site < 1 << 31:
+        raise ValueError("site must be in 0..2^31-1")
+    return _b.WTConvBlockDesc(B, C, H, W, *h_code, *y_code, norm, eps, gate, drop, p, site)
+
+
+def _empty(shape, dtype, channels_last: bool, device) -> torch.Tensor:
+    return torch.empty(shape, dtype=dtype, device=device,
+                       memory_format=torch.channels_last if channels_last else torch.contiguous_format)
+
+
+def _grad(wanted: bool, shape, device):
+    return torch.empty(shape, dtype=torch.float32, device=device) if wanted else None
+
+
+def _ws_size(desc) -> int:
+    n = _b.load_library().wtconv_block_workspace_size(ctypes.byref(desc))
+    if n == ctypes.c_size_t(-1).value:
+        raise _b.WTConvError(2, _b.wtconv_status_string(2))
+    return int(n)
+
+
+def wtconv_block_workspace_size(y, h=None, *, kind: str = "layer", gate=None) -> int:
+    """Bytes of workspace of a backward call: of the norm from h's type and memory order into y's (default: the
+    same), or of the residual with stream y, block output h and this gate. Makes no device call."""
+    h = y if h is None else h
+    d = _desc(y, _act("h", h, y), _act("y", y), _code(_NORMS, kind, "kind"), gate=_gate_code(gate, y))
+    return _ws_size(d)
+
+
+def wtconv_block_route(y, h=None, *, kind: str = "layer", backward: bool = False) -> str:
+    """"fused" or "generic": how a norm from h's type and memory order into y's, or the residual with stream y and
+    block output h, runs. Makes no device call."""
+    h = y if h is None else h
+    d = _desc(y, _act("h", h, y), _act("y", y), _code(_NORMS, kind, "kind"))
+    r = _b.load_library().wtconv_block_route(ctypes.byref(d), int(backward))
+    if r < 0:
+        raise _b.WTConvError(2, _b.wtconv_status_string(2))
+    return _b.ROUTES[r]
+
+
+def wtconv_norm_fwd(x, weight=None, bias=None, *, kind: str = "layer", eps: float = 1e-6, channels_last=None,
+                    dtype=None, y=None, stream=None):
+    """y = norm(x) * weight + bias over the channels of each pixel. kind: "layer" or "rms"; weight, bias [C] fp32 or
+    None. y has x's type and memory order unless `dtype` or `channels_last` (True, False) say otherwise, or `y` is
+    given."""
+    _b._require_gpu(x, weight=weight, bias=bias, y=y)
+    if _elsewhere(x, stream):
+        return _enter(wtconv_norm_fwd, x, stream, (x, weight, bias, y), x, weight, bias, kind=kind, eps=eps,
+                      channels_last=channels_last, dtype=dtype, y=y)
+    hc = _act("x", x)
+    C = x.shape[1]
+    _b._check_f32("weight", weight, (C,), x)
+    _b._check_f32("bias", bias, (C,), x)
+    if y is None:
+        y = _empty(x.shape, dtype or x.dtype, hc[1] == _b.WTCONV_NHWC if channels_last is None else channels_last,
+                   x.device)
+    elif (dtype is not None and y.dtype != dtype) or (
+            channels_last is not None and not y.is_contiguous(
+                memory_format=torch.channels_last if channels_last else torch.contiguous_format)):
+        raise ValueError("y differs from the dtype or memory order asked for")
+    d = _desc(x, hc, _act("y", y, x), _code(_NORMS, kind, "kind"), eps)
+    _b._check(_b.load_library().wtconv_norm_fwd(ctypes.byref(d), x.data_ptr(), _b._ptr(weight), _b._ptr(bias),
+                                                y.data_ptr(), _b._stream(None)))
+    return y
+
+
+def wtconv_norm_bwd(x, dy, weight=None, bias=None, *, kind: str = "layer", eps: float = 1e-6, want=None, dx=None,
+                    ws=None, stream=None):
+    """(dx, dweight, dbias) of wtconv_norm_fwd; dx has x's type and memory order. `want`: the names of the
+    gradients to compute (default: dx, and those of the parameters given); the others are None. `ws`: a workspace
+    of wtconv_block_workspace_size bytes (allocated if None)."""
+    _b._require_gpu(x, dy=dy, weight=weight, bias=bias, dx=dx, ws=ws)
+    if _elsewhere(x, stream):
+        return _enter(wtconv_norm_bwd, x, stream, (x, dy, weight, bias, dx, ws), x, dy, weight, bias, kind=kind,
+                      eps=eps, want=want, dx=dx, ws=ws)
+    hc = _act("x", x)
+    C = x.shape[1]
+    _b._check_f32("weight", weight, (C,), x)
+    _b._check_f32("bias", bias, (C,), x)
+    if want is None:
+        want = ("dx",) + (("dweight",) if weight is not None else ()) + (("dbias",) if bias is not None else ())
+    else:
+        _wanted(want, ("dx", "dweight", "dbias"))
+    d = _desc(x, hc, _act("dy", dy, x), _code(_NORMS, kind, "kind"), eps)
+    if "dx" not in want:
+        dx = None
+    elif dx is None:
+        dx = torch.empty_like(x)
+    elif _act("dx", dx, x) != hc:
+        raise ValueError("dx must have x's type and memory order")
+    dweight, dbias = (_grad(n in want, (C,), x.device) for n in ("dweight", "dbias"))
+    if ws is None:
+        ws = _b._workspace(_ws_size(d), x.device)
+    _b._check(_b.load_library().wtconv_norm_bwd(
+        ctypes.byref(d), x.data_ptr(), dy.data_ptr(), _b._ptr(weight), _b._ptr(dx), _b._ptr(dweight), _b._ptr(dbias),
+        _b._ws_ptr(ws), _b._ws_bytes(ws), _b._stream(None)))
+    return dx, dweight, dbias
+
+
+def _wanted(want, names) -> None:
+    for n in want:
+        if n not in names:
+            raise ValueError(f"want names gradients among {', '.join(names)}; got {n!r}")
+
+
+def _residual_desc(x, h, kind, weight, bias, eps, gate, x_scale, drop, p, rng, site):
+    C = x.shape[1] if x.dim() == 4 else 0
+    xc, hc = _act("x", x), _act("h", h, x)
+    norm, mode = _code(_NORMS, kind, "kind"), _code(_DROPS, drop, "drop")
+    if norm == 0 and (weight is not None or bias is not None):
+        raise ValueError("weight and bias need a norm (kind)")
+    _b._check_f32("weight", weight, (C,), x)
+    _b._check_f32("bias", bias, (C,), x)
+    _b._check_f32("x_scale", x_scale, (C,), x)
+    if mode:
+        _rng(rng, x)
+    return _desc(x, hc, xc, norm, eps, _gate_code(gate, x), mode, p if mode else 0.0, site)
+
+
+def wtconv_residual_fwd(x, h, *, kind: str = "none", weight=None, bias=None, eps: float = 1e-6, gate=None,
+                        x_scale=None, drop: str = "none", p: float = 0.0, rng=None, site: int = 0, out=None,
+                        stream=None):
+    """out = x_scale * x + gate * D(norm(h) * weight + bias). x and out share type and memory order, h has its own.
+    kind: "none", "layer" or "rms"; gate: [C] or [B, C]; x_scale: [C]; drop: "none", "element" or "sample", with
+    probability p from rng (int64 {seed, offset} on the GPU) and site. Parameters are fp32."""
+    _b._require_gpu(x, h=h, weight=weight, bias=bias, gate=gate, x_scale=x_scale, rng=rng, out=out)
+    if _elsewhere(x, stream):
+        return _enter(wtconv_residual_fwd, x, stream, (x, h, weight, bias, gate, x_scale, rng, out), x, h, kind=kind,
+                      weight=weight, bias=bias, eps=eps, gate=gate, x_scale=x_scale, drop=drop, p=p, rng=rng,
+                      site=site, out=out)
+    d = _residual_desc(x, h, kind, weight, bias, eps, gate, x_scale, drop, p, rng, site)
+    if out is None:
+        out = torch.empty_like(x)
+    elif _act("out", out, x) != (d.y_dtype, d.y_layout):
+        raise ValueError("out must have x's type and memory order")
+    _b._check(_b.load_library().wtconv_residual_fwd(
+        ctypes.byref(d), x.data_ptr(), h.data_ptr(), _b._ptr(weight), _b._ptr(bias), _b._ptr(gate), _b._ptr(x_scale),
+        _b._ptr(rng), out.data_ptr(), _b._stream(None)))
+    return out
+
+
+def wtconv_residual_bwd(dout, h, *, x=None, kind: str = "none", weight=None, bias=None, eps: float = 1e-6, gate=None,
+                        x_scale=None, drop: str = "none", p: float = 0.0, rng=None, site: int = 0, want=None,
+                        dx=None, dh=None, ws=None, stream=None):
+    """(dx, dh, (dweight, dbias, dgate, dx_scale)) of wtconv_residual_fwd. Without an x_scale dx is dout itself
+    (unless a dx to write is given); x is needed for dx_scale only. `want`: the names of the gradients to compute
+    (default: dx, dh and those of the parameters given); the others are None."""
+    _b._require_gpu(dout, h=h, x=x, weight=weight, bias=bias, gate=gate, x_scale=x_scale, rng=rng, dx=dx, dh=dh, ws=ws)
+    if _elsewhere(dout, stream):
+        return _enter(wtconv_residual_bwd, dout, stream,
+                      (dout, h, x, weight, bias, gate, x_scale, rng, dx, dh, ws), dout, h, x=x, kind=kind,
+                      weight=weight, bias=bias, eps=eps, gate=gate, x_scale=x_scale, drop=drop, p=p, rng=rng,
+                      site=site, want=want, dx=dx, dh=dh, ws=ws)
+    d = _residual_desc(dout, h, kind, weight, bias, eps, gate, x_scale, drop, p, rng, site)
+    yc, hc = (d.y_dtype, d.y_layout), (d.h_dtype, d.h_layout)
+    if want is None:
+        given = (True, True, weight is not None, bias is not None, gate is not None, x_scale is not None)
+        want = tuple(n for n, g in zip(GRADS, given) if g)
+    else:
+        _wanted(want, GRADS)
+        if "dgate" in want and gate is None:
+            raise ValueError("dgate needs a gate")
+        if d.norm == 0 and ("dweight" in want or "dbias" in want):
+            raise ValueError("dweight and dbias need a norm (kind)")
+    if "dx_scale" in want:
+        if x is None:
+            raise ValueError("dx_scale needs x")
+        if _act("x", x, dout) != yc:
+            raise ValueError("x must have dout's type and memory order")
+    alias = "dx" in want and dx is None and x_scale is None
+    if "dx" not in want:
+        dx = None
+    elif dx is not None:
+        if _act("dx", dx, dout) != yc:
+            raise ValueError("dx must have dout's type and memory order")
+    elif not alias:
+        dx = torch.empty_like(dout)
+    if "dh" not in want:
+        dh = None
+    elif dh is None:
+        dh = torch.empty_like(h)
+    elif _act("dh", dh, h) != hc:
+        raise ValueError("dh must have h's type and memory order")
+    C = dout.shape[1]
+    dweight, dbias = (_grad(n in want, (C,), dout.device) for n in ("dweight", "dbias"))
+    dgate = _grad("dgate" in want, gate.shape if gate is not None else (), dout.device)
+    dx_scale = _grad("dx_scale" in want, (C,), dout.device)
+    if ws is None:
+        ws = _b._workspace(_ws_size(d), dout.device)
+    _b._check(_b.load_library().wtconv_residual_bwd(
+        ctypes.byref(d), _b._ptr(x) if dx_scale is not None else 0, h.data_ptr(), dout.data_ptr(), _b._ptr(weight),
+        _b._ptr(bias), _b._ptr(gate), _b._ptr(x_scale), _b._ptr(rng), _b._ptr(dx), _b._ptr(dh), _b._ptr(dweight),
+        _b._ptr(dbias), _b._ptr(dgate), _b._ptr(dx_scale), _b._ws_ptr(ws), _b._ws_bytes(ws), _b._stream(None)))
+    return (dout if alias else dx), dh, (dweight, dbias, dgate, dx_scale)
+
+
+def wtconv_dropout(x, p: float, rng, *, site: int = 0, mode: str = "element", y=None, stream=None):
+    """y = D(x): elements (mode "element") or whole samples b (mode "sample") dropped with probability p by the bits
+    of rng (int64 {seed, offset} on the GPU) and site; what is kept is scaled. The mask is never stored: the
+    gradient is the same call on dy."""
+    _b._require_gpu(x, rng=rng, y=y)
+    if _elsewhere(x, stream):
+        return _enter(wtconv_dropout, x, stream, (x, rng, y), x, p, rng, site=site, mode=mode, y=y)
+    c = _act("x", x)
+    drop = _code(_DROPS, mode, "mode")
+    if drop == 0:
+        raise ValueError("mode must be element or sample")
+    _rng(rng, x)
+    if y is None:
+        y = torch.empty_like(x)
+    elif _act("y", y, x) != c:
+        raise ValueError("y must have x's type and memory order")
+    d = _desc(x, c, c, drop=drop, p=p, site=site)
+    _b._check(_b.load_library().wtconv_dropout(ctypes.byref(d), x.data_ptr(), rng.data_ptr(), y.data_ptr(),
+                                               _b._stream(None)))
+    return y

@@ -1,0 +1,94 @@
+// The block operators: channel norm, block residual and counter dropout.
+//
+// A row is the C channels of one pixel (b, p), p < HW. With h the norm's
+// input (or the block's output) and y the result (for the residual, x and y
+// are the residual stream):
+//   z = (h - mean) r, r = 1 / sqrt(var + eps)   (layer; rms: mean = 0, var = mean of h^2; none: z = h)
+//   v = z w + b,  t = D(v),  y = s x + g t
+// and backwards, for dy:
+//   dx = s dy, ds = sum dy x, dg = sum dy t, dv = D'(g dy), dw = sum dv z, db = sum dv, u = dv w,
+//   dh = r (u - mean(u) - z mean(u z))          (rms: without mean(u); none: dh = dv)
+// The norm alone is the case without x, g and D.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "wtconv_device.h"
+
+namespace wtc {
+
+enum { NORM_NONE = 0, NORM_LAYER = 1, NORM_RMS = 2 };
+enum { GATE_NONE = 0, GATE_CHANNEL = 1, GATE_SAMPLE = 2 };
+enum { DROP_NONE = 0, DROP_ELEMENT = 1, DROP_SAMPLE = 2 };
+
+// Channels that share one generator call: 16 of its 128 bits each.
+constexpr int CG = 8;
+
+struct BlockArgs {
+    const void* h;
+    const void* x;      // residual stream in (null: none)
+    void* y;            // forward result
+    const void* dy;
+    void* dx;           // null: not wanted
+    void* dh;           // null: not wanted
+    const float *w, *b, *gate, *xs;   // null: 1, 0, 1, 1
+    const unsigned long long* rng;    // seed, offset
+    float *dw, *db, *dg, *dxs;        // null: not wanted
+    float* ws;
+    int B, C, HW;
+    int h_cl, y_cl;     // channels last
+    int norm, gate_mode, drop;
+    float eps;
+    uint32_t thr;       // an element is kept when its 16 bits are >= thr
+    float keep;         // 65536 / (65536 - thr); 0 where thr = 65536
+    uint32_t site;
+};
+
+// The sums over rows that the parameter gradients need. Each workgroup of a
+// backward kernel adds over a contiguous range of tiles (a tile: some rows
+// of one sample) and leaves its sums in its slot of the workspace; a second
+// stage adds the slots in order, so results do not depend on timing. With a
+// gate per sample, a workgroup writes the gate gradient of a sample whose
+// tiles are all its own, and leaves at most two partial sums (its first and
+// its last sample) for the second stage.
+struct Partition {
+    long long tiles;    // all tiles
+    long long tps;      // tiles per sample (samples count only with a gate per sample: else one)
+    long long per_wg;   // tiles per workgroup
+    int wgs;
+    int nsum;           // channel sums a slot holds
+    int partials;       // 0, or 2: partial gate gradients per slot
+};
+
+// Places of the channel sums in a slot; -1: not wanted.
+struct SumSlots {
+    int dw, db, dg, dxs, count;
+};
+inline SumSlots sum_slots(const BlockArgs& a) {
+    SumSlots s{-1, -1, -1, -1, 0};
+    if (a.dw) s.dw = s.count++;
+    if (a.db) s.db = s.count++;
+    if (a.dg && a.gate_mode == GATE_CHANNEL) s.dg = s.count++;
+    if (a.dxs) s.dxs = s.count++;
+    return s;
+}
+
+// How a call is served: by which kernels, and with how much workspace.
+enum { BLOCK_GENERIC = 0, BLOCK_FUSED = 1 };
+int block_route(const BlockArgs& a, int h_bf16, int y_bf16, bool backward);
+size_t block_bwd_workspace_bytes(const BlockArgs& a, int h_bf16, int y_bf16);
+hipError_t block_fwd_launch(const BlockArgs& a, int h_bf16, int y_bf16, hipStream_t s);
+hipError_t block_bwd_launch(const BlockArgs& a, int h_bf16, int y_bf16, hipStream_t s);
+hipError_t dropout_launch(const BlockArgs& a, int bf16, hipStream_t s);
+
+// generic kernels (any size and layout)
+size_t block_generic_bwd_bytes(const BlockArgs& a);
+hipError_t block_generic_fwd(const BlockArgs& a, int h_bf16, int y_bf16, hipStream_t s);
+hipError_t block_generic_bwd(const BlockArgs& a, int h_bf16, int y_bf16, hipStream_t s);
+
+// second stage
+hipError_t block_finalize(const BlockArgs& a, const Partition& p, const float* ws, hipStream_t s);
+
+}  // namespace wtc

@@ -1,0 +1,361 @@
+// Block operators, generic kernels: any number of channels, any plane, either
+// layout on either side. A workgroup takes PX rows (pixels) and 256 / PX
+// lanes of each; it reads its rows once for the mean, once for the variance
+// and once for the result (from cache where they fit), so nothing limits C.
+// The register kernels of the other files serve the sizes that they cover;
+// this one serves the rest: rows wider than their registers.
+#include "wtconv_block_device.h"
+
+namespace wtc {
+namespace {
+
+constexpr int T = 256;
+
+// Lanes of one wavefront walk along the contiguous axis: pixels where both
+// sides are planar or mixed (64 pixels, 4 lanes a row), channels in rows.
+int generic_px(const BlockArgs& a) { return a.h_cl && a.y_cl ? 1 : 64; }
+
+struct At {
+    size_t base;
+    size_t step;   // between channels
+};
+__device__ __forceinline__ At at(const BlockArgs& a, int cl, long long row) {
+    const long long b = row / a.HW, p = row - b * a.HW;
+    return cl ? At{(size_t)row * a.C, 1} : At{(size_t)b * a.C * a.HW + p, (size_t)a.HW};
+}
+
+// Sum over the lanes of each row (thread = lane * PX + pixel), by a tree in
+// LDS; every lane gets it.
+__device__ float row_sum(float v, int px, int PX, float* red) {
+    const int t = threadIdx.x;
+    __syncthreads();
+    red[t] = v;
+    for (int n = T / 2; n >= PX; n >>= 1) {
+        __syncthreads();
+        if (t < n) red[t] += red[t + n];
+    }
+    __syncthreads();
+    return red[px];
+}
+
+struct Stats {
+    float mean, r;
+};
+template <typename TH>
+__device__ Stats row_stats(const BlockArgs& a, const TH* h, const At& ah, bool live, int lane, int lanes, int px,
+                           int PX, float* red) {
+    Stats s{0.f, 1.f};
+    if (a.norm == NORM_NONE) return s;
+    if (a.norm == NORM_LAYER) {
+        float sum = 0.f;
+        if (live)
+            for (int c = lane; c < a.C; c += lanes) sum += widen(h[ah.base + c * ah.step]);
+        s.mean = row_sum(sum, px, PX, red) / (float)a.C;
+    }
+    float sq = 0.f;
+    if (live)
+        for (int c = lane; c < a.C; c += lanes) {
+            const float d = widen(h[ah.base + c * ah.step]) - s.mean;
+            sq = fmaf(d, d, sq);
+        }
+    s.r = 1.f / sqrtf(row_sum(sq, px, PX, red) / (float)a.C + a.eps);
+    return s;
+}
+
+// Keep bits of a row's channels 8 g .. 8 g + 7.
+__device__ __forceinline__ uint32_t group_keep(const BlockArgs& a, long long row, int g, bool sample) {
+    if (a.drop == DROP_NONE) return 0xffu;
+    if (a.drop == DROP_SAMPLE) return sample ? 0xffu : 0u;
+    const Philox gen(a.rng, a.site);
+    const uint32_t G = (uint32_t)cdiv(a.C, CG);
+    return keep_bits(gen((uint32_t)row * G + (uint32_t)g), a.thr);
+}
+
+template <typename TH, typename TY>
+__global__ __launch_bounds__(T) void k_generic_fwd(BlockArgs a, int PX) {
+    __shared__ float red[T];
+    const TH* h = (const TH*)a.h;
+    const TY* x = (const TY*)a.x;
+    TY* y = (TY*)a.y;
+    const int px = threadIdx.x % PX, lane = threadIdx.x / PX, lanes = T / PX;
+    const long long rows = (long long)a.B * a.HW, G = cdiv(a.C, CG);
+    for (long long r0 = (long long)blockIdx.x * PX; r0 < rows; r0 += (long long)gridDim.x * PX) {
+        const long long row = r0 + px;
+        const bool live = row < rows;
+        const At ah = at(a, a.h_cl, live ? row : 0), ay = at(a, a.y_cl, live ? row : 0);
+        const int b = live ? (int)(row / a.HW) : 0;
+        const Stats s = row_stats(a, h, ah, live, lane, lanes, px, PX, red);
+        if (!live) continue;
+        const bool kept = a.drop != DROP_SAMPLE || sample_kept(a, b);
+        const float* gate = a.gate ? a.gate + (a.gate_mode == GATE_SAMPLE ? (size_t)b * a.C : 0) : nullptr;
+        for (int g = lane; g < G; g += lanes) {
+            const uint32_t m = group_keep(a, row, g, kept);
+            for (int i = 0; i < CG; ++i) {
+                const int c = g * CG + i;
+                if (c >= a.C) break;
+                float v = (widen(h[ah.base + c * ah.step]) - s.mean) * s.r;
+                if (a.w) v *= a.w[c];
+                if (a.b) v += a.b[c];
+                v = m >> i & 1 ? v * a.keep : 0.f;
+                if (gate) v *= gate[c];
+                if (x) v += (a.xs ? a.xs[c] : 1.f) * widen(x[ay.base + c * ay.step]);
+                y[ay.base + c * ay.step] = narrow_to<TY>(v);
+            }
+        }
+    }
+}
+
+// dv and z of one element, from its dy and h.
+struct Elem {
+    float z, t, dv;
+};
+__device__ __forceinline__ Elem elem(const BlockArgs& a, const float* gate, const Stats& s, int c, bool kept, float h,
+                                     float dy) {
+    Elem e;
+    e.z = (h - s.mean) * s.r;
+    float v = e.z;
+    if (a.w) v *= a.w[c];
+    if (a.b) v += a.b[c];
+    e.t = kept ? v * a.keep : 0.f;
+    e.dv = kept ? (gate ? dy * gate[c] : dy) * a.keep : 0.f;
+    return e;
+}
+
+// dx, dh, and the mean and r of each row for the parameter gradients.
+template <typename TH, typename TY>
+__global__ __launch_bounds__(T) void k_generic_bwd(BlockArgs a, int PX, float2* stats) {
+    __shared__ float red[T];
+    const TH* h = (const TH*)a.h;
+    const TY* dy = (const TY*)a.dy;
+    TH* dh = (TH*)a.dh;
+    TY* dx = (TY*)a.dx;
+    const int px = threadIdx.x % PX, lane = threadIdx.x / PX, lanes = T / PX;
+    const long long rows = (long long)a.B * a.HW, G = cdiv(a.C, CG);
+    for (long long r0 = (long long)blockIdx.x * PX; r0 < rows; r0 += (long long)gridDim.x * PX) {
+        const long long row = r0 + px;
+        const bool live = row < rows;
+        const At ah = at(a, a.h_cl, live ? row : 0), ay = at(a, a.y_cl, live ? row : 0);
+        const int b = live ? (int)(row / a.HW) : 0;
+        const bool kept = a.drop != DROP_SAMPLE || sample_kept(a, b);
+        const float* gate = a.gate ? a.gate + (a.gate_mode == GATE_SAMPLE ? (size_t)b * a.C : 0) : nullptr;
+        Stats s{0.f, 1.f};
+        float m1 = 0.f, m2 = 0.f;
+        if (a.norm != NORM_NONE) {
+            s = row_stats(a, h, ah, live, lane, lanes, px, PX, red);
+            if (live && lane == 0) stats[row] = make_float2(s.mean, s.r);
+            if (live && kept && a.dh)
+                for (int g = lane; g < G; g += lanes) {
+                    const uint32_t m = group_keep(a, row, g, kept);
+                    for (int i = 0; i < CG; ++i) {
+                        const int c = g * CG + i;
+                        if (c >= a.C) break;
+                        const Elem e = elem(a, gate, s, c, m >> i & 1, widen(h[ah.base + c * ah.step]),
+                                            widen(dy[ay.base + c * ay.step]));
+                        const float u = a.w ? e.dv * a.w[c] : e.dv;
+                        m1 += u;
+                        m2 = fmaf(u, e.z, m2);
+                    }
+                }
+            m1 = a.norm == NORM_LAYER ? row_sum(m1, px, PX, red) / (float)a.C : 0.f;
+            m2 = row_sum(m2, px, PX, red) / (float)a.C;
+        }
+        if (!live) continue;
+        for (int g = lane; g < G; g += lanes) {
+            const uint32_t m = group_keep(a, row, g, kept);
+            for (int i = 0; i < CG; ++i) {
+                const int c = g * CG + i;
+                if (c >= a.C) break;
+                const float d = widen(dy[ay.base + c * ay.step]);
+                if (dx) dx[ay.base + c * ay.step] = narrow_to<TY>(a.xs ? d * a.xs[c] : d);
+                if (!dh) continue;
+                float o = 0.f;   // a dropped sample's h is not looked at
+                if (kept) {
+                    const float hv = a.norm != NORM_NONE ? widen(h[ah.base + c * ah.step]) : 0.f;
+                    const Elem e = elem(a, gate, s, c, m >> i & 1, hv, d);
+                    const float u = a.w ? e.dv * a.w[c] : e.dv;
+                    o = a.norm == NORM_NONE ? u : s.r * (u - m1 - e.z * m2);
+                }
+                dh[ah.base + c * ah.step] = narrow_to<TH>(o);
+            }
+        }
+    }
+}
+
+// Parameter gradients: a thread owns the eight channels of one group and adds
+// over its workgroup's rows (a tile is one row here).
+template <typename TH, typename TY>
+__global__ __launch_bounds__(T) void k_generic_grads(BlockArgs a, const float2* stats, Partition pt, SumSlots sl,
+                                                     float* slots) {
+    const TH* h = (const TH*)a.h;
+    const TY* x = (const TY*)a.x;
+    const TY* dy = (const TY*)a.dy;
+    const int g = blockIdx.x * T + threadIdx.x, c0 = g * CG, n = min(CG, a.C - c0);
+    if (n <= 0) return;
+    float* slot = slots + (size_t)blockIdx.y * (pt.nsum + pt.partials) * a.C;
+    float dw[CG] = {}, db[CG] = {}, dg[CG] = {}, ds[CG] = {};
+    const long long t0 = blockIdx.y * pt.per_wg, t1 = min(t0 + pt.per_wg, pt.tiles);
+    const bool by_sample = a.dg && a.gate_mode == GATE_SAMPLE;
+    for (long long row = t0; row < t1; ++row) {
+        const int b = (int)(row / a.HW);
+        const At ah = at(a, a.h_cl, row), ay = at(a, a.y_cl, row);
+        const bool kept = a.drop != DROP_SAMPLE || sample_kept(a, b);
+        const uint32_t m = group_keep(a, row, g, kept);
+        const float* gate = a.gate ? a.gate + (a.gate_mode == GATE_SAMPLE ? (size_t)b * a.C : 0) : nullptr;
+        Stats s{0.f, 1.f};
+        if (a.norm != NORM_NONE) s = Stats{stats[row].x, stats[row].y};
+#pragma unroll
+        for (int i = 0; i < CG; ++i) {
+            if (i >= n) break;
+            const int c = c0 + i;
+            const float d = widen(dy[ay.base + c * ay.step]);
+            if (a.dxs) ds[i] = fmaf(d, widen(x[ay.base + c * ay.step]), ds[i]);
+            if (kept && a.h) {
+                const Elem e = elem(a, gate, s, c, m >> i & 1, widen(h[ah.base + c * ah.step]), d);
+                dw[i] = fmaf(e.dv, e.z, dw[i]);
+                db[i] += e.dv;
+                dg[i] = fmaf(d, e.t, dg[i]);
+            }
+        }
+        // the last row of this sample in the workgroup's range
+        if (by_sample && (row + 1 == t1 || (row + 1) % pt.tps == 0)) {
+            const long long s0 = b * pt.tps;
+            const bool whole = s0 >= t0 && s0 + pt.tps <= t1;
+            float* to = whole ? a.dg + (size_t)b * a.C
+                              : slot + (size_t)(pt.nsum + (b == t0 / pt.tps ? 0 : 1)) * a.C;
+#pragma unroll
+            for (int i = 0; i < CG; ++i)
+                if (i < n) {
+                    to[c0 + i] = dg[i];
+                    dg[i] = 0.f;
+                }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < CG; ++i)
+        if (i < n) {
+            if (sl.dw >= 0) slot[(size_t)sl.dw * a.C + c0 + i] = dw[i];
+            if (sl.db >= 0) slot[(size_t)sl.db * a.C + c0 + i] = db[i];
+            if (sl.dg >= 0) slot[(size_t)sl.dg * a.C + c0 + i] = dg[i];
+            if (sl.dxs >= 0) slot[(size_t)sl.dxs * a.C + c0 + i] = ds[i];
+        }
+}
+
+// Second stage. A workgroup takes 16 channels of one sum: 64 lanes a channel
+// add the slots k = lane, lane + 64, ..., and a fixed tree joins them.
+// Blocks past the channel sums join the partial gate gradients of one
+// sample each, over the workgroups that its tiles lie in.
+constexpr int FC = 16, FL = 64;
+__global__ __launch_bounds__(FC * FL) void k_finalize(BlockArgs a, Partition pt, SumSlots sl, const float* slots,
+                                                      int cblocks) {
+    __shared__ float red[FL][FC];
+    const int ci = threadIdx.x % FC, lane = threadIdx.x / FC;
+    const size_t slot = (size_t)(pt.nsum + pt.partials) * a.C;
+    const long long items = (long long)cblocks * (pt.nsum + (pt.partials ? a.B : 0));
+    for (long long item = blockIdx.x; item < items; item += gridDim.x) {
+        const long long what = item / cblocks;
+        const int c = (int)(item - what * cblocks) * FC + ci;
+        float* dst;
+        float sum = 0.f;
+        if (what < pt.nsum) {
+            dst = what == sl.dw ? a.dw : what == sl.db ? a.db : what == sl.dg ? a.dg : a.dxs;
+            if (c < a.C) {
+#pragma unroll 4
+                for (int k = lane; k < pt.wgs; k += FL) sum += slots[k * slot + what * a.C + c];
+            }
+        } else {
+            const long long b = what - pt.nsum, k0 = b * pt.tps / pt.per_wg, k1 = ((b + 1) * pt.tps - 1) / pt.per_wg;
+            if (k0 == k1) continue;   // written by its one workgroup (the same for the whole block)
+            dst = a.dg + b * a.C;
+            if (c < a.C)
+                for (long long k = k0 + lane; k <= k1; k += FL)
+                    sum += slots[k * slot + (size_t)(pt.nsum + (k * pt.per_wg / pt.tps == b ? 0 : 1)) * a.C + c];
+        }
+        red[lane][ci] = sum;
+        for (int n = FL / 2; n > 0; n >>= 1) {
+            __syncthreads();
+            if (lane < n) red[lane][ci] += red[lane + n][ci];
+        }
+        if (lane == 0 && c < a.C) dst[c] = red[0][ci];
+        __syncthreads();
+    }
+}
+
+// One row a tile; as many workgroups as give each CU a few, each with enough
+// rows that its slot (nsum rows of its own) is little beside what it reads.
+Partition generic_partition(const BlockArgs& a) {
+    Partition p{};
+    const bool by_sample = a.dg && a.gate_mode == GATE_SAMPLE;
+    p.tiles = (long long)a.B * a.HW;
+    p.tps = by_sample ? a.HW : p.tiles;
+    p.per_wg = (p.tiles + 1023) / 1024;
+    if (p.per_wg < 16) p.per_wg = 16;
+    p.wgs = (int)((p.tiles + p.per_wg - 1) / p.per_wg);
+    p.nsum = sum_slots(a).count;
+    p.partials = by_sample && p.per_wg % p.tps ? 2 : 0;
+    return p;
+}
+
+size_t slots_bytes(const BlockArgs& a, const Partition& p) {
+    return (size_t)p.wgs * (p.nsum + p.partials) * a.C * sizeof(float);
+}
+
+size_t stats_bytes(const BlockArgs& a) {
+    return a.norm == NORM_NONE ? 0 : ((size_t)a.B * a.HW * sizeof(float2) + 255) / 256 * 256;
+}
+
+// Workgroups for n items; the kernels loop over what is left.
+unsigned grid_of(long long n) { return (unsigned)(n < (1 << 20) ? n : (1 << 20)); }
+
+}  // namespace
+
+hipError_t block_finalize(const BlockArgs& a, const Partition& p, const float* slots, hipStream_t s) {
+    const int cblocks = cdiv(a.C, FC);
+    const long long items = (long long)cblocks * (p.nsum + (p.partials ? a.B : 0));
+    if (items == 0) return hipSuccess;
+    hipLaunchKernelGGL(k_finalize, dim3(grid_of(items)), dim3(FC * FL), 0, s, a, p, sum_slots(a), slots, cblocks);
+    return hipGetLastError();
+}
+
+size_t block_generic_bwd_bytes(const BlockArgs& a) { return stats_bytes(a) + slots_bytes(a, generic_partition(a)); }
+
+#define WTC_TYPES(KERNEL, GRID, ...)                                                                       \
+    do {                                                                                                   \
+        if (h_bf16 && y_bf16)                                                                              \
+            hipLaunchKernelGGL((KERNEL<bf16_t, bf16_t>), GRID, dim3(T), 0, s, __VA_ARGS__);                \
+        else if (h_bf16)                                                                                   \
+            hipLaunchKernelGGL((KERNEL<bf16_t, float>), GRID, dim3(T), 0, s, __VA_ARGS__);                 \
+        else if (y_bf16)                                                                                   \
+            hipLaunchKernelGGL((KERNEL<float, bf16_t>), GRID, dim3(T), 0, s, __VA_ARGS__);                 \
+        else                                                                                               \
+            hipLaunchKernelGGL((KERNEL<float, float>), GRID, dim3(T), 0, s, __VA_ARGS__);                  \
+    } while (0)
+
+hipError_t block_generic_fwd(const BlockArgs& a, int h_bf16, int y_bf16, hipStream_t s) {
+    const int PX = generic_px(a);
+    const long long rows = (long long)a.B * a.HW;
+    if (rows == 0) return hipSuccess;
+    WTC_TYPES(k_generic_fwd, dim3(grid_of((rows + PX - 1) / PX)), a, PX);
+    return hipGetLastError();
+}
+
+hipError_t block_generic_bwd(const BlockArgs& a, int h_bf16, int y_bf16, hipStream_t s) {
+    const int PX = generic_px(a);
+    const long long rows = (long long)a.B * a.HW;
+    float2* stats = (float2*)a.ws;
+    if (rows > 0) {
+        WTC_TYPES(k_generic_bwd, dim3(grid_of((rows + PX - 1) / PX)), a, PX, stats);
+        hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    const Partition p = generic_partition(a);
+    float* slots = (float*)((char*)a.ws + stats_bytes(a));
+    const SumSlots sl = sum_slots(a);
+    if (p.wgs > 0 && (sl.count || (a.dg && a.gate_mode == GATE_SAMPLE))) {
+        WTC_TYPES(k_generic_grads, dim3((unsigned)cdiv(cdiv(a.C, CG), T), (unsigned)p.wgs), a, stats, p, sl, slots);
+        hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    return block_finalize(a, p, slots, s);
+}
+
+}  // namespace wtc
