@@ -88,6 +88,12 @@ size_t block_generic_bwd_bytes(const BlockArgs& a);
 hipError_t block_generic_fwd(const BlockArgs& a, int h_bf16, int y_bf16, hipStream_t s);
 hipError_t block_generic_bwd(const BlockArgs& a, int h_bf16, int y_bf16, hipStream_t s);
 
+// rows in registers (both sides channels last)
+bool rows_cover(const BlockArgs& a);
+size_t rows_bwd_bytes(const BlockArgs& a);
+hipError_t rows_fwd(const BlockArgs& a, int h_bf16, int y_bf16, hipStream_t s);
+hipError_t rows_bwd(const BlockArgs& a, int h_bf16, int y_bf16, hipStream_t s);
+
 // second stage
 hipError_t block_finalize(const BlockArgs& a, const Partition& p, const float* ws, hipStream_t s);
 

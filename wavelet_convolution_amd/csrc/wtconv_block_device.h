@@ -53,6 +53,146 @@ __device__ __forceinline__ bool sample_kept(const BlockArgs& a, int b) {
     return (g((uint32_t)b).x & 0xffffu) >= a.thr;
 }
 
+// Sum over aligned groups of N lanes (N a power of two up to 64), in every
+// lane: data-parallel moves within a row of 16 lanes (pairs, quads, half
+// mirror, mirror), then the two row swaps.
+template <int CTRL>
+__device__ __forceinline__ float dpp_mov(float v) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), CTRL, 0xf, 0xf, true));
+}
+template <int N>
+__device__ __forceinline__ float lane_sum(float v) {
+    if constexpr (N >= 2) v += dpp_mov<0xB1>(v);    // lanes 1 0 3 2
+    if constexpr (N >= 4) v += dpp_mov<0x4E>(v);    // lanes 2 3 0 1
+    if constexpr (N >= 8) v += dpp_mov<0x141>(v);   // half mirror: the other quad of eight
+    if constexpr (N >= 16) v += dpp_mov<0x140>(v);  // mirror: the other half of sixteen
+    if constexpr (N >= 32) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    if constexpr (N >= 64) {
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    return v;
+}
+// The same over lanes N apart: lanes l, l + N, ... up to 64 (N >= 4).
+template <int N>
+__device__ __forceinline__ float stride_sum(float v) {
+    if constexpr (N <= 4) v += dpp_mov<0x124>(v);   // rotate by 4 within sixteen,
+    if constexpr (N <= 8) v += dpp_mov<0x128>(v);   // by 8
+    if constexpr (N <= 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// N consecutive activations in their storage format, at addresses aligned to
+// the element only (the vector memory unit takes 16 bytes at any such
+// address): rows of an odd width and planes of an odd size need no other path
+// than their last, partial vector.
+typedef uint32_t words4 __attribute__((ext_vector_type(4)));
+typedef uint32_t words2 __attribute__((ext_vector_type(2)));
+typedef words4 words4_any __attribute__((aligned(2)));
+typedef words2 words2_any __attribute__((aligned(2)));
+typedef uint32_t word_any __attribute__((aligned(2)));
+
+template <typename T, int N>
+struct Vec {
+    static constexpr int WORDS = N * Act<T>::BYTES / 4;
+    uint32_t w[WORDS];
+
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ void load(const T* __restrict__ p, int n) {
+        if (n >= N) {
+            if constexpr (WORDS % 4 == 0) {
+#pragma unroll
+                for (int i = 0; i < WORDS; i += 4) {
+                    const words4 q = *(const words4_any*)((const char*)p + 4 * i);
+                    w[i] = q.x;
+                    w[i + 1] = q.y;
+                    w[i + 2] = q.z;
+                    w[i + 3] = q.w;
+                }
+            } else if constexpr (WORDS == 2) {
+                const words2 q = *(const words2_any*)p;
+                w[0] = q.x;
+                w[1] = q.y;
+            } else {
+                static_assert(WORDS == 1, "");
+                w[0] = *(const word_any*)p;
+            }
+        } else {
+            zero();
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (i < n) {
+                    if constexpr (sizeof(T) == 4)
+                        w[i] = __float_as_uint(p[i]);
+                    else
+                        w[i / 2] |= (uint32_t)p[i] << (16 * (i % 2));
+                }
+        }
+    }
+    __device__ __forceinline__ float operator[](int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        return __uint_as_float(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    }
+};
+
+// The first n of N fp32 values, rounded to T.
+template <typename T, int N>
+__device__ __forceinline__ void store_vec(T* __restrict__ p, const float (&v)[N], int n) {
+    constexpr int WORDS = N * Act<T>::BYTES / 4;
+    uint32_t w[WORDS];
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+        if constexpr (sizeof(T) == 4)
+            w[i] = __float_as_uint(v[i]);
+        else
+            w[i] = narrow_bf16x2(v[2 * i], v[2 * i + 1]);
+    }
+    if (n >= N) {
+        if constexpr (WORDS % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < WORDS; i += 4) *(words4_any*)((char*)p + 4 * i) = words4{w[i], w[i + 1], w[i + 2], w[i + 3]};
+        } else if constexpr (WORDS == 2) {
+            *(words2_any*)p = words2{w[0], w[1]};
+        } else {
+            static_assert(WORDS == 1, "");
+            *(word_any*)p = w[0];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < n) {
+                if constexpr (sizeof(T) == 4)
+                    p[i] = v[i];
+                else
+                    p[i] = (bf16_t)(i % 2 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu);
+            }
+    }
+}
+
+// Eight channels of a parameter from c on (n of them exist); `none` where
+// there is no such parameter.
+__device__ __forceinline__ void load_param(const float* __restrict__ p, int c, int n, float none, float (&v)[CG]) {
+    if (!p) {
+#pragma unroll
+        for (int i = 0; i < CG; ++i) v[i] = none;
+        return;
+    }
+    Vec<float, CG> q;
+    q.load(p + c, n);
+#pragma unroll
+    for (int i = 0; i < CG; ++i) v[i] = q[i];
+}
+
 template <typename T> __device__ __forceinline__ T narrow_to(float f);
 template <> __device__ __forceinline__ float narrow_to<float>(float f) { return f; }
 template <> __device__ __forceinline__ bf16_t narrow_to<bf16_t>(float f) { return narrow_bf16(f); }
