@@ -23,6 +23,7 @@ SOURCES = ["wtconv_fused.hip", "wtconv_tiled.hip", "wtconv_bwdw.hip", "wtconv_na
            "wtconv_peaks.hip", "wtconv_layout.hip", "wtconv_dw.hip", "wtconv_bwd1.hip",
            "wtconv_block_api.hip", "wtconv_block.hip", "wtconv_block_generic.hip", "wtconv_block_rows.hip",
            "wtconv_block_dropout.hip",
+           *(f"wtconv_block_tile_{orders}_{way}.hip" for orders in ("pp", "pr", "rp") for way in ("fwd", "bwd")),
            *(f"wtconv_fam{h}_{kind}.hip" for h in (56, 28, 14, 7) for kind in ("data", "bw"))]
 ARCH = os.environ.get("WTCONV_OFFLOAD_ARCH", "gfx950")
 

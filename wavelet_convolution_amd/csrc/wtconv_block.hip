@@ -1,20 +1,85 @@
-// Block operators: which kernels serve a call.
+// Block operators: which kernels serve a call. Rows (both sides channels last)
+// are held in registers by the row kernels up to 16,384 channels, tiles with
+// a planar side by the tile kernels up to 2,048; wider ones take the generic
+// kernels.
 #include "wtconv_block.h"
+#include "wtconv_block_tile.h"
 
 namespace wtc {
 
-int block_route(const BlockArgs& a, int, int, bool) { return rows_cover(a) ? BLOCK_FUSED : BLOCK_GENERIC; }
+template <> hipError_t tile_fwd_launch<false, false>(const BlockArgs&, int, int, const TileShape&, hipStream_t);
+template <> hipError_t tile_fwd_launch<false, true>(const BlockArgs&, int, int, const TileShape&, hipStream_t);
+template <> hipError_t tile_fwd_launch<true, false>(const BlockArgs&, int, int, const TileShape&, hipStream_t);
+template <>
+hipError_t tile_bwd_launch<false, false>(const BlockArgs&, int, int, const TileShape&, const Partition&, hipStream_t);
+template <>
+hipError_t tile_bwd_launch<false, true>(const BlockArgs&, int, int, const TileShape&, const Partition&, hipStream_t);
+template <>
+hipError_t tile_bwd_launch<true, false>(const BlockArgs&, int, int, const TileShape&, const Partition&, hipStream_t);
 
-size_t block_bwd_workspace_bytes(const BlockArgs& a, int, int) {
-    return rows_cover(a) ? rows_bwd_bytes(a) : block_generic_bwd_bytes(a);
+namespace {
+
+// Tiles per workgroup: enough workgroups for every CU to hold several, few
+// enough that their sums are little beside the activations.
+Partition tile_partition(const BlockArgs& a, const TileShape& t) {
+    Partition p{};
+    const bool by_sample = a.dg && a.gate_mode == GATE_SAMPLE;
+    p.tps = t.tps;
+    p.tiles = (long long)a.B * t.tps;
+    p.per_wg = (p.tiles + 1023) / 1024;
+    if (p.per_wg < 1) p.per_wg = 1;
+    p.wgs = (int)((p.tiles + p.per_wg - 1) / p.per_wg);
+    p.nsum = sum_slots(a).count;
+    p.partials = by_sample && p.per_wg % p.tps ? 2 : 0;
+    return p;
+}
+
+size_t tile_bwd_bytes(const BlockArgs& a, const TileShape& t) {
+    const Partition p = tile_partition(a, t);
+    return (size_t)p.wgs * (p.nsum + p.partials) * a.C * sizeof(float);
+}
+
+hipError_t tile_fwd(const BlockArgs& a, int h_bf16, int y_bf16, const TileShape& t, hipStream_t s) {
+    if (a.B == 0) return hipSuccess;
+    if (a.h_cl) return tile_fwd_launch<true, false>(a, h_bf16, y_bf16, t, s);
+    if (a.y_cl) return tile_fwd_launch<false, true>(a, h_bf16, y_bf16, t, s);
+    return tile_fwd_launch<false, false>(a, h_bf16, y_bf16, t, s);
+}
+
+hipError_t tile_bwd(const BlockArgs& a, int h_bf16, int y_bf16, const TileShape& t, hipStream_t s) {
+    const Partition p = tile_partition(a, t);
+    if (p.wgs > 0) {
+        const hipError_t err = a.h_cl   ? tile_bwd_launch<true, false>(a, h_bf16, y_bf16, t, p, s)
+                               : a.y_cl ? tile_bwd_launch<false, true>(a, h_bf16, y_bf16, t, p, s)
+                                        : tile_bwd_launch<false, false>(a, h_bf16, y_bf16, t, p, s);
+        if (err != hipSuccess) return err;
+    }
+    return block_finalize(a, p, a.ws, s);
+}
+
+}  // namespace
+
+int block_route(const BlockArgs& a, int h_bf16, int y_bf16, bool backward) {
+    const int pv = backward ? bwd_pv(h_bf16, y_bf16) : fwd_pv(h_bf16, y_bf16);
+    return rows_cover(a) || (!(a.h_cl && a.y_cl) && tile_shape(a, pv).cl) ? BLOCK_FUSED : BLOCK_GENERIC;
+}
+
+size_t block_bwd_workspace_bytes(const BlockArgs& a, int h_bf16, int y_bf16) {
+    if (a.h_cl && a.y_cl) return rows_cover(a) ? rows_bwd_bytes(a) : block_generic_bwd_bytes(a);
+    const TileShape t = tile_shape(a, bwd_pv(h_bf16, y_bf16));
+    return t.cl ? tile_bwd_bytes(a, t) : block_generic_bwd_bytes(a);
 }
 
 hipError_t block_fwd_launch(const BlockArgs& a, int h_bf16, int y_bf16, hipStream_t s) {
-    return rows_cover(a) ? rows_fwd(a, h_bf16, y_bf16, s) : block_generic_fwd(a, h_bf16, y_bf16, s);
+    if (rows_cover(a)) return rows_fwd(a, h_bf16, y_bf16, s);
+    const TileShape t = a.h_cl && a.y_cl ? TileShape{} : tile_shape(a, fwd_pv(h_bf16, y_bf16));
+    return t.cl ? tile_fwd(a, h_bf16, y_bf16, t, s) : block_generic_fwd(a, h_bf16, y_bf16, s);
 }
 
 hipError_t block_bwd_launch(const BlockArgs& a, int h_bf16, int y_bf16, hipStream_t s) {
-    return rows_cover(a) ? rows_bwd(a, h_bf16, y_bf16, s) : block_generic_bwd(a, h_bf16, y_bf16, s);
+    if (rows_cover(a)) return rows_bwd(a, h_bf16, y_bf16, s);
+    const TileShape t = a.h_cl && a.y_cl ? TileShape{} : tile_shape(a, bwd_pv(h_bf16, y_bf16));
+    return t.cl ? tile_bwd(a, h_bf16, y_bf16, t, s) : block_generic_bwd(a, h_bf16, y_bf16, s);
 }
 
 }  // namespace wtc
