@@ -35,16 +35,36 @@ struct Philox {
     }
 };
 
-// Bit e set: element e of the group is kept.
-__device__ __forceinline__ uint32_t keep_bits(const uint4& r, uint32_t thr) {
+// Bit 7 - e set: element e of the group is dropped (the sign of its 16 bits
+// less the threshold, shifted in from the right).
+__device__ __forceinline__ uint32_t drop_bits(const uint4& r, uint32_t thr) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        m |= ((w[i] & 0xffffu) >= thr ? 1u : 0u) << (2 * i);
-        m |= ((w[i] >> 16) >= thr ? 1u : 0u) << (2 * i + 1);
+        m = __builtin_amdgcn_alignbit(m, (w[i] & 0xffffu) - thr, 31);
+        m = __builtin_amdgcn_alignbit(m, (w[i] >> 16) - thr, 31);
     }
     return m;
+}
+constexpr uint32_t ALL_DROPPED = 0xffu;
+
+// v, or zero (whatever v is) where element e is dropped: the bit spread over
+// a word, without a comparison's lane mask.
+__device__ __forceinline__ float kept(float v, uint32_t m, int e) {
+    const uint32_t d = (uint32_t)((int32_t)(m << (24 + e)) >> 31);
+    return __uint_as_float(__float_as_uint(v) & ~d);
+}
+
+// Drop bits of the eight channels from c on, in a row whose first group is
+// row_group: two generator groups where c is not a multiple of eight (the
+// last lane of a row of an odd width).
+__device__ __forceinline__ uint32_t drop_bits_at(const Philox& gen, uint32_t row_group, int c, bool odd, uint32_t thr) {
+    const uint32_t g = row_group + (uint32_t)(c / CG);
+    const uint32_t m = drop_bits(gen(g), thr);
+    if (!odd) return m;   // the same for every lane
+    const int s = c % CG;
+    return s ? ((m << 8 | drop_bits(gen(g + 1), thr)) >> (8 - s)) & 0xffu : m;
 }
 
 // Whole samples take a counter of their own: the site with its top bit set.
@@ -52,6 +72,10 @@ __device__ __forceinline__ bool sample_kept(const BlockArgs& a, int b) {
     const Philox g(a.rng, a.site | 0x80000000u);
     return (g((uint32_t)b).x & 0xffffu) >= a.thr;
 }
+
+template <typename T> __device__ __forceinline__ T narrow_to(float f);
+template <> __device__ __forceinline__ float narrow_to<float>(float f) { return f; }
+template <> __device__ __forceinline__ bf16_t narrow_to<bf16_t>(float f) { return narrow_bf16(f); }
 
 // Sum over aligned groups of N lanes (N a power of two up to 64), in every
 // lane: data-parallel moves within a row of 16 lanes (pairs, quads, half
@@ -91,8 +115,8 @@ __device__ __forceinline__ float stride_sum(float v) {
 
 // N consecutive activations in their storage format, at addresses aligned to
 // the element only (the vector memory unit takes 16 bytes at any such
-// address): rows of an odd width and planes of an odd size need no other path
-// than their last, partial vector.
+// address). Where a row's or a plane's length is no multiple of the vector,
+// its last vector moves back to end with it, and overlaps its neighbour.
 typedef uint32_t words4 __attribute__((ext_vector_type(4)));
 typedef uint32_t words2 __attribute__((ext_vector_type(2)));
 typedef words4 words4_any __attribute__((aligned(2)));
@@ -108,36 +132,40 @@ struct Vec {
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) w[i] = 0;
     }
-    __device__ __forceinline__ void load(const T* __restrict__ p, int n) {
-        if (n >= N) {
-            if constexpr (WORDS % 4 == 0) {
+    __device__ __forceinline__ void load(const T* __restrict__ p) {
+        if constexpr (WORDS % 4 == 0) {
 #pragma unroll
-                for (int i = 0; i < WORDS; i += 4) {
-                    const words4 q = *(const words4_any*)((const char*)p + 4 * i);
-                    w[i] = q.x;
-                    w[i + 1] = q.y;
-                    w[i + 2] = q.z;
-                    w[i + 3] = q.w;
-                }
-            } else if constexpr (WORDS == 2) {
-                const words2 q = *(const words2_any*)p;
-                w[0] = q.x;
-                w[1] = q.y;
-            } else {
-                static_assert(WORDS == 1, "");
-                w[0] = *(const word_any*)p;
+            for (int i = 0; i < WORDS; i += 4) {
+                const words4 q = *(const words4_any*)((const char*)p + 4 * i);
+                w[i] = q.x;
+                w[i + 1] = q.y;
+                w[i + 2] = q.z;
+                w[i + 3] = q.w;
             }
+        } else if constexpr (WORDS == 2) {
+            const words2 q = *(const words2_any*)p;
+            w[0] = q.x;
+            w[1] = q.y;
         } else {
-            zero();
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (i < n) {
-                    if constexpr (sizeof(T) == 4)
-                        w[i] = __float_as_uint(p[i]);
-                    else
-                        w[i / 2] |= (uint32_t)p[i] << (16 * (i % 2));
-                }
+            static_assert(WORDS == 1, "");
+            w[0] = *(const word_any*)p;
         }
+    }
+    // the first n elements, zeros past them
+    __device__ __forceinline__ void load_part(const T* __restrict__ p, int n) {
+        zero();
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < n) {
+                if constexpr (sizeof(T) == 4)
+                    w[i] = __float_as_uint(p[i]);
+                else
+                    w[i / 2] |= (uint32_t)p[i] << (16 * (i % 2));
+            }
+    }
+    __device__ __forceinline__ void renew() {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) asm volatile("" : "+v"(w[i]));
     }
     __device__ __forceinline__ float operator[](int i) const {
         if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
@@ -145,9 +173,9 @@ struct Vec {
     }
 };
 
-// The first n of N fp32 values, rounded to T.
+// N fp32 values, rounded to T.
 template <typename T, int N>
-__device__ __forceinline__ void store_vec(T* __restrict__ p, const float (&v)[N], int n) {
+__device__ __forceinline__ void store_vec(T* __restrict__ p, const float (&v)[N]) {
     constexpr int WORDS = N * Act<T>::BYTES / 4;
     uint32_t w[WORDS];
 #pragma unroll
@@ -157,44 +185,43 @@ __device__ __forceinline__ void store_vec(T* __restrict__ p, const float (&v)[N]
         else
             w[i] = narrow_bf16x2(v[2 * i], v[2 * i + 1]);
     }
-    if (n >= N) {
-        if constexpr (WORDS % 4 == 0) {
+    if constexpr (WORDS % 4 == 0) {
 #pragma unroll
-            for (int i = 0; i < WORDS; i += 4) *(words4_any*)((char*)p + 4 * i) = words4{w[i], w[i + 1], w[i + 2], w[i + 3]};
-        } else if constexpr (WORDS == 2) {
-            *(words2_any*)p = words2{w[0], w[1]};
-        } else {
-            static_assert(WORDS == 1, "");
-            *(word_any*)p = w[0];
-        }
+        for (int i = 0; i < WORDS; i += 4) *(words4_any*)((char*)p + 4 * i) = words4{w[i], w[i + 1], w[i + 2], w[i + 3]};
+    } else if constexpr (WORDS == 2) {
+        *(words2_any*)p = words2{w[0], w[1]};
     } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (i < n) {
-                if constexpr (sizeof(T) == 4)
-                    p[i] = v[i];
-                else
-                    p[i] = (bf16_t)(i % 2 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu);
-            }
+        static_assert(WORDS == 1, "");
+        *(word_any*)p = w[0];
     }
 }
+// The first n of them.
+template <typename T, int N>
+__device__ __forceinline__ void store_part(T* __restrict__ p, const float (&v)[N], int n) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (i < n) p[i] = narrow_to<T>(v[i]);
+}
 
-// Eight channels of a parameter from c on (n of them exist); `none` where
-// there is no such parameter.
-__device__ __forceinline__ void load_param(const float* __restrict__ p, int c, int n, float none, float (&v)[CG]) {
+// Eight channels of a parameter from c on; `none` where there is no such
+// parameter. PART: the first n channels only.
+template <bool PART = false>
+__device__ __forceinline__ void load_param(const float* __restrict__ p, int c, float none, float (&v)[CG], int n = CG) {
     if (!p) {
 #pragma unroll
         for (int i = 0; i < CG; ++i) v[i] = none;
         return;
     }
+    // loaded where it is used: held over a loop, parameters cost more
+    // registers than their next read from cache costs time
+    asm volatile("" : "+v"(c));
     Vec<float, CG> q;
-    q.load(p + c, n);
+    if constexpr (PART)
+        q.load_part(p, n);
+    else
+        q.load(p + c);
 #pragma unroll
     for (int i = 0; i < CG; ++i) v[i] = q[i];
 }
-
-template <typename T> __device__ __forceinline__ T narrow_to(float f);
-template <> __device__ __forceinline__ float narrow_to<float>(float f) { return f; }
-template <> __device__ __forceinline__ bf16_t narrow_to<bf16_t>(float f) { return narrow_bf16(f); }
 
 }  // namespace wtc

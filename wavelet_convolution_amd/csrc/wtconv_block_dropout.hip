@@ -31,13 +31,13 @@ __global__ __launch_bounds__(T) void k_dropout_generic(BlockArgs a) {
         const size_t at = (a.h_cl ? (size_t)row * a.C : (size_t)b * a.C * a.HW + (row - b * a.HW)) + g * CG * step;
         uint32_t m;
         if (a.drop == DROP_SAMPLE) {
-            m = sample_kept(a, (int)b) ? 0xffu : 0u;
+            m = sample_kept(a, (int)b) ? 0u : ALL_DROPPED;
         } else {
             const Philox gen(a.rng, a.site);
-            m = keep_bits(gen((uint32_t)row * (uint32_t)G + (uint32_t)g), a.thr);
+            m = drop_bits(gen((uint32_t)row * (uint32_t)G + (uint32_t)g), a.thr);
         }
         for (int i = 0; i < CG && g * CG + i < a.C; ++i)
-            y[at + i * step] = narrow_to<X>(m >> i & 1 ? widen(h[at + i * step]) * a.keep : 0.f);
+            y[at + i * step] = narrow_to<X>(kept(widen(h[at + i * step]) * a.keep, m, i));
     }
 }
 

@@ -62,13 +62,13 @@ __device__ Stats row_stats(const BlockArgs& a, const TH* h, const At& ah, bool l
     return s;
 }
 
-// Keep bits of a row's channels 8 g .. 8 g + 7.
-__device__ __forceinline__ uint32_t group_keep(const BlockArgs& a, long long row, int g, bool sample) {
-    if (a.drop == DROP_NONE) return 0xffu;
-    if (a.drop == DROP_SAMPLE) return sample ? 0xffu : 0u;
+// Drop bits of a row's channels 8 g .. 8 g + 7.
+__device__ __forceinline__ uint32_t group_drop(const BlockArgs& a, long long row, int g, bool sample) {
+    if (a.drop == DROP_NONE) return 0u;
+    if (a.drop == DROP_SAMPLE) return sample ? 0u : ALL_DROPPED;
     const Philox gen(a.rng, a.site);
     const uint32_t G = (uint32_t)cdiv(a.C, CG);
-    return keep_bits(gen((uint32_t)row * G + (uint32_t)g), a.thr);
+    return drop_bits(gen((uint32_t)row * G + (uint32_t)g), a.thr);
 }
 
 template <typename TH, typename TY>
@@ -86,18 +86,18 @@ __global__ __launch_bounds__(T) void k_generic_fwd(BlockArgs a, int PX) {
         const int b = live ? (int)(row / a.HW) : 0;
         const Stats s = row_stats(a, h, ah, live, lane, lanes, px, PX, red);
         if (!live) continue;
-        const bool kept = a.drop != DROP_SAMPLE || sample_kept(a, b);
+        const bool in = a.drop != DROP_SAMPLE || sample_kept(a, b);
         const float* gate = a.gate ? a.gate + (a.gate_mode == GATE_SAMPLE ? (size_t)b * a.C : 0) : nullptr;
         for (int g = lane; g < G; g += lanes) {
-            const uint32_t m = group_keep(a, row, g, kept);
+            const uint32_t m = group_drop(a, row, g, in);
             for (int i = 0; i < CG; ++i) {
                 const int c = g * CG + i;
                 if (c >= a.C) break;
                 float v = (widen(h[ah.base + c * ah.step]) - s.mean) * s.r;
                 if (a.w) v *= a.w[c];
                 if (a.b) v += a.b[c];
-                v = m >> i & 1 ? v * a.keep : 0.f;
                 if (gate) v *= gate[c];
+                v = kept(v * a.keep, m, i);
                 if (x) v += (a.xs ? a.xs[c] : 1.f) * widen(x[ay.base + c * ay.step]);
                 y[ay.base + c * ay.step] = narrow_to<TY>(v);
             }
@@ -109,15 +109,15 @@ __global__ __launch_bounds__(T) void k_generic_fwd(BlockArgs a, int PX) {
 struct Elem {
     float z, t, dv;
 };
-__device__ __forceinline__ Elem elem(const BlockArgs& a, const float* gate, const Stats& s, int c, bool kept, float h,
+__device__ __forceinline__ Elem elem(const BlockArgs& a, const float* gate, const Stats& s, int c, bool keep, float h,
                                      float dy) {
     Elem e;
     e.z = (h - s.mean) * s.r;
     float v = e.z;
     if (a.w) v *= a.w[c];
     if (a.b) v += a.b[c];
-    e.t = kept ? v * a.keep : 0.f;
-    e.dv = kept ? (gate ? dy * gate[c] : dy) * a.keep : 0.f;
+    e.t = keep ? v * a.keep : 0.f;
+    e.dv = keep ? (gate ? dy * gate[c] : dy) * a.keep : 0.f;
     return e;
 }
 
@@ -136,20 +136,20 @@ __global__ __launch_bounds__(T) void k_generic_bwd(BlockArgs a, int PX, float2* 
         const bool live = row < rows;
         const At ah = at(a, a.h_cl, live ? row : 0), ay = at(a, a.y_cl, live ? row : 0);
         const int b = live ? (int)(row / a.HW) : 0;
-        const bool kept = a.drop != DROP_SAMPLE || sample_kept(a, b);
+        const bool in = a.drop != DROP_SAMPLE || sample_kept(a, b);
         const float* gate = a.gate ? a.gate + (a.gate_mode == GATE_SAMPLE ? (size_t)b * a.C : 0) : nullptr;
         Stats s{0.f, 1.f};
         float m1 = 0.f, m2 = 0.f;
         if (a.norm != NORM_NONE) {
             s = row_stats(a, h, ah, live, lane, lanes, px, PX, red);
             if (live && lane == 0) stats[row] = make_float2(s.mean, s.r);
-            if (live && kept && a.dh)
+            if (live && in && a.dh)
                 for (int g = lane; g < G; g += lanes) {
-                    const uint32_t m = group_keep(a, row, g, kept);
+                    const uint32_t m = group_drop(a, row, g, in);
                     for (int i = 0; i < CG; ++i) {
                         const int c = g * CG + i;
                         if (c >= a.C) break;
-                        const Elem e = elem(a, gate, s, c, m >> i & 1, widen(h[ah.base + c * ah.step]),
+                        const Elem e = elem(a, gate, s, c, !(m >> (7 - i) & 1), widen(h[ah.base + c * ah.step]),
                                             widen(dy[ay.base + c * ay.step]));
                         const float u = a.w ? e.dv * a.w[c] : e.dv;
                         m1 += u;
@@ -161,7 +161,7 @@ __global__ __launch_bounds__(T) void k_generic_bwd(BlockArgs a, int PX, float2* 
         }
         if (!live) continue;
         for (int g = lane; g < G; g += lanes) {
-            const uint32_t m = group_keep(a, row, g, kept);
+            const uint32_t m = group_drop(a, row, g, in);
             for (int i = 0; i < CG; ++i) {
                 const int c = g * CG + i;
                 if (c >= a.C) break;
@@ -169,9 +169,9 @@ __global__ __launch_bounds__(T) void k_generic_bwd(BlockArgs a, int PX, float2* 
                 if (dx) dx[ay.base + c * ay.step] = narrow_to<TY>(a.xs ? d * a.xs[c] : d);
                 if (!dh) continue;
                 float o = 0.f;   // a dropped sample's h is not looked at
-                if (kept) {
+                if (in) {
                     const float hv = a.norm != NORM_NONE ? widen(h[ah.base + c * ah.step]) : 0.f;
-                    const Elem e = elem(a, gate, s, c, m >> i & 1, hv, d);
+                    const Elem e = elem(a, gate, s, c, !(m >> (7 - i) & 1), hv, d);
                     const float u = a.w ? e.dv * a.w[c] : e.dv;
                     o = a.norm == NORM_NONE ? u : s.r * (u - m1 - e.z * m2);
                 }
@@ -198,8 +198,8 @@ __global__ __launch_bounds__(T) void k_generic_grads(BlockArgs a, const float2* 
     for (long long row = t0; row < t1; ++row) {
         const int b = (int)(row / a.HW);
         const At ah = at(a, a.h_cl, row), ay = at(a, a.y_cl, row);
-        const bool kept = a.drop != DROP_SAMPLE || sample_kept(a, b);
-        const uint32_t m = group_keep(a, row, g, kept);
+        const bool in = a.drop != DROP_SAMPLE || sample_kept(a, b);
+        const uint32_t m = group_drop(a, row, g, in);
         const float* gate = a.gate ? a.gate + (a.gate_mode == GATE_SAMPLE ? (size_t)b * a.C : 0) : nullptr;
         Stats s{0.f, 1.f};
         if (a.norm != NORM_NONE) s = Stats{stats[row].x, stats[row].y};
@@ -209,8 +209,8 @@ __global__ __launch_bounds__(T) void k_generic_grads(BlockArgs a, const float2* 
             const int c = c0 + i;
             const float d = widen(dy[ay.base + c * ay.step]);
             if (a.dxs) ds[i] = fmaf(d, widen(x[ay.base + c * ay.step]), ds[i]);
-            if (kept && a.h) {
-                const Elem e = elem(a, gate, s, c, m >> i & 1, widen(h[ah.base + c * ah.step]), d);
+            if (in && a.h) {
+                const Elem e = elem(a, gate, s, c, !(m >> (7 - i) & 1), widen(h[ah.base + c * ah.step]), d);
                 dw[i] = fmaf(e.dv, e.z, dw[i]);
                 db[i] += e.dv;
                 dg[i] = fmaf(d, e.t, dg[i]);
@@ -259,7 +259,7 @@ __global__ __launch_bounds__(FC * FL) void k_finalize(BlockArgs a, Partition pt,
         if (what < pt.nsum) {
             dst = what == sl.dw ? a.dw : what == sl.db ? a.db : what == sl.dg ? a.dg : a.dxs;
             if (c < a.C) {
-#pragma unroll 4
+#pragma unroll 8
                 for (int k = lane; k < pt.wgs; k += FL) sum += slots[k * slot + what * a.C + c];
             }
         } else {

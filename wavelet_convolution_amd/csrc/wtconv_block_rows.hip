@@ -63,10 +63,52 @@ struct RowSum {
     }
 };
 
+// Where a lane's vectors of eight channels stand. The last vector of a row
+// whose C is no multiple of eight moves back to end with the row; `twice`
+// names (as drop bits) the channels that it shares with its neighbour: both
+// do the same work on them and store the same values, but sums over a row
+// take them once. Rows of fewer than eight channels are one part of a vector
+// (L = 1).
+template <int L, int NV>
+struct Lanes {
+    static constexpr bool PART = L == 1;
+    int c[NV];
+    bool on[NV];
+    uint32_t twice[NV];
+    int n;   // PART: channels in all
+    __device__ __forceinline__ Lanes(int C, int lane) {
+        n = C;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int first = (v * L + lane) * CG;
+            on[v] = first < C;
+            c[v] = PART ? 0 : min(first, C - CG);
+            twice[v] = PART ? ALL_DROPPED >> min(C, CG) : ALL_DROPPED & ~(ALL_DROPPED >> (first - c[v]));
+        }
+    }
+    template <typename T>
+    __device__ __forceinline__ void load(Vec<T, CG>& q, const T* __restrict__ row, int v) const {
+        if constexpr (PART)
+            q.load_part(row, n);
+        else
+            q.load(row + c[v]);
+    }
+    template <typename T>
+    __device__ __forceinline__ void store(T* __restrict__ row, const float (&o)[CG], int v) const {
+        if constexpr (PART)
+            store_part<T, CG>(row, o, n);
+        else
+            store_vec<T, CG>(row + c[v], o);
+    }
+    __device__ __forceinline__ void param(const float* p, int v, float none, float (&o)[CG]) const {
+        load_param<PART>(p, c[v], none, o, n);
+    }
+};
+
 // mean and r of a row: the variance about the mean in a second sum over the
-// registers (no difference of large sums). Channels past C do not count.
+// registers (no difference of large sums).
 template <typename TH, int NV, int L>
-__device__ __forceinline__ void row_stats(const BlockArgs& a, const Vec<TH, CG> (&h)[NV], const int (&n)[NV],
+__device__ __forceinline__ void row_stats(const BlockArgs& a, const Vec<TH, CG> (&h)[NV], const Lanes<L, NV>& at,
                                           RowSum<L>& sum, float& mean, float& r) {
     mean = 0.f;
     r = 1.f;
@@ -76,18 +118,20 @@ __device__ __forceinline__ void row_stats(const BlockArgs& a, const Vec<TH, CG> 
         float s = 0.f;
 #pragma unroll
         for (int v = 0; v < NV; ++v)
+            if (at.on[v])
 #pragma unroll
-            for (int i = 0; i < CG; ++i) s += h[v][i];   // zeros past C
+                for (int i = 0; i < CG; ++i) s += kept(h[v][i], at.twice[v], i);
         mean = sum.one(s) * inv;
     }
     float q = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
+        if (at.on[v])
 #pragma unroll
-        for (int i = 0; i < CG; ++i) {
-            const float d = i < n[v] ? h[v][i] - mean : 0.f;
-            q = fmaf(d, d, q);
-        }
+            for (int i = 0; i < CG; ++i) {
+                const float d = kept(h[v][i] - mean, at.twice[v], i);
+                q = fmaf(d, d, q);
+            }
     r = 1.f / sqrtf(sum.one(q) * inv + a.eps);
 }
 
@@ -97,161 +141,196 @@ __global__ __launch_bounds__(threads_of(L)) void k_rows_fwd(BlockArgs a) {
     constexpr bool HOIST = NV == 1;
     __shared__ float red[L > 64 ? 4 * L / 64 : 1];
     RowSum<L> sum{red};
-    const int lane = threadIdx.x % L, gi = threadIdx.x / L;
+    const Lanes<L, NV> at(a.C, threadIdx.x % L);
+    const int gi = threadIdx.x / L;
     const long long rows = (long long)a.B * a.HW;
     const uint32_t G = (uint32_t)cdiv(a.C, CG);
-    int c[NV], n[NV];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        c[v] = (v * L + lane) * CG;
-        n[v] = max(0, min(CG, a.C - c[v]));
-    }
-    float w[CG], b[CG], gt[CG], xs[CG];
+    // y = s x + D'(z wg + bg), with the gate and D's factor in wg and bg
+    float wg[CG], bg[CG], xs[CG];
     const bool by_sample = a.gate_mode == GATE_SAMPLE;
     auto params = [&](int v, long long bi) {
-        load_param(a.w, c[v], n[v], 1.f, w);
-        load_param(a.b, c[v], n[v], 0.f, b);
-        load_param(a.xs, c[v], n[v], 1.f, xs);
-        load_param(by_sample ? a.gate + bi * a.C : a.gate, c[v], n[v], 1.f, gt);
+        float g[CG];
+        at.param(a.w, v, 1.f, wg);
+        at.param(a.b, v, 0.f, bg);
+        at.param(a.xs, v, 1.f, xs);
+        at.param(by_sample ? a.gate + bi * a.C : a.gate, v, 1.f, g);
+#pragma unroll
+        for (int i = 0; i < CG; ++i) {
+            g[i] *= a.keep;
+            wg[i] *= g[i];
+            bg[i] *= g[i];
+        }
     };
-    if constexpr (HOIST) {
-        if (a.w) load_param(a.w, c[0], n[0], 1.f, w);
-        if (a.b) load_param(a.b, c[0], n[0], 0.f, b);
-        if (a.xs) load_param(a.xs, c[0], n[0], 1.f, xs);
-        if (a.gate && !by_sample) load_param(a.gate, c[0], n[0], 1.f, gt);
-    }
+    if (HOIST && !by_sample && at.on[0]) params(0, 0);
     for (long long r0 = (long long)blockIdx.x * NG; r0 < rows; r0 += (long long)gridDim.x * NG) {
         const long long row = r0 + gi;
         const bool live = row < rows;
         const long long bi = by_sample || a.drop == DROP_SAMPLE ? (live ? row / a.HW : 0) : 0;
-        const bool kept = live && (a.drop != DROP_SAMPLE || sample_kept(a, (int)bi));
-        const TH* hp = (const TH*)a.h + row * a.C;
-        const TY* xp = (const TY*)a.x + row * a.C;
+        const bool in = live && (a.drop != DROP_SAMPLE || sample_kept(a, (int)bi));
         Vec<TH, CG> h[NV];
         Vec<TY, CG> x[NV];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             h[v].zero();   // a dropped sample's h is not looked at
-            if (kept && n[v] > 0) h[v].load(hp + c[v], n[v]);
-            x[v].zero();
-            if (a.x && live && n[v] > 0) x[v].load(xp + c[v], n[v]);
+            if (in && at.on[v]) at.load(h[v], (const TH*)a.h + row * a.C, v);
+            if (a.x && live && at.on[v]) at.load(x[v], (const TY*)a.x + row * a.C, v);
         }
-        if constexpr (HOIST)
-            if (by_sample && live && n[0] > 0) load_param(a.gate + bi * a.C, c[0], n[0], 1.f, gt);
+        if (HOIST && by_sample && at.on[0]) params(0, bi);
         float mean, r;
-        row_stats<TH, NV, L>(a, h, n, sum, mean, r);
+        row_stats<TH, NV, L>(a, h, at, sum, mean, r);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            if (!live || n[v] <= 0) continue;
+            if (!live || !at.on[v]) continue;
             if constexpr (!HOIST) params(v, bi);
-            uint32_t m = kept ? 0xffu : 0u;
-            if (a.drop == DROP_ELEMENT) {
-                const Philox gen(a.rng, a.site);
-                m = keep_bits(gen((uint32_t)row * G + (uint32_t)(c[v] / CG)), a.thr);
-            }
             float o[CG];
 #pragma unroll
-            for (int i = 0; i < CG; ++i) {
-                o[i] = (h[v][i] - mean) * r;
-                if (!HOIST || a.w) o[i] *= w[i];
-                if (!HOIST || a.b) o[i] += b[i];
-                if (a.drop != DROP_NONE) o[i] = m >> i & 1 ? o[i] * a.keep : 0.f;
-                if (!HOIST || a.gate) o[i] *= gt[i];
-                if (a.x) o[i] += !HOIST || a.xs ? xs[i] * x[v][i] : x[v][i];
+            for (int i = 0; i < CG; ++i) o[i] = fmaf((h[v][i] - mean) * r, wg[i], bg[i]);
+            if (a.drop != DROP_NONE) {
+                uint32_t m = in ? 0u : ALL_DROPPED;
+                if (a.drop == DROP_ELEMENT)
+                    m = drop_bits_at(Philox(a.rng, a.site), (uint32_t)row * G, at.c[v], a.C % CG != 0, a.thr);
+#pragma unroll
+                for (int i = 0; i < CG; ++i) o[i] = kept(o[i], m, i);
             }
-            store_vec<TY, CG>((TY*)a.y + row * a.C + c[v], o, n[v]);
+            if (a.x) {
+#pragma unroll
+                for (int i = 0; i < CG; ++i) o[i] = fmaf(xs[i], x[v][i], o[i]);
+            }
+            at.store((TY*)a.y + row * a.C, o, v);
         }
     }
 }
 
+// Over the rows of one gate (all of them, or a sample's): with e = dy where it
+// is kept, S1 = sum e z and S0 = sum e give
+//   dw = g k S1, db = g k S0, dg = k (w S1 + b S0)          (k: D's factor),
+// so the loop adds two sums, whatever is wanted. Where every row has a gate
+// of its own (HW = 1), e holds the gate and dg is written row by row.
 template <typename TH, typename TY, int L, int NV>
 __global__ __launch_bounds__(threads_of(L)) void k_rows_bwd(BlockArgs a, Partition pt, SumSlots sl, float* slots) {
-    constexpr int T = threads_of(L), NG = T / L;
+    constexpr int T = threads_of(L), NG = T / L, W = L * NV * CG;   // W: channels that the lanes hold
     __shared__ float red[L > 64 ? 4 * L / 64 : 1];
-    __shared__ float join[NG > 1 ? NG * L * NV * CG : 1];
+    // with a gate per sample: dw, db [2][W]; then, where NG > 1, one sum of each group [NG][W]
+    extern __shared__ float lds[];
     RowSum<L> sum{red};
     const int lane = threadIdx.x % L, gi = threadIdx.x / L;
+    const Lanes<L, NV> at(a.C, lane);
     const uint32_t G = (uint32_t)cdiv(a.C, CG);
-    const bool sample_gate = a.gate_mode == GATE_SAMPLE;
-    const bool each_row = a.dg && sample_gate && a.HW == 1;   // a row is a sample: its gate gradient is written at once
-    const bool by_sample = a.dg && sample_gate && !each_row;
+    const bool sample_gate = a.gate_mode == GATE_SAMPLE, by_sample = sample_gate && a.HW > 1;
+    const bool each_row = sample_gate && a.HW == 1;
+    float *acc = lds, *join = lds + (by_sample ? 2 * W : 0);
     // rows of a sample of the partition (all rows, unless samples count)
     const long long rows = (long long)a.B * a.HW, rps = by_sample ? a.HW : rows;
-    int c[NV], n[NV];
-    float dw[NV][CG] = {}, db[NV][CG] = {}, dg[NV][CG] = {}, ds[NV][CG] = {};
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        c[v] = (v * L + lane) * CG;
-        n[v] = max(0, min(CG, a.C - c[v]));
+    float s1[NV][CG] = {}, s0[NV][CG] = {}, sx[NV][CG] = {};
+    if (by_sample) {
+        for (int e = threadIdx.x; e < 2 * W; e += T) acc[e] = 0.f;
+        __syncthreads();
     }
     float* slot = slots + (size_t)blockIdx.x * (pt.nsum + pt.partials) * a.C;
-    // sums over the workgroup's groups of lanes, in order, then out
-    auto put = [&](float (&s)[NV][CG], float* to) {
+    // sum over the workgroup's groups of lanes, in order; PER channels of it
+    // are then a thread's: its own vectors' where NG = 1 (channels that two
+    // lanes share are the same in both)
+    constexpr int PER = NG > 1 ? cdiv(W, T) : NV * CG;
+    auto channel = [&](int q) {   // C: none
+        if constexpr (NG > 1) return (int)min((int)threadIdx.x + q * T, a.C);
+        return at.on[q / CG] ? at.c[q / CG] + q % CG : a.C;
+    };
+    auto place = [&](int q) {   // in acc: one for each thread and q
+        if constexpr (NG > 1) return (int)threadIdx.x + q * T;
+        return (q / CG * L + lane) * CG + q % CG;
+    };
+    auto joined = [&](const float (&s)[NV][CG], float (&t)[PER]) {
         if constexpr (NG > 1) {
             __syncthreads();
 #pragma unroll
             for (int v = 0; v < NV; ++v)
+                if (at.on[v])
 #pragma unroll
-                for (int i = 0; i < CG; ++i) join[(gi * NV + v) * L * CG + lane * CG + i] = s[v][i];
+                    for (int i = 0; i < CG; ++i) join[gi * W + at.c[v] + i] = s[v][i];
             __syncthreads();
-            for (int e = threadIdx.x; e < NV * L * CG; e += T) {
-                float t = 0.f;
 #pragma unroll
-                for (int g = 0; g < NG; ++g) t += join[g * NV * L * CG + e];
-                if (e < a.C) to[e] = t;   // element e of the lanes' vectors is channel e
+            for (int q = 0; q < PER; ++q) {
+                t[q] = 0.f;
+                const int e = channel(q);
+                if (e < a.C)
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) t[q] += join[g * W + e];
             }
         } else {
 #pragma unroll
-            for (int v = 0; v < NV; ++v)
-                if (n[v] > 0) store_vec<float, CG>(to + c[v], s[v], n[v]);
+            for (int q = 0; q < PER; ++q) t[q] = s[q / CG][q % CG];
+        }
+    };
+    // what a gate's rows give
+    auto finish = [&](const float* gate, float* dgp) {
+        float t1[PER], t0[PER];
+        joined(s1, t1);
+        joined(s0, t0);
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+            const int e = channel(q);
+            if (e >= a.C) continue;
+            if (dgp) dgp[e] = a.keep * ((a.w ? a.w[e] : 1.f) * t1[q] + (a.b ? a.b[e] : 0.f) * t0[q]);
+            const float g = (gate ? gate[e] : 1.f) * a.keep;
+            if (by_sample) {
+                acc[place(q)] += g * t1[q];
+                acc[W + place(q)] += g * t0[q];
+            } else {
+                if (sl.dw >= 0) slot[(size_t)sl.dw * a.C + e] = g * t1[q];
+                if (sl.db >= 0) slot[(size_t)sl.db * a.C + e] = g * t0[q];
+            }
         }
     };
     const long long t0 = blockIdx.x * pt.per_wg, t1 = min(t0 + pt.per_wg, pt.tiles);
     for (long long t = t0; t < t1; ++t) {
-        const long long s = by_sample ? t / pt.tps : 0, in = (t - s * pt.tps) * NG + gi, row = s * rps + in;
-        const bool live = in < rps;
+        const long long s = by_sample ? t / pt.tps : 0, r0 = (t - s * pt.tps) * NG + gi, row = s * rps + r0;
+        const bool live = r0 < rps;
         const long long bi = by_sample ? s : sample_gate || a.drop == DROP_SAMPLE ? (live ? row / a.HW : 0) : 0;
-        const bool kept = live && (a.drop != DROP_SAMPLE || sample_kept(a, (int)bi));
+        const bool in = live && (a.drop != DROP_SAMPLE || sample_kept(a, (int)bi));
         Vec<TH, CG> h[NV];
-        Vec<TY, CG> d[NV];
+        Vec<TY, CG> d[NV], x[NV];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             h[v].zero();
-            if (kept && n[v] > 0) h[v].load((const TH*)a.h + row * a.C + c[v], n[v]);
+            if (in && at.on[v]) at.load(h[v], (const TH*)a.h + row * a.C, v);
             d[v].zero();
-            if (live && n[v] > 0) d[v].load((const TY*)a.dy + row * a.C + c[v], n[v]);
+            if (live && at.on[v]) at.load(d[v], (const TY*)a.dy + row * a.C, v);
+            if (a.dxs && live && at.on[v]) at.load(x[v], (const TY*)a.x + row * a.C, v);
         }
         float mean, r;
-        row_stats<TH, NV, L>(a, h, n, sum, mean, r);
+        row_stats<TH, NV, L>(a, h, at, sum, mean, r);
         float m1 = 0.f, m2 = 0.f;
-        float dv[NV][CG];
+        float u[NV][CG];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            float w[CG], b[CG], gt[CG];
-            const bool on = live && n[v] > 0;
-            load_param(on ? a.w : nullptr, c[v], n[v], 1.f, w);
-            load_param(on ? a.b : nullptr, c[v], n[v], 0.f, b);
-            load_param(!on ? nullptr : sample_gate ? a.gate + bi * a.C : a.gate, c[v], n[v], 1.f, gt);
-            uint32_t m = kept ? 0xffu : 0u;
-            if (a.drop == DROP_ELEMENT && on) {
-                const Philox gen(a.rng, a.site);
-                m = keep_bits(gen((uint32_t)row * G + (uint32_t)(c[v] / CG)), a.thr);
+            if (!live || !at.on[v]) continue;
+            float gw[CG], w[CG], g[CG];
+            at.param(a.w, v, 1.f, w);
+            at.param(sample_gate ? a.gate + bi * a.C : a.gate, v, 1.f, g);
+#pragma unroll
+            for (int i = 0; i < CG; ++i) gw[i] = w[i] * g[i] * a.keep;
+            uint32_t m = in ? 0u : ALL_DROPPED;
+            if (a.drop == DROP_ELEMENT)
+                m = drop_bits_at(Philox(a.rng, a.site), (uint32_t)row * G, at.c[v], a.C % CG != 0, a.thr);
+            if (each_row && a.dg) {
+                float b[CG], o[CG];
+                at.param(a.b, v, 0.f, b);
+#pragma unroll
+                for (int i = 0; i < CG; ++i)
+                    o[i] = kept(d[v][i], m, i) * fmaf((h[v][i] - mean) * r, w[i], b[i]) * a.keep;
+                at.store(a.dg + row * a.C, o, v);
             }
-            float row_dg[CG];
 #pragma unroll
             for (int i = 0; i < CG; ++i) {
-                const bool k = m >> i & 1;
-                const float z = (h[v][i] - mean) * r, di = d[v][i];   // di = 0 past C
-                dv[v][i] = k ? di * gt[i] * a.keep : 0.f;
-                row_dg[i] = k ? di * (fmaf(z, w[i], b[i]) * a.keep) : 0.f;
-                dw[v][i] = fmaf(dv[v][i], z, dw[v][i]);
-                db[v][i] += dv[v][i];
-                dg[v][i] += row_dg[i];
-                dv[v][i] *= w[i];   // u from here on
-                m1 += dv[v][i];
-                m2 = fmaf(dv[v][i], z, m2);
+                const float z = (h[v][i] - mean) * r, e = kept(d[v][i], m, i);
+                const float eg = each_row ? e * g[i] : e;
+                s1[v][i] = fmaf(eg, z, s1[v][i]);
+                s0[v][i] += eg;
+                u[v][i] = e * gw[i];
+                const float once = kept(u[v][i], at.twice[v], i);
+                m1 += once;
+                m2 = fmaf(once, z, m2);
             }
-            if (each_row && on) store_vec<float, CG>(a.dg + row * a.C + c[v], row_dg, n[v]);
         }
         if (a.norm != NORM_NONE && a.dh) {
             const float inv = 1.f / (float)a.C;
@@ -261,44 +340,59 @@ __global__ __launch_bounds__(threads_of(L)) void k_rows_bwd(BlockArgs a, Partiti
         }
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            if (!live || n[v] <= 0) continue;
+            if (!live || !at.on[v]) continue;
             if (a.dh) {
                 float o[CG];
 #pragma unroll
                 for (int i = 0; i < CG; ++i) {
                     const float z = (h[v][i] - mean) * r;
-                    o[i] = a.norm == NORM_NONE ? dv[v][i] : r * (dv[v][i] - m1 - z * m2);
+                    o[i] = a.norm == NORM_NONE ? u[v][i] : r * (u[v][i] - m1 - z * m2);
                 }
-                store_vec<TH, CG>((TH*)a.dh + row * a.C + c[v], o, n[v]);
+                at.store((TH*)a.dh + row * a.C, o, v);
             }
             if (a.dx) {
                 float xs[CG], o[CG];
-                load_param(a.xs, c[v], n[v], 1.f, xs);
+                at.param(a.xs, v, 1.f, xs);
 #pragma unroll
                 for (int i = 0; i < CG; ++i) o[i] = d[v][i] * xs[i];
-                store_vec<TY, CG>((TY*)a.dx + row * a.C + c[v], o, n[v]);
+                at.store((TY*)a.dx + row * a.C, o, v);
             }
             if (a.dxs) {
-                Vec<TY, CG> x;
-                x.load((const TY*)a.x + row * a.C + c[v], n[v]);
 #pragma unroll
-                for (int i = 0; i < CG; ++i) ds[v][i] = fmaf(d[v][i], x[i], ds[v][i]);
+                for (int i = 0; i < CG; ++i) sx[v][i] = fmaf(d[v][i], x[v][i], sx[v][i]);
             }
         }
         // the last tile of this sample in the workgroup's range
         if (by_sample && (t + 1 == t1 || (t + 1) % pt.tps == 0)) {
             const bool whole = s * pt.tps >= t0 && (s + 1) * pt.tps <= t1;
-            put(dg, whole ? a.dg + s * a.C : slot + (size_t)(pt.nsum + (s == t0 / pt.tps ? 0 : 1)) * a.C);
+            finish(a.gate + s * a.C,
+                   !a.dg   ? nullptr
+                   : whole ? a.dg + s * a.C
+                           : slot + (size_t)(pt.nsum + (s == t0 / pt.tps ? 0 : 1)) * a.C);
 #pragma unroll
             for (int v = 0; v < NV; ++v)
 #pragma unroll
-                for (int i = 0; i < CG; ++i) dg[v][i] = 0.f;
+                for (int i = 0; i < CG; ++i) s1[v][i] = s0[v][i] = 0.f;
         }
     }
-    if (sl.dw >= 0) put(dw, slot + (size_t)sl.dw * a.C);
-    if (sl.db >= 0) put(db, slot + (size_t)sl.db * a.C);
-    if (sl.dg >= 0) put(dg, slot + (size_t)sl.dg * a.C);
-    if (sl.dxs >= 0) put(ds, slot + (size_t)sl.dxs * a.C);
+    if (by_sample) {   // each thread wrote the places that it reads here
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+            const int e = channel(q);
+            if (e >= a.C) continue;
+            if (sl.dw >= 0) slot[(size_t)sl.dw * a.C + e] = acc[place(q)];
+            if (sl.db >= 0) slot[(size_t)sl.db * a.C + e] = acc[W + place(q)];
+        }
+    } else {
+        finish(each_row ? nullptr : a.gate, sl.dg >= 0 ? slot + (size_t)sl.dg * a.C : nullptr);
+    }
+    if (sl.dxs >= 0) {
+        float tx[PER];
+        joined(sx, tx);
+#pragma unroll
+        for (int q = 0; q < PER; ++q)
+            if (channel(q) < a.C) slot[(size_t)sl.dxs * a.C + channel(q)] = tx[q];
+    }
 }
 
 // The layouts of a row over lanes, by its vectors of eight channels: the
@@ -307,7 +401,7 @@ __global__ __launch_bounds__(threads_of(L)) void k_rows_bwd(BlockArgs a, Partiti
 template <template <int, int> class F, class... A>
 auto for_row(int C, A... args) {
     const int vecs = cdiv(C, CG);
-    if (vecs <= 1) return F<1, 1>::call(args...);
+    if (vecs <= 1) return F<1, 1>::call(args...);   // the only one for C < 8
     if (vecs <= 4) return F<4, 1>::call(args...);
     if (vecs <= 8) return F<8, 1>::call(args...);
     if (vecs <= 16) return F<16, 1>::call(args...);
@@ -329,7 +423,7 @@ struct GroupsOf {
 Partition rows_partition(const BlockArgs& a) {
     const int NG = for_row<GroupsOf>(a.C);
     Partition p{};
-    const bool by_sample = a.dg && a.gate_mode == GATE_SAMPLE && a.HW > 1;
+    const bool by_sample = a.gate_mode == GATE_SAMPLE && a.HW > 1;
     const long long rows = (long long)a.B * a.HW, rps = by_sample ? a.HW : rows;
     p.tps = (rps + NG - 1) / NG;
     p.tiles = by_sample ? a.B * p.tps : p.tps;
@@ -337,7 +431,7 @@ Partition rows_partition(const BlockArgs& a) {
     if (p.per_wg < 4) p.per_wg = 4;
     p.wgs = (int)((p.tiles + p.per_wg - 1) / p.per_wg);
     p.nsum = sum_slots(a).count;
-    p.partials = by_sample && p.per_wg % p.tps ? 2 : 0;
+    p.partials = by_sample && a.dg && p.per_wg % p.tps ? 2 : 0;
     return p;
 }
 
@@ -360,8 +454,10 @@ struct Bwd {
     template <int L, int NV>
     struct F {
         static hipError_t call(const BlockArgs* a, const Partition* p, hipStream_t s) {
-            constexpr int T = threads_of(L);
-            hipLaunchKernelGGL((k_rows_bwd<TH, TY, L, NV>), dim3((unsigned)p->wgs), dim3(T), 0, s, *a, *p,
+            constexpr int T = threads_of(L), W = L * NV * CG;
+            const bool by_sample = a->gate_mode == GATE_SAMPLE && a->HW > 1;
+            const size_t lds = sizeof(float) * ((by_sample ? 2 * W : 0) + (T / L > 1 ? T / L * W : 0));
+            hipLaunchKernelGGL((k_rows_bwd<TH, TY, L, NV>), dim3((unsigned)p->wgs), dim3(T), lds, s, *a, *p,
                                sum_slots(*a), a->ws);
             return hipGetLastError();
         }

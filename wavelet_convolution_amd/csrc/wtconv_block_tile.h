@@ -10,10 +10,10 @@
 // wavefronts stand side by side along the channels and cover all of them;
 // their sums over channels meet in LDS, one barrier each.
 //
-// Planes end inside a vector (HW not a multiple of PV): the last pixel lane
-// moves back to the plane's last PV pixels and does some of its neighbour's
-// work again (the same values to the same addresses); the backward kernel
-// leaves those pixels out of its sums.
+// Where HW is no multiple of PV, or C of eight, the last lane along it moves
+// back to end with it and does some of its neighbour's work again: the same
+// values to the same addresses. Sums take the elements that two lanes share
+// once, by a weight of 0 or 1. (So a tile needs HW >= PV and C >= 8.)
 #pragma once
 
 #include "wtconv_block_device.h"
@@ -28,56 +28,64 @@ struct Patch {   // [8 channels] x [PV pixels]
 #pragma unroll
         for (int i = 0; i < NVEC; ++i) v[i].zero();
     }
-    // nc channels and np pixels exist (0: none)
-    __device__ __forceinline__ void load(const T* __restrict__ p, size_t step, int nc, int np) {
-        const int nv = CLAST ? np : nc, len = CLAST ? nc : np;
+    // p is the sample's first element, the same for every lane, and off
+    // (bytes) the lane's place in it
+    __device__ __forceinline__ void load(const T* __restrict__ p, uint32_t off, size_t step) {
 #pragma unroll
-        for (int i = 0; i < NVEC; ++i) {
-            if (i < nv)
-                v[i].load(p + i * step, len);
-            else
-                v[i].zero();
-        }
+        for (int i = 0; i < NVEC; ++i) v[i].load((const T*)((const char*)(p + i * step) + off));
+    }
+    // From here on the words are new to the compiler: what it made of them
+    // before (widened values, twice the registers in bf16) is made again
+    // rather than held.
+    __device__ __forceinline__ void renew() {
+#pragma unroll
+        for (int i = 0; i < NVEC; ++i) v[i].renew();
     }
     __device__ __forceinline__ float at(int ch, int px) const { return CLAST ? v[px][ch] : v[ch][px]; }
 };
 
 // f(channel, pixel) for every element, rounded and stored.
 template <typename T, bool CLAST, int PV, class F>
-__device__ __forceinline__ void store_patch(T* __restrict__ p, size_t step, int nc, int np, F&& f) {
+__device__ __forceinline__ void store_patch(T* __restrict__ p, uint32_t off, size_t step, F&& f) {
     constexpr int NVEC = CLAST ? PV : CG, LEN = CLAST ? CG : PV;
-    const int nv = CLAST ? np : nc, len = CLAST ? nc : np;
 #pragma unroll
     for (int i = 0; i < NVEC; ++i) {
-        if (i >= nv) break;
         float o[LEN];
 #pragma unroll
         for (int k = 0; k < LEN; ++k) o[k] = CLAST ? f(k, i) : f(i, k);
-        store_vec<T, LEN>(p + i * step, o, len);
+        store_vec<T, LEN>((T*)((char*)(p + i * step) + off), o);
     }
 }
 
-// Where a lane stands in its tile.
-template <int CL, int PV>
-struct Place {
-    static constexpr int PL = 64 / CL, PX = PL * PV;   // pixel lanes, pixels of a tile
-    int c0, nc;      // channels
-    int p0, np;      // pixels
-    int skip;        // pixels at the front that the neighbour has too
-    __device__ __forceinline__ Place(const BlockArgs& a, int tile) {
-        const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-        c0 = (wave * CL + lane % CL) * CG;
-        nc = max(0, min(CG, a.C - c0));
-        p0 = tile * PX + lane / CL * PV;
-        np = max(0, min(PV, a.HW - p0));
-        skip = 0;
-        if (np > 0 && np < PV && a.HW >= PV) {
-            skip = PV - np;
-            p0 -= skip;
-            np = PV;
-        }
-        if (nc == 0) np = 0;
+// A lane's channels: eight from c on, of which the first `shared` are the
+// neighbour's too.
+template <int CL>
+struct Channels {
+    int c, shared;
+    bool on;
+    __device__ __forceinline__ Channels(int C) {
+        const int first = (threadIdx.x / 64 * CL + threadIdx.x % CL) * CG;
+        on = first < C;
+        c = min(first, C - CG);
+        shared = on ? first - c : CG;
     }
+    __device__ __forceinline__ float weight(int i) const { return i < shared ? 0.f : 1.f; }
+};
+
+// A lane's pixels in a tile: PV from p on, of which the first `shared` are
+// the neighbour's too.
+template <int CL, int PV>
+struct Pixels {
+    static constexpr int PL = 64 / CL, PX = PL * PV;   // pixel lanes, pixels of a tile
+    int p, shared;
+    bool on;
+    __device__ __forceinline__ Pixels(int HW, int tile) {
+        const int first = tile * PX + threadIdx.x % 64 / CL * PV;
+        on = first < HW;
+        p = min(first, HW - PV);
+        shared = on ? first - p : PV;
+    }
+    __device__ __forceinline__ float weight(int j) const { return j < shared ? 0.f : 1.f; }
 };
 
 // Sums over all channels of PV pixel values (K sets of them) in every lane.
@@ -112,10 +120,10 @@ __device__ __forceinline__ void channel_sums(float (&s)[K][PV], float* red, int&
             for (int j = 0; j < PV; ++j) s[k][j] += buf[((w * K + k) * PL + pl) * PV + j];
 }
 
-// mean and r of a lane's pixels.
+// mean and r of a lane's pixels; f: the weights of its channels.
 template <typename TH, bool HCL, int CL, int PV>
-__device__ __forceinline__ void patch_stats(const BlockArgs& a, const Patch<TH, HCL, PV>& h, int nc, float* red,
-                                            int& turn, float (&mean)[PV], float (&r)[PV]) {
+__device__ __forceinline__ void patch_stats(const BlockArgs& a, Patch<TH, HCL, PV>& h, const float (&f)[CG],
+                                            float* red, int& turn, float (&mean)[PV], float (&r)[PV]) {
 #pragma unroll
     for (int j = 0; j < PV; ++j) {
         mean[j] = 0.f;
@@ -129,9 +137,10 @@ __device__ __forceinline__ void patch_stats(const BlockArgs& a, const Patch<TH, 
         for (int j = 0; j < PV; ++j) {
             s[0][j] = 0.f;
 #pragma unroll
-            for (int i = 0; i < CG; ++i) s[0][j] += h.at(i, j);   // zeros past C
+            for (int i = 0; i < CG; ++i) s[0][j] = fmaf(h.at(i, j), f[i], s[0][j]);
         }
         channel_sums<CL, PV, 1>(s, red, turn);
+        h.renew();
 #pragma unroll
         for (int j = 0; j < PV; ++j) mean[j] = s[0][j] * inv;
     }
@@ -140,26 +149,27 @@ __device__ __forceinline__ void patch_stats(const BlockArgs& a, const Patch<TH, 
         s[0][j] = 0.f;
 #pragma unroll
         for (int i = 0; i < CG; ++i) {
-            const float d = i < nc ? h.at(i, j) - mean[j] : 0.f;
-            s[0][j] = fmaf(d, d, s[0][j]);
+            const float d = h.at(i, j) - mean[j];
+            s[0][j] = fmaf(d * f[i], d, s[0][j]);
         }
     }
     channel_sums<CL, PV, 1>(s, red, turn);
+    h.renew();
 #pragma unroll
     for (int j = 0; j < PV; ++j) r[j] = 1.f / sqrtf(s[0][j] * inv + a.eps);
 }
 
-// Keep bits of a lane's pixels (eight channels each).
+// Drop bits of a lane's pixels (eight channels each).
 template <int PV>
-__device__ __forceinline__ void patch_keep(const BlockArgs& a, long long row0, int c0, bool kept, uint32_t (&m)[PV]) {
+__device__ __forceinline__ void patch_drop(const BlockArgs& a, long long row, int c, bool in, uint32_t (&m)[PV]) {
     if (a.drop == DROP_ELEMENT) {
         const Philox gen(a.rng, a.site);
-        const uint32_t G = (uint32_t)cdiv(a.C, CG), g0 = (uint32_t)row0 * G + (uint32_t)(c0 / CG);
+        const uint32_t G = (uint32_t)cdiv(a.C, CG);
 #pragma unroll
-        for (int j = 0; j < PV; ++j) m[j] = keep_bits(gen(g0 + j * G), a.thr);
+        for (int j = 0; j < PV; ++j) m[j] = drop_bits_at(gen, (uint32_t)(row + j) * G, c, a.C % CG != 0, a.thr);
     } else {
 #pragma unroll
-        for (int j = 0; j < PV; ++j) m[j] = kept ? 0xffu : 0u;
+        for (int j = 0; j < PV; ++j) m[j] = in ? 0u : ALL_DROPPED;
     }
 }
 
@@ -167,103 +177,151 @@ template <typename TH, bool HCL, typename TY, bool YCL, int CL, int PV, int MAXT
 __global__ __launch_bounds__(MAXT) void k_tile_fwd(BlockArgs a, long long tiles, int tps) {
     extern __shared__ float red[];
     int turn = 0;
+    const Channels<CL> ch(a.C);
+    const size_t sh = HCL ? a.C : a.HW, sy = YCL ? a.C : a.HW;
     for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
         const long long b = t / tps;
-        const Place<CL, PV> at(a, (int)(t - b * tps));
-        const bool kept = a.drop != DROP_SAMPLE || sample_kept(a, (int)b);
+        const Pixels<CL, PV> px(a.HW, (int)(t - b * tps));
+        const bool in = a.drop != DROP_SAMPLE || sample_kept(a, (int)b), on = ch.on && px.on;
         const size_t first = (size_t)b * a.C * a.HW;
-        const size_t planar = first + (size_t)at.c0 * a.HW + at.p0, rows = first + (size_t)at.p0 * a.C + at.c0;
+        const uint32_t planar = (uint32_t)ch.c * a.HW + px.p, rows = (uint32_t)px.p * a.C + ch.c;
+        const uint32_t oh = (HCL ? rows : planar) * sizeof(TH), oy = (YCL ? rows : planar) * sizeof(TY);
         Patch<TH, HCL, PV> h;
         Patch<TY, YCL, PV> x;
-        h.load((const TH*)a.h + (HCL ? rows : planar), HCL ? a.C : a.HW, at.nc, kept ? at.np : 0);
-        if (a.x) x.load((const TY*)a.x + (YCL ? rows : planar), YCL ? a.C : a.HW, at.nc, at.np);
-        float mean[PV], r[PV];
-        patch_stats<TH, HCL, CL, PV>(a, h, at.nc, red, turn, mean, r);
-        if (at.np <= 0) continue;
+        h.zero();   // a dropped sample's h is not looked at
+        if (on) {
+            if (in) h.load((const TH*)a.h + first, oh, sh);
+            if (a.x) x.load((const TY*)a.x + first, oy, sy);
+        }
+        float mean[PV], r[PV], f[CG];
+#pragma unroll
+        for (int i = 0; i < CG; ++i) f[i] = ch.weight(i);
+        patch_stats<TH, HCL, CL, PV>(a, h, f, red, turn, mean, r);
+        if (!on) continue;
         uint32_t m[PV];
-        if (a.drop != DROP_NONE) patch_keep<PV>(a, b * a.HW + at.p0, at.c0, kept, m);
-        float w[CG], bb[CG], g[CG], xs[CG];
-        load_param(a.w, at.c0, at.nc, 1.f, w);
-        load_param(a.b, at.c0, at.nc, 0.f, bb);
-        load_param(a.gate_mode == GATE_SAMPLE ? a.gate + b * a.C : a.gate, at.c0, at.nc, 1.f, g);
-        load_param(a.xs, at.c0, at.nc, 1.f, xs);
-        store_patch<TY, YCL, PV>((TY*)a.y + (YCL ? rows : planar), YCL ? a.C : a.HW, at.nc, at.np, [&](int i, int j) {
-            float o = (h.at(i, j) - mean[j]) * r[j];
-            o = o * w[i] + bb[i];
-            if (a.drop != DROP_NONE) o = m[j] >> i & 1 ? o * a.keep : 0.f;
-            o *= g[i];
-            if (a.x) o = fmaf(xs[i], x.at(i, j), o);
-            return o;
+        if (a.drop != DROP_NONE) patch_drop<PV>(a, b * a.HW + px.p, ch.c, in, m);
+        // y = s x + D'(z wg + bg), with the gate and D's factor in wg and bg
+        float wg[CG], bg[CG], g[CG], xs[CG];
+        load_param(a.w, ch.c, 1.f, wg);
+        load_param(a.b, ch.c, 0.f, bg);
+        load_param(a.gate_mode == GATE_SAMPLE ? a.gate + b * a.C : a.gate, ch.c, 1.f, g);
+        load_param(a.xs, ch.c, 1.f, xs);
+#pragma unroll
+        for (int i = 0; i < CG; ++i) {
+            g[i] *= a.keep;
+            wg[i] *= g[i];
+            bg[i] *= g[i];
+        }
+        store_patch<TY, YCL, PV>((TY*)a.y + first, oy, sy, [&](int i, int j) {
+            float o = fmaf((h.at(i, j) - mean[j]) * r[j], wg[i], bg[i]);
+            if (a.drop != DROP_NONE) o = kept(o, m[j], i);
+            return a.x ? fmaf(xs[i], x.at(i, j), o) : o;
         });
     }
 }
 
+// Over the pixels of one gate (all of them, or a sample's): with e = dy where
+// it is kept, S1 = sum e z and S0 = sum e give
+//   dw = g k S1, db = g k S0, dg = k (w S1 + b S0)          (k: D's factor),
+// so the loop adds two sums, whatever is wanted. With a gate per sample, dw
+// and db add up over a workgroup's samples in LDS.
 template <typename TH, bool HCL, typename TY, bool YCL, int CL, int PV, int MAXT>
 __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, SumSlots sl, float* slots) {
-    extern __shared__ float red[];
+    extern __shared__ float lds[];
+    const bool by_sample = a.gate_mode == GATE_SAMPLE;
+    const Channels<CL> ch(a.C);
+    const size_t sh = HCL ? a.C : a.HW, sy = YCL ? a.C : a.HW;
+    // with a gate per sample: dw, db [2][lanes' channels], each of its own lane
+    const int W = blockDim.x / 64 * CL * CG, own = (threadIdx.x / 64 * CL + threadIdx.x % CL) * CG;
+    float *acc = lds + own, *red = lds + (by_sample ? 2 * W : 0);
     int turn = 0;
-    float dw[CG] = {}, db[CG] = {}, dg[CG] = {}, ds[CG] = {};
+    float s1[CG] = {}, s0[CG] = {}, sx[CG] = {};
     float* slot = slots + (size_t)blockIdx.x * (pt.nsum + pt.partials) * a.C;
-    const bool sample_gate = a.gate_mode == GATE_SAMPLE, by_sample = a.dg && sample_gate;
-    const int lane = threadIdx.x % 64, c0 = (threadIdx.x / 64 * CL + lane % CL) * CG;
-    const int nc = max(0, min(CG, a.C - c0));
-    // sums over the pixel lanes; a wavefront's channels are its own
-    auto put = [&](float (&s)[CG], float* to) {
+    const bool writes = threadIdx.x % 64 < CL && ch.on;   // the lane that writes its channels' sums
+    auto pixel_sums = [&](float (&s)[CG]) {
 #pragma unroll
         for (int i = 0; i < CG; ++i) s[i] = stride_sum<CL>(s[i]);
-        if (lane < CL && nc > 0) store_vec<float, CG>(to + c0, s, nc);
     };
+    // what a gate's pixels give: dg, and s1 and s0 as parts of dw and db
+    auto finish = [&](const float* gate, float* dgp) {
+        pixel_sums(s1);
+        pixel_sums(s0);
+        if (!writes) return;
+        float w[CG], bb[CG], g[CG];
+        load_param(a.w, ch.c, 1.f, w);
+        load_param(a.b, ch.c, 0.f, bb);
+        load_param(gate, ch.c, 1.f, g);
+#pragma unroll
+        for (int i = 0; i < CG; ++i) {
+            w[i] = a.keep * fmaf(w[i], s1[i], bb[i] * s0[i]);
+            s1[i] *= g[i] * a.keep;
+            s0[i] *= g[i] * a.keep;
+        }
+        if (dgp) store_vec<float, CG>(dgp + ch.c, w);
+    };
+    if (by_sample && writes) {
+#pragma unroll
+        for (int i = 0; i < CG; ++i) acc[i] = acc[W + i] = 0.f;
+    }
     const long long t0 = blockIdx.x * pt.per_wg, t1 = min(t0 + pt.per_wg, pt.tiles);
     for (long long t = t0; t < t1; ++t) {
         const long long b = t / pt.tps;
-        const Place<CL, PV> at(a, (int)(t - b * pt.tps));
-        const bool kept = a.drop != DROP_SAMPLE || sample_kept(a, (int)b);
+        const Pixels<CL, PV> px(a.HW, (int)(t - b * pt.tps));
+        const bool in = a.drop != DROP_SAMPLE || sample_kept(a, (int)b), on = ch.on && px.on;
         const size_t first = (size_t)b * a.C * a.HW;
-        const size_t planar = first + (size_t)at.c0 * a.HW + at.p0, rows = first + (size_t)at.p0 * a.C + at.c0;
-        const size_t oh = HCL ? rows : planar, oy = YCL ? rows : planar;
-        const size_t sh = HCL ? a.C : a.HW, sy = YCL ? a.C : a.HW;
+        const uint32_t planar = (uint32_t)ch.c * a.HW + px.p, rows = (uint32_t)px.p * a.C + ch.c;
+        const uint32_t oh = (HCL ? rows : planar) * sizeof(TH), oy = (YCL ? rows : planar) * sizeof(TY);
         Patch<TH, HCL, PV> h;
         Patch<TY, YCL, PV> d;
-        h.load((const TH*)a.h + oh, sh, at.nc, kept ? at.np : 0);
-        d.load((const TY*)a.dy + oy, sy, at.nc, at.np);
-        if (a.dxs) {
+        h.zero();
+        d.zero();
+        if (on) {
+            if (in) h.load((const TH*)a.h + first, oh, sh);
+            d.load((const TY*)a.dy + first, oy, sy);
+        }
+        float fp[PV];
+#pragma unroll
+        for (int j = 0; j < PV; ++j) fp[j] = px.weight(j);
+        if (a.dxs && on) {
             Patch<TY, YCL, PV> x;
-            x.load((const TY*)a.x + oy, sy, at.nc, at.np);
+            x.load((const TY*)a.x + first, oy, sy);
 #pragma unroll
             for (int i = 0; i < CG; ++i)
 #pragma unroll
-                for (int j = 0; j < PV; ++j) ds[i] = fmaf(j >= at.skip ? d.at(i, j) : 0.f, x.at(i, j), ds[i]);
+                for (int j = 0; j < PV; ++j) sx[i] = fmaf(d.at(i, j) * fp[j], x.at(i, j), sx[i]);
         }
-        if (a.dx && at.np > 0) {
+        if (a.dx && on) {
             float xs[CG];
-            load_param(a.xs, at.c0, at.nc, 1.f, xs);
-            store_patch<TY, YCL, PV>((TY*)a.dx + oy, sy, at.nc, at.np,
-                                     [&](int i, int j) { return d.at(i, j) * xs[i]; });
+            load_param(a.xs, ch.c, 1.f, xs);
+            store_patch<TY, YCL, PV>((TY*)a.dx + first, oy, sy, [&](int i, int j) { return d.at(i, j) * xs[i]; });
         }
-        float mean[PV], r[PV];
-        patch_stats<TH, HCL, CL, PV>(a, h, at.nc, red, turn, mean, r);
+        d.renew();
+        float mean[PV], r[PV], f[CG];
+#pragma unroll
+        for (int i = 0; i < CG; ++i) f[i] = ch.weight(i);
+        patch_stats<TH, HCL, CL, PV>(a, h, f, red, turn, mean, r);
         uint32_t m[PV];
-        patch_keep<PV>(a, b * a.HW + at.p0, at.c0, kept, m);
-        float w[CG], bb[CG], g[CG];
-        load_param(a.w, at.c0, at.nc, 1.f, w);
-        load_param(a.b, at.c0, at.nc, 0.f, bb);
-        load_param(sample_gate ? a.gate + b * a.C : a.gate, at.c0, at.nc, 1.f, g);
+        patch_drop<PV>(a, b * a.HW + px.p, ch.c, in, m);
+        float gw[CG];   // u = e gw
+        const float* gate = by_sample ? a.gate + b * a.C : a.gate;
+        {
+            float g[CG];
+            load_param(a.w, ch.c, 1.f, gw);
+            load_param(gate, ch.c, 1.f, g);
+#pragma unroll
+            for (int i = 0; i < CG; ++i) gw[i] *= g[i] * a.keep;
+        }
         float ms[2][PV] = {};
 #pragma unroll
         for (int i = 0; i < CG; ++i)
 #pragma unroll
             for (int j = 0; j < PV; ++j) {
-                // dy is zero past the channels and past the plane
-                const bool k = m[j] >> i & 1;
-                const float z = (h.at(i, j) - mean[j]) * r[j], di = d.at(i, j);
-                const float dv = k ? di * g[i] * a.keep : 0.f, u = dv * w[i];
+                const float z = (h.at(i, j) - mean[j]) * r[j], e = kept(d.at(i, j), m[j], i), u = e * (gw[i] * f[i]);
                 ms[0][j] += u;
                 ms[1][j] = fmaf(u, z, ms[1][j]);
-                const bool own = j >= at.skip;
-                const float dvo = own ? dv : 0.f;
-                dw[i] = fmaf(dvo, z, dw[i]);
-                db[i] += dvo;
-                dg[i] = fmaf(own && k ? di : 0.f, fmaf(z, w[i], bb[i]) * a.keep, dg[i]);
+                const float once = e * fp[j];
+                s1[i] = fmaf(once, z, s1[i]);
+                s0[i] += once;
             }
         if (a.dh) {
             if (a.norm != NORM_NONE) {
@@ -275,32 +333,48 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
                     ms[1][j] *= inv;
                 }
             }
-            // z and u are made again from h and dy rather than kept: an
-            // operand that the compiler cannot follow keeps it from holding
-            // 16 PV values across the sums
-            float keep = a.keep;
+            h.renew();   // z and u are made again, too
+            d.renew();
 #pragma unroll
-            for (int j = 0; j < PV; ++j) asm volatile("" : "+v"(mean[j]));
-            asm volatile("" : "+v"(keep));
-            if (at.np > 0)
-                store_patch<TH, HCL, PV>((TH*)a.dh + oh, sh, at.nc, at.np, [&](int i, int j) {
-                    const float u = m[j] >> i & 1 ? d.at(i, j) * g[i] * keep * w[i] : 0.f;
-                    const float z = (h.at(i, j) - mean[j]) * r[j];
+            for (int j = 0; j < PV; ++j) asm volatile("" : "+v"(m[j]));
+            if (on)
+                store_patch<TH, HCL, PV>((TH*)a.dh + first, oh, sh, [&](int i, int j) {
+                    const float u = kept(d.at(i, j), m[j], i) * gw[i], z = (h.at(i, j) - mean[j]) * r[j];
                     return a.norm == NORM_NONE ? u : r[j] * (u - ms[0][j] - z * ms[1][j]);
                 });
         }
         // the last tile of this sample in the workgroup's range
         if (by_sample && (t + 1 == t1 || (t + 1) % pt.tps == 0)) {
             const bool whole = b * pt.tps >= t0 && (b + 1) * pt.tps <= t1;
-            put(dg, whole ? a.dg + b * a.C : slot + (size_t)(pt.nsum + (b == t0 / pt.tps ? 0 : 1)) * a.C);
+            finish(gate, !a.dg   ? nullptr
+                         : whole ? a.dg + b * a.C
+                                 : slot + (size_t)(pt.nsum + (b == t0 / pt.tps ? 0 : 1)) * a.C);
+            if (writes) {
 #pragma unroll
-            for (int i = 0; i < CG; ++i) dg[i] = 0.f;
+                for (int i = 0; i < CG; ++i) {
+                    acc[i] += s1[i];
+                    acc[W + i] += s0[i];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < CG; ++i) s1[i] = s0[i] = 0.f;
         }
     }
-    if (sl.dw >= 0) put(dw, slot + (size_t)sl.dw * a.C);
-    if (sl.db >= 0) put(db, slot + (size_t)sl.db * a.C);
-    if (sl.dg >= 0) put(dg, slot + (size_t)sl.dg * a.C);
-    if (sl.dxs >= 0) put(ds, slot + (size_t)sl.dxs * a.C);
+    if (!by_sample) {
+        finish(a.gate, sl.dg >= 0 ? slot + (size_t)sl.dg * a.C : nullptr);
+    } else if (writes) {
+#pragma unroll
+        for (int i = 0; i < CG; ++i) {
+            s1[i] = acc[i];
+            s0[i] = acc[W + i];
+        }
+    }
+    if (writes && sl.dw >= 0) store_vec<float, CG>(slot + (size_t)sl.dw * a.C + ch.c, s1);
+    if (writes && sl.db >= 0) store_vec<float, CG>(slot + (size_t)sl.db * a.C + ch.c, s0);
+    if (sl.dxs >= 0) {
+        pixel_sums(sx);
+        if (writes) store_vec<float, CG>(slot + (size_t)sl.dxs * a.C + ch.c, sx);
+    }
 }
 
 // The shape of a call's tiles.
@@ -310,9 +384,13 @@ struct TileShape {
 };
 // Channel lanes: the choice among 4, 8 and 16 with the fewest wavefronts over
 // a sample (idle lanes past C and past the plane cost as much as busy ones).
-// cl = 0: more channels than sixteen wavefronts hold.
+// cl = 0: fewer channels or pixels than a lane's, more channels than sixteen
+// wavefronts hold, or a sample of 2^30 elements.
 inline TileShape tile_shape(const BlockArgs& a, int pv) {
     TileShape best{};
+    if (a.C < CG || a.HW < pv) return best;
+    // a lane's place in its sample is a 32-bit number of bytes
+    if ((uint64_t)a.C * a.HW * sizeof(float) >= 1ull << 32) return best;
     long long least = 0;
     for (int cl : {8, 4, 16}) {
         const int nw = cdiv(a.C, cl * CG), px = 64 / cl * pv, tps = cdiv(a.HW, px);
@@ -366,9 +444,10 @@ hipError_t tile_fwd_typed(const BlockArgs& a, const TileShape& t, hipStream_t s)
 template <typename TH, bool HCL, typename TY, bool YCL, int PV>
 hipError_t tile_bwd_typed(const BlockArgs& a, const TileShape& t, const Partition& p, hipStream_t s) {
     const dim3 grid((unsigned)p.wgs), block(64 * t.nw);
+    const size_t lds = tile_lds(t) + (a.gate_mode == GATE_SAMPLE ? sizeof(float) * 2 * t.nw * t.cl * CG : 0);
 #define WTC_CALL(CL, MAXT)                                                                                          \
     [&] {                                                                                                          \
-        hipLaunchKernelGGL((k_tile_bwd<TH, HCL, TY, YCL, CL, PV, MAXT>), grid, block, tile_lds(t), s, a, p,        \
+        hipLaunchKernelGGL((k_tile_bwd<TH, HCL, TY, YCL, CL, PV, MAXT>), grid, block, lds, s, a, p,                \
                            sum_slots(a), a.ws);                                                                    \
         return hipGetLastError();                                                                                  \
     }()
