@@ -41,6 +41,7 @@ struct BlockArgs {
     int h_cl, y_cl;     // channels last
     int norm, gate_mode, drop;
     float eps;
+    float inv_c;        // 1 / C
     uint32_t thr;       // an element is kept when its 16 bits are >= thr
     float keep;         // 65536 / (65536 - thr); 0 where thr = 65536
     uint32_t site;

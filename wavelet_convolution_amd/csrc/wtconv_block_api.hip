@@ -49,6 +49,7 @@ wtc::BlockArgs args_of(const wtconv_block_desc_t* d) {
     a.y_cl = same || d->y_layout == WTCONV_NHWC;
     a.norm = d->norm;
     a.eps = d->eps;
+    a.inv_c = 1.f / (float)d->C;
     a.gate_mode = d->gate;
     a.drop = wtc::DROP_NONE;
     a.keep = 1.f;

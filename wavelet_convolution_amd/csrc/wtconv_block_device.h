@@ -9,6 +9,9 @@ namespace wtc {
 // Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as
 // easy as 1, 2, 3", 2011): ten rounds of two 32 x 32 -> 64 bit products on a
 // 128-bit counter, the key stepped by two constants each round.
+__device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) {
+    return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96);
+}
 struct Philox {
     uint32_t k0, k1, site, o0, o1;
     __device__ __forceinline__ Philox(const unsigned long long* rng, uint32_t site_) : site(site_) {
@@ -23,7 +26,7 @@ struct Philox {
 #pragma unroll
         for (int i = 0; i < 10; ++i) {
             const uint64_t p = (uint64_t)c0 * 0xD2511F53u, q = (uint64_t)c2 * 0xCD9E8D57u;
-            const uint32_t n0 = (uint32_t)(q >> 32) ^ c1 ^ a, n2 = (uint32_t)(p >> 32) ^ c3 ^ b;
+            const uint32_t n0 = xor3((uint32_t)(q >> 32), c1, a), n2 = xor3((uint32_t)(p >> 32), c3, b);
             c1 = (uint32_t)q;
             c3 = (uint32_t)p;
             c0 = n0;
@@ -49,12 +52,13 @@ __device__ __forceinline__ uint32_t drop_bits(const uint4& r, uint32_t thr) {
 }
 constexpr uint32_t ALL_DROPPED = 0xffu;
 
-// v, or zero (whatever v is) where element e is dropped: the bit spread over
-// a word, without a comparison's lane mask.
-__device__ __forceinline__ float kept(float v, uint32_t m, int e) {
-    const uint32_t d = (uint32_t)((int32_t)(m << (24 + e)) >> 31);
+// v, or zero (whatever v is) where the bit is set: the bit spread over a
+// word, without a comparison's lane mask.
+__device__ __forceinline__ float zero_if(float v, uint32_t m, int bit) {
+    const uint32_t d = (uint32_t)((int32_t)(m << (31 - bit)) >> 31);
     return __uint_as_float(__float_as_uint(v) & ~d);
 }
+__device__ __forceinline__ float kept(float v, uint32_t m, int e) { return zero_if(v, m, 7 - e); }
 
 // Drop bits of the eight channels from c on, in a row whose first group is
 // row_group: two generator groups where c is not a multiple of eight (the

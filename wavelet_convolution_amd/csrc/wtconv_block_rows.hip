@@ -113,7 +113,7 @@ __device__ __forceinline__ void row_stats(const BlockArgs& a, const Vec<TH, CG> 
     mean = 0.f;
     r = 1.f;
     if (a.norm == NORM_NONE) return;
-    const float inv = 1.f / (float)a.C;
+    const float inv = a.inv_c;
     if (a.norm == NORM_LAYER) {
         float s = 0.f;
 #pragma unroll
@@ -132,7 +132,7 @@ __device__ __forceinline__ void row_stats(const BlockArgs& a, const Vec<TH, CG> 
                 const float d = kept(h[v][i] - mean, at.twice[v], i);
                 q = fmaf(d, d, q);
             }
-    r = 1.f / sqrtf(sum.one(q) * inv + a.eps);
+    r = rsqrtf(sum.one(q) * inv + a.eps);
 }
 
 template <typename TH, typename TY, int L, int NV>
@@ -333,7 +333,7 @@ __global__ __launch_bounds__(threads_of(L)) void k_rows_bwd(BlockArgs a, Partiti
             }
         }
         if (a.norm != NORM_NONE && a.dh) {
-            const float inv = 1.f / (float)a.C;
+            const float inv = a.inv_c;
             sum.two(m1, m2);
             m1 = a.norm == NORM_LAYER ? m1 * inv : 0.f;
             m2 *= inv;

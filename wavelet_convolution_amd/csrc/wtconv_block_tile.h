@@ -13,7 +13,15 @@
 // Where HW is no multiple of PV, or C of eight, the last lane along it moves
 // back to end with it and does some of its neighbour's work again: the same
 // values to the same addresses. Sums take the elements that two lanes share
-// once, by a weight of 0 or 1. (So a tile needs HW >= PV and C >= 8.)
+// once. (So a tile needs HW >= PV and C >= 8.)
+//
+// Small planes are bound by the chain of latencies (arguments, loads, two
+// sums over channels, stores) and by instruction fetch, large ones by memory
+// with the vector instructions of an element close behind (a wavefront's
+// instruction takes four cycles: 10 instructions an element are as long as 4
+// bytes of it): so what a call does not use is compiled out (X, DROP), the
+// rare cases sit behind one branch for the whole patch, and the generator's
+// rounds stay a loop over pixels.
 #pragma once
 
 #include "wtconv_block_device.h"
@@ -69,7 +77,6 @@ struct Channels {
         c = min(first, C - CG);
         shared = on ? first - c : CG;
     }
-    __device__ __forceinline__ float weight(int i) const { return i < shared ? 0.f : 1.f; }
 };
 
 // A lane's pixels in a tile: PV from p on, of which the first `shared` are
@@ -78,14 +85,14 @@ template <int CL, int PV>
 struct Pixels {
     static constexpr int PL = 64 / CL, PX = PL * PV;   // pixel lanes, pixels of a tile
     int p, shared;
-    bool on;
+    bool on, last;   // last: the plane ends in this tile
     __device__ __forceinline__ Pixels(int HW, int tile) {
         const int first = tile * PX + threadIdx.x % 64 / CL * PV;
         on = first < HW;
         p = min(first, HW - PV);
         shared = on ? first - p : PV;
+        last = (tile + 1) * PX >= HW;
     }
-    __device__ __forceinline__ float weight(int j) const { return j < shared ? 0.f : 1.f; }
 };
 
 // Sums over all channels of PV pixel values (K sets of them) in every lane.
@@ -120,9 +127,13 @@ __device__ __forceinline__ void channel_sums(float (&s)[K][PV], float* red, int&
             for (int j = 0; j < PV; ++j) s[k][j] += buf[((w * K + k) * PL + pl) * PV + j];
 }
 
-// mean and r of a lane's pixels; f: the weights of its channels.
+// Sums over the lane's own channels come in two steps: over all eight, and
+// where C is no multiple of eight once more without those that the neighbour
+// has (a second pass rather than a branch around two forms of the first: the
+// compiler would hold what the two have in common).
+// mean and r of a lane's pixels.
 template <typename TH, bool HCL, int CL, int PV>
-__device__ __forceinline__ void patch_stats(const BlockArgs& a, Patch<TH, HCL, PV>& h, const float (&f)[CG],
+__device__ __forceinline__ void patch_stats(const BlockArgs& a, Patch<TH, HCL, PV>& h, const Channels<CL>& ch,
                                             float* red, int& turn, float (&mean)[PV], float (&r)[PV]) {
 #pragma unroll
     for (int j = 0; j < PV; ++j) {
@@ -130,17 +141,26 @@ __device__ __forceinline__ void patch_stats(const BlockArgs& a, Patch<TH, HCL, P
         r[j] = 1.f;
     }
     if (a.norm == NORM_NONE) return;
-    const float inv = 1.f / (float)a.C;
+    const float inv = a.inv_c;
     float s[1][PV];
     if (a.norm == NORM_LAYER) {
 #pragma unroll
         for (int j = 0; j < PV; ++j) {
             s[0][j] = 0.f;
 #pragma unroll
-            for (int i = 0; i < CG; ++i) s[0][j] = fmaf(h.at(i, j), f[i], s[0][j]);
+            for (int i = 0; i < CG; ++i) s[0][j] += h.at(i, j);
+        }
+        h.renew();
+        if (a.C % CG) {
+#pragma unroll
+            for (int j = 0; j < PV; ++j) {
+                s[0][j] = 0.f;
+#pragma unroll
+                for (int i = 0; i < CG; ++i) s[0][j] += i < ch.shared ? 0.f : h.at(i, j);
+            }
+            h.renew();
         }
         channel_sums<CL, PV, 1>(s, red, turn);
-        h.renew();
 #pragma unroll
         for (int j = 0; j < PV; ++j) mean[j] = s[0][j] * inv;
     }
@@ -150,39 +170,65 @@ __device__ __forceinline__ void patch_stats(const BlockArgs& a, Patch<TH, HCL, P
 #pragma unroll
         for (int i = 0; i < CG; ++i) {
             const float d = h.at(i, j) - mean[j];
-            s[0][j] = fmaf(d * f[i], d, s[0][j]);
+            s[0][j] = fmaf(d, d, s[0][j]);
         }
+        s[0][j] = ch.on ? s[0][j] : 0.f;
+    }
+    h.renew();
+    if (a.C % CG) {
+#pragma unroll
+        for (int j = 0; j < PV; ++j) {
+            s[0][j] = 0.f;
+#pragma unroll
+            for (int i = 0; i < CG; ++i) {
+                const float d = i < ch.shared ? 0.f : h.at(i, j) - mean[j];
+                s[0][j] = fmaf(d, d, s[0][j]);
+            }
+        }
+        h.renew();
     }
     channel_sums<CL, PV, 1>(s, red, turn);
-    h.renew();
 #pragma unroll
-    for (int j = 0; j < PV; ++j) r[j] = 1.f / sqrtf(s[0][j] * inv + a.eps);
+    for (int j = 0; j < PV; ++j) r[j] = rsqrtf(s[0][j] * inv + a.eps);
 }
 
-// Drop bits of a lane's pixels (eight channels each).
+// Drop bits of a lane's elements: a byte for each pixel, the first at the top
+// of a word.
 template <int PV>
-__device__ __forceinline__ void patch_drop(const BlockArgs& a, long long row, int c, bool in, uint32_t (&m)[PV]) {
-    if (a.drop == DROP_ELEMENT) {
+struct Drops {
+    uint32_t w[(PV + 3) / 4];
+    __device__ __forceinline__ void draw(const BlockArgs& a, uint32_t row, int c) {
         const Philox gen(a.rng, a.site);
         const uint32_t G = (uint32_t)cdiv(a.C, CG);
+        uint32_t g = row * G;   // fewer than 2^32 groups in all
 #pragma unroll
-        for (int j = 0; j < PV; ++j) m[j] = drop_bits_at(gen, (uint32_t)(row + j) * G, c, a.C % CG != 0, a.thr);
-    } else {
-#pragma unroll
-        for (int j = 0; j < PV; ++j) m[j] = in ? 0u : ALL_DROPPED;
+        for (int k = 0; k < (PV + 3) / 4; ++k) {
+            uint32_t m = 0;
+#pragma unroll 2
+            for (int j = 0; j < 4 && j < PV; ++j, g += G) m = m << 8 | drop_bits_at(gen, g, c, a.C % CG != 0, a.thr);
+            w[k] = m;
+        }
     }
-}
+    __device__ __forceinline__ float kept(float v, int i, int j) const {
+        return zero_if(v, w[j / 4], 8 * ((PV < 4 ? PV : 4) - 1 - j % 4) + 7 - i);
+    }
+    __device__ __forceinline__ void renew() {
+#pragma unroll
+        for (int k = 0; k < (PV + 3) / 4; ++k) asm volatile("" : "+v"(w[k]));
+    }
+};
 
-template <typename TH, bool HCL, typename TY, bool YCL, int CL, int PV, int MAXT>
-__global__ __launch_bounds__(MAXT) void k_tile_fwd(BlockArgs a, long long tiles, int tps) {
+// X: a residual (else a norm alone); DROP: elements are dropped.
+template <typename TH, bool HCL, typename TY, bool YCL, int CL, int PV, int MAXT, bool X, bool DROP>
+__global__ __launch_bounds__(MAXT) void k_tile_fwd(BlockArgs a, unsigned tiles, unsigned tps) {
     extern __shared__ float red[];
     int turn = 0;
     const Channels<CL> ch(a.C);
     const size_t sh = HCL ? a.C : a.HW, sy = YCL ? a.C : a.HW;
-    for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const long long b = t / tps;
+    for (unsigned t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const unsigned b = t / tps;
         const Pixels<CL, PV> px(a.HW, (int)(t - b * tps));
-        const bool in = a.drop != DROP_SAMPLE || sample_kept(a, (int)b), on = ch.on && px.on;
+        const bool in = !X || a.drop != DROP_SAMPLE || sample_kept(a, (int)b), on = ch.on && px.on;
         const size_t first = (size_t)b * a.C * a.HW;
         const uint32_t planar = (uint32_t)ch.c * a.HW + px.p, rows = (uint32_t)px.p * a.C + ch.c;
         const uint32_t oh = (HCL ? rows : planar) * sizeof(TH), oy = (YCL ? rows : planar) * sizeof(TY);
@@ -191,31 +237,33 @@ __global__ __launch_bounds__(MAXT) void k_tile_fwd(BlockArgs a, long long tiles,
         h.zero();   // a dropped sample's h is not looked at
         if (on) {
             if (in) h.load((const TH*)a.h + first, oh, sh);
-            if (a.x) x.load((const TY*)a.x + first, oy, sy);
+            if constexpr (X) x.load((const TY*)a.x + first, oy, sy);
         }
-        float mean[PV], r[PV], f[CG];
-#pragma unroll
-        for (int i = 0; i < CG; ++i) f[i] = ch.weight(i);
-        patch_stats<TH, HCL, CL, PV>(a, h, f, red, turn, mean, r);
-        if (!on) continue;
-        uint32_t m[PV];
-        if (a.drop != DROP_NONE) patch_drop<PV>(a, b * a.HW + px.p, ch.c, in, m);
         // y = s x + D'(z wg + bg), with the gate and D's factor in wg and bg
-        float wg[CG], bg[CG], g[CG], xs[CG];
+        float wg[CG], bg[CG], xs[CG];
         load_param(a.w, ch.c, 1.f, wg);
         load_param(a.b, ch.c, 0.f, bg);
-        load_param(a.gate_mode == GATE_SAMPLE ? a.gate + b * a.C : a.gate, ch.c, 1.f, g);
-        load_param(a.xs, ch.c, 1.f, xs);
+        if constexpr (X) {
+            float g[CG];
+            load_param(a.gate_mode == GATE_SAMPLE ? a.gate + (size_t)b * a.C : a.gate, ch.c, 1.f, g);
+            load_param(a.xs, ch.c, 1.f, xs);
 #pragma unroll
-        for (int i = 0; i < CG; ++i) {
-            g[i] *= a.keep;
-            wg[i] *= g[i];
-            bg[i] *= g[i];
+            for (int i = 0; i < CG; ++i) {
+                g[i] *= a.keep;
+                wg[i] = in ? wg[i] * g[i] : 0.f;
+                bg[i] = in ? bg[i] * g[i] : 0.f;
+            }
         }
+        float mean[PV], r[PV];
+        patch_stats<TH, HCL, CL, PV>(a, h, ch, red, turn, mean, r);
+        if (!on) continue;
+        Drops<PV> drop;
+        if constexpr (DROP) drop.draw(a, (uint32_t)b * a.HW + px.p, ch.c);
         store_patch<TY, YCL, PV>((TY*)a.y + first, oy, sy, [&](int i, int j) {
             float o = fmaf((h.at(i, j) - mean[j]) * r[j], wg[i], bg[i]);
-            if (a.drop != DROP_NONE) o = kept(o, m[j], i);
-            return a.x ? fmaf(xs[i], x.at(i, j), o) : o;
+            if constexpr (DROP) o = drop.kept(o, i, j);
+            if constexpr (X) o = fmaf(xs[i], x.at(i, j), o);
+            return o;
         });
     }
 }
@@ -225,7 +273,7 @@ __global__ __launch_bounds__(MAXT) void k_tile_fwd(BlockArgs a, long long tiles,
 //   dw = g k S1, db = g k S0, dg = k (w S1 + b S0)          (k: D's factor),
 // so the loop adds two sums, whatever is wanted. With a gate per sample, dw
 // and db add up over a workgroup's samples in LDS.
-template <typename TH, bool HCL, typename TY, bool YCL, int CL, int PV, int MAXT>
+template <typename TH, bool HCL, typename TY, bool YCL, int CL, int PV, int MAXT, bool DROP>
 __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, SumSlots sl, float* slots) {
     extern __shared__ float lds[];
     const bool by_sample = a.gate_mode == GATE_SAMPLE;
@@ -263,10 +311,11 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
 #pragma unroll
         for (int i = 0; i < CG; ++i) acc[i] = acc[W + i] = 0.f;
     }
-    const long long t0 = blockIdx.x * pt.per_wg, t1 = min(t0 + pt.per_wg, pt.tiles);
-    for (long long t = t0; t < t1; ++t) {
-        const long long b = t / pt.tps;
-        const Pixels<CL, PV> px(a.HW, (int)(t - b * pt.tps));
+    const unsigned tps = (unsigned)pt.tps, t0 = blockIdx.x * (unsigned)pt.per_wg;
+    const unsigned t1 = min(t0 + (unsigned)pt.per_wg, (unsigned)pt.tiles);
+    for (unsigned t = t0; t < t1; ++t) {
+        const unsigned b = t / tps;
+        const Pixels<CL, PV> px(a.HW, (int)(t - b * tps));
         const bool in = a.drop != DROP_SAMPLE || sample_kept(a, (int)b), on = ch.on && px.on;
         const size_t first = (size_t)b * a.C * a.HW;
         const uint32_t planar = (uint32_t)ch.c * a.HW + px.p, rows = (uint32_t)px.p * a.C + ch.c;
@@ -279,16 +328,13 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
             if (in) h.load((const TH*)a.h + first, oh, sh);
             d.load((const TY*)a.dy + first, oy, sy);
         }
-        float fp[PV];
-#pragma unroll
-        for (int j = 0; j < PV; ++j) fp[j] = px.weight(j);
         if (a.dxs && on) {
             Patch<TY, YCL, PV> x;
             x.load((const TY*)a.x + first, oy, sy);
 #pragma unroll
             for (int i = 0; i < CG; ++i)
 #pragma unroll
-                for (int j = 0; j < PV; ++j) sx[i] = fmaf(d.at(i, j) * fp[j], x.at(i, j), sx[i]);
+                for (int j = 0; j < PV; ++j) sx[i] += j < px.shared ? 0.f : d.at(i, j) * x.at(i, j);
         }
         if (a.dx && on) {
             float xs[CG];
@@ -296,14 +342,19 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
             store_patch<TY, YCL, PV>((TY*)a.dx + first, oy, sy, [&](int i, int j) { return d.at(i, j) * xs[i]; });
         }
         d.renew();
-        float mean[PV], r[PV], f[CG];
-#pragma unroll
-        for (int i = 0; i < CG; ++i) f[i] = ch.weight(i);
-        patch_stats<TH, HCL, CL, PV>(a, h, f, red, turn, mean, r);
-        uint32_t m[PV];
-        patch_drop<PV>(a, b * a.HW + px.p, ch.c, in, m);
+        float mean[PV], r[PV];
+        patch_stats<TH, HCL, CL, PV>(a, h, ch, red, turn, mean, r);
+        if (!in) d.zero();   // the same for every lane: no gradient passes a dropped sample
+        Drops<PV> drop;
+        if constexpr (DROP) {
+            if (on) drop.draw(a, (uint32_t)b * a.HW + px.p, ch.c);
+        }
+        auto kept = [&](float v, int i, int j) {
+            if constexpr (DROP) return drop.kept(v, i, j);
+            return v;
+        };
         float gw[CG];   // u = e gw
-        const float* gate = by_sample ? a.gate + b * a.C : a.gate;
+        const float* gate = by_sample ? a.gate + (size_t)b * a.C : a.gate;
         {
             float g[CG];
             load_param(a.w, ch.c, 1.f, gw);
@@ -311,44 +362,83 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
 #pragma unroll
             for (int i = 0; i < CG; ++i) gw[i] *= g[i] * a.keep;
         }
-        float ms[2][PV] = {};
+        // over pixels, for the channels' gradients, and over channels, for the
+        // norm's; then again without what a neighbour has
+        float p1[CG] = {}, p0[CG] = {}, ms[2][PV] = {};
 #pragma unroll
         for (int i = 0; i < CG; ++i)
 #pragma unroll
             for (int j = 0; j < PV; ++j) {
-                const float z = (h.at(i, j) - mean[j]) * r[j], e = kept(d.at(i, j), m[j], i), u = e * (gw[i] * f[i]);
+                const float z = (h.at(i, j) - mean[j]) * r[j], e = kept(d.at(i, j), i, j), u = e * gw[i];
+                p1[i] = fmaf(e, z, p1[i]);
+                p0[i] += e;
                 ms[0][j] += u;
                 ms[1][j] = fmaf(u, z, ms[1][j]);
-                const float once = e * fp[j];
-                s1[i] = fmaf(once, z, s1[i]);
-                s0[i] += once;
             }
+        auto renew = [&] {
+            h.renew();
+            d.renew();
+            if constexpr (DROP) drop.renew();
+        };
+        renew();
+        if (px.last && a.HW % PV) {   // a tile at the end of such a plane
+#pragma unroll
+            for (int i = 0; i < CG; ++i) {
+                p1[i] = p0[i] = 0.f;
+#pragma unroll
+                for (int j = 0; j < PV; ++j) {
+                    const float z = (h.at(i, j) - mean[j]) * r[j];
+                    const float e = j < px.shared ? 0.f : kept(d.at(i, j), i, j);
+                    p1[i] += j < px.shared ? 0.f : e * z;
+                    p0[i] += e;
+                }
+            }
+            renew();
+        }
+#pragma unroll
+        for (int i = 0; i < CG; ++i) {
+            s1[i] += p1[i];
+            s0[i] += p0[i];
+        }
         if (a.dh) {
             if (a.norm != NORM_NONE) {
-                const float inv = 1.f / (float)a.C;
+                if (a.C % CG) {
+#pragma unroll
+                    for (int j = 0; j < PV; ++j) {
+                        ms[0][j] = ms[1][j] = 0.f;
+#pragma unroll
+                        for (int i = 0; i < CG; ++i) {
+                            const float u = i < ch.shared ? 0.f : kept(d.at(i, j), i, j) * gw[i];
+                            ms[0][j] += u;
+                            ms[1][j] += i < ch.shared ? 0.f : u * ((h.at(i, j) - mean[j]) * r[j]);
+                        }
+                    }
+                    renew();
+                }
+                const float inv = a.inv_c;
                 channel_sums<CL, PV, 2>(ms, red, turn);
 #pragma unroll
                 for (int j = 0; j < PV; ++j) {
                     ms[0][j] = a.norm == NORM_LAYER ? ms[0][j] * inv : 0.f;
                     ms[1][j] *= inv;
                 }
-            }
-            h.renew();   // z and u are made again, too
-            d.renew();
+            } else {
+                h.zero();   // dh = u
 #pragma unroll
-            for (int j = 0; j < PV; ++j) asm volatile("" : "+v"(m[j]));
+                for (int j = 0; j < PV; ++j) ms[0][j] = ms[1][j] = 0.f;
+            }
             if (on)
                 store_patch<TH, HCL, PV>((TH*)a.dh + first, oh, sh, [&](int i, int j) {
-                    const float u = kept(d.at(i, j), m[j], i) * gw[i], z = (h.at(i, j) - mean[j]) * r[j];
-                    return a.norm == NORM_NONE ? u : r[j] * (u - ms[0][j] - z * ms[1][j]);
+                    const float u = kept(d.at(i, j), i, j) * gw[i], z = (h.at(i, j) - mean[j]) * r[j];
+                    return r[j] * (u - ms[0][j] - z * ms[1][j]);
                 });
         }
         // the last tile of this sample in the workgroup's range
-        if (by_sample && (t + 1 == t1 || (t + 1) % pt.tps == 0)) {
-            const bool whole = b * pt.tps >= t0 && (b + 1) * pt.tps <= t1;
+        if (by_sample && (t + 1 == t1 || (t + 1) % tps == 0)) {
+            const bool whole = b * tps >= t0 && (b + 1) * tps <= t1;
             finish(gate, !a.dg   ? nullptr
-                         : whole ? a.dg + b * a.C
-                                 : slot + (size_t)(pt.nsum + (b == t0 / pt.tps ? 0 : 1)) * a.C);
+                         : whole ? a.dg + (size_t)b * a.C
+                                 : slot + (size_t)(pt.nsum + (b == t0 / tps ? 0 : 1)) * a.C);
             if (writes) {
 #pragma unroll
                 for (int i = 0; i < CG; ++i) {
@@ -385,7 +475,7 @@ struct TileShape {
 // Channel lanes: the choice among 4, 8 and 16 with the fewest wavefronts over
 // a sample (idle lanes past C and past the plane cost as much as busy ones).
 // cl = 0: fewer channels or pixels than a lane's, more channels than sixteen
-// wavefronts hold, or a sample of 2^30 elements.
+// wavefronts hold, a sample of 2^30 elements, or 2^30 tiles.
 inline TileShape tile_shape(const BlockArgs& a, int pv) {
     TileShape best{};
     if (a.C < CG || a.HW < pv) return best;
@@ -395,6 +485,7 @@ inline TileShape tile_shape(const BlockArgs& a, int pv) {
     for (int cl : {8, 4, 16}) {
         const int nw = cdiv(a.C, cl * CG), px = 64 / cl * pv, tps = cdiv(a.HW, px);
         const long long waves = (long long)nw * tps;
+        if ((long long)a.B * tps >= 1ll << 30) continue;   // tiles are counted in 32 bits
         if (nw > (cl == 16 ? 16 : 8) || (best.cl && waves >= least)) continue;
         best = TileShape{cl, pv, nw, px, tps};
         least = waves;
@@ -427,15 +518,36 @@ inline size_t tile_lds(const TileShape& t) { return t.nw > 1 ? (size_t)2 * t.nw 
     if (t.nw <= 8) return CALL(16, 512);           \
     return CALL(16, 1024);
 
+template <typename TH, bool HCL, typename TY, bool YCL, int PV, bool X, bool DROP>
+hipError_t tile_fwd_mode(const BlockArgs& a, const TileShape& t, hipStream_t s) {
+    const unsigned tiles = (unsigned)a.B * (unsigned)t.tps;
+    const dim3 grid(tiles < (1u << 21) ? tiles : (1u << 21)), block(64 * t.nw);
+#define WTC_CALL(CL, MAXT)                                                                                     \
+    [&] {                                                                                                      \
+        hipLaunchKernelGGL((k_tile_fwd<TH, HCL, TY, YCL, CL, PV, MAXT, X, DROP>), grid, block, tile_lds(t), s, \
+                           a, tiles, (unsigned)t.tps);                                                         \
+        return hipGetLastError();                                                                              \
+    }()
+    WTC_TILE_SHAPES(WTC_CALL)
+#undef WTC_CALL
+}
+
 template <typename TH, bool HCL, typename TY, bool YCL, int PV>
 hipError_t tile_fwd_typed(const BlockArgs& a, const TileShape& t, hipStream_t s) {
-    const long long tiles = (long long)a.B * t.tps;
-    const dim3 grid((unsigned)(tiles < (1 << 21) ? tiles : (1 << 21))), block(64 * t.nw);
-#define WTC_CALL(CL, MAXT)                                                                                          \
-    [&] {                                                                                                          \
-        hipLaunchKernelGGL((k_tile_fwd<TH, HCL, TY, YCL, CL, PV, MAXT>), grid, block, tile_lds(t), s, a, tiles,    \
-                           t.tps);                                                                                 \
-        return hipGetLastError();                                                                                  \
+    if (!a.x) return tile_fwd_mode<TH, HCL, TY, YCL, PV, false, false>(a, t, s);
+    if (a.drop == DROP_ELEMENT) return tile_fwd_mode<TH, HCL, TY, YCL, PV, true, true>(a, t, s);
+    return tile_fwd_mode<TH, HCL, TY, YCL, PV, true, false>(a, t, s);
+}
+
+template <typename TH, bool HCL, typename TY, bool YCL, int PV, bool DROP>
+hipError_t tile_bwd_mode(const BlockArgs& a, const TileShape& t, const Partition& p, hipStream_t s) {
+    const dim3 grid((unsigned)p.wgs), block(64 * t.nw);
+    const size_t lds = tile_lds(t) + (a.gate_mode == GATE_SAMPLE ? sizeof(float) * 2 * t.nw * t.cl * CG : 0);
+#define WTC_CALL(CL, MAXT)                                                                                     \
+    [&] {                                                                                                      \
+        hipLaunchKernelGGL((k_tile_bwd<TH, HCL, TY, YCL, CL, PV, MAXT, DROP>), grid, block, lds, s, a, p,      \
+                           sum_slots(a), a.ws);                                                                \
+        return hipGetLastError();                                                                              \
     }()
     WTC_TILE_SHAPES(WTC_CALL)
 #undef WTC_CALL
@@ -443,16 +555,8 @@ hipError_t tile_fwd_typed(const BlockArgs& a, const TileShape& t, hipStream_t s)
 
 template <typename TH, bool HCL, typename TY, bool YCL, int PV>
 hipError_t tile_bwd_typed(const BlockArgs& a, const TileShape& t, const Partition& p, hipStream_t s) {
-    const dim3 grid((unsigned)p.wgs), block(64 * t.nw);
-    const size_t lds = tile_lds(t) + (a.gate_mode == GATE_SAMPLE ? sizeof(float) * 2 * t.nw * t.cl * CG : 0);
-#define WTC_CALL(CL, MAXT)                                                                                          \
-    [&] {                                                                                                          \
-        hipLaunchKernelGGL((k_tile_bwd<TH, HCL, TY, YCL, CL, PV, MAXT>), grid, block, lds, s, a, p,                \
-                           sum_slots(a), a.ws);                                                                    \
-        return hipGetLastError();                                                                                  \
-    }()
-    WTC_TILE_SHAPES(WTC_CALL)
-#undef WTC_CALL
+    if (a.drop == DROP_ELEMENT) return tile_bwd_mode<TH, HCL, TY, YCL, PV, true>(a, t, p, s);
+    return tile_bwd_mode<TH, HCL, TY, YCL, PV, false>(a, t, p, s);
 }
 
 #define WTC_TILE_FWD(HCL, YCL)                                                                                       \
