@@ -90,8 +90,29 @@ def _empty(shape, dtype, channels_last: bool, device) -> torch.Tensor:
                        memory_format=torch.channels_last if channels_last else torch.contiguous_format)
 
 
-def _grad(wanted: bool, shape, device):
-    return torch.empty(shape, dtype=torch.float32, device=device) if wanted else None
+def _grad(wanted: bool, shape, act):
+    return act.new_empty(shape, dtype=torch.float32) if wanted else None
+
+
+# the current stream's handle, without the Stream object around it where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(act) -> int:
+    if _raw_stream is None:
+        return torch.cuda.current_stream(act.device).cuda_stream
+    return _raw_stream(act.device.index)
+
+
+def _workspace(desc, act, ws):
+    """(pointer, bytes) of the workspace, and the tensor that holds it."""
+    if ws is None:
+        n = _ws_size(desc)
+        if n == 0:
+            return 0, 0, None
+        ws = act.new_empty(n + 256, dtype=torch.uint8)
+    p = _b._ws_ptr(ws)
+    return p, _b._ws_bytes(ws), ws
 
 
 def _ws_size(desc) -> int:
@@ -134,15 +155,19 @@ def wtconv_norm_fwd(x, weight=None, bias=None, *, kind: str = "layer", eps: floa
     _b._check_f32("weight", weight, (C,), x)
     _b._check_f32("bias", bias, (C,), x)
     if y is None:
-        y = _empty(x.shape, dtype or x.dtype, hc[1] == _b.WTCONV_NHWC if channels_last is None else channels_last,
-                   x.device)
+        same = channels_last is None or bool(channels_last) == (hc[1] == _b.WTCONV_NHWC)
+        if same and (dtype is None or dtype == x.dtype):
+            y = torch.empty_like(x)
+        else:
+            y = _empty(x.shape, dtype or x.dtype, hc[1] == _b.WTCONV_NHWC if channels_last is None else channels_last,
+                       x.device)
     elif (dtype is not None and y.dtype != dtype) or (
             channels_last is not None and not y.is_contiguous(
                 memory_format=torch.channels_last if channels_last else torch.contiguous_format)):
         raise ValueError("y differs from the dtype or memory order asked for")
     d = _desc(x, hc, _act("y", y, x), _code(_NORMS, kind, "kind"), eps)
     _b._check(_b.load_library().wtconv_norm_fwd(ctypes.byref(d), x.data_ptr(), _b._ptr(weight), _b._ptr(bias),
-                                                y.data_ptr(), _b._stream(None)))
+                                                y.data_ptr(), _stream(x)))
     return y
 
 
@@ -170,12 +195,11 @@ def wtconv_norm_bwd(x, dy, weight=None, bias=None, *, kind: str = "layer", eps: 
         dx = torch.empty_like(x)
     elif _act("dx", dx, x) != hc:
         raise ValueError("dx must have x's type and memory order")
-    dweight, dbias = (_grad(n in want, (C,), x.device) for n in ("dweight", "dbias"))
-    if ws is None:
-        ws = _b._workspace(_ws_size(d), x.device)
+    dweight, dbias = (_grad(n in want, (C,), x) for n in ("dweight", "dbias"))
+    wp, wn, ws = _workspace(d, x, ws)
     _b._check(_b.load_library().wtconv_norm_bwd(
         ctypes.byref(d), x.data_ptr(), dy.data_ptr(), _b._ptr(weight), _b._ptr(dx), _b._ptr(dweight), _b._ptr(dbias),
-        _b._ws_ptr(ws), _b._ws_bytes(ws), _b._stream(None)))
+        wp, wn, _stream(x)))
     return dx, dweight, dbias
 
 
@@ -217,7 +241,7 @@ def wtconv_residual_fwd(x, h, *, kind: str = "none", weight=None, bias=None, eps
         raise ValueError("out must have x's type and memory order")
     _b._check(_b.load_library().wtconv_residual_fwd(
         ctypes.byref(d), x.data_ptr(), h.data_ptr(), _b._ptr(weight), _b._ptr(bias), _b._ptr(gate), _b._ptr(x_scale),
-        _b._ptr(rng), out.data_ptr(), _b._stream(None)))
+        _b._ptr(rng), out.data_ptr(), _stream(x)))
     return out
 
 
@@ -264,15 +288,14 @@ def wtconv_residual_bwd(dout, h, *, x=None, kind: str = "none", weight=None, bia
     elif _act("dh", dh, h) != hc:
         raise ValueError("dh must have h's type and memory order")
     C = dout.shape[1]
-    dweight, dbias = (_grad(n in want, (C,), dout.device) for n in ("dweight", "dbias"))
-    dgate = _grad("dgate" in want, gate.shape if gate is not None else (), dout.device)
-    dx_scale = _grad("dx_scale" in want, (C,), dout.device)
-    if ws is None:
-        ws = _b._workspace(_ws_size(d), dout.device)
+    dweight, dbias = (_grad(n in want, (C,), dout) for n in ("dweight", "dbias"))
+    dgate = _grad("dgate" in want, gate.shape if gate is not None else (), dout)
+    dx_scale = _grad("dx_scale" in want, (C,), dout)
+    wp, wn, ws = _workspace(d, dout, ws)
     _b._check(_b.load_library().wtconv_residual_bwd(
         ctypes.byref(d), _b._ptr(x) if dx_scale is not None else 0, h.data_ptr(), dout.data_ptr(), _b._ptr(weight),
         _b._ptr(bias), _b._ptr(gate), _b._ptr(x_scale), _b._ptr(rng), _b._ptr(dx), _b._ptr(dh), _b._ptr(dweight),
-        _b._ptr(dbias), _b._ptr(dgate), _b._ptr(dx_scale), _b._ws_ptr(ws), _b._ws_bytes(ws), _b._stream(None)))
+        _b._ptr(dbias), _b._ptr(dgate), _b._ptr(dx_scale), wp, wn, _stream(dout)))
     return (dout if alias else dx), dh, (dweight, dbias, dgate, dx_scale)
 
 
@@ -294,5 +317,5 @@ def wtconv_dropout(x, p: float, rng, *, site: int = 0, mode: str = "element", y=
         raise ValueError("y must have x's type and memory order")
     d = _desc(x, c, c, drop=drop, p=p, site=site)
     _b._check(_b.load_library().wtconv_dropout(ctypes.byref(d), x.data_ptr(), rng.data_ptr(), y.data_ptr(),
-                                               _b._stream(None)))
+                                               _stream(x)))
     return y

@@ -16,13 +16,17 @@ struct Philox {
     uint32_t k0, k1, site, o0, o1;
     __device__ __forceinline__ Philox(const unsigned long long* rng, uint32_t site_) : site(site_) {
         const unsigned long long seed = rng[0], off = rng[1];
-        k0 = (uint32_t)seed;
-        k1 = (uint32_t)(seed >> 32);
-        o0 = (uint32_t)off;
-        o1 = (uint32_t)(off >> 32);
+        // the same in every lane: scalar registers
+        k0 = __builtin_amdgcn_readfirstlane((uint32_t)seed);
+        k1 = __builtin_amdgcn_readfirstlane((uint32_t)(seed >> 32));
+        o0 = __builtin_amdgcn_readfirstlane((uint32_t)off);
+        o1 = __builtin_amdgcn_readfirstlane((uint32_t)(off >> 32));
     }
     __device__ __forceinline__ uint4 operator()(uint32_t group) const {
         uint32_t c0 = group, c1 = site, c2 = o0, c3 = o1, a = k0, b = k1;
+        // the ten keys of each half are made again by the scalar unit, not
+        // held in twenty of its registers
+        asm volatile("" : "+s"(a), "+s"(b));
 #pragma unroll
         for (int i = 0; i < 10; ++i) {
             const uint64_t p = (uint64_t)c0 * 0xD2511F53u, q = (uint64_t)c2 * 0xCD9E8D57u;

@@ -24,6 +24,8 @@
 // rounds stay a loop over pixels.
 #pragma once
 
+#include <type_traits>
+
 #include "wtconv_block_device.h"
 
 namespace wtc {
@@ -62,6 +64,7 @@ __device__ __forceinline__ void store_patch(T* __restrict__ p, uint32_t off, siz
 #pragma unroll
         for (int k = 0; k < LEN; ++k) o[k] = CLAST ? f(k, i) : f(i, k);
         store_vec<T, LEN>((T*)((char*)(p + i * step) + off), o);
+        __builtin_amdgcn_sched_barrier(0);   // a vector at a time: fewer values in flight
     }
 }
 
@@ -328,13 +331,25 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
             if (in) h.load((const TH*)a.h + first, oh, sh);
             d.load((const TY*)a.dy + first, oy, sy);
         }
+        // a tile at the end of a plane whose size is no multiple of PV: sums
+        // over pixels leave out what a neighbour has
+        const bool ends = px.last && a.HW % PV;
         if (a.dxs && on) {
             Patch<TY, YCL, PV> x;
             x.load((const TY*)a.x + first, oy, sy);
+            auto add = [&](auto masked) {
+                d.renew();   // the two forms have nothing to hold in common
 #pragma unroll
-            for (int i = 0; i < CG; ++i)
+                for (int i = 0; i < CG; ++i)
 #pragma unroll
-                for (int j = 0; j < PV; ++j) sx[i] += j < px.shared ? 0.f : d.at(i, j) * x.at(i, j);
+                    for (int j = 0; j < PV; ++j)
+                        sx[i] = fmaf(masked && j < px.shared ? 0.f : d.at(i, j),
+                                     masked && j < px.shared ? 0.f : x.at(i, j), sx[i]);
+            };
+            if (ends)
+                add(std::true_type{});
+            else
+                add(std::false_type{});
         }
         if (a.dx && on) {
             float xs[CG];
@@ -353,6 +368,11 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
             if constexpr (DROP) return drop.kept(v, i, j);
             return v;
         };
+        auto renew = [&] {
+            h.renew();
+            d.renew();
+            if constexpr (DROP) drop.renew();
+        };
         float gw[CG];   // u = e gw
         const float* gate = by_sample ? a.gate + (size_t)b * a.C : a.gate;
         {
@@ -363,74 +383,49 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
             for (int i = 0; i < CG; ++i) gw[i] *= g[i] * a.keep;
         }
         // over pixels, for the channels' gradients, and over channels, for the
-        // norm's; then again without what a neighbour has
-        float p1[CG] = {}, p0[CG] = {}, ms[2][PV] = {};
+        // norm's, without what a neighbour has; z = h r + c
+        float ms[2][PV] = {}, c[PV];
 #pragma unroll
-        for (int i = 0; i < CG; ++i)
-#pragma unroll
-            for (int j = 0; j < PV; ++j) {
-                const float z = (h.at(i, j) - mean[j]) * r[j], e = kept(d.at(i, j), i, j), u = e * gw[i];
-                p1[i] = fmaf(e, z, p1[i]);
-                p0[i] += e;
-                ms[0][j] += u;
-                ms[1][j] = fmaf(u, z, ms[1][j]);
-            }
-        auto renew = [&] {
-            h.renew();
-            d.renew();
-            if constexpr (DROP) drop.renew();
-        };
-        renew();
-        if (px.last && a.HW % PV) {   // a tile at the end of such a plane
+        for (int j = 0; j < PV; ++j) c[j] = -mean[j] * r[j];
+        auto sums = [&](auto masked) {
+            renew();
 #pragma unroll
             for (int i = 0; i < CG; ++i) {
-                p1[i] = p0[i] = 0.f;
 #pragma unroll
                 for (int j = 0; j < PV; ++j) {
-                    const float z = (h.at(i, j) - mean[j]) * r[j];
-                    const float e = j < px.shared ? 0.f : kept(d.at(i, j), i, j);
-                    p1[i] += j < px.shared ? 0.f : e * z;
-                    p0[i] += e;
+                    const float z = fmaf(h.at(i, j), r[j], c[j]), e = kept(d.at(i, j), i, j), u = e * gw[i];
+                    ms[0][j] += masked && i < ch.shared ? 0.f : u;
+                    ms[1][j] += masked && i < ch.shared ? 0.f : u * z;
+                    s0[i] += masked && j < px.shared ? 0.f : e;
+                    s1[i] += masked && j < px.shared ? 0.f : e * z;
                 }
+                __builtin_amdgcn_sched_barrier(0);   // a channel at a time: fewer values in flight
             }
-            renew();
-        }
-#pragma unroll
-        for (int i = 0; i < CG; ++i) {
-            s1[i] += p1[i];
-            s0[i] += p0[i];
-        }
+        };
+        if (ends || a.C % CG)
+            sums(std::true_type{});
+        else
+            sums(std::false_type{});
         if (a.dh) {
+            // dh = r (u - m1 - z m2) = u r + h c2 + c1
+            float c1[PV], c2[PV];
             if (a.norm != NORM_NONE) {
-                if (a.C % CG) {
-#pragma unroll
-                    for (int j = 0; j < PV; ++j) {
-                        ms[0][j] = ms[1][j] = 0.f;
-#pragma unroll
-                        for (int i = 0; i < CG; ++i) {
-                            const float u = i < ch.shared ? 0.f : kept(d.at(i, j), i, j) * gw[i];
-                            ms[0][j] += u;
-                            ms[1][j] += i < ch.shared ? 0.f : u * ((h.at(i, j) - mean[j]) * r[j]);
-                        }
-                    }
-                    renew();
-                }
-                const float inv = a.inv_c;
                 channel_sums<CL, PV, 2>(ms, red, turn);
 #pragma unroll
                 for (int j = 0; j < PV; ++j) {
-                    ms[0][j] = a.norm == NORM_LAYER ? ms[0][j] * inv : 0.f;
-                    ms[1][j] *= inv;
+                    const float m1 = a.norm == NORM_LAYER ? ms[0][j] * a.inv_c : 0.f, m2 = ms[1][j] * a.inv_c;
+                    c2[j] = -r[j] * r[j] * m2;
+                    c1[j] = -r[j] * fmaf(c[j], m2, m1);
                 }
             } else {
                 h.zero();   // dh = u
 #pragma unroll
-                for (int j = 0; j < PV; ++j) ms[0][j] = ms[1][j] = 0.f;
+                for (int j = 0; j < PV; ++j) c1[j] = c2[j] = 0.f;
             }
+            renew();
             if (on)
                 store_patch<TH, HCL, PV>((TH*)a.dh + first, oh, sh, [&](int i, int j) {
-                    const float u = kept(d.at(i, j), i, j) * gw[i], z = (h.at(i, j) - mean[j]) * r[j];
-                    return r[j] * (u - ms[0][j] - z * ms[1][j]);
+                    return fmaf(kept(d.at(i, j), i, j) * gw[i], r[j], fmaf(h.at(i, j), c2[j], c1[j]));
                 });
         }
         // the last tile of this sample in the workgroup's range
