@@ -26,6 +26,14 @@ enum { DROP_NONE = 0, DROP_ELEMENT = 1, DROP_SAMPLE = 2 };
 // Channels that share one generator call: 16 of its 128 bits each.
 constexpr int CG = 8;
 
+// What a call has and wants, as bits: the backward tiles test them inside
+// their loop (a test of a bit there is two scalar instructions; conditions
+// kept over the loop were most of its scalar registers).
+enum : uint32_t {
+    HAS_W = 1, HAS_GATE = 2, HAS_XS = 4, WANT_DX = 8, WANT_DH = 16, WANT_DXS = 32, LAYER = 64, RMS = 128,
+    BY_SAMPLE = 256, DROPS_SAMPLES = 512
+};
+
 struct BlockArgs {
     const void* h;
     const void* x;      // residual stream in (null: none)
@@ -45,6 +53,7 @@ struct BlockArgs {
     uint32_t thr;       // an element is kept when its 16 bits are >= thr
     float keep;         // 65536 / (65536 - thr); 0 where thr = 65536
     uint32_t site;
+    uint32_t flags;     // of the backward tile kernels, set at their launch
 };
 
 // The sums over rows that the parameter gradients need. Each workgroup of a

@@ -20,7 +20,7 @@ hipError_t tile_bwd_launch<true, false>(const BlockArgs&, int, int, const TileSh
 namespace {
 
 // Tiles per workgroup: two rounds of workgroups over the card (256 CUs with
-// twelve wavefronts each at the kernels' registers). More tiles each leave the
+// sixteen wavefronts each at the kernels' registers). More tiles each leave the
 // last round ragged (64x96x56x56 with gate, dropout and residual scale: 75.6
 // us at one round, 69.6 at two, 69.1 at six), fewer write more partial sums.
 Partition tile_partition(const BlockArgs& a, const TileShape& t) {
@@ -28,7 +28,7 @@ Partition tile_partition(const BlockArgs& a, const TileShape& t) {
     const bool by_sample = a.dg && a.gate_mode == GATE_SAMPLE;
     p.tps = t.tps;
     p.tiles = (long long)a.B * t.tps;
-    const long long wgs = 2 * 256 * 12 / t.nw;
+    const long long wgs = 2 * 256 * 16 / t.nw;
     p.per_wg = (p.tiles + wgs - 1) / wgs;
     if (p.per_wg < 1) p.per_wg = 1;
     p.wgs = (int)((p.tiles + p.per_wg - 1) / p.per_wg);

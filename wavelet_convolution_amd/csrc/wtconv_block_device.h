@@ -214,8 +214,9 @@ __device__ __forceinline__ void store_part(T* __restrict__ p, const float (&v)[N
 // Eight channels of a parameter from c on; `none` where there is no such
 // parameter. PART: the first n channels only.
 template <bool PART = false>
-__device__ __forceinline__ void load_param(const float* __restrict__ p, int c, float none, float (&v)[CG], int n = CG) {
-    if (!p) {
+__device__ __forceinline__ void load_param_if(bool has, const float* __restrict__ p, int c, float none, float (&v)[CG],
+                                              int n = CG) {
+    if (!has) {
 #pragma unroll
         for (int i = 0; i < CG; ++i) v[i] = none;
         return;
@@ -230,6 +231,10 @@ __device__ __forceinline__ void load_param(const float* __restrict__ p, int c, f
         q.load(p + c);
 #pragma unroll
     for (int i = 0; i < CG; ++i) v[i] = q[i];
+}
+template <bool PART = false>
+__device__ __forceinline__ void load_param(const float* __restrict__ p, int c, float none, float (&v)[CG], int n = CG) {
+    load_param_if<PART>(p != nullptr, p, c, none, v, n);
 }
 
 }  // namespace wtc

@@ -13,7 +13,7 @@
 // Where HW is no multiple of PV, or C of eight, the last lane along it moves
 // back to end with it and does some of its neighbour's work again: the same
 // values to the same addresses. Sums take the elements that two lanes share
-// once. (So a tile needs HW >= PV and C >= 8.)
+// once (kernels of their own, ODD). So a tile needs HW >= PV and C >= 8.
 //
 // Small planes are bound by the chain of latencies (arguments, loads, two
 // sums over channels, stores) and by instruction fetch, large ones by memory
@@ -68,6 +68,14 @@ __device__ __forceinline__ void store_patch(T* __restrict__ p, uint32_t off, siz
     }
 }
 
+// v, or zero where element k is one of the `shared` that a neighbour has too.
+// ODD: there may be such elements.
+template <bool ODD>
+__device__ __forceinline__ float once(float v, int k, int shared) {
+    if constexpr (ODD) return k < shared ? 0.f : v;
+    return v;
+}
+
 // A lane's channels: eight from c on, of which the first `shared` are the
 // neighbour's too.
 template <int CL>
@@ -88,13 +96,12 @@ template <int CL, int PV>
 struct Pixels {
     static constexpr int PL = 64 / CL, PX = PL * PV;   // pixel lanes, pixels of a tile
     int p, shared;
-    bool on, last;   // last: the plane ends in this tile
+    bool on;
     __device__ __forceinline__ Pixels(int HW, int tile) {
         const int first = tile * PX + threadIdx.x % 64 / CL * PV;
         on = first < HW;
         p = min(first, HW - PV);
         shared = on ? first - p : PV;
-        last = (tile + 1) * PX >= HW;
     }
 };
 
@@ -123,6 +130,7 @@ __device__ __forceinline__ void channel_sums(float (&s)[K][PV], float* red, int&
     for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int j = 0; j < PV; ++j) s[k][j] = 0.f;
+#pragma unroll 2
     for (int w = 0; w < nw; ++w)
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -130,69 +138,87 @@ __device__ __forceinline__ void channel_sums(float (&s)[K][PV], float* red, int&
             for (int j = 0; j < PV; ++j) s[k][j] += buf[((w * K + k) * PL + pl) * PV + j];
 }
 
-// Sums over the lane's own channels come in two steps: over all eight, and
-// where C is no multiple of eight once more without those that the neighbour
-// has (a second pass rather than a branch around two forms of the first: the
-// compiler would hold what the two have in common).
-// mean and r of a lane's pixels.
-template <typename TH, bool HCL, int CL, int PV>
-__device__ __forceinline__ void patch_stats(const BlockArgs& a, Patch<TH, HCL, PV>& h, const Channels<CL>& ch,
-                                            float* red, int& turn, float (&mean)[PV], float (&r)[PV]) {
+// mean and r of a lane's pixels. Each wavefront takes the mean of its own
+// channels and the squares about that mean, and the wavefronts' pairs join
+// exactly (Chan, Golub, LeVeque, "Updating formulae and a pairwise algorithm
+// for computing sample variances", 1979): sum of squares about the common
+// mean = sum over wavefronts of their own + n (their mean - mean)^2. One
+// barrier, and no difference of large sums.
+template <typename TH, bool HCL, int CL, int PV, bool ODD>
+__device__ __forceinline__ void patch_stats(const BlockArgs& a, bool layer, Patch<TH, HCL, PV>& h,
+                                            const Channels<CL>& ch, float* red, int& turn, float (&mean)[PV],
+                                            float (&r)[PV]) {
+    constexpr int WC = CL * CG, PL = 64 / CL;   // channels of a full wavefront, pixel lanes
+    const int nw = blockDim.x / 64, wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    float s[2][PV];
 #pragma unroll
-    for (int j = 0; j < PV; ++j) {
-        mean[j] = 0.f;
-        r[j] = 1.f;
-    }
-    if (a.norm == NORM_NONE) return;
-    const float inv = a.inv_c;
-    float s[1][PV];
-    if (a.norm == NORM_LAYER) {
+    for (int j = 0; j < PV; ++j) s[0][j] = mean[j] = 0.f;
+    if (layer) {
+        // channels of this wavefront (a scalar: the same for its lanes)
+        const float n = (float)min(WC, a.C - __builtin_amdgcn_readfirstlane(wave) * WC);
 #pragma unroll
         for (int j = 0; j < PV; ++j) {
-            s[0][j] = 0.f;
 #pragma unroll
-            for (int i = 0; i < CG; ++i) s[0][j] += h.at(i, j);
+            for (int i = 0; i < CG; ++i) s[0][j] += once<ODD>(h.at(i, j), i, ch.shared);
         }
         h.renew();
-        if (a.C % CG) {
+        const float inv = __builtin_amdgcn_rcpf(n);   // a mean near the exact one does
 #pragma unroll
-            for (int j = 0; j < PV; ++j) {
-                s[0][j] = 0.f;
-#pragma unroll
-                for (int i = 0; i < CG; ++i) s[0][j] += i < ch.shared ? 0.f : h.at(i, j);
-            }
-            h.renew();
+        for (int j = 0; j < PV; ++j) {
+            s[0][j] = lane_sum<CL>(s[0][j]);
+            mean[j] = s[0][j] * inv;
         }
-        channel_sums<CL, PV, 1>(s, red, turn);
-#pragma unroll
-        for (int j = 0; j < PV; ++j) mean[j] = s[0][j] * inv;
     }
 #pragma unroll
     for (int j = 0; j < PV; ++j) {
-        s[0][j] = 0.f;
+        s[1][j] = 0.f;
 #pragma unroll
         for (int i = 0; i < CG; ++i) {
-            const float d = h.at(i, j) - mean[j];
-            s[0][j] = fmaf(d, d, s[0][j]);
+            const float d = once<ODD>(h.at(i, j) - mean[j], i, ch.shared);
+            s[1][j] = fmaf(d, d, s[1][j]);
         }
-        s[0][j] = ch.on ? s[0][j] : 0.f;
+        s[1][j] = ch.on ? s[1][j] : 0.f;
     }
     h.renew();
-    if (a.C % CG) {
 #pragma unroll
-        for (int j = 0; j < PV; ++j) {
-            s[0][j] = 0.f;
+    for (int j = 0; j < PV; ++j) s[1][j] = lane_sum<CL>(s[1][j]);
+    if (nw > 1) {
+        float* buf = red + (size_t)turn * nw * 2 * PL * PV;
+        turn ^= 1;
+        const int pl = lane / CL;
+        // a wavefront's sum about the mean that it took, and that mean
+        if (lane % CL == 0) {
 #pragma unroll
-            for (int i = 0; i < CG; ++i) {
-                const float d = i < ch.shared ? 0.f : h.at(i, j) - mean[j];
-                s[0][j] = fmaf(d, d, s[0][j]);
+            for (int j = 0; j < PV; ++j) {
+                buf[((wave * 2) * PL + pl) * PV + j] = mean[j];
+                buf[((wave * 2 + 1) * PL + pl) * PV + j] = s[1][j];
             }
         }
-        h.renew();
-    }
-    channel_sums<CL, PV, 1>(s, red, turn);
+        __syncthreads();
+        if (layer) {
 #pragma unroll
-    for (int j = 0; j < PV; ++j) r[j] = rsqrtf(s[0][j] * inv + a.eps);
+            for (int j = 0; j < PV; ++j) mean[j] = 0.f;
+#pragma unroll 2
+            for (int w = 0; w < nw; ++w) {
+                const float part = (float)min(WC, a.C - w * WC) * a.inv_c;
+#pragma unroll
+                for (int j = 0; j < PV; ++j) mean[j] = fmaf(buf[((w * 2) * PL + pl) * PV + j], part, mean[j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < PV; ++j) s[1][j] = 0.f;
+#pragma unroll 2
+        for (int w = 0; w < nw; ++w) {
+            const float n = (float)min(WC, a.C - w * WC);
+#pragma unroll
+            for (int j = 0; j < PV; ++j) {
+                const float d = buf[((w * 2) * PL + pl) * PV + j] - mean[j];   // zero for rms
+                s[1][j] += fmaf(d * n, d, buf[((w * 2 + 1) * PL + pl) * PV + j]);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < PV; ++j) r[j] = rsqrtf(s[1][j] * a.inv_c + a.eps);
 }
 
 // Drop bits of a lane's elements: a byte for each pixel, the first at the top
@@ -222,7 +248,7 @@ struct Drops {
 };
 
 // X: a residual (else a norm alone); DROP: elements are dropped.
-template <typename TH, bool HCL, typename TY, bool YCL, int CL, int PV, int MAXT, bool X, bool DROP>
+template <typename TH, bool HCL, typename TY, bool YCL, int CL, int PV, int MAXT, bool X, bool DROP, bool ODD>
 __global__ __launch_bounds__(MAXT) void k_tile_fwd(BlockArgs a, unsigned tiles, unsigned tps) {
     extern __shared__ float red[];
     int turn = 0;
@@ -257,8 +283,11 @@ __global__ __launch_bounds__(MAXT) void k_tile_fwd(BlockArgs a, unsigned tiles, 
                 bg[i] = in ? bg[i] * g[i] : 0.f;
             }
         }
-        float mean[PV], r[PV];
-        patch_stats<TH, HCL, CL, PV>(a, h, ch, red, turn, mean, r);
+        float mean[PV] = {}, r[PV];
+#pragma unroll
+        for (int j = 0; j < PV; ++j) r[j] = 1.f;
+        if (a.norm != NORM_NONE)
+            patch_stats<TH, HCL, CL, PV, ODD>(a, a.norm == NORM_LAYER, h, ch, red, turn, mean, r);
         if (!on) continue;
         Drops<PV> drop;
         if constexpr (DROP) drop.draw(a, (uint32_t)b * a.HW + px.p, ch.c);
@@ -274,17 +303,17 @@ __global__ __launch_bounds__(MAXT) void k_tile_fwd(BlockArgs a, unsigned tiles, 
 // Over the pixels of one gate (all of them, or a sample's): with e = dy where
 // it is kept, S1 = sum e z and S0 = sum e give
 //   dw = g k S1, db = g k S0, dg = k (w S1 + b S0)          (k: D's factor),
-// so the loop adds two sums, whatever is wanted. With a gate per sample, dw
+// so the loop adds two sums, whatever is wanted (X: a residual; else a norm
+// alone, whose dw and db they are). With a gate per sample, dw
 // and db add up over a workgroup's samples in LDS.
-template <typename TH, bool HCL, typename TY, bool YCL, int CL, int PV, int MAXT, bool DROP>
+template <typename TH, bool HCL, typename TY, bool YCL, int CL, int PV, int MAXT, bool X, bool DROP, bool ODD>
 __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, SumSlots sl, float* slots) {
     extern __shared__ float lds[];
-    const bool by_sample = a.gate_mode == GATE_SAMPLE;
     const Channels<CL> ch(a.C);
     const size_t sh = HCL ? a.C : a.HW, sy = YCL ? a.C : a.HW;
     // with a gate per sample: dw, db [2][lanes' channels], each of its own lane
     const int W = blockDim.x / 64 * CL * CG, own = (threadIdx.x / 64 * CL + threadIdx.x % CL) * CG;
-    float *acc = lds + own, *red = lds + (by_sample ? 2 * W : 0);
+    float *acc = lds + own, *red = lds + (X && (a.flags & BY_SAMPLE) ? 2 * W : 0);
     int turn = 0;
     float s1[CG] = {}, s0[CG] = {}, sx[CG] = {};
     float* slot = slots + (size_t)blockIdx.x * (pt.nsum + pt.partials) * a.C;
@@ -297,7 +326,7 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
     auto finish = [&](const float* gate, float* dgp) {
         pixel_sums(s1);
         pixel_sums(s0);
-        if (!writes) return;
+        if (!X || !writes) return;
         float w[CG], bb[CG], g[CG];
         load_param(a.w, ch.c, 1.f, w);
         load_param(a.b, ch.c, 0.f, bb);
@@ -310,16 +339,18 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
         }
         if (dgp) store_vec<float, CG>(dgp + ch.c, w);
     };
-    if (by_sample && writes) {
+    if (X && (a.flags & BY_SAMPLE) && writes) {
 #pragma unroll
         for (int i = 0; i < CG; ++i) acc[i] = acc[W + i] = 0.f;
     }
     const unsigned tps = (unsigned)pt.tps, t0 = blockIdx.x * (unsigned)pt.per_wg;
     const unsigned t1 = min(t0 + (unsigned)pt.per_wg, (unsigned)pt.tiles);
     for (unsigned t = t0; t < t1; ++t) {
+        uint32_t fl = a.flags;
+        asm volatile("" : "+s"(fl));   // tested here, not before the loop
         const unsigned b = t / tps;
         const Pixels<CL, PV> px(a.HW, (int)(t - b * tps));
-        const bool in = a.drop != DROP_SAMPLE || sample_kept(a, (int)b), on = ch.on && px.on;
+        const bool in = !X || !(fl & DROPS_SAMPLES) || sample_kept(a, (int)b), on = ch.on && px.on;
         const size_t first = (size_t)b * a.C * a.HW;
         const uint32_t planar = (uint32_t)ch.c * a.HW + px.p, rows = (uint32_t)px.p * a.C + ch.c;
         const uint32_t oh = (HCL ? rows : planar) * sizeof(TH), oy = (YCL ? rows : planar) * sizeof(TY);
@@ -331,35 +362,27 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
             if (in) h.load((const TH*)a.h + first, oh, sh);
             d.load((const TY*)a.dy + first, oy, sy);
         }
-        // a tile at the end of a plane whose size is no multiple of PV: sums
-        // over pixels leave out what a neighbour has
-        const bool ends = px.last && a.HW % PV;
-        if (a.dxs && on) {
+        if (X && (fl & WANT_DXS) && on) {
             Patch<TY, YCL, PV> x;
             x.load((const TY*)a.x + first, oy, sy);
-            auto add = [&](auto masked) {
-                d.renew();   // the two forms have nothing to hold in common
 #pragma unroll
-                for (int i = 0; i < CG; ++i)
+            for (int i = 0; i < CG; ++i)
 #pragma unroll
-                    for (int j = 0; j < PV; ++j)
-                        sx[i] = fmaf(masked && j < px.shared ? 0.f : d.at(i, j),
-                                     masked && j < px.shared ? 0.f : x.at(i, j), sx[i]);
-            };
-            if (ends)
-                add(std::true_type{});
-            else
-                add(std::false_type{});
+                for (int j = 0; j < PV; ++j)
+                    sx[i] = fmaf(once<ODD>(d.at(i, j), j, px.shared), once<ODD>(x.at(i, j), j, px.shared), sx[i]);
+            d.renew();
         }
-        if (a.dx && on) {
+        if (X && (fl & WANT_DX) && on) {
             float xs[CG];
-            load_param(a.xs, ch.c, 1.f, xs);
+            load_param_if(fl & HAS_XS, a.xs, ch.c, 1.f, xs);
             store_patch<TY, YCL, PV>((TY*)a.dx + first, oy, sy, [&](int i, int j) { return d.at(i, j) * xs[i]; });
         }
         d.renew();
-        float mean[PV], r[PV];
-        patch_stats<TH, HCL, CL, PV>(a, h, ch, red, turn, mean, r);
-        if (!in) d.zero();   // the same for every lane: no gradient passes a dropped sample
+        float mean[PV] = {}, r[PV];
+#pragma unroll
+        for (int j = 0; j < PV; ++j) r[j] = 1.f;
+        if (fl & (LAYER | RMS)) patch_stats<TH, HCL, CL, PV, ODD>(a, fl & LAYER, h, ch, red, turn, mean, r);
+        if (X && !in) d.zero();   // the same for every lane: no gradient passes a dropped sample
         Drops<PV> drop;
         if constexpr (DROP) {
             if (on) drop.draw(a, (uint32_t)b * a.HW + px.p, ch.c);
@@ -374,46 +397,48 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
             if constexpr (DROP) drop.renew();
         };
         float gw[CG];   // u = e gw
-        const float* gate = by_sample ? a.gate + (size_t)b * a.C : a.gate;
+        const float* gate = X ? a.gate + (fl & BY_SAMPLE ? (size_t)b * a.C : 0) : nullptr;
         {
-            float g[CG];
-            load_param(a.w, ch.c, 1.f, gw);
-            load_param(gate, ch.c, 1.f, g);
+            load_param_if(fl & HAS_W, a.w, ch.c, 1.f, gw);
+            if constexpr (X) {
+                float g[CG];
+                load_param_if(fl & HAS_GATE, gate, ch.c, 1.f, g);
 #pragma unroll
-            for (int i = 0; i < CG; ++i) gw[i] *= g[i] * a.keep;
+                for (int i = 0; i < CG; ++i) gw[i] *= g[i] * a.keep;
+            }
         }
         // over pixels, for the channels' gradients, and over channels, for the
         // norm's, without what a neighbour has; z = h r + c
         float ms[2][PV] = {}, c[PV];
 #pragma unroll
         for (int j = 0; j < PV; ++j) c[j] = -mean[j] * r[j];
-        auto sums = [&](auto masked) {
-            renew();
 #pragma unroll
-            for (int i = 0; i < CG; ++i) {
+        for (int i = 0; i < CG; ++i) {
+            const float g = once<ODD>(gw[i], i, ch.shared);
 #pragma unroll
-                for (int j = 0; j < PV; ++j) {
-                    const float z = fmaf(h.at(i, j), r[j], c[j]), e = kept(d.at(i, j), i, j), u = e * gw[i];
-                    ms[0][j] += masked && i < ch.shared ? 0.f : u;
-                    ms[1][j] += masked && i < ch.shared ? 0.f : u * z;
-                    s0[i] += masked && j < px.shared ? 0.f : e;
-                    s1[i] += masked && j < px.shared ? 0.f : e * z;
-                }
-                __builtin_amdgcn_sched_barrier(0);   // a channel at a time: fewer values in flight
+            for (int j = 0; j < PV; ++j) {
+                const float z = fmaf(h.at(i, j), r[j], c[j]), e = kept(d.at(i, j), i, j), u = e * g;
+                ms[0][j] += u;
+                ms[1][j] = fmaf(u, z, ms[1][j]);
+                const float own = once<ODD>(e, j, px.shared);
+                s0[i] += own;
+                s1[i] = ODD ? s1[i] + once<ODD>(own * z, j, px.shared) : fmaf(own, z, s1[i]);
             }
-        };
-        if (ends || a.C % CG)
-            sums(std::true_type{});
-        else
-            sums(std::false_type{});
-        if (a.dh) {
+            // a channel at a time, here and not where the sums are used:
+            // fewer values in flight
+            asm volatile("" : "+v"(s0[i]), "+v"(s1[i]));
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int j = 0; j < PV; ++j) asm volatile("" : "+v"(ms[0][j]), "+v"(ms[1][j]));
+        if (fl & WANT_DH) {
             // dh = r (u - m1 - z m2) = u r + h c2 + c1
             float c1[PV], c2[PV];
-            if (a.norm != NORM_NONE) {
+            if (fl & (LAYER | RMS)) {
                 channel_sums<CL, PV, 2>(ms, red, turn);
 #pragma unroll
                 for (int j = 0; j < PV; ++j) {
-                    const float m1 = a.norm == NORM_LAYER ? ms[0][j] * a.inv_c : 0.f, m2 = ms[1][j] * a.inv_c;
+                    const float m1 = fl & LAYER ? ms[0][j] * a.inv_c : 0.f, m2 = ms[1][j] * a.inv_c;
                     c2[j] = -r[j] * r[j] * m2;
                     c1[j] = -r[j] * fmaf(c[j], m2, m1);
                 }
@@ -429,7 +454,7 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
                 });
         }
         // the last tile of this sample in the workgroup's range
-        if (by_sample && (t + 1 == t1 || (t + 1) % tps == 0)) {
+        if (X && (fl & BY_SAMPLE) && (t + 1 == t1 || (t + 1) % tps == 0)) {
             const bool whole = b * tps >= t0 && (b + 1) * tps <= t1;
             finish(gate, !a.dg   ? nullptr
                          : whole ? a.dg + (size_t)b * a.C
@@ -445,7 +470,7 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
             for (int i = 0; i < CG; ++i) s1[i] = s0[i] = 0.f;
         }
     }
-    if (!by_sample) {
+    if (!X || !(a.flags & BY_SAMPLE)) {
         finish(a.gate, sl.dg >= 0 ? slot + (size_t)sl.dg * a.C : nullptr);
     } else if (writes) {
 #pragma unroll
@@ -456,7 +481,7 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
     }
     if (writes && sl.dw >= 0) store_vec<float, CG>(slot + (size_t)sl.dw * a.C + ch.c, s1);
     if (writes && sl.db >= 0) store_vec<float, CG>(slot + (size_t)sl.db * a.C + ch.c, s0);
-    if (sl.dxs >= 0) {
+    if (X && sl.dxs >= 0) {
         pixel_sums(sx);
         if (writes) store_vec<float, CG>(slot + (size_t)sl.dxs * a.C + ch.c, sx);
     }
@@ -513,18 +538,24 @@ inline size_t tile_lds(const TileShape& t) { return t.nw > 1 ? (size_t)2 * t.nw 
     if (t.nw <= 8) return CALL(16, 512);           \
     return CALL(16, 1024);
 
-template <typename TH, bool HCL, typename TY, bool YCL, int PV, bool X, bool DROP>
-hipError_t tile_fwd_mode(const BlockArgs& a, const TileShape& t, hipStream_t s) {
+template <typename TH, bool HCL, typename TY, bool YCL, int PV, bool X, bool DROP, bool ODD>
+hipError_t tile_fwd_odd(const BlockArgs& a, const TileShape& t, hipStream_t s) {
     const unsigned tiles = (unsigned)a.B * (unsigned)t.tps;
     const dim3 grid(tiles < (1u << 21) ? tiles : (1u << 21)), block(64 * t.nw);
 #define WTC_CALL(CL, MAXT)                                                                                     \
     [&] {                                                                                                      \
-        hipLaunchKernelGGL((k_tile_fwd<TH, HCL, TY, YCL, CL, PV, MAXT, X, DROP>), grid, block, tile_lds(t), s, \
-                           a, tiles, (unsigned)t.tps);                                                         \
+        hipLaunchKernelGGL((k_tile_fwd<TH, HCL, TY, YCL, CL, PV, MAXT, X, DROP, ODD>), grid, block, tile_lds(t), \
+                           s, a, tiles, (unsigned)t.tps);                                                      \
         return hipGetLastError();                                                                              \
     }()
     WTC_TILE_SHAPES(WTC_CALL)
 #undef WTC_CALL
+}
+
+template <typename TH, bool HCL, typename TY, bool YCL, int PV, bool X, bool DROP>
+hipError_t tile_fwd_mode(const BlockArgs& a, const TileShape& t, hipStream_t s) {
+    if (a.C % CG) return tile_fwd_odd<TH, HCL, TY, YCL, PV, X, DROP, true>(a, t, s);
+    return tile_fwd_odd<TH, HCL, TY, YCL, PV, X, DROP, false>(a, t, s);
 }
 
 template <typename TH, bool HCL, typename TY, bool YCL, int PV>
@@ -534,13 +565,17 @@ hipError_t tile_fwd_typed(const BlockArgs& a, const TileShape& t, hipStream_t s)
     return tile_fwd_mode<TH, HCL, TY, YCL, PV, true, false>(a, t, s);
 }
 
-template <typename TH, bool HCL, typename TY, bool YCL, int PV, bool DROP>
-hipError_t tile_bwd_mode(const BlockArgs& a, const TileShape& t, const Partition& p, hipStream_t s) {
+template <typename TH, bool HCL, typename TY, bool YCL, int PV, bool X, bool DROP, bool ODD>
+hipError_t tile_bwd_odd(BlockArgs a, const TileShape& t, const Partition& p, hipStream_t s) {
+    a.flags = (a.w ? HAS_W : 0) | (a.gate ? HAS_GATE : 0) | (a.xs ? HAS_XS : 0) | (a.dx ? WANT_DX : 0) |
+              (a.dh ? WANT_DH : 0) | (a.dxs ? WANT_DXS : 0) | (a.norm == NORM_LAYER ? LAYER : 0) |
+              (a.norm == NORM_RMS ? RMS : 0) | (a.gate_mode == GATE_SAMPLE ? BY_SAMPLE : 0) |
+              (a.drop == DROP_SAMPLE ? DROPS_SAMPLES : 0);
     const dim3 grid((unsigned)p.wgs), block(64 * t.nw);
     const size_t lds = tile_lds(t) + (a.gate_mode == GATE_SAMPLE ? sizeof(float) * 2 * t.nw * t.cl * CG : 0);
 #define WTC_CALL(CL, MAXT)                                                                                     \
     [&] {                                                                                                      \
-        hipLaunchKernelGGL((k_tile_bwd<TH, HCL, TY, YCL, CL, PV, MAXT, DROP>), grid, block, lds, s, a, p,      \
+        hipLaunchKernelGGL((k_tile_bwd<TH, HCL, TY, YCL, CL, PV, MAXT, X, DROP, ODD>), grid, block, lds, s, a, p, \
                            sum_slots(a), a.ws);                                                                \
         return hipGetLastError();                                                                              \
     }()
@@ -548,10 +583,18 @@ hipError_t tile_bwd_mode(const BlockArgs& a, const TileShape& t, const Partition
 #undef WTC_CALL
 }
 
+template <typename TH, bool HCL, typename TY, bool YCL, int PV, bool X, bool DROP>
+hipError_t tile_bwd_mode(const BlockArgs& a, const TileShape& t, const Partition& p, hipStream_t s) {
+    if (a.C % CG || a.HW % PV) return tile_bwd_odd<TH, HCL, TY, YCL, PV, X, DROP, true>(a, t, p, s);
+    return tile_bwd_odd<TH, HCL, TY, YCL, PV, X, DROP, false>(a, t, p, s);
+}
+
 template <typename TH, bool HCL, typename TY, bool YCL, int PV>
 hipError_t tile_bwd_typed(const BlockArgs& a, const TileShape& t, const Partition& p, hipStream_t s) {
-    if (a.drop == DROP_ELEMENT) return tile_bwd_mode<TH, HCL, TY, YCL, PV, true>(a, t, p, s);
-    return tile_bwd_mode<TH, HCL, TY, YCL, PV, false>(a, t, p, s);
+    if (a.drop == DROP_ELEMENT) return tile_bwd_mode<TH, HCL, TY, YCL, PV, true, true>(a, t, p, s);
+    if (a.gate || a.xs || a.dx || a.dxs || a.drop != DROP_NONE)
+        return tile_bwd_mode<TH, HCL, TY, YCL, PV, true, false>(a, t, p, s);
+    return tile_bwd_mode<TH, HCL, TY, YCL, PV, false, false>(a, t, p, s);
 }
 
 #define WTC_TILE_FWD(HCL, YCL)                                                                                       \
