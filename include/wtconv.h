@@ -325,7 +325,7 @@ size_t wtconv_block_workspace_size(const wtconv_block_desc_t *desc);
    read once and held in registers) or WTCONV_ROUTE_GENERIC (rows wider than
    that: read once per statistic). -1 if the descriptor is invalid. No device
    call is made. */
-int32_t wtconv_block_route(const wtconv_block_desc_t *desc, int32_t backward);
+int32_t wtconv_block_route(const wtconv_block_desc_t *desc);
 
 /* y = norm(x) * weight + bias. The descriptor has a norm, no gate, no drop. */
 wtconv_status_t wtconv_norm_fwd(const wtconv_block_desc_t *desc, const void *x, const float *weight,

@@ -72,7 +72,7 @@ def test_bad_descriptors(lib, kw, status):
     assert lib.wtconv_residual_bwd(ctypes.byref(d), *P[:3], None, None, None, None, P[3], *[None] * 6, P[4], 1 << 30,
                                    None) == status
     assert lib.wtconv_block_workspace_size(ctypes.byref(d)) == ctypes.c_size_t(-1).value
-    assert lib.wtconv_block_route(ctypes.byref(d), 0) == -1
+    assert lib.wtconv_block_route(ctypes.byref(d)) == -1
     if kw.get("drop") is None and kw.get("gate") is None and kw.get("norm") is None:
         assert lib.wtconv_norm_fwd(ctypes.byref(d), P[0], None, None, P[1], None) == status
     assert lib.wtconv_norm_fwd(None, P[0], None, None, P[1], None) == 1

@@ -85,7 +85,7 @@ def load_library() -> ctypes.CDLL:
             _PB = ctypes.POINTER(WTConvBlockDesc)
             lib.wtconv_block_workspace_size.argtypes = [_PB]
             lib.wtconv_block_workspace_size.restype = _SZ
-            lib.wtconv_block_route.argtypes = [_PB, ctypes.c_int32]
+            lib.wtconv_block_route.argtypes = [_PB]
             lib.wtconv_block_route.restype = ctypes.c_int32
             for name, n in (("wtconv_norm_fwd", 5), ("wtconv_residual_fwd", 9), ("wtconv_dropout", 4)):
                 fn = getattr(lib, name)

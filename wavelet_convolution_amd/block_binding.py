@@ -130,12 +130,12 @@ def wtconv_block_workspace_size(y, h=None, *, kind: str = "layer", gate=None) ->
     return _ws_size(d)
 
 
-def wtconv_block_route(y, h=None, *, kind: str = "layer", backward: bool = False) -> str:
+def wtconv_block_route(y, h=None, *, kind: str = "layer") -> str:
     """"fused" or "generic": how a norm from h's type and memory order into y's, or the residual with stream y and
     block output h, runs. Makes no device call."""
     h = y if h is None else h
     d = _desc(y, _act("h", h, y), _act("y", y), _code(_NORMS, kind, "kind"))
-    r = _b.load_library().wtconv_block_route(ctypes.byref(d), int(backward))
+    r = _b.load_library().wtconv_block_route(ctypes.byref(d))
     if r < 0:
         raise _b.WTConvError(2, _b.wtconv_status_string(2))
     return _b.ROUTES[r]

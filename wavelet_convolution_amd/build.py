@@ -21,7 +21,7 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libwtconv.so")
 SOURCES = ["wtconv_fused.hip", "wtconv_tiled.hip", "wtconv_bwdw.hip", "wtconv_naive.hip", "wtconv_api.hip",
            "wtconv_peaks.hip", "wtconv_layout.hip", "wtconv_dw.hip", "wtconv_bwd1.hip",
-           "wtconv_block_api.hip", "wtconv_block.hip", "wtconv_block_generic.hip", "wtconv_block_rows.hip",
+           "wtconv_block_api.hip", "wtconv_block.hip", "wtconv_block_generic.hip", "wtconv_block_rows_fwd.hip", "wtconv_block_rows_bwd.hip",
            "wtconv_block_dropout.hip",
            *(f"wtconv_block_tile_{orders}_{way}.hip" for orders in ("pp", "pr", "rp") for way in ("fwd", "bwd")),
            *(f"wtconv_fam{h}_{kind}.hip" for h in (56, 28, 14, 7) for kind in ("data", "bw"))]

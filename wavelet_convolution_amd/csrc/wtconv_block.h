@@ -26,12 +26,12 @@ enum { DROP_NONE = 0, DROP_ELEMENT = 1, DROP_SAMPLE = 2 };
 // Channels that share one generator call: 16 of its 128 bits each.
 constexpr int CG = 8;
 
-// What a call has and wants, as bits: the backward tiles test them inside
+// What a call has and wants, as bits: the backward kernels test them inside
 // their loop (a test of a bit there is two scalar instructions; conditions
 // kept over the loop were most of its scalar registers).
 enum : uint32_t {
     HAS_W = 1, HAS_GATE = 2, HAS_XS = 4, WANT_DX = 8, WANT_DH = 16, WANT_DXS = 32, LAYER = 64, RMS = 128,
-    BY_SAMPLE = 256, DROPS_SAMPLES = 512
+    BY_SAMPLE = 256, DROPS_SAMPLES = 512, EACH_ROW = 1024
 };
 
 struct BlockArgs {
@@ -53,12 +53,14 @@ struct BlockArgs {
     uint32_t thr;       // an element is kept when its 16 bits are >= thr
     float keep;         // 65536 / (65536 - thr); 0 where thr = 65536
     uint32_t site;
-    uint32_t flags;     // of the backward tile kernels, set at their launch
+    uint32_t flags;     // of the backward kernels, set at their launch
 };
 
 // The sums over rows that the parameter gradients need. Each workgroup of a
 // backward kernel adds over a contiguous range of tiles (a tile: some rows
-// of one sample) and leaves its sums in its slot of the workspace; a second
+// of one sample; the ranges differ by one tile at most, evenly over the
+// workgroups, so that the CUs' shares differ little), and leaves its sums in
+// its slot of the workspace; a second
 // stage adds the slots in order, so results do not depend on timing. With a
 // gate per sample, a workgroup writes the gate gradient of a sample whose
 // tiles are all its own, and leaves at most two partial sums (its first and
@@ -66,10 +68,11 @@ struct BlockArgs {
 struct Partition {
     long long tiles;    // all tiles
     long long tps;      // tiles per sample (samples count only with a gate per sample: else one)
-    long long per_wg;   // tiles per workgroup
-    int wgs;
+    int wgs;            // as many as are resident at once, at most one a tile
     int nsum;           // channel sums a slot holds
     int partials;       // 0, or 2: partial gate gradients per slot
+    __host__ __device__ long long begin(long long wg) const { return wg * tiles / wgs; }
+    __host__ __device__ long long owner(long long tile) const { return ((tile + 1) * wgs - 1) / tiles; }
 };
 
 // Places of the channel sums in a slot; -1: not wanted.
@@ -85,9 +88,22 @@ inline SumSlots sum_slots(const BlockArgs& a) {
     return s;
 }
 
+inline uint32_t block_flags(const BlockArgs& a) {
+    const bool sample = a.gate_mode == GATE_SAMPLE;
+    return (a.w ? HAS_W : 0) | (a.gate ? HAS_GATE : 0) | (a.xs ? HAS_XS : 0) | (a.dx ? WANT_DX : 0) |
+           (a.dh ? WANT_DH : 0) | (a.dxs ? WANT_DXS : 0) | (a.norm == NORM_LAYER ? LAYER : 0) |
+           (a.norm == NORM_RMS ? RMS : 0) | (sample && a.HW > 1 ? BY_SAMPLE : 0) |
+           (a.drop == DROP_SAMPLE ? DROPS_SAMPLES : 0) | (sample && a.HW == 1 ? EACH_ROW : 0);
+}
+
+// A backward call that is more than a norm's.
+inline bool block_residual(const BlockArgs& a) {
+    return a.gate || a.xs || a.dx || a.dxs || a.drop != DROP_NONE;
+}
+
 // How a call is served: by which kernels, and with how much workspace.
 enum { BLOCK_GENERIC = 0, BLOCK_FUSED = 1 };
-int block_route(const BlockArgs& a, int h_bf16, int y_bf16, bool backward);
+int block_route(const BlockArgs& a, int h_bf16, int y_bf16);
 size_t block_bwd_workspace_bytes(const BlockArgs& a, int h_bf16, int y_bf16);
 hipError_t block_fwd_launch(const BlockArgs& a, int h_bf16, int y_bf16, hipStream_t s);
 hipError_t block_bwd_launch(const BlockArgs& a, int h_bf16, int y_bf16, hipStream_t s);

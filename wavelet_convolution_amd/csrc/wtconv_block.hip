@@ -19,21 +19,21 @@ hipError_t tile_bwd_launch<true, false>(const BlockArgs&, int, int, const TileSh
 
 namespace {
 
-// Tiles per workgroup: two rounds of workgroups over the card (256 CUs with
-// sixteen wavefronts each at the kernels' registers). More tiles each leave the
-// last round ragged (64x96x56x56 with gate, dropout and residual scale: 75.6
-// us at one round, 69.6 at two, 69.1 at six), fewer write more partial sums.
+// One tile a workgroup where the card takes them in two rounds, else as many
+// workgroups as it holds at once (256 CUs, three wavefronts a SIMD at the
+// kernels' registers), each with an even share: residual backward
+// 64x96x56x56, 1,600 tiles: 58.3 us at a tile each, 61.7 at 1,024 workgroups,
+// 79.5 at 1,280; 32x128x128x128, 8,192 tiles: 162 us at 1,536 (the card's fill
+// there), 170 at 1,280, 174 at 2,048, 178 at a tile each.
 Partition tile_partition(const BlockArgs& a, const TileShape& t) {
     Partition p{};
     const bool by_sample = a.dg && a.gate_mode == GATE_SAMPLE;
     p.tps = t.tps;
     p.tiles = (long long)a.B * t.tps;
-    const long long wgs = 2 * 256 * 16 / t.nw;
-    p.per_wg = (p.tiles + wgs - 1) / wgs;
-    if (p.per_wg < 1) p.per_wg = 1;
-    p.wgs = (int)((p.tiles + p.per_wg - 1) / p.per_wg);
+    const long long wgs = 256 * (t.nw > 12 ? 1 : 12 / t.nw);
+    p.wgs = (int)(p.tiles <= 2 * wgs ? p.tiles : wgs);
     p.nsum = sum_slots(a).count;
-    p.partials = by_sample && p.per_wg % p.tps ? 2 : 0;
+    p.partials = by_sample && p.tps > 1 ? 2 : 0;
     return p;
 }
 
@@ -62,26 +62,25 @@ hipError_t tile_bwd(const BlockArgs& a, int h_bf16, int y_bf16, const TileShape&
 
 }  // namespace
 
-int block_route(const BlockArgs& a, int h_bf16, int y_bf16, bool backward) {
-    const int pv = backward ? bwd_pv(h_bf16, y_bf16) : fwd_pv(h_bf16, y_bf16);
-    return rows_cover(a) || (!(a.h_cl && a.y_cl) && tile_shape(a, pv).cl) ? BLOCK_FUSED : BLOCK_GENERIC;
+int block_route(const BlockArgs& a, int h_bf16, int y_bf16) {
+    return rows_cover(a) || (!(a.h_cl && a.y_cl) && tile_shape(a, patch_pixels(h_bf16, y_bf16)).cl) ? BLOCK_FUSED : BLOCK_GENERIC;
 }
 
 size_t block_bwd_workspace_bytes(const BlockArgs& a, int h_bf16, int y_bf16) {
     if (a.h_cl && a.y_cl) return rows_cover(a) ? rows_bwd_bytes(a) : block_generic_bwd_bytes(a);
-    const TileShape t = tile_shape(a, bwd_pv(h_bf16, y_bf16));
+    const TileShape t = tile_shape(a, patch_pixels(h_bf16, y_bf16));
     return t.cl ? tile_bwd_bytes(a, t) : block_generic_bwd_bytes(a);
 }
 
 hipError_t block_fwd_launch(const BlockArgs& a, int h_bf16, int y_bf16, hipStream_t s) {
     if (rows_cover(a)) return rows_fwd(a, h_bf16, y_bf16, s);
-    const TileShape t = a.h_cl && a.y_cl ? TileShape{} : tile_shape(a, fwd_pv(h_bf16, y_bf16));
+    const TileShape t = a.h_cl && a.y_cl ? TileShape{} : tile_shape(a, patch_pixels(h_bf16, y_bf16));
     return t.cl ? tile_fwd(a, h_bf16, y_bf16, t, s) : block_generic_fwd(a, h_bf16, y_bf16, s);
 }
 
 hipError_t block_bwd_launch(const BlockArgs& a, int h_bf16, int y_bf16, hipStream_t s) {
     if (rows_cover(a)) return rows_bwd(a, h_bf16, y_bf16, s);
-    const TileShape t = a.h_cl && a.y_cl ? TileShape{} : tile_shape(a, bwd_pv(h_bf16, y_bf16));
+    const TileShape t = a.h_cl && a.y_cl ? TileShape{} : tile_shape(a, patch_pixels(h_bf16, y_bf16));
     return t.cl ? tile_bwd(a, h_bf16, y_bf16, t, s) : block_generic_bwd(a, h_bf16, y_bf16, s);
 }
 

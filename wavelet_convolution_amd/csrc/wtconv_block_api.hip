@@ -115,9 +115,9 @@ size_t wtconv_block_workspace_size(const wtconv_block_desc_t* d) {
     return check_desc(d) == WTCONV_OK ? workspace(d) : (size_t)-1;
 }
 
-int32_t wtconv_block_route(const wtconv_block_desc_t* d, int32_t backward) {
+int32_t wtconv_block_route(const wtconv_block_desc_t* d) {
     if (check_desc(d) != WTCONV_OK) return -1;
-    const int r = wtc::block_route(args_of(d), d->h_dtype == WTCONV_BF16, d->y_dtype == WTCONV_BF16, backward != 0);
+    const int r = wtc::block_route(args_of(d), d->h_dtype == WTCONV_BF16, d->y_dtype == WTCONV_BF16);
     return r == wtc::BLOCK_FUSED ? WTCONV_ROUTE_FUSED : WTCONV_ROUTE_GENERIC;
 }
 

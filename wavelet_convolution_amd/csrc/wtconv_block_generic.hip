@@ -193,7 +193,7 @@ __global__ __launch_bounds__(T) void k_generic_grads(BlockArgs a, const float2* 
     if (n <= 0) return;
     float* slot = slots + (size_t)blockIdx.y * (pt.nsum + pt.partials) * a.C;
     float dw[CG] = {}, db[CG] = {}, dg[CG] = {}, ds[CG] = {};
-    const long long t0 = blockIdx.y * pt.per_wg, t1 = min(t0 + pt.per_wg, pt.tiles);
+    const long long t0 = pt.begin(blockIdx.y), t1 = pt.begin(blockIdx.y + 1);
     const bool by_sample = a.dg && a.gate_mode == GATE_SAMPLE;
     for (long long row = t0; row < t1; ++row) {
         const int b = (int)(row / a.HW);
@@ -240,42 +240,61 @@ __global__ __launch_bounds__(T) void k_generic_grads(BlockArgs a, const float2* 
         }
 }
 
-// Second stage. A workgroup takes 16 channels of one sum: 64 lanes a channel
-// add the slots k = lane, lane + 64, ..., and a fixed tree joins them.
-// Blocks past the channel sums join the partial gate gradients of one
-// sample each, over the workgroups that its tiles lie in.
-constexpr int FC = 16, FL = 64;
-__global__ __launch_bounds__(FC * FL) void k_finalize(BlockArgs a, Partition pt, SumSlots sl, const float* slots,
-                                                      int cblocks) {
-    __shared__ float red[FL][FC];
-    const int ci = threadIdx.x % FC, lane = threadIdx.x / FC;
+// Second stage. A workgroup takes 16 channels of one sum: a lane adds four
+// channels (16 bytes) of the slots k = l, l + 256, ..., data-parallel moves
+// join a wavefront's 16 lanes of the same channels, and LDS the 16
+// wavefronts, all in a fixed order. Latency is all of its time, so its loads
+// are few, wide and in flight together, with one barrier after them. Blocks
+// past the channel sums join the partial gate gradients of one sample each,
+// over the workgroups that its tiles lie in.
+constexpr int FC = 16, FT = 1024, FL = FT * 4 / FC;
+__global__ __launch_bounds__(FT) void k_finalize(BlockArgs a, Partition pt, SumSlots sl, const float* slots,
+                                                 int cblocks) {
+    __shared__ float red[FT / 64][FC];
+    const int quad = threadIdx.x % (FC / 4), lane = threadIdx.x / (FC / 4);
     const size_t slot = (size_t)(pt.nsum + pt.partials) * a.C;
     const long long items = (long long)cblocks * (pt.nsum + (pt.partials ? a.B : 0));
     for (long long item = blockIdx.x; item < items; item += gridDim.x) {
         const long long what = item / cblocks;
-        const int c = (int)(item - what * cblocks) * FC + ci;
+        const int c0 = (int)(item - what * cblocks) * FC, c = c0 + quad * 4;
         float* dst;
-        float sum = 0.f;
+        float sum[4] = {};
+        auto add = [&](const float* p) {
+            if (c + 4 <= a.C) {
+                Vec<float, 4> v;
+                v.load(p + c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[i] += v[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (c + i < a.C) sum[i] += p[c + i];
+            }
+        };
         if (what < pt.nsum) {
             dst = what == sl.dw ? a.dw : what == sl.db ? a.db : what == sl.dg ? a.dg : a.dxs;
-            if (c < a.C) {
-#pragma unroll 8
-                for (int k = lane; k < pt.wgs; k += FL) sum += slots[k * slot + what * a.C + c];
-            }
+#pragma unroll 4
+            for (int k = lane; k < pt.wgs; k += FL) add(slots + k * slot + what * a.C);
         } else {
-            const long long b = what - pt.nsum, k0 = b * pt.tps / pt.per_wg, k1 = ((b + 1) * pt.tps - 1) / pt.per_wg;
+            const long long b = what - pt.nsum, k0 = pt.owner(b * pt.tps), k1 = pt.owner((b + 1) * pt.tps - 1);
             if (k0 == k1) continue;   // written by its one workgroup (the same for the whole block)
             dst = a.dg + b * a.C;
-            if (c < a.C)
-                for (long long k = k0 + lane; k <= k1; k += FL)
-                    sum += slots[k * slot + (size_t)(pt.nsum + (k * pt.per_wg / pt.tps == b ? 0 : 1)) * a.C + c];
+            for (long long k = k0 + lane; k <= k1; k += FL)
+                add(slots + k * slot + (size_t)(pt.nsum + (pt.begin(k) / pt.tps == b ? 0 : 1)) * a.C);
         }
-        red[lane][ci] = sum;
-        for (int n = FL / 2; n > 0; n >>= 1) {
-            __syncthreads();
-            if (lane < n) red[lane][ci] += red[lane + n][ci];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] = stride_sum<4>(sum[i]);
+        if (threadIdx.x % 64 < 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) red[threadIdx.x / 64][quad * 4 + i] = sum[i];
         }
-        if (lane == 0 && c < a.C) dst[c] = red[0][ci];
+        __syncthreads();
+        if (threadIdx.x < FC && c0 + (int)threadIdx.x < a.C) {
+            float t = 0.f;
+#pragma unroll
+            for (int w = 0; w < FT / 64; ++w) t += red[w][threadIdx.x];
+            dst[c0 + threadIdx.x] = t;
+        }
         __syncthreads();
     }
 }
@@ -287,11 +306,9 @@ Partition generic_partition(const BlockArgs& a) {
     const bool by_sample = a.dg && a.gate_mode == GATE_SAMPLE;
     p.tiles = (long long)a.B * a.HW;
     p.tps = by_sample ? a.HW : p.tiles;
-    p.per_wg = (p.tiles + 1023) / 1024;
-    if (p.per_wg < 16) p.per_wg = 16;
-    p.wgs = (int)((p.tiles + p.per_wg - 1) / p.per_wg);
+    p.wgs = (int)(p.tiles < 16384 ? (p.tiles + 15) / 16 : 1024);
     p.nsum = sum_slots(a).count;
-    p.partials = by_sample && p.per_wg % p.tps ? 2 : 0;
+    p.partials = by_sample ? 2 : 0;
     return p;
 }
 
@@ -312,7 +329,7 @@ hipError_t block_finalize(const BlockArgs& a, const Partition& p, const float* s
     const int cblocks = cdiv(a.C, FC);
     const long long items = (long long)cblocks * (p.nsum + (p.partials ? a.B : 0));
     if (items == 0) return hipSuccess;
-    hipLaunchKernelGGL(k_finalize, dim3(grid_of(items)), dim3(FC * FL), 0, s, a, p, sum_slots(a), slots, cblocks);
+    hipLaunchKernelGGL(k_finalize, dim3(grid_of(items)), dim3(FT), 0, s, a, p, sum_slots(a), slots, cblocks);
     return hipGetLastError();
 }
 

@@ -51,6 +51,23 @@ struct Patch {   // [8 channels] x [PV pixels]
 #pragma unroll
         for (int i = 0; i < NVEC; ++i) v[i].renew();
     }
+    // zeros in the place of what is dropped
+    template <class D>
+    __device__ __forceinline__ void drop(const D& m) {
+        constexpr int PER = 4 / (int)sizeof(T);   // elements a word
+#pragma unroll
+        for (int i = 0; i < NVEC; ++i)
+#pragma unroll
+            for (int k = 0; k < LEN; k += PER) {
+                const uint32_t lo = CLAST ? m.spread(k, i) : m.spread(i, k);
+                uint32_t gone = lo;
+                if constexpr (PER == 2) {
+                    const uint32_t hi = CLAST ? m.spread(k + 1, i) : m.spread(i, k + 1);
+                    gone = (lo & 0xffffu) | (hi & 0xffff0000u);
+                }
+                v[i].w[k / PER] &= ~gone;
+            }
+    }
     __device__ __forceinline__ float at(int ch, int px) const { return CLAST ? v[px][ch] : v[ch][px]; }
 };
 
@@ -239,12 +256,13 @@ struct Drops {
         }
     }
     __device__ __forceinline__ float kept(float v, int i, int j) const {
-        return zero_if(v, w[j / 4], 8 * ((PV < 4 ? PV : 4) - 1 - j % 4) + 7 - i);
+        return zero_if(v, w[j / 4], bit(i, j));
     }
-    __device__ __forceinline__ void renew() {
-#pragma unroll
-        for (int k = 0; k < (PV + 3) / 4; ++k) asm volatile("" : "+v"(w[k]));
+    // all ones where the element is dropped
+    __device__ __forceinline__ uint32_t spread(int i, int j) const {
+        return (uint32_t)((int32_t)(w[j / 4] << (31 - bit(i, j))) >> 31);
     }
+    static constexpr int bit(int i, int j) { return 8 * ((PV < 4 ? PV : 4) - 1 - j % 4) + 7 - i; }
 };
 
 // X: a residual (else a norm alone); DROP: elements are dropped.
@@ -343,8 +361,7 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
 #pragma unroll
         for (int i = 0; i < CG; ++i) acc[i] = acc[W + i] = 0.f;
     }
-    const unsigned tps = (unsigned)pt.tps, t0 = blockIdx.x * (unsigned)pt.per_wg;
-    const unsigned t1 = min(t0 + (unsigned)pt.per_wg, (unsigned)pt.tiles);
+    const unsigned tps = (unsigned)pt.tps, t0 = (unsigned)pt.begin(blockIdx.x), t1 = (unsigned)pt.begin(blockIdx.x + 1);
     for (unsigned t = t0; t < t1; ++t) {
         uint32_t fl = a.flags;
         asm volatile("" : "+s"(fl));   // tested here, not before the loop
@@ -382,19 +399,18 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
 #pragma unroll
         for (int j = 0; j < PV; ++j) r[j] = 1.f;
         if (fl & (LAYER | RMS)) patch_stats<TH, HCL, CL, PV, ODD>(a, fl & LAYER, h, ch, red, turn, mean, r);
+        // from here on d holds e, dy where it is kept
         if (X && !in) d.zero();   // the same for every lane: no gradient passes a dropped sample
-        Drops<PV> drop;
         if constexpr (DROP) {
-            if (on) drop.draw(a, (uint32_t)b * a.HW + px.p, ch.c);
+            if (on) {
+                Drops<PV> drop;
+                drop.draw(a, (uint32_t)b * a.HW + px.p, ch.c);
+                d.drop(drop);
+            }
         }
-        auto kept = [&](float v, int i, int j) {
-            if constexpr (DROP) return drop.kept(v, i, j);
-            return v;
-        };
         auto renew = [&] {
             h.renew();
             d.renew();
-            if constexpr (DROP) drop.renew();
         };
         float gw[CG];   // u = e gw
         const float* gate = X ? a.gate + (fl & BY_SAMPLE ? (size_t)b * a.C : 0) : nullptr;
@@ -417,7 +433,7 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
             const float g = once<ODD>(gw[i], i, ch.shared);
 #pragma unroll
             for (int j = 0; j < PV; ++j) {
-                const float z = fmaf(h.at(i, j), r[j], c[j]), e = kept(d.at(i, j), i, j), u = e * g;
+                const float z = fmaf(h.at(i, j), r[j], c[j]), e = d.at(i, j), u = e * g;
                 ms[0][j] += u;
                 ms[1][j] = fmaf(u, z, ms[1][j]);
                 const float own = once<ODD>(e, j, px.shared);
@@ -450,7 +466,7 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
             renew();
             if (on)
                 store_patch<TH, HCL, PV>((TH*)a.dh + first, oh, sh, [&](int i, int j) {
-                    return fmaf(kept(d.at(i, j), i, j) * gw[i], r[j], fmaf(h.at(i, j), c2[j], c1[j]));
+                    return fmaf(d.at(i, j) * gw[i], r[j], fmaf(h.at(i, j), c2[j], c1[j]));
                 });
         }
         // the last tile of this sample in the workgroup's range
@@ -503,24 +519,23 @@ inline TileShape tile_shape(const BlockArgs& a, int pv) {
     if ((uint64_t)a.C * a.HW * sizeof(float) >= 1ull << 32) return best;
     long long least = 0;
     for (int cl : {8, 4, 16}) {
-        const int nw = cdiv(a.C, cl * CG), px = 64 / cl * pv, tps = cdiv(a.HW, px);
+        const int nw = cdiv(a.C, cl * CG);
+        if (nw > (cl == 16 ? 16 : 8)) continue;
+        const int v = nw > 8 ? 4 : pv, px = 64 / cl * v, tps = cdiv(a.HW, px);
         const long long waves = (long long)nw * tps;
         if ((long long)a.B * tps >= 1ll << 30) continue;   // tiles are counted in 32 bits
-        if (nw > (cl == 16 ? 16 : 8) || (best.cl && waves >= least)) continue;
-        best = TileShape{cl, pv, nw, px, tps};
+        if (best.cl && waves >= least) continue;
+        best = TileShape{cl, v, nw, px, tps};
         least = waves;
     }
     return best;
 }
 
-#ifndef WTC_PVF
-#define WTC_PVF 8
-#endif
-#ifndef WTC_PVB
-#define WTC_PVB 4
-#endif
-inline int fwd_pv(int h_bf16, int y_bf16) { return h_bf16 && y_bf16 ? WTC_PVF : 4; }
-inline int bwd_pv(int h_bf16, int y_bf16) { return h_bf16 && y_bf16 ? WTC_PVB : 4; }
+// Pixels of a lane: 16 bytes of a plane in bf16 (a tile's fixed costs are
+// spread over twice the elements of 8-byte lanes: residual forward
+// 32x128x128x128 81 against 106 us, its backward 162 against 201), 16 bytes in
+// fp32; 4 where more than eight wavefronts share the registers.
+inline int patch_pixels(int h_bf16, int y_bf16) { return h_bf16 && y_bf16 ? 8 : 4; }
 
 // One file each for the three pairs of memory orders, forwards and backwards.
 template <bool HCL, bool YCL>
@@ -531,20 +546,20 @@ hipError_t tile_bwd_launch(const BlockArgs& a, int h_bf16, int y_bf16, const Til
 
 inline size_t tile_lds(const TileShape& t) { return t.nw > 1 ? (size_t)2 * t.nw * 2 * t.px * sizeof(float) : 0; }
 
-// CALL(CL, MAXT) for the shape's channel lanes and wavefronts.
+// CALL(CL, PV, MAXT) for the shape's channel lanes and wavefronts.
 #define WTC_TILE_SHAPES(CALL)                      \
-    if (t.cl == 4) return CALL(4, 512);            \
-    if (t.cl == 8) return CALL(8, 512);            \
-    if (t.nw <= 8) return CALL(16, 512);           \
-    return CALL(16, 1024);
+    if (t.cl == 4) return CALL(4, PV, 512);        \
+    if (t.cl == 8) return CALL(8, PV, 512);        \
+    if (t.nw <= 8) return CALL(16, PV, 512);       \
+    return CALL(16, 4, 1024);
 
 template <typename TH, bool HCL, typename TY, bool YCL, int PV, bool X, bool DROP, bool ODD>
 hipError_t tile_fwd_odd(const BlockArgs& a, const TileShape& t, hipStream_t s) {
     const unsigned tiles = (unsigned)a.B * (unsigned)t.tps;
     const dim3 grid(tiles < (1u << 21) ? tiles : (1u << 21)), block(64 * t.nw);
-#define WTC_CALL(CL, MAXT)                                                                                     \
+#define WTC_CALL(CL, PX, MAXT)                                                                                     \
     [&] {                                                                                                      \
-        hipLaunchKernelGGL((k_tile_fwd<TH, HCL, TY, YCL, CL, PV, MAXT, X, DROP, ODD>), grid, block, tile_lds(t), \
+        hipLaunchKernelGGL((k_tile_fwd<TH, HCL, TY, YCL, CL, PX, MAXT, X, DROP, ODD>), grid, block, tile_lds(t), \
                            s, a, tiles, (unsigned)t.tps);                                                      \
         return hipGetLastError();                                                                              \
     }()
@@ -567,15 +582,12 @@ hipError_t tile_fwd_typed(const BlockArgs& a, const TileShape& t, hipStream_t s)
 
 template <typename TH, bool HCL, typename TY, bool YCL, int PV, bool X, bool DROP, bool ODD>
 hipError_t tile_bwd_odd(BlockArgs a, const TileShape& t, const Partition& p, hipStream_t s) {
-    a.flags = (a.w ? HAS_W : 0) | (a.gate ? HAS_GATE : 0) | (a.xs ? HAS_XS : 0) | (a.dx ? WANT_DX : 0) |
-              (a.dh ? WANT_DH : 0) | (a.dxs ? WANT_DXS : 0) | (a.norm == NORM_LAYER ? LAYER : 0) |
-              (a.norm == NORM_RMS ? RMS : 0) | (a.gate_mode == GATE_SAMPLE ? BY_SAMPLE : 0) |
-              (a.drop == DROP_SAMPLE ? DROPS_SAMPLES : 0);
+    a.flags = block_flags(a);
     const dim3 grid((unsigned)p.wgs), block(64 * t.nw);
     const size_t lds = tile_lds(t) + (a.gate_mode == GATE_SAMPLE ? sizeof(float) * 2 * t.nw * t.cl * CG : 0);
-#define WTC_CALL(CL, MAXT)                                                                                     \
+#define WTC_CALL(CL, PX, MAXT)                                                                                     \
     [&] {                                                                                                      \
-        hipLaunchKernelGGL((k_tile_bwd<TH, HCL, TY, YCL, CL, PV, MAXT, X, DROP, ODD>), grid, block, lds, s, a, p, \
+        hipLaunchKernelGGL((k_tile_bwd<TH, HCL, TY, YCL, CL, PX, MAXT, X, DROP, ODD>), grid, block, lds, s, a, p, \
                            sum_slots(a), a.ws);                                                                \
         return hipGetLastError();                                                                              \
     }()
@@ -585,14 +597,14 @@ hipError_t tile_bwd_odd(BlockArgs a, const TileShape& t, const Partition& p, hip
 
 template <typename TH, bool HCL, typename TY, bool YCL, int PV, bool X, bool DROP>
 hipError_t tile_bwd_mode(const BlockArgs& a, const TileShape& t, const Partition& p, hipStream_t s) {
-    if (a.C % CG || a.HW % PV) return tile_bwd_odd<TH, HCL, TY, YCL, PV, X, DROP, true>(a, t, p, s);
+    if (a.C % CG || a.HW % t.pv) return tile_bwd_odd<TH, HCL, TY, YCL, PV, X, DROP, true>(a, t, p, s);
     return tile_bwd_odd<TH, HCL, TY, YCL, PV, X, DROP, false>(a, t, p, s);
 }
 
 template <typename TH, bool HCL, typename TY, bool YCL, int PV>
 hipError_t tile_bwd_typed(const BlockArgs& a, const TileShape& t, const Partition& p, hipStream_t s) {
     if (a.drop == DROP_ELEMENT) return tile_bwd_mode<TH, HCL, TY, YCL, PV, true, true>(a, t, p, s);
-    if (a.gate || a.xs || a.dx || a.dxs || a.drop != DROP_NONE)
+    if (block_residual(a))
         return tile_bwd_mode<TH, HCL, TY, YCL, PV, true, false>(a, t, p, s);
     return tile_bwd_mode<TH, HCL, TY, YCL, PV, false, false>(a, t, p, s);
 }
@@ -601,7 +613,7 @@ hipError_t tile_bwd_typed(const BlockArgs& a, const TileShape& t, const Partitio
     template <>                                                                                                      \
     hipError_t tile_fwd_launch<HCL, YCL>(const BlockArgs& a, int h_bf16, int y_bf16, const TileShape& t,             \
                                          hipStream_t s) {                                                            \
-        if (h_bf16 && y_bf16) return tile_fwd_typed<bf16_t, HCL, bf16_t, YCL, WTC_PVF>(a, t, s);                           \
+        if (h_bf16 && y_bf16) return tile_fwd_typed<bf16_t, HCL, bf16_t, YCL, 8>(a, t, s);                           \
         if (h_bf16) return tile_fwd_typed<bf16_t, HCL, float, YCL, 4>(a, t, s);                                      \
         if (y_bf16) return tile_fwd_typed<float, HCL, bf16_t, YCL, 4>(a, t, s);                                      \
         return tile_fwd_typed<float, HCL, float, YCL, 4>(a, t, s);                                                   \
@@ -611,7 +623,7 @@ hipError_t tile_bwd_typed(const BlockArgs& a, const TileShape& t, const Partitio
     template <>                                                                                                      \
     hipError_t tile_bwd_launch<HCL, YCL>(const BlockArgs& a, int h_bf16, int y_bf16, const TileShape& t,             \
                                          const Partition& p, hipStream_t s) {                                        \
-        if (h_bf16 && y_bf16) return tile_bwd_typed<bf16_t, HCL, bf16_t, YCL, WTC_PVB>(a, t, p, s);                        \
+        if (h_bf16 && y_bf16) return tile_bwd_typed<bf16_t, HCL, bf16_t, YCL, 8>(a, t, p, s);                        \
         if (h_bf16) return tile_bwd_typed<bf16_t, HCL, float, YCL, 4>(a, t, p, s);                                   \
         if (y_bf16) return tile_bwd_typed<float, HCL, bf16_t, YCL, 4>(a, t, p, s);                                   \
         return tile_bwd_typed<float, HCL, float, YCL, 4>(a, t, p, s);                                                \
