@@ -30,61 +30,6 @@
 
 namespace wtc {
 
-template <typename T, bool CLAST, int PV>
-struct Patch {   // [8 channels] x [PV pixels]
-    static constexpr int NVEC = CLAST ? PV : CG, LEN = CLAST ? CG : PV;
-    Vec<T, LEN> v[NVEC];
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int i = 0; i < NVEC; ++i) v[i].zero();
-    }
-    // p is the sample's first element, the same for every lane, and off
-    // (bytes) the lane's place in it
-    __device__ __forceinline__ void load(const T* __restrict__ p, uint32_t off, size_t step) {
-#pragma unroll
-        for (int i = 0; i < NVEC; ++i) v[i].load((const T*)((const char*)(p + i * step) + off));
-    }
-    // From here on the words are new to the compiler: what it made of them
-    // before (widened values, twice the registers in bf16) is made again
-    // rather than held.
-    __device__ __forceinline__ void renew() {
-#pragma unroll
-        for (int i = 0; i < NVEC; ++i) v[i].renew();
-    }
-    // zeros in the place of what is dropped
-    template <class D>
-    __device__ __forceinline__ void drop(const D& m) {
-        constexpr int PER = 4 / (int)sizeof(T);   // elements a word
-#pragma unroll
-        for (int i = 0; i < NVEC; ++i)
-#pragma unroll
-            for (int k = 0; k < LEN; k += PER) {
-                const uint32_t lo = CLAST ? m.spread(k, i) : m.spread(i, k);
-                uint32_t gone = lo;
-                if constexpr (PER == 2) {
-                    const uint32_t hi = CLAST ? m.spread(k + 1, i) : m.spread(i, k + 1);
-                    gone = (lo & 0xffffu) | (hi & 0xffff0000u);
-                }
-                v[i].w[k / PER] &= ~gone;
-            }
-    }
-    __device__ __forceinline__ float at(int ch, int px) const { return CLAST ? v[px][ch] : v[ch][px]; }
-};
-
-// f(channel, pixel) for every element, rounded and stored.
-template <typename T, bool CLAST, int PV, class F>
-__device__ __forceinline__ void store_patch(T* __restrict__ p, uint32_t off, size_t step, F&& f) {
-    constexpr int NVEC = CLAST ? PV : CG, LEN = CLAST ? CG : PV;
-#pragma unroll
-    for (int i = 0; i < NVEC; ++i) {
-        float o[LEN];
-#pragma unroll
-        for (int k = 0; k < LEN; ++k) o[k] = CLAST ? f(k, i) : f(i, k);
-        store_vec<T, LEN>((T*)((char*)(p + i * step) + off), o);
-        __builtin_amdgcn_sched_barrier(0);   // a vector at a time: fewer values in flight
-    }
-}
-
 // v, or zero where element k is one of the `shared` that a neighbour has too.
 // ODD: there may be such elements.
 template <bool ODD>
@@ -238,33 +183,6 @@ __device__ __forceinline__ void patch_stats(const BlockArgs& a, bool layer, Patc
     for (int j = 0; j < PV; ++j) r[j] = rsqrtf(s[1][j] * a.inv_c + a.eps);
 }
 
-// Drop bits of a lane's elements: a byte for each pixel, the first at the top
-// of a word.
-template <int PV>
-struct Drops {
-    uint32_t w[(PV + 3) / 4];
-    __device__ __forceinline__ void draw(const BlockArgs& a, uint32_t row, int c) {
-        const Philox gen(a.rng, a.site);
-        const uint32_t G = (uint32_t)cdiv(a.C, CG);
-        uint32_t g = row * G;   // fewer than 2^32 groups in all
-#pragma unroll
-        for (int k = 0; k < (PV + 3) / 4; ++k) {
-            uint32_t m = 0;
-#pragma unroll 2
-            for (int j = 0; j < 4 && j < PV; ++j, g += G) m = m << 8 | drop_bits_at(gen, g, c, a.C % CG != 0, a.thr);
-            w[k] = m;
-        }
-    }
-    __device__ __forceinline__ float kept(float v, int i, int j) const {
-        return zero_if(v, w[j / 4], bit(i, j));
-    }
-    // all ones where the element is dropped
-    __device__ __forceinline__ uint32_t spread(int i, int j) const {
-        return (uint32_t)((int32_t)(w[j / 4] << (31 - bit(i, j))) >> 31);
-    }
-    static constexpr int bit(int i, int j) { return 8 * ((PV < 4 ? PV : 4) - 1 - j % 4) + 7 - i; }
-};
-
 // X: a residual (else a norm alone); DROP: elements are dropped.
 template <typename TH, bool HCL, typename TY, bool YCL, int CL, int PV, int MAXT, bool X, bool DROP, bool ODD>
 __global__ __launch_bounds__(MAXT) void k_tile_fwd(BlockArgs a, unsigned tiles, unsigned tps) {
@@ -308,7 +226,7 @@ __global__ __launch_bounds__(MAXT) void k_tile_fwd(BlockArgs a, unsigned tiles, 
             patch_stats<TH, HCL, CL, PV, ODD>(a, a.norm == NORM_LAYER, h, ch, red, turn, mean, r);
         if (!on) continue;
         Drops<PV> drop;
-        if constexpr (DROP) drop.draw(a, (uint32_t)b * a.HW + px.p, ch.c);
+        if constexpr (DROP) drop.template draw<ODD>(a, (uint32_t)b * a.HW + px.p, ch.c);
         store_patch<TY, YCL, PV>((TY*)a.y + first, oy, sy, [&](int i, int j) {
             float o = fmaf((h.at(i, j) - mean[j]) * r[j], wg[i], bg[i]);
             if constexpr (DROP) o = drop.kept(o, i, j);
@@ -404,7 +322,7 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
         if constexpr (DROP) {
             if (on) {
                 Drops<PV> drop;
-                drop.draw(a, (uint32_t)b * a.HW + px.p, ch.c);
+                drop.template draw<ODD>(a, (uint32_t)b * a.HW + px.p, ch.c);
                 d.drop(drop);
             }
         }
