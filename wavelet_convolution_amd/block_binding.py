@@ -28,6 +28,25 @@ def _code(table: dict, value, what: str) -> int:
         raise ValueError(f"{what} must be one of {', '.join(map(str, table))}; got {value!r}") from None
 
 
+def _on_gpu(act, **tensors) -> None:
+    """The binding's refusal of host tensors (and of those of another GPU); the quick test first."""
+    if isinstance(act, torch.Tensor) and act.is_cuda:
+        dev = act.device
+        for t in tensors.values():
+            if t is not None and not (isinstance(t, torch.Tensor) and t.device == dev):
+                break
+        else:
+            return
+    _b._require_gpu(act, **tensors)
+
+
+def _vector(name: str, t, act) -> None:
+    """A parameter of one fp32 number a channel."""
+    if t is not None and not (t.dtype is torch.float32 and t.dim() == 1 and t.numel() == act.shape[1]
+                              and t.is_contiguous()):
+        _b._check_f32(name, t, (act.shape[1],), act)
+
+
 def _act(name: str, t: torch.Tensor, like: torch.Tensor | None = None) -> tuple[int, int]:
     """(dtype, layout) codes of an activation tensor."""
     if t.dim() != 4 or (like is not None and t.shape != like.shape):
@@ -47,11 +66,10 @@ def _rng(rng, act: torch.Tensor) -> None:
 def _gate_code(gate, act: torch.Tensor) -> int:
     if gate is None:
         return 0
-    B, C = act.shape[:2]
     if gate.dim() == 1:
-        _b._check_f32("gate", gate, (C,), act)
+        _vector("gate", gate, act)
         return 1
-    _b._check_f32("gate", gate, (B, C), act)
+    _b._check_f32("gate", gate, tuple(act.shape[:2]), act)
     return 2
 
 
@@ -146,14 +164,13 @@ def wtconv_norm_fwd(x, weight=None, bias=None, *, kind: str = "layer", eps: floa
     """y = norm(x) * weight + bias over the channels of each pixel. kind: "layer" or "rms"; weight, bias [C] fp32 or
     None. y has x's type and memory order unless `dtype` or `channels_last` (True, False) say otherwise, or `y` is
     given."""
-    _b._require_gpu(x, weight=weight, bias=bias, y=y)
+    _on_gpu(x, weight=weight, bias=bias, y=y)
     if _elsewhere(x, stream):
         return _enter(wtconv_norm_fwd, x, stream, (x, weight, bias, y), x, weight, bias, kind=kind, eps=eps,
                       channels_last=channels_last, dtype=dtype, y=y)
     hc = _act("x", x)
-    C = x.shape[1]
-    _b._check_f32("weight", weight, (C,), x)
-    _b._check_f32("bias", bias, (C,), x)
+    _vector("weight", weight, x)
+    _vector("bias", bias, x)
     if y is None:
         same = channels_last is None or bool(channels_last) == (hc[1] == _b.WTCONV_NHWC)
         if same and (dtype is None or dtype == x.dtype):
@@ -176,14 +193,14 @@ def wtconv_norm_bwd(x, dy, weight=None, bias=None, *, kind: str = "layer", eps: 
     """(dx, dweight, dbias) of wtconv_norm_fwd; dx has x's type and memory order. `want`: the names of the
     gradients to compute (default: dx, and those of the parameters given); the others are None. `ws`: a workspace
     of wtconv_block_workspace_size bytes (allocated if None)."""
-    _b._require_gpu(x, dy=dy, weight=weight, bias=bias, dx=dx, ws=ws)
+    _on_gpu(x, dy=dy, weight=weight, bias=bias, dx=dx, ws=ws)
     if _elsewhere(x, stream):
         return _enter(wtconv_norm_bwd, x, stream, (x, dy, weight, bias, dx, ws), x, dy, weight, bias, kind=kind,
                       eps=eps, want=want, dx=dx, ws=ws)
     hc = _act("x", x)
     C = x.shape[1]
-    _b._check_f32("weight", weight, (C,), x)
-    _b._check_f32("bias", bias, (C,), x)
+    _vector("weight", weight, x)
+    _vector("bias", bias, x)
     if want is None:
         want = ("dx",) + (("dweight",) if weight is not None else ()) + (("dbias",) if bias is not None else ())
     else:
@@ -210,14 +227,13 @@ def _wanted(want, names) -> None:
 
 
 def _residual_desc(x, h, kind, weight, bias, eps, gate, x_scale, drop, p, rng, site):
-    C = x.shape[1] if x.dim() == 4 else 0
     xc, hc = _act("x", x), _act("h", h, x)
     norm, mode = _code(_NORMS, kind, "kind"), _code(_DROPS, drop, "drop")
     if norm == 0 and (weight is not None or bias is not None):
         raise ValueError("weight and bias need a norm (kind)")
-    _b._check_f32("weight", weight, (C,), x)
-    _b._check_f32("bias", bias, (C,), x)
-    _b._check_f32("x_scale", x_scale, (C,), x)
+    _vector("weight", weight, x)
+    _vector("bias", bias, x)
+    _vector("x_scale", x_scale, x)
     if mode:
         _rng(rng, x)
     return _desc(x, hc, xc, norm, eps, _gate_code(gate, x), mode, p if mode else 0.0, site)
@@ -229,7 +245,7 @@ def wtconv_residual_fwd(x, h, *, kind: str = "none", weight=None, bias=None, eps
     """out = x_scale * x + gate * D(norm(h) * weight + bias). x and out share type and memory order, h has its own.
     kind: "none", "layer" or "rms"; gate: [C] or [B, C]; x_scale: [C]; drop: "none", "element" or "sample", with
     probability p from rng (int64 {seed, offset} on the GPU) and site. Parameters are fp32."""
-    _b._require_gpu(x, h=h, weight=weight, bias=bias, gate=gate, x_scale=x_scale, rng=rng, out=out)
+    _on_gpu(x, h=h, weight=weight, bias=bias, gate=gate, x_scale=x_scale, rng=rng, out=out)
     if _elsewhere(x, stream):
         return _enter(wtconv_residual_fwd, x, stream, (x, h, weight, bias, gate, x_scale, rng, out), x, h, kind=kind,
                       weight=weight, bias=bias, eps=eps, gate=gate, x_scale=x_scale, drop=drop, p=p, rng=rng,
@@ -251,7 +267,7 @@ def wtconv_residual_bwd(dout, h, *, x=None, kind: str = "none", weight=None, bia
     """(dx, dh, (dweight, dbias, dgate, dx_scale)) of wtconv_residual_fwd. Without an x_scale dx is dout itself
     (unless a dx to write is given); x is needed for dx_scale only. `want`: the names of the gradients to compute
     (default: dx, dh and those of the parameters given); the others are None."""
-    _b._require_gpu(dout, h=h, x=x, weight=weight, bias=bias, gate=gate, x_scale=x_scale, rng=rng, dx=dx, dh=dh, ws=ws)
+    _on_gpu(dout, h=h, x=x, weight=weight, bias=bias, gate=gate, x_scale=x_scale, rng=rng, dx=dx, dh=dh, ws=ws)
     if _elsewhere(dout, stream):
         return _enter(wtconv_residual_bwd, dout, stream,
                       (dout, h, x, weight, bias, gate, x_scale, rng, dx, dh, ws), dout, h, x=x, kind=kind,
@@ -303,7 +319,7 @@ def wtconv_dropout(x, p: float, rng, *, site: int = 0, mode: str = "element", y=
     """y = D(x): elements (mode "element") or whole samples b (mode "sample") dropped with probability p by the bits
     of rng (int64 {seed, offset} on the GPU) and site; what is kept is scaled. The mask is never stored: the
     gradient is the same call on dy."""
-    _b._require_gpu(x, rng=rng, y=y)
+    _on_gpu(x, rng=rng, y=y)
     if _elsewhere(x, stream):
         return _enter(wtconv_dropout, x, stream, (x, rng, y), x, p, rng, site=site, mode=mode, y=y)
     c = _act("x", x)

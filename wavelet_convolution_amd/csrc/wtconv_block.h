@@ -54,6 +54,7 @@ struct BlockArgs {
     float keep;         // 65536 / (65536 - thr); 0 where thr = 65536
     uint32_t site;
     uint32_t flags;     // of the backward kernels, set at their launch
+    uint32_t near;      // neighbouring tiles share cache lines: keep them on one XCD
 };
 
 // The sums over rows that the parameter gradients need. Each workgroup of a

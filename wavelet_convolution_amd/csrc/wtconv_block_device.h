@@ -85,6 +85,14 @@ template <typename T> __device__ __forceinline__ T narrow_to(float f);
 template <> __device__ __forceinline__ float narrow_to<float>(float f) { return f; }
 template <> __device__ __forceinline__ bf16_t narrow_to<bf16_t>(float f) { return narrow_bf16(f); }
 
+// Workgroups go to the eight XCDs in turn, each with an L2 of its own. The
+// i-th of n workgroups takes this piece of work, so that neighbouring pieces
+// (tiles of a plane that share a cache line) are on one XCD.
+__device__ __forceinline__ unsigned xcd_order(unsigned i, unsigned n) {
+    const unsigned xcd = i % 8, share = n / 8, more = n % 8;
+    return xcd * share + min(xcd, more) + i / 8;
+}
+
 // Sum over aligned groups of N lanes (N a power of two up to 64), in every
 // lane: data-parallel moves within a row of 16 lanes (pairs, quads, half
 // mirror, mirror), then the two row swaps.

@@ -190,7 +190,7 @@ __global__ __launch_bounds__(MAXT) void k_tile_fwd(BlockArgs a, unsigned tiles, 
     int turn = 0;
     const Channels<CL> ch(a.C);
     const size_t sh = HCL ? a.C : a.HW, sy = YCL ? a.C : a.HW;
-    for (unsigned t = blockIdx.x; t < tiles; t += gridDim.x) {
+    for (unsigned t = a.near ? xcd_order(blockIdx.x, gridDim.x) : blockIdx.x; t < tiles; t += gridDim.x) {
         const unsigned b = t / tps;
         const Pixels<CL, PV> px(a.HW, (int)(t - b * tps));
         const bool in = !X || a.drop != DROP_SAMPLE || sample_kept(a, (int)b), on = ch.on && px.on;
@@ -252,7 +252,8 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
     float *acc = lds + own, *red = lds + (X && (a.flags & BY_SAMPLE) ? 2 * W : 0);
     int turn = 0;
     float s1[CG] = {}, s0[CG] = {}, sx[CG] = {};
-    float* slot = slots + (size_t)blockIdx.x * (pt.nsum + pt.partials) * a.C;
+    const unsigned wg = a.near ? xcd_order(blockIdx.x, gridDim.x) : blockIdx.x;
+    float* slot = slots + (size_t)wg * (pt.nsum + pt.partials) * a.C;
     const bool writes = threadIdx.x % 64 < CL && ch.on;   // the lane that writes its channels' sums
     auto pixel_sums = [&](float (&s)[CG]) {
 #pragma unroll
@@ -279,7 +280,7 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
 #pragma unroll
         for (int i = 0; i < CG; ++i) acc[i] = acc[W + i] = 0.f;
     }
-    const unsigned tps = (unsigned)pt.tps, t0 = (unsigned)pt.begin(blockIdx.x), t1 = (unsigned)pt.begin(blockIdx.x + 1);
+    const unsigned tps = (unsigned)pt.tps, t0 = (unsigned)pt.begin(wg), t1 = (unsigned)pt.begin(wg + 1);
     for (unsigned t = t0; t < t1; ++t) {
         uint32_t fl = a.flags;
         asm volatile("" : "+s"(fl));   // tested here, not before the loop
@@ -428,9 +429,24 @@ struct TileShape {
 };
 // Channel lanes: the choice among 4, 8 and 16 with the fewest wavefronts over
 // a sample (idle lanes past C and past the plane cost as much as busy ones).
+// Sixteen leave 64-byte pieces of a plane and many workgroups of few
+// wavefronts, so they need a twentieth fewer (64x384x14x14: 28.0 us backward
+// against 29.4 with eight; 32x128x100x100 at the same number: 167 against
+// 139). Between four and eight at the same number, four have a plane's pieces
+// longer and eight fewer wavefronts to a barrier: eight forwards (32x128x127x125
+// 52 us against 59), four backwards where that is three or four wavefronts (216
+// against 249; 64x64x64x64, two: 54.5 against 50.9).
+//
+// Pixels of a lane: 16 bytes of a plane in bf16 (a tile's fixed costs are
+// spread over twice the elements of 8-byte lanes: residual forward
+// 32x128x128x128 81 against 106 us, its backward 162 against 201), unless
+// that leaves less than a wavefront a SIMD, which is all latency (64x768x7x7
+// residual backward 28.2 us with eight pixels, 21.3 with four); 4 in fp32, and
+// where more than eight wavefronts share the registers.
+//
 // cl = 0: fewer channels or pixels than a lane's, more channels than sixteen
 // wavefronts hold, a sample of 2^30 elements, or 2^30 tiles.
-inline TileShape tile_shape(const BlockArgs& a, int pv) {
+inline TileShape tile_shape_of(const BlockArgs& a, int pv, bool backward) {
     TileShape best{};
     if (a.C < CG || a.HW < pv) return best;
     // a lane's place in its sample is a 32-bit number of bytes
@@ -442,18 +458,22 @@ inline TileShape tile_shape(const BlockArgs& a, int pv) {
         const int v = nw > 8 ? 4 : pv, px = 64 / cl * v, tps = cdiv(a.HW, px);
         const long long waves = (long long)nw * tps;
         if ((long long)a.B * tps >= 1ll << 30) continue;   // tiles are counted in 32 bits
-        if (best.cl && waves >= least) continue;
+        const bool better = cl == 16  ? waves * 21 <= least * 20
+                            : cl == 4 ? waves < least || (waves == least && backward && nw >= 3 && nw <= 4)
+                                      : waves < least;
+        if (best.cl && !better) continue;
         best = TileShape{cl, v, nw, px, tps};
         least = waves;
     }
     return best;
 }
-
-// Pixels of a lane: 16 bytes of a plane in bf16 (a tile's fixed costs are
-// spread over twice the elements of 8-byte lanes: residual forward
-// 32x128x128x128 81 against 106 us, its backward 162 against 201), 16 bytes in
-// fp32; 4 where more than eight wavefronts share the registers.
-inline int patch_pixels(int h_bf16, int y_bf16) { return h_bf16 && y_bf16 ? 8 : 4; }
+inline TileShape tile_shape(const BlockArgs& a, int h_bf16, int y_bf16, bool backward) {
+    if (h_bf16 && y_bf16) {
+        const TileShape t = tile_shape_of(a, 8, backward);
+        if (t.cl && (long long)a.B * t.tps * t.nw >= 4 * 256) return t;
+    }
+    return tile_shape_of(a, 4, backward);
+}
 
 // One file each for the three pairs of memory orders, forwards and backwards.
 template <bool HCL, bool YCL>
@@ -527,11 +547,13 @@ hipError_t tile_bwd_typed(const BlockArgs& a, const TileShape& t, const Partitio
     return tile_bwd_mode<TH, HCL, TY, YCL, PV, false, false>(a, t, p, s);
 }
 
+// Eight pixels a lane, or four, for bf16 on both sides; four else.
 #define WTC_TILE_FWD(HCL, YCL)                                                                                       \
     template <>                                                                                                      \
     hipError_t tile_fwd_launch<HCL, YCL>(const BlockArgs& a, int h_bf16, int y_bf16, const TileShape& t,             \
                                          hipStream_t s) {                                                            \
-        if (h_bf16 && y_bf16) return tile_fwd_typed<bf16_t, HCL, bf16_t, YCL, 8>(a, t, s);                           \
+        if (h_bf16 && y_bf16 && t.pv == 8) return tile_fwd_typed<bf16_t, HCL, bf16_t, YCL, 8>(a, t, s);              \
+        if (h_bf16 && y_bf16) return tile_fwd_typed<bf16_t, HCL, bf16_t, YCL, 4>(a, t, s);                           \
         if (h_bf16) return tile_fwd_typed<bf16_t, HCL, float, YCL, 4>(a, t, s);                                      \
         if (y_bf16) return tile_fwd_typed<float, HCL, bf16_t, YCL, 4>(a, t, s);                                      \
         return tile_fwd_typed<float, HCL, float, YCL, 4>(a, t, s);                                                   \
@@ -541,7 +563,8 @@ hipError_t tile_bwd_typed(const BlockArgs& a, const TileShape& t, const Partitio
     template <>                                                                                                      \
     hipError_t tile_bwd_launch<HCL, YCL>(const BlockArgs& a, int h_bf16, int y_bf16, const TileShape& t,             \
                                          const Partition& p, hipStream_t s) {                                        \
-        if (h_bf16 && y_bf16) return tile_bwd_typed<bf16_t, HCL, bf16_t, YCL, 8>(a, t, p, s);                        \
+        if (h_bf16 && y_bf16 && t.pv == 8) return tile_bwd_typed<bf16_t, HCL, bf16_t, YCL, 8>(a, t, p, s);           \
+        if (h_bf16 && y_bf16) return tile_bwd_typed<bf16_t, HCL, bf16_t, YCL, 4>(a, t, p, s);                        \
         if (h_bf16) return tile_bwd_typed<bf16_t, HCL, float, YCL, 4>(a, t, p, s);                                   \
         if (y_bf16) return tile_bwd_typed<float, HCL, bf16_t, YCL, 4>(a, t, p, s);                                   \
         return tile_bwd_typed<float, HCL, float, YCL, 4>(a, t, p, s);                                                \
