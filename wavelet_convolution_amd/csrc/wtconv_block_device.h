@@ -116,7 +116,13 @@ __device__ __forceinline__ float lane_sum(float v) {
     }
     return v;
 }
-// The same over lanes N apart: lanes l, l + N, ... up to 64 (N >= 4).
+// v of lane K of each quad, in all four lanes.
+template <int K>
+__device__ __forceinline__ float quad_lane(float v) {
+    return dpp_mov<K * 0x55>(v);   // lanes K K K K
+}
+
+// lane_sum over lanes N apart: lanes l, l + N, ... up to 64 (N >= 4).
 template <int N>
 __device__ __forceinline__ float stride_sum(float v) {
     if constexpr (N <= 4) v += dpp_mov<0x124>(v);   // rotate by 4 within sixteen,

@@ -67,38 +67,44 @@ struct Pixels {
     }
 };
 
-// Sums over all channels of PV pixel values (K sets of them) in every lane.
-// The wavefronts' sums go to one of two buffers in turn.
-template <int CL, int PV, int K>
-__device__ __forceinline__ void channel_sums(float (&s)[K][PV], float* red, int& turn) {
-    constexpr int PL = 64 / CL;
+// The exchange between wavefronts. Every lane of a wavefront has its sums of
+// two values at its PV pixels; they go to one of two buffers in LDS in turn
+// (one barrier an exchange). What they come to over all wavefronts is worked
+// out once a quad: lane q of four takes pixels q and q + 4, and hands its
+// results round by data-parallel moves.
+template <int CL, int PV>
+struct Exchange {
+    static constexpr int PL = 64 / CL, OWN = PV / 4;   // pixels of a lane of the quad
+    float* red;                                        // [2 turns][nw][2 values][PL * PV]
+    int turn = 0;
+    const float* buf;
+
+    __device__ __forceinline__ void put(const float (&a)[PV], const float (&b)[PV]) {
+        const int nw = blockDim.x / 64, lane = threadIdx.x % 64, wave = threadIdx.x / 64, pl = lane / CL;
+        float* to = red + turn * nw * 2 * PL * PV;
+        turn ^= 1;
+        if (lane % CL == 0) {
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int j = 0; j < PV; ++j) s[k][j] = lane_sum<CL>(s[k][j]);
-    const int nw = blockDim.x / 64;
-    if (nw == 1) return;
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, pl = lane / CL;
-    float* buf = red + (size_t)turn * nw * 2 * PL * PV;
-    turn ^= 1;
-    if (lane % CL == 0) {
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-            for (int j = 0; j < PV; ++j) buf[((wave * K + k) * PL + pl) * PV + j] = s[k][j];
+            for (int j = 0; j < PV; ++j) {
+                to[(wave * 2 * PL + pl) * PV + j] = a[j];
+                to[((wave * 2 + 1) * PL + pl) * PV + j] = b[j];
+            }
+        }
+        __syncthreads();
+        buf = to + pl * PV + lane % 4;
     }
-    __syncthreads();
+    // value k (0 or 1) of wavefront w at this lane's i-th pixel of the quad's
+    __device__ __forceinline__ float get(int w, int k, int i) const { return buf[(w * 2 + k) * PL * PV + 4 * i]; }
+    static __device__ __forceinline__ void round_quad(const float (&own)[OWN], float (&all)[PV]) {
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int j = 0; j < PV; ++j) s[k][j] = 0.f;
-#pragma unroll 2
-    for (int w = 0; w < nw; ++w)
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-            for (int j = 0; j < PV; ++j) s[k][j] += buf[((w * K + k) * PL + pl) * PV + j];
-}
+        for (int i = 0; i < OWN; ++i) {
+            all[4 * i] = quad_lane<0>(own[i]);
+            all[4 * i + 1] = quad_lane<1>(own[i]);
+            all[4 * i + 2] = quad_lane<2>(own[i]);
+            all[4 * i + 3] = quad_lane<3>(own[i]);
+        }
+    }
+};
 
 // mean and r of a lane's pixels. Each wavefront takes the mean of its own
 // channels and the squares about that mean, and the wavefronts' pairs join
@@ -108,10 +114,10 @@ __device__ __forceinline__ void channel_sums(float (&s)[K][PV], float* red, int&
 // barrier, and no difference of large sums.
 template <typename TH, bool HCL, int CL, int PV, bool ODD>
 __device__ __forceinline__ void patch_stats(const BlockArgs& a, bool layer, Patch<TH, HCL, PV>& h,
-                                            const Channels<CL>& ch, float* red, int& turn, float (&mean)[PV],
+                                            const Channels<CL>& ch, Exchange<CL, PV>& ex, float (&mean)[PV],
                                             float (&r)[PV]) {
-    constexpr int WC = CL * CG, PL = 64 / CL;   // channels of a full wavefront, pixel lanes
-    const int nw = blockDim.x / 64, wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    constexpr int WC = CL * CG, OWN = Exchange<CL, PV>::OWN;   // WC: channels of a full wavefront
+    const int nw = blockDim.x / 64, wave = threadIdx.x / 64;
     float s[2][PV];
 #pragma unroll
     for (int j = 0; j < PV; ++j) s[0][j] = mean[j] = 0.f;
@@ -144,50 +150,42 @@ __device__ __forceinline__ void patch_stats(const BlockArgs& a, bool layer, Patc
     h.renew();
 #pragma unroll
     for (int j = 0; j < PV; ++j) s[1][j] = lane_sum<CL>(s[1][j]);
-    if (nw > 1) {
-        float* buf = red + (size_t)turn * nw * 2 * PL * PV;
-        turn ^= 1;
-        const int pl = lane / CL;
-        // a wavefront's sum about the mean that it took, and that mean
-        if (lane % CL == 0) {
+    if (nw == 1) {
 #pragma unroll
-            for (int j = 0; j < PV; ++j) {
-                buf[((wave * 2) * PL + pl) * PV + j] = mean[j];
-                buf[((wave * 2 + 1) * PL + pl) * PV + j] = s[1][j];
-            }
-        }
-        __syncthreads();
-        if (layer) {
-#pragma unroll
-            for (int j = 0; j < PV; ++j) mean[j] = 0.f;
-#pragma unroll 2
-            for (int w = 0; w < nw; ++w) {
-                const float part = (float)min(WC, a.C - w * WC) * a.inv_c;
-#pragma unroll
-                for (int j = 0; j < PV; ++j) mean[j] = fmaf(buf[((w * 2) * PL + pl) * PV + j], part, mean[j]);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < PV; ++j) s[1][j] = 0.f;
-#pragma unroll 2
+        for (int j = 0; j < PV; ++j) r[j] = rsqrtf(s[1][j] * a.inv_c + a.eps);
+        return;
+    }
+    // a wavefront's squares about the mean that it took, and that mean
+    ex.put(mean, s[1]);
+    float m[OWN] = {}, q[OWN] = {};
+    if (layer) {
+#pragma unroll 4
         for (int w = 0; w < nw; ++w) {
-            const float n = (float)min(WC, a.C - w * WC);
+            const float part = (float)min(WC, a.C - w * WC) * a.inv_c;
 #pragma unroll
-            for (int j = 0; j < PV; ++j) {
-                const float d = buf[((w * 2) * PL + pl) * PV + j] - mean[j];   // zero for rms
-                s[1][j] += fmaf(d * n, d, buf[((w * 2 + 1) * PL + pl) * PV + j]);
-            }
+            for (int i = 0; i < OWN; ++i) m[i] = fmaf(ex.get(w, 0, i), part, m[i]);
+        }
+    }
+#pragma unroll 4
+    for (int w = 0; w < nw; ++w) {
+        const float n = (float)min(WC, a.C - w * WC);
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) {
+            const float d = ex.get(w, 0, i) - m[i];   // zero for rms
+            q[i] += fmaf(d * n, d, ex.get(w, 1, i));
         }
     }
 #pragma unroll
-    for (int j = 0; j < PV; ++j) r[j] = rsqrtf(s[1][j] * a.inv_c + a.eps);
+    for (int i = 0; i < OWN; ++i) q[i] = rsqrtf(q[i] * a.inv_c + a.eps);
+    ex.round_quad(m, mean);
+    ex.round_quad(q, r);
 }
 
 // X: a residual (else a norm alone); DROP: elements are dropped.
 template <typename TH, bool HCL, typename TY, bool YCL, int CL, int PV, int MAXT, bool X, bool DROP, bool ODD>
 __global__ __launch_bounds__(MAXT) void k_tile_fwd(BlockArgs a, unsigned tiles, unsigned tps) {
     extern __shared__ float red[];
-    int turn = 0;
+    Exchange<CL, PV> ex{red};
     const Channels<CL> ch(a.C);
     const size_t sh = HCL ? a.C : a.HW, sy = YCL ? a.C : a.HW;
     for (unsigned t = a.near ? xcd_order(blockIdx.x, gridDim.x) : blockIdx.x; t < tiles; t += gridDim.x) {
@@ -199,11 +197,11 @@ __global__ __launch_bounds__(MAXT) void k_tile_fwd(BlockArgs a, unsigned tiles, 
         const uint32_t oh = (HCL ? rows : planar) * sizeof(TH), oy = (YCL ? rows : planar) * sizeof(TY);
         Patch<TH, HCL, PV> h;
         Patch<TY, YCL, PV> x;
-        h.zero();   // a dropped sample's h is not looked at
-        if (on) {
-            if (in) h.load((const TH*)a.h + first, oh, sh);
-            if constexpr (X) x.load((const TY*)a.x + first, oy, sy);
-        }
+        // lanes that have nothing of their own read their neighbours' and count
+        // zeros; a dropped sample's h is not looked at
+        if (in) h.load((const TH*)a.h + first, oh, sh);
+        if constexpr (X) x.load((const TY*)a.x + first, oy, sy);
+        if (!in || !on) h.zero();
         // y = s x + D'(z wg + bg), with the gate and D's factor in wg and bg
         float wg[CG], bg[CG], xs[CG];
         load_param(a.w, ch.c, 1.f, wg);
@@ -223,7 +221,7 @@ __global__ __launch_bounds__(MAXT) void k_tile_fwd(BlockArgs a, unsigned tiles, 
 #pragma unroll
         for (int j = 0; j < PV; ++j) r[j] = 1.f;
         if (a.norm != NORM_NONE)
-            patch_stats<TH, HCL, CL, PV, ODD>(a, a.norm == NORM_LAYER, h, ch, red, turn, mean, r);
+            patch_stats<TH, HCL, CL, PV, ODD>(a, a.norm == NORM_LAYER, h, ch, ex, mean, r);
         if (!on) continue;
         Drops<PV> drop;
         if constexpr (DROP) drop.template draw<ODD>(a, (uint32_t)b * a.HW + px.p, ch.c);
@@ -249,8 +247,9 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
     const size_t sh = HCL ? a.C : a.HW, sy = YCL ? a.C : a.HW;
     // with a gate per sample: dw, db [2][lanes' channels], each of its own lane
     const int W = blockDim.x / 64 * CL * CG, own = (threadIdx.x / 64 * CL + threadIdx.x % CL) * CG;
-    float *acc = lds + own, *red = lds + (X && (a.flags & BY_SAMPLE) ? 2 * W : 0);
-    int turn = 0;
+    float* acc = lds + own;
+    using EX = Exchange<CL, PV>;
+    EX ex{lds + (X && (a.flags & BY_SAMPLE) ? 2 * W : 0)};
     float s1[CG] = {}, s0[CG] = {}, sx[CG] = {};
     const unsigned wg = a.near ? xcd_order(blockIdx.x, gridDim.x) : blockIdx.x;
     float* slot = slots + (size_t)wg * (pt.nsum + pt.partials) * a.C;
@@ -292,12 +291,10 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
         const uint32_t oh = (HCL ? rows : planar) * sizeof(TH), oy = (YCL ? rows : planar) * sizeof(TY);
         Patch<TH, HCL, PV> h;
         Patch<TY, YCL, PV> d;
-        h.zero();
-        d.zero();
-        if (on) {
-            if (in) h.load((const TH*)a.h + first, oh, sh);
-            d.load((const TY*)a.dy + first, oy, sy);
-        }
+        if (in) h.load((const TH*)a.h + first, oh, sh);
+        d.load((const TY*)a.dy + first, oy, sy);
+        if (!in || !on) h.zero();
+        if (!on) d.zero();   // lanes that have nothing of their own count zeros
         if (X && (fl & WANT_DXS) && on) {
             Patch<TY, YCL, PV> x;
             x.load((const TY*)a.x + first, oy, sy);
@@ -317,7 +314,7 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
         float mean[PV] = {}, r[PV];
 #pragma unroll
         for (int j = 0; j < PV; ++j) r[j] = 1.f;
-        if (fl & (LAYER | RMS)) patch_stats<TH, HCL, CL, PV, ODD>(a, fl & LAYER, h, ch, red, turn, mean, r);
+        if (fl & (LAYER | RMS)) patch_stats<TH, HCL, CL, PV, ODD>(a, fl & LAYER, h, ch, ex, mean, r);
         // from here on d holds e, dy where it is kept
         if (X && !in) d.zero();   // the same for every lane: no gradient passes a dropped sample
         if constexpr (DROP) {
@@ -370,7 +367,25 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
             // dh = r (u - m1 - z m2) = u r + h c2 + c1
             float c1[PV], c2[PV];
             if (fl & (LAYER | RMS)) {
-                channel_sums<CL, PV, 2>(ms, red, turn);
+#pragma unroll
+                for (int j = 0; j < PV; ++j) {
+                    ms[0][j] = lane_sum<CL>(ms[0][j]);
+                    ms[1][j] = lane_sum<CL>(ms[1][j]);
+                }
+                const int nw = blockDim.x / 64;
+                if (nw > 1) {
+                    ex.put(ms[0], ms[1]);
+                    float m1[EX::OWN] = {}, m2[EX::OWN] = {};
+#pragma unroll 4
+                    for (int w = 0; w < nw; ++w)
+#pragma unroll
+                        for (int i = 0; i < EX::OWN; ++i) {
+                            m1[i] += ex.get(w, 0, i);
+                            m2[i] += ex.get(w, 1, i);
+                        }
+                    ex.round_quad(m1, ms[0]);
+                    ex.round_quad(m2, ms[1]);
+                }
 #pragma unroll
                 for (int j = 0; j < PV; ++j) {
                     const float m1 = fl & LAYER ? ms[0][j] * a.inv_c : 0.f, m2 = ms[1][j] * a.inv_c;
