@@ -129,6 +129,18 @@ def test_workspace_grows_with_the_rows_only_so_far(lib):
     assert lib.wtconv_block_workspace_size(ctypes.byref(d)) < 1 << 28
 
 
+@pytest.mark.parametrize("kw,fused", [
+    (dict(C=8, H=1, W=4), 1), (dict(C=7), 0), (dict(H=1, W=3), 0), (dict(C=2048), 1), (dict(C=2049), 0),
+    (dict(C=1, y_layout=1), 1), (dict(C=7, H=1, W=1, y_layout=1), 1), (dict(C=16384, y_layout=1), 1),
+    (dict(C=16385, y_layout=1), 0), (dict(h_layout=0, C=8), 1), (dict(h_layout=0, C=8, H=1, W=2), 0),
+    (dict(h_dtype=0, y_dtype=0, C=2048, H=512, W=1024), 0), (dict(h_dtype=0, y_dtype=0, C=2047, H=512, W=1024), 1),
+])
+def test_routes(lib, kw, fused):
+    """What the register kernels cover: rows up to 16,384 channels; with a planar side 8 to 2,048 channels, four
+    pixels and samples under 4 GiB in fp32."""
+    assert lib.wtconv_block_route(ctypes.byref(_d(**kw))) == fused
+
+
 def test_empty_batch(lib):
     """B = 0: the forward calls return without launching; parameters are still checked."""
     d = _d(B=0)
@@ -311,6 +323,35 @@ def test_residual_many_rows(shape, order):
     for gate, drop in itertools.product(("channel", "sample"), (("element", 0.5), ("sample", 0.5))):
         print(f"[many rows] {shape} {order} {gate} {drop}", flush=True)
         _residual_case(shape, "bf16", "bf16", *order, "layer", gate, *drop, True)
+
+
+# grids that fill the card, where lanes hold eight bf16 pixels: four, eight and
+# sixteen channel lanes, one to eight wavefronts, vectors that share elements at
+# the end of channels, of pixels and of both, workgroups with several tiles of
+# several samples, and several workgroups to a sample
+FULL = [(350, 96, 9, 13), (350, 90, 8, 14), (1030, 30, 9, 13), (1030, 16, 3, 5), (520, 65, 7, 8), (520, 64, 7, 7),
+        (520, 200, 4, 8), (520, 203, 5, 5), (130, 1000, 5, 6), (530, 1000, 3, 4), (5, 72, 90, 97)]
+
+
+@on_gpu
+@pytest.mark.parametrize("order", [o for o in ORDERS if o != (1, 1)])
+@pytest.mark.parametrize("shape", FULL, ids=_shape_id)
+def test_full_grids(shape, order):
+    n = sum(shape) + 7 * order[0] + 13 * order[1]
+    print(f"[full norm] {shape} {order}", flush=True)
+    _norm_case(shape, "bf16", "bf16", *order, "layer" if n % 3 else "rms", affine=n % 4 > 0)
+    for i in range(3):   # one of each drop
+        kind, gate, (drop, p), xs = MODES[(n * 5 + 20 * i) % len(MODES)]
+        print(f"[full residual] {shape} {order} {kind} {gate} {drop} {xs}", flush=True)
+        _residual_case(shape, "bf16", "bf16", *order, kind, gate, drop, p, xs, seed=i)
+
+
+@on_gpu
+def test_few_samples_over_many_workgroups():
+    """A sample's tiles lie in many workgroups, and a workgroup's tiles in two samples."""
+    for order in ((1, 0), (0, 1)):
+        print(f"[shared samples] {order}", flush=True)
+        _residual_case((5, 1000, 61, 57), "bf16", "bf16", *order, "layer", "sample", "element", 0.3, True)
 
 
 @on_gpu
