@@ -447,10 +447,11 @@ struct TileShape {
 // Sixteen leave 64-byte pieces of a plane and many workgroups of few
 // wavefronts, so they need a twentieth fewer (64x384x14x14: 28.0 us backward
 // against 29.4 with eight; 32x128x100x100 at the same number: 167 against
-// 139). Between four and eight at the same number, four have a plane's pieces
-// longer and eight fewer wavefronts to a barrier: eight forwards (32x128x127x125
-// 52 us against 59), four backwards where that is three or four wavefronts (216
-// against 249; 64x64x64x64, two: 54.5 against 50.9).
+// 139). Between four and eight at about the same number (one in 64), four have
+// a plane's pieces longer and eight fewer wavefronts to a barrier: eight
+// forwards (32x128x127x125 52 us against 59), four backwards where that is
+// three or four wavefronts (207 against 252, 32x128x100x100 125 against 136;
+// 64x64x64x64, two: 54.5 against 50.9).
 //
 // Pixels of a lane: 16 bytes of a plane in bf16 (a tile's fixed costs are
 // spread over twice the elements of 8-byte lanes: residual forward
@@ -474,7 +475,7 @@ inline TileShape tile_shape_of(const BlockArgs& a, int pv, bool backward) {
         const long long waves = (long long)nw * tps;
         if ((long long)a.B * tps >= 1ll << 30) continue;   // tiles are counted in 32 bits
         const bool better = cl == 16  ? waves * 21 <= least * 20
-                            : cl == 4 ? waves < least || (waves == least && backward && nw >= 3 && nw <= 4)
+                            : cl == 4 ? waves < least || (backward && nw >= 3 && nw <= 4 && waves * 64 <= least * 65)
                                       : waves < least;
         if (best.cl && !better) continue;
         best = TileShape{cl, v, nw, px, tps};
