@@ -309,9 +309,16 @@ def block_context(torch, wt, cfg, steps: int):
     depthwise convolution, and this library at L = 0 (the same depthwise
     convolution through its own kernels). bf16 activations and block weights;
     the WTConv parameters are fp32. The linear layers run on flattened 2-D
-    rows (plain matrix products)."""
+    rows (plain matrix products).
+
+    The first mixer's block also with this library's channel norm and block
+    residual in the place of torch's (`wtconv_own_norm_residual`), and as it is
+    trained, with dropout on the hidden rows, a layer scale and whole samples
+    dropped: torch's operators (`wtconv_train`) and this library's
+    (`wtconv_train_own`)."""
     import torch.nn.functional as F
 
+    from wavelet_convolution_amd.block import block_residual, channel_norm, counter_dropout, dropout_rng
     from wavelet_convolution_amd.module import wtconv
 
     dev = torch.device("cuda:0")
@@ -350,12 +357,40 @@ def block_context(torch, wt, cfg, steps: int):
         h = F.linear(h, w2, b2)
         return x + h.reshape(B, H, W, C).permute(0, 3, 1, 2)
 
+    own_w, own_b, gamma = (t.detach().float().requires_grad_(True) for t in (ln_w, ln_b, 0.1 * torch.ones_like(ln_w)))
+    rng = dropout_rng(7, dev)
+    p_hidden, p_sample = 0.1, 0.2
+
+    def own_block(x, train):
+        h = channel_norm(wtconv(x, wt_wb, wt_wl, wt_sc), own_w, own_b, channels_last=True)
+        h = F.gelu(F.linear(h.permute(0, 2, 3, 1).reshape(-1, C), w1, b1))
+        if train:
+            h = counter_dropout(h.view(-1, 4 * C, 1, 1), p_hidden, rng, site=0).view(-1, 4 * C)
+        h = F.linear(h, w2, b2).view(B, H, W, C).permute(0, 3, 1, 2)
+        if not train:
+            return block_residual(x, h)
+        return block_residual(x, h, gate=gamma, drop="sample", p=p_sample, rng=rng, site=1)
+
+    def torch_train_block(x):
+        h = wtconv(x, wt_wb, wt_wl, wt_sc).permute(0, 2, 3, 1).reshape(-1, C)
+        h = F.dropout(F.gelu(F.linear(F.layer_norm(h, (C,), ln_w, ln_b, eps=1e-6), w1, b1)), p_hidden)
+        h = F.linear(h, w2, b2).reshape(B, H, W, C).permute(0, 3, 1, 2) * gamma.to(dt).view(1, C, 1, 1)
+        keep = (torch.rand(B, 1, 1, 1, device=dev) >= p_sample).to(dt) / (1 - p_sample)
+        return x + h * keep
+
+    blocks = {name: (lambda x, mixer=mixer: block(x, mixer)) for name, mixer in mixers.items()}
+    blocks["wtconv_own_norm_residual"] = lambda x: own_block(x, False)
+    blocks["wtconv_train"] = torch_train_block
+    blocks["wtconv_train_own"] = lambda x: own_block(x, True)
+
     out = {"what": f"ConvNeXt-style block (mixer, LayerNorm, {C}->{4 * C}->{C} MLP with GELU, residual), "
                    f"{B}x{C}x{H}x{W} {cfg.dtype}, forward + backward", "steps": steps}
-    for name, mixer in mixers.items():
-        def step(i, mixer=mixer):
+    for name, run in blocks.items():
+        def step(i, run=run):
             x = xs[i % nsets]
-            block(x, mixer).backward(gs[i % nsets])
+            run(x).backward(gs[i % nsets])
+            if name == "wtconv_train_own":
+                rng[1] += 1
 
         for i in range(2):
             step(i)
@@ -366,6 +401,9 @@ def block_context(torch, wt, cfg, steps: int):
         torch.cuda.synchronize()
         out[f"{name}_ms_per_step"] = round(1e3 * (time.perf_counter() - t0) / steps, 4)
     out["wtconv_over_torch_depthwise"] = round(out["wtconv_ms_per_step"] / out["torch_depthwise_ms_per_step"], 3)
+    out["own_norm_residual_over_torch"] = round(out["wtconv_own_norm_residual_ms_per_step"] / out["wtconv_ms_per_step"],
+                                                3)
+    out["train_own_over_torch"] = round(out["wtconv_train_own_ms_per_step"] / out["wtconv_train_ms_per_step"], 3)
     out["wtconv_over_this_library_L0"] = round(out["wtconv_ms_per_step"] / out["this_library_L0_ms_per_step"], 3)
     del xs, gs
     torch.cuda.empty_cache()
