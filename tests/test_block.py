@@ -738,6 +738,61 @@ def test_block_as_used(dt):
 
 
 @on_gpu
+def test_training_step_captured():
+    """Norm, dropout, residual and their backward through autograd in one graph, with the generator's step inside:
+    every replay equals the eager step for the same state, and the masks move on."""
+    B, C, H = 4, 32, 14
+    torch.manual_seed(1)
+    norm = blk.ChannelNorm2d(C, channels_last=True, device="cuda")
+    drop = blk.CounterDropout(0.25, site=1)
+    end = blk.BlockResidual2d(C, norm="rms", layer_scale=0.5, x_scale=True, drop="sample", p=0.3, site=2,
+                              device="cuda")
+    rng = blk.dropout_rng(5)
+    x = torch.randn(B, C, H, H, device="cuda").requires_grad_()
+    dy = torch.randn(B, C, H, H, device="cuda")
+    leaves = [x, *norm.parameters(), *end.parameters()]
+
+    def step():
+        out = end(x, drop(norm(x), rng), rng)
+        grads = torch.autograd.grad(out, leaves, dy)
+        rng[1] += 1
+        return [out.detach(), *grads]
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    outs = []
+    for k in range(3):
+        rng[1] = 10 + k
+        g.replay()
+        torch.cuda.synchronize()
+        assert int(rng[1]) == 11 + k
+        replayed = [t.clone() for t in got]
+        rng[1] = 10 + k
+        for a, b in zip(replayed, step()):
+            assert torch.equal(a, b)
+        outs.append(replayed[0])
+    assert not torch.equal(outs[0], outs[1])
+
+
+@on_gpu
+def test_second_derivatives_are_refused():
+    x = torch.randn(2, 16, 4, 4, device="cuda", requires_grad=True)
+    rng = blk.dropout_rng(1)
+    for fn in (lambda: blk.channel_norm(x), lambda: blk.block_residual(x, x, kind="rms"),
+               lambda: blk.counter_dropout(x, 0.5, rng)):
+        g, = torch.autograd.grad(fn().square().sum(), x, create_graph=True)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            g.sum().backward()
+
+
+@on_gpu
 def test_functions_keep_inputs_only_and_take_any_view():
     """Autograd keeps the inputs alone (no mask, no statistics, no output); strided and expanded views are copied."""
     x = torch.randn(4, 32, 14, 14, device="cuda", requires_grad=True)

@@ -11,7 +11,8 @@ layer's [B, H, W, C] rows are ``rows.permute(0, 3, 1, 2)``; tokens [B, S, C]
 are H = 1, W = S), fp32 or bf16; parameters are fp32. The backward passes keep
 the inputs only: row statistics and dropout masks are computed again. Every
 step of the computation runs in libwtconv.so. Tensors must be on the GPU:
-there is no CPU path.
+there is no CPU path. A second derivative
+raises an error.
 
 Dropout reads its seed and offset from a tensor on the GPU (`dropout_rng`).
 One tensor serves a whole model, each use with a site number of its own; the
@@ -21,6 +22,7 @@ caller changes the offset once per step, after the backward pass:
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import binding as _b
 from . import block_binding as _bb
@@ -62,6 +64,7 @@ class ChannelNormFunction(torch.autograd.Function):
         return _bb.wtconv_norm_fwd(x, weight, bias, channels_last=channels_last, dtype=dtype, **ctx.opts)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, bias = ctx.saved_tensors
         want = _names(ctx, ((0, "dx"), (1, "dweight"), (2, "dbias")))
@@ -84,6 +87,7 @@ class BlockResidualFunction(torch.autograd.Function):
                                        **ctx.opts)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         x, h, weight, bias, gate, x_scale, rng = ctx.saved_tensors
         if x is not None or _dense(dout) is not dout:
@@ -108,6 +112,7 @@ class CounterDropoutFunction(torch.autograd.Function):
         return _bb.wtconv_dropout(_dense(x), p, rng, **ctx.opts)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         rng, = ctx.saved_tensors
         return _bb.wtconv_dropout(_dense(dy), ctx.p, rng, **ctx.opts), None, None, None, None
