@@ -309,7 +309,7 @@ typedef struct {
     int32_t h_dtype, h_layout;   /* the norm's x; the block's output h; dropout's x and y */
     int32_t y_dtype, y_layout;   /* the norm's y; the residual's x and out (dropout: ignored) */
     int32_t norm;                /* wtconv_norm_t */
-    float eps;                   /* > 0 where there is a norm */
+    float eps;                   /* normal and > 0 (FLT_MIN at least) where there is a norm */
     int32_t gate;                /* wtconv_gate_t (residual only) */
     int32_t drop;                /* wtconv_drop_t (residual and dropout) */
     double p;                    /* 0..1, read where drop is not NONE */

@@ -61,7 +61,7 @@ def _residual(lib, d, x=P[0], h=P[1], w=None, b=None, gate=None, xs=None, rng=No
 @pytest.mark.parametrize("kw,status", [
     (dict(B=-1), 1), (dict(C=0), 1), (dict(H=0), 1), (dict(W=-3), 1), (dict(h_dtype=2), 1), (dict(y_dtype=-1), 1),
     (dict(h_layout=2), 1), (dict(y_layout=9), 1), (dict(norm=3), 1), (dict(norm=-1), 1), (dict(eps=0.0), 1),
-    (dict(eps=-1e-6), 1), (dict(eps=float("nan")), 1), (dict(eps=float("inf")), 1), (dict(gate=3), 1),
+    (dict(eps=-1e-6), 1), (dict(eps=1e-40), 1), (dict(eps=float("nan")), 1), (dict(eps=float("inf")), 1), (dict(gate=3), 1),
     (dict(drop=4), 1), (dict(drop=1, p=-0.1), 1), (dict(drop=1, p=1.01), 1), (dict(drop=2, p=float("nan")), 1),
     (dict(drop=1, p=0.1, site=-1), 1), (dict(H=1 << 16, W=1 << 15), 2), (dict(B=1 << 20, C=1 << 12), 2),
     (dict(drop=1, p=0.1, B=1 << 14, C=8, H=512, W=512), 2),   # 2^32 groups
@@ -459,6 +459,24 @@ def test_dropped_samples_do_not_count(order):
 
 @on_gpu
 @pytest.mark.parametrize("order", ORDERS)
+@pytest.mark.parametrize("shape", [(3, 24, 5, 7), (2, 5, 3, 3), (4, 17, 8, 8), (1030, 16, 3, 5)], ids=_shape_id)
+def test_dropped_elements_do_not_count(shape, order):
+    """Without a norm a dropped element's h is not looked at: NaN and infinities there show in no result."""
+    def poison(d):
+        seed, off = (int(v) for v in d["rng"].cpu())
+        mask, _ = keep_mask(shape, "element", 0.4, seed, off, 5)
+        bad = torch.where(torch.rand(shape, generator=torch.Generator().manual_seed(1)) < 0.5, float("nan"),
+                          float("inf")).to(d["h"].dtype)
+        d["h"].copy_(torch.where(mask, d["h"].cpu(), bad))
+        y = bb.wtconv_dropout(d["h"], 0.4, d["rng"], site=5)
+        assert bool(y.isfinite().all())
+
+    for gate, (h_dt, y_dt) in itertools.product(("channel", "sample"), PAIRS):
+        _residual_case(shape, h_dt, y_dt, *order, "none", gate, "element", 0.4, True, edit=poison)
+
+
+@on_gpu
+@pytest.mark.parametrize("order", ORDERS)
 @pytest.mark.parametrize("kind", ["layer", "rms"])
 def test_special_rows(kind, order):
     """Rows of zeros, of one value (no variance), far from zero, of the type's lowest value, with an infinity or a
@@ -838,3 +856,33 @@ def test_long_offsets():
     last = planes[-1:, :, -1:, -5:].contiguous()
     ref = Ref(last, kind="rms")
     check("planes", y[-1:, :, -1:, -5:].contiguous(), ref.out, ref.out_bound)
+
+
+@on_gpu
+@pytest.mark.parametrize("order", [(1, 1), (0, 1), (1, 0)])
+def test_long_offsets_backward(order):
+    """More than 2^31 elements, all zeros but the last pixels: those pixels' gradients, and the parameters' from them
+    alone."""
+    C, last = 8, 5
+    B, H, W = ((1 << 28) + 4096) // 4096, 64, 64
+    g = torch.Generator().manual_seed(3)
+    tail = {n: torch.randn(1, C, 1, last, generator=g) for n in ("h", "dy")}
+
+    def full(cl, t):
+        x = torch.zeros((B, H, W, C) if cl else (B, C, H, W), dtype=torch.bfloat16, device="cuda")
+        x = x.permute(0, 3, 1, 2) if cl else x
+        x[-1:, :, -1:, -last:] = t.to(torch.bfloat16).cuda()
+        return x
+
+    h, dy = full(order[0], tail["h"]), full(order[1], tail["dy"])
+    w = (1 + 0.2 * torch.randn(C, generator=g)).cuda()
+    gate, xs = torch.randn(C, generator=g).cuda(), torch.randn(C, generator=g).cuda()
+    opts = dict(kind="rms", weight=w, gate=gate, x_scale=xs)
+    dx, dh, grads = bb.wtconv_residual_bwd(dy, h, x=dy, **opts)
+    ends = [t[-1:, :, -1:, -last:].contiguous() for t in (h, dy)]
+    ref = Ref(ends[0], x=ends[1], dy=ends[1], **opts)
+    for name, t in (("dx", dx), ("dh", dh)):
+        check(name, t[-1:, :, -1:, -last:].contiguous(), ref.grads[name], ref.bounds[name])
+    for name, t in zip(("dweight", "dbias", "dgate", "dx_scale"), grads):
+        if t is not None:
+            check(name, t, ref.grads[name], ref.bounds[name])

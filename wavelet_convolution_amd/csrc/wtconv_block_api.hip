@@ -2,6 +2,7 @@
 // dispatch. Nothing is launched unless every check passes.
 #include <hip/hip_runtime.h>
 
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -23,7 +24,8 @@ wtconv_status_t check_desc(const wtconv_block_desc_t* d) {
     for (int lo : {d->h_layout, d->y_layout})
         if (lo != WTCONV_NCHW && lo != WTCONV_NHWC) return WTCONV_ERR_INVALID_ARG;
     if (d->norm < WTCONV_NORM_NONE || d->norm > WTCONV_NORM_RMS) return WTCONV_ERR_INVALID_ARG;
-    if (d->norm != WTCONV_NORM_NONE && !(d->eps > 0.f && isfinite(d->eps))) return WTCONV_ERR_INVALID_ARG;
+    // a denormal eps would leave a row of zeros an infinite reciprocal root
+    if (d->norm != WTCONV_NORM_NONE && !(d->eps >= FLT_MIN && isfinite(d->eps))) return WTCONV_ERR_INVALID_ARG;
     if (d->gate < WTCONV_GATE_NONE || d->gate > WTCONV_GATE_SAMPLE) return WTCONV_ERR_INVALID_ARG;
     if (d->drop < WTCONV_DROP_NONE || d->drop > WTCONV_DROP_SAMPLE) return WTCONV_ERR_INVALID_ARG;
     if (d->drop != WTCONV_DROP_NONE && (!(d->p >= 0. && d->p <= 1.) || d->site < 0)) return WTCONV_ERR_INVALID_ARG;

@@ -178,6 +178,10 @@ __global__ __launch_bounds__(threads_of(L)) void k_rows_bwd(BlockArgs a, Partiti
                                                 at.c[v], ODD, a.thr);
 #pragma unroll
                 for (int i = 0; i < CG; ++i) d[v][i] = kept(d[v][i], m, i);
+                if (!(fl & (LAYER | RMS))) {   // 0 times NaN is no 0
+#pragma unroll
+                    for (int i = 0; i < CG; ++i) h[v][i] = kept(h[v][i], m, i);
+                }
             }
 #pragma unroll
             for (int i = 0; i < CG; ++i) h[v][i] = (h[v][i] - mean) * r;   // z from here on

@@ -322,6 +322,7 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
                 Drops<PV> drop;
                 drop.template draw<ODD>(a, (uint32_t)b * a.HW + px.p, ch.c);
                 d.drop(drop);
+                if (!(fl & (LAYER | RMS))) h.drop(drop);   // 0 times NaN is no 0
             }
         }
         auto renew = [&] {
