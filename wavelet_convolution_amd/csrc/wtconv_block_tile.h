@@ -24,8 +24,6 @@
 // rounds stay a loop over pixels.
 #pragma once
 
-#include <type_traits>
-
 #include "wtconv_block_device.h"
 
 namespace wtc {
