@@ -346,6 +346,26 @@ def test_full_grids(shape, order):
         _residual_case(shape, "bf16", "bf16", *order, kind, gate, drop, p, xs, seed=i)
 
 
+# what the register kernels do not cover: fewer channels than a group, fewer
+# pixels than a vector, more channels than a tile's; rows of a sample in one
+# and in several workgroups, more rows than the workgroups' first shares
+GENERIC = [(64, 7, 20, 21), (3, 5, 1, 2000), (40, 302, 1, 2), (700, 3, 2, 3), (4, 2500, 14, 14), (9, 6, 30, 31),
+           (2, 3, 600, 500), (300, 1, 3, 3)]
+
+
+@on_gpu
+@pytest.mark.parametrize("order", [o for o in ORDERS if o != (1, 1)])
+@pytest.mark.parametrize("shape", GENERIC, ids=_shape_id)
+def test_generic_sizes(shape, order):
+    n = sum(shape) + 7 * order[0] + 13 * order[1]
+    for i in range(6):
+        kind, gate, (drop, p), xs = MODES[(n * 5 + 11 * i) % len(MODES)]
+        h_dt, y_dt = PAIRS[(n + i) % 4]
+        print(f"[generic] {shape} {order} {kind} {gate} {drop} {xs} {h_dt} {y_dt}", flush=True)
+        _residual_case(shape, h_dt, y_dt, *order, kind, gate, drop, p, xs, seed=i)
+    _norm_case(shape, *PAIRS[n % 4], *order, ("layer", "rms")[n % 2], affine=True)
+
+
 @on_gpu
 def test_few_samples_over_many_workgroups():
     """A sample's tiles lie in many workgroups, and a workgroup's tiles in two samples."""

@@ -3,7 +3,10 @@
 // lanes of each; it reads its rows once for the mean, once for the variance
 // and once for the result (from cache where they fit), so nothing limits C.
 // The register kernels of the other files serve the sizes that they cover;
-// this one serves the rest: rows wider than their registers.
+// these serve the rest: fewer channels or pixels than a lane's vectors, and
+// rows wider than the registers. Latency is most of their time, so the rows
+// of a workgroup are as few as leave the wavefronts' loads whole pieces of
+// memory.
 #include "wtconv_block_device.h"
 
 namespace wtc {
@@ -11,9 +14,26 @@ namespace {
 
 constexpr int T = 256;
 
-// Lanes of one wavefront walk along the contiguous axis: pixels where both
-// sides are planar or mixed (64 pixels, 4 lanes a row), channels in rows.
-int generic_px(const BlockArgs& a) { return a.h_cl && a.y_cl ? 1 : 64; }
+// The power of two at or below n.
+int pow2_below(long long n) {
+    int p = 1;
+    while (2ll * p <= n && p < T) p *= 2;
+    return p;
+}
+
+// Rows of a workgroup: neighbouring threads stand on neighbouring rows where a
+// side is planar, and on neighbouring channels in rows. Planes: a thread a row
+// where there are fewer channels than a group (64x7x56x56 norm forward, bf16:
+// 9.3 us, with four lanes a row 12.7); else as many as a sample has, and fewer
+// (16 bytes of a plane at least) while that leaves the card empty (4x2500x14x14
+// norm forward 56 us, with 64 rows a workgroup 468; 62x347x2x1 7 against 58).
+int generic_px(const BlockArgs& a) {
+    if (a.h_cl && a.y_cl) return 1;
+    if (a.C < CG) return T;
+    int px = 64;
+    while (px > 8 && (long long)a.B * a.HW / px < 1024) px /= 2;
+    return px < a.HW ? px : pow2_below(a.HW);
+}
 
 struct At {
     size_t base;
@@ -49,11 +69,13 @@ __device__ Stats row_stats(const BlockArgs& a, const TH* h, const At& ah, bool l
     if (a.norm == NORM_LAYER) {
         float sum = 0.f;
         if (live)
+#pragma unroll 4
             for (int c = lane; c < a.C; c += lanes) sum += widen(h[ah.base + c * ah.step]);
         s.mean = row_sum(sum, px, PX, red) / (float)a.C;
     }
     float sq = 0.f;
     if (live)
+#pragma unroll 4
         for (int c = lane; c < a.C; c += lanes) {
             const float d = widen(h[ah.base + c * ah.step]) - s.mean;
             sq = fmaf(d, d, sq);
@@ -182,62 +204,76 @@ __global__ __launch_bounds__(T) void k_generic_bwd(BlockArgs a, int PX, float2* 
 }
 
 // Parameter gradients: a thread owns the eight channels of one group and adds
-// over its workgroup's rows (a tile is one row here).
+// every RL-th row of its workgroup's range (a tile is one row here); the RL
+// threads of a group join in LDS, in a fixed order.
 template <typename TH, typename TY>
 __global__ __launch_bounds__(T) void k_generic_grads(BlockArgs a, const float2* stats, Partition pt, SumSlots sl,
-                                                     float* slots) {
+                                                     float* slots, int RL) {
+    __shared__ float red[T][CG + 1];   // an odd step: no two lanes on one bank
     const TH* h = (const TH*)a.h;
     const TY* x = (const TY*)a.x;
     const TY* dy = (const TY*)a.dy;
-    const int g = blockIdx.x * T + threadIdx.x, c0 = g * CG, n = min(CG, a.C - c0);
-    if (n <= 0) return;
+    const int t = threadIdx.x, ri = t % RL;
+    const int g = blockIdx.x * (T / RL) + t / RL, c0 = g * CG, n = min(CG, a.C - c0);   // n <= 0: no such group
+    const bool writes = ri == 0 && n > 0;
     float* slot = slots + (size_t)blockIdx.y * (pt.nsum + pt.partials) * a.C;
     float dw[CG] = {}, db[CG] = {}, dg[CG] = {}, ds[CG] = {};
     const long long t0 = pt.begin(blockIdx.y), t1 = pt.begin(blockIdx.y + 1);
     const bool by_sample = a.dg && a.gate_mode == GATE_SAMPLE;
-    for (long long row = t0; row < t1; ++row) {
-        const int b = (int)(row / a.HW);
-        const At ah = at(a, a.h_cl, row), ay = at(a, a.y_cl, row);
-        const bool in = a.drop != DROP_SAMPLE || sample_kept(a, b);
-        const uint32_t m = group_drop(a, row, g, in);
-        const float* gate = a.gate ? a.gate + (a.gate_mode == GATE_SAMPLE ? (size_t)b * a.C : 0) : nullptr;
-        Stats s{0.f, 1.f};
-        if (a.norm != NORM_NONE) s = Stats{stats[row].x, stats[row].y};
+    // the sum over the rows' threads, stored by one of them
+    auto store = [&](const float (&v)[CG], float* to) {
+        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < CG; ++i) {
-            if (i >= n) break;
-            const int c = c0 + i;
-            const float d = widen(dy[ay.base + c * ay.step]);
-            if (a.dxs) ds[i] = fmaf(d, widen(x[ay.base + c * ay.step]), ds[i]);
-            if (in && a.h) {
-                const Elem e = elem(a, gate, s, c, !(m >> (7 - i) & 1), widen(h[ah.base + c * ah.step]), d);
-                dw[i] = fmaf(e.dv, e.z, dw[i]);
-                db[i] += e.dv;
-                dg[i] = fmaf(d, e.t, dg[i]);
+        for (int i = 0; i < CG; ++i) red[t][i] = v[i];
+        for (int k = RL / 2; k > 0; k /= 2) {
+            __syncthreads();
+            if (ri < k)
+#pragma unroll
+                for (int i = 0; i < CG; ++i) red[t][i] += red[t + k][i];
+        }
+        if (!writes) return;
+#pragma unroll
+        for (int i = 0; i < CG; ++i)
+            if (i < n) to[c0 + i] = red[t][i];
+    };
+    for (long long from = t0; from < t1;) {
+        // the rows of one sample in the range, where samples count, else all
+        const long long b0 = from / pt.tps, to = by_sample ? min(t1, (b0 + 1) * pt.tps) : t1;
+        for (long long row = from + ri; row < to; row += RL) {
+            const int b = (int)(row / a.HW);
+            const At ah = at(a, a.h_cl, row), ay = at(a, a.y_cl, row);
+            const bool in = a.drop != DROP_SAMPLE || sample_kept(a, b);
+            const uint32_t m = n > 0 ? group_drop(a, row, g, in) : 0u;
+            const float* gate = a.gate ? a.gate + (a.gate_mode == GATE_SAMPLE ? (size_t)b * a.C : 0) : nullptr;
+            Stats s{0.f, 1.f};
+            if (a.norm != NORM_NONE) s = Stats{stats[row].x, stats[row].y};
+#pragma unroll
+            for (int i = 0; i < CG; ++i) {
+                if (i >= n) break;
+                const int c = c0 + i;
+                const float d = widen(dy[ay.base + c * ay.step]);
+                if (a.dxs) ds[i] = fmaf(d, widen(x[ay.base + c * ay.step]), ds[i]);
+                if (in && a.h) {
+                    const Elem e = elem(a, gate, s, c, !(m >> (7 - i) & 1), widen(h[ah.base + c * ah.step]), d);
+                    dw[i] = fmaf(e.dv, e.z, dw[i]);
+                    db[i] += e.dv;
+                    dg[i] = fmaf(d, e.t, dg[i]);
+                }
             }
         }
-        // the last row of this sample in the workgroup's range
-        if (by_sample && (row + 1 == t1 || (row + 1) % pt.tps == 0)) {
-            const long long s0 = b * pt.tps;
-            const bool whole = s0 >= t0 && s0 + pt.tps <= t1;
-            float* to = whole ? a.dg + (size_t)b * a.C
-                              : slot + (size_t)(pt.nsum + (b == t0 / pt.tps ? 0 : 1)) * a.C;
+        if (by_sample) {
+            const bool whole = b0 * pt.tps >= t0 && (b0 + 1) * pt.tps <= t1;
+            store(dg, whole ? a.dg + (size_t)b0 * a.C
+                            : slot + (size_t)(pt.nsum + (b0 == t0 / pt.tps ? 0 : 1)) * a.C);
 #pragma unroll
-            for (int i = 0; i < CG; ++i)
-                if (i < n) {
-                    to[c0 + i] = dg[i];
-                    dg[i] = 0.f;
-                }
+            for (int i = 0; i < CG; ++i) dg[i] = 0.f;
         }
+        from = to;
     }
-#pragma unroll
-    for (int i = 0; i < CG; ++i)
-        if (i < n) {
-            if (sl.dw >= 0) slot[(size_t)sl.dw * a.C + c0 + i] = dw[i];
-            if (sl.db >= 0) slot[(size_t)sl.db * a.C + c0 + i] = db[i];
-            if (sl.dg >= 0) slot[(size_t)sl.dg * a.C + c0 + i] = dg[i];
-            if (sl.dxs >= 0) slot[(size_t)sl.dxs * a.C + c0 + i] = ds[i];
-        }
+    if (sl.dw >= 0) store(dw, slot + (size_t)sl.dw * a.C);
+    if (sl.db >= 0) store(db, slot + (size_t)sl.db * a.C);
+    if (sl.dg >= 0) store(dg, slot + (size_t)sl.dg * a.C);
+    if (sl.dxs >= 0) store(ds, slot + (size_t)sl.dxs * a.C);
 }
 
 // Second stage. A workgroup takes 16 channels of one sum: a lane adds four
@@ -299,16 +335,26 @@ __global__ __launch_bounds__(FT) void k_finalize(BlockArgs a, Partition pt, SumS
     }
 }
 
-// One row a tile; as many workgroups as give each CU a few, each with enough
-// rows that its slot (nsum rows of its own) is little beside what it reads.
+// Threads that share a group of the parameter gradients: neighbouring rows of
+// a plane (a sample's, where samples count), and what the groups leave over.
+int grads_rl(const BlockArgs& a) {
+    const int most = a.gate_mode == GATE_SAMPLE ? pow2_below(a.HW) : T;
+    int rl = a.h_cl && a.y_cl ? 1 : min(64, pow2_below(a.HW));
+    while (rl < most && rl * cdiv(a.C, CG) <= T / 2) rl *= 2;
+    return rl < most ? rl : most;
+}
+
+// One row a tile; each thread takes a few rows, so that a workgroup's slot
+// (nsum rows of its own) is little beside what it reads.
 Partition generic_partition(const BlockArgs& a) {
     Partition p{};
-    const bool by_sample = a.dg && a.gate_mode == GATE_SAMPLE;
+    const bool sample = a.gate_mode == GATE_SAMPLE;
     p.tiles = (long long)a.B * a.HW;
-    p.tps = by_sample ? a.HW : p.tiles;
-    p.wgs = (int)(p.tiles < 16384 ? (p.tiles + 15) / 16 : 1024);
+    p.tps = a.dg && sample ? a.HW : p.tiles;
+    const int rl = grads_rl(a), per = max(8, sample ? rl : 2 * rl);
+    p.wgs = (int)min(1024ll, (p.tiles + per - 1) / per);
     p.nsum = sum_slots(a).count;
-    p.partials = by_sample ? 2 : 0;
+    p.partials = a.dg && sample ? 2 : 0;
     return p;
 }
 
@@ -368,7 +414,9 @@ hipError_t block_generic_bwd(const BlockArgs& a, int h_bf16, int y_bf16, hipStre
     float* slots = (float*)((char*)a.ws + stats_bytes(a));
     const SumSlots sl = sum_slots(a);
     if (p.wgs > 0 && (sl.count || (a.dg && a.gate_mode == GATE_SAMPLE))) {
-        WTC_TYPES(k_generic_grads, dim3((unsigned)cdiv(cdiv(a.C, CG), T), (unsigned)p.wgs), a, stats, p, sl, slots);
+        const int rl = grads_rl(a);
+        WTC_TYPES(k_generic_grads, dim3((unsigned)cdiv(cdiv(a.C, CG), T / rl), (unsigned)p.wgs), a, stats, p, sl, slots,
+                  rl);
         hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
     }
