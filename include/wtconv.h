@@ -288,10 +288,12 @@ wtconv_status_t wtconv_naive_bwd_weight(const wtconv_desc_t *desc, const void *x
  * when its 16 bits (word (c%8)/2, low half for even c) are >= T. With
  * WTCONV_DROP_SAMPLE (stochastic depth) whole samples b are kept or dropped,
  * by the low half of word 0 of counter (b, site + 2^31, ...); a dropped
- * sample's h does not influence any result.
+ * sample's h does not influence any result, nor, without a norm, does a
+ * dropped element's.
  *
  * Pointers need the alignment of their element type only; outputs must not
- * overlap inputs or each other. B = 0 writes nothing but zero parameter
+ * overlap inputs or each other, and backward calls that may run at the same
+ * time need workspaces of their own (two captured graphs, too). B = 0 writes nothing but zero parameter
  * gradients. Gradients of parameters are summed in a fixed order (bitwise
  * reproducible) in fp32. A channels-last side with one pixel per sample (or
  * with one channel) has the same memory order as a planar one.

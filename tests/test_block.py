@@ -685,6 +685,28 @@ def test_another_stream():
 
 
 @on_gpu
+def test_two_streams_at_once():
+    """Calls that run side by side on two streams share nothing."""
+    ds = [_make((32, 96, 28, 28), "bf16", "bf16", 1, 0, seed=k) for k in (20, 21)]
+
+    def run(d, s):
+        opts = dict(kind="layer", weight=d["weight"], bias=d["bias"], gate=d["gate_s"], x_scale=d["x_scale"],
+                    drop="element", p=0.2, rng=d["rng"], stream=s)
+        dx, dh, g = bb.wtconv_residual_bwd(d["dy"], d["h"], x=d["x"], **opts)
+        return [bb.wtconv_residual_fwd(d["x"], d["h"], **opts), dx, dh, *g]
+
+    want = [run(d, None) for d in ds]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ds]
+    got = [[run(d, s) for d, s in zip(ds, streams)] for _ in range(8)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for a, b in zip(pair, want):
+            for t, u in zip(a, b):
+                assert torch.equal(t, u)
+
+
+@on_gpu
 def test_captured_and_replayed():
     """Forward, backward and dropout captured in one graph: every replay equals the eager calls for the values that
     its inputs hold then, the generator's state among them; a second graph of the same calls shares nothing."""

@@ -4,10 +4,14 @@
 // the two means of the backward pass are sums over those lanes (within a
 // wavefront by data-parallel moves, L > 64 through LDS). A workgroup takes
 // several rows at once where L is small, and loops over its rows, so a lane's
-// channels never change: parameters are loaded once (NV = 1), and parameter
-// gradients add up in registers, then over the workgroup's rows in LDS, then
-// over workgroups in the second stage.
-// Bound by memory: 2 + 2 (+ 2) bytes an element forwards in bf16.
+// channels never change: parameters are loaded once for its rows where they
+// are one vector (NV = 1), and parameter gradients add up in registers, then
+// over the workgroup's rows in LDS, then over workgroups in the second stage.
+// Forwards memory is the bound (bf16, card's copy rate 5.2 TB/s): norm
+// 32,768 x 768 in 21.0 us, 4.8 TB/s; residual into an fp32 stream of that size
+// 71.5 us, 4.9. Backwards vector instructions and latency beside it: norm
+// 38.6 us, 3.9 TB/s; residual with dropout and a gate per sample,
+// 32,768 x 1,024 with an fp32 stream, 72 us, 3.7.
 #pragma once
 
 #include "wtconv_block_device.h"

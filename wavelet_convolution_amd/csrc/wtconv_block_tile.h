@@ -15,13 +15,17 @@
 // values to the same addresses. Sums take the elements that two lanes share
 // once (kernels of their own, ODD). So a tile needs HW >= PV and C >= 8.
 //
-// Small planes are bound by the chain of latencies (arguments, loads, two
-// sums over channels, stores) and by instruction fetch, large ones by memory
-// with the vector instructions of an element close behind (a wavefront's
-// instruction takes four cycles: 10 instructions an element are as long as 4
-// bytes of it): so what a call does not use is compiled out (X, DROP), the
-// rare cases sit behind one branch for the whole patch, and the generator's
-// rounds stay a loop over pixels.
+// What bounds them (bf16, time of a call on the stream): forwards memory, where
+// planes are large (norm 64x96x56x56 15.2 us, 5.1 of the card's 5.2 TB/s;
+// residual 32x128x128x128 80 us, 5.0 TB/s), and for small ones the chain of
+// latencies: arguments, loads, the sums over channels, stores (residual
+// 64x384x14x14 9.6 us, 3.0 TB/s). Backwards the same chain, twice as long, at
+// three wavefronts a SIMD (the registers' limit): norm 64x192x28x28 19.7 us (2.9
+// TB/s), residual with element dropout 64x96x56x56 54 us (3.6 TB/s), 32x128x128x128
+// 164 us (4.1 TB/s); at 29 and 50 vector instructions an element their issue
+// alone is 7.0, 24 and 85 us. So what a call does not use is compiled out (X,
+// DROP), the rare cases sit behind one branch for the whole patch, and the
+// generator's rounds stay a loop over pixels.
 #pragma once
 
 #include "wtconv_block_device.h"
