@@ -324,8 +324,10 @@ typedef struct {
 size_t wtconv_block_workspace_size(const wtconv_block_desc_t *desc);
 
 /* How the norm or residual of `desc` runs: WTCONV_ROUTE_FUSED (each row is
-   read once and held in registers) or WTCONV_ROUTE_GENERIC (rows wider than
-   that: read once per statistic). -1 if the descriptor is invalid. No device
+   read once and held in registers) or WTCONV_ROUTE_GENERIC (each row is read
+   once per statistic: channels-last rows of more than 16,384 channels; with a
+   planar side fewer than 8 or more than 2,048 channels, or fewer than four
+   pixels). -1 if the descriptor is invalid. No device
    call is made. */
 int32_t wtconv_block_route(const wtconv_block_desc_t *desc);
 

@@ -1,7 +1,7 @@
 // Block operators: which kernels serve a call. Rows (both sides channels last)
 // are held in registers by the row kernels up to 16,384 channels, tiles with
-// a planar side by the tile kernels up to 2,048; wider ones take the generic
-// kernels.
+// a planar side by the tile kernels from 8 to 2,048 (four pixels at least);
+// the others take the generic kernels.
 #include "wtconv_block.h"
 #include "wtconv_block_tile.h"
 
