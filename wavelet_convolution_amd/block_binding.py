@@ -108,8 +108,11 @@ def _empty(shape, dtype, channels_last: bool, device) -> torch.Tensor:
                        memory_format=torch.channels_last if channels_last else torch.contiguous_format)
 
 
-def _grad(wanted: bool, shape, act):
-    return act.new_empty(shape, dtype=torch.float32) if wanted else None
+def _grad(wanted: bool, param, act):
+    """A gradient to be written: like its parameter (checked before), or [C] without one."""
+    if not wanted:
+        return None
+    return act.new_empty(act.shape[1], dtype=torch.float32) if param is None else torch.empty_like(param)
 
 
 # the current stream's handle, without the Stream object around it where torch offers that
@@ -124,13 +127,13 @@ def _stream(act) -> int:
 
 def _workspace(desc, act, ws):
     """(pointer, bytes) of the workspace, and the tensor that holds it."""
-    if ws is None:
-        n = _ws_size(desc)
-        if n == 0:
-            return 0, 0, None
-        ws = act.new_empty(n + 256, dtype=torch.uint8)
-    p = _b._ws_ptr(ws)
-    return p, _b._ws_bytes(ws), ws
+    if ws is not None:
+        return _b._ws_ptr(ws), _b._ws_bytes(ws), ws
+    n = _ws_size(desc)
+    if n == 0:
+        return 0, 0, None
+    ws = act.new_empty(n + 256, dtype=torch.uint8)
+    return _b._ws_ptr(ws), n, ws
 
 
 def _ws_size(desc) -> int:
@@ -198,21 +201,17 @@ def wtconv_norm_bwd(x, dy, weight=None, bias=None, *, kind: str = "layer", eps: 
         return _enter(wtconv_norm_bwd, x, stream, (x, dy, weight, bias, dx, ws), x, dy, weight, bias, kind=kind,
                       eps=eps, want=want, dx=dx, ws=ws)
     hc = _act("x", x)
-    C = x.shape[1]
     _vector("weight", weight, x)
     _vector("bias", bias, x)
-    if want is None:
-        want = ("dx",) + (("dweight",) if weight is not None else ()) + (("dbias",) if bias is not None else ())
-    else:
-        _wanted(want, ("dx", "dweight", "dbias"))
+    wants = (True, weight is not None, bias is not None) if want is None else _wanted(want, ("dx", "dweight", "dbias"))
     d = _desc(x, hc, _act("dy", dy, x), _code(_NORMS, kind, "kind"), eps)
-    if "dx" not in want:
+    if not wants[0]:
         dx = None
     elif dx is None:
         dx = torch.empty_like(x)
     elif _act("dx", dx, x) != hc:
         raise ValueError("dx must have x's type and memory order")
-    dweight, dbias = (_grad(n in want, (C,), x) for n in ("dweight", "dbias"))
+    dweight, dbias = _grad(wants[1], weight, x), _grad(wants[2], bias, x)
     wp, wn, ws = _workspace(d, x, ws)
     _b._check(_b.load_library().wtconv_norm_bwd(
         ctypes.byref(d), x.data_ptr(), dy.data_ptr(), _b._ptr(weight), _b._ptr(dx), _b._ptr(dweight), _b._ptr(dbias),
@@ -220,10 +219,13 @@ def wtconv_norm_bwd(x, dy, weight=None, bias=None, *, kind: str = "layer", eps: 
     return dx, dweight, dbias
 
 
-def _wanted(want, names) -> None:
+def _wanted(want, names) -> tuple:
+    """For each of the names whether it is wanted."""
+    want = tuple(want)
     for n in want:
         if n not in names:
             raise ValueError(f"want names gradients among {', '.join(names)}; got {n!r}")
+    return tuple(n in want for n in names)
 
 
 def _residual_desc(x, h, kind, weight, bias, eps, gate, x_scale, drop, p, rng, site):
@@ -276,37 +278,33 @@ def wtconv_residual_bwd(dout, h, *, x=None, kind: str = "none", weight=None, bia
     d = _residual_desc(dout, h, kind, weight, bias, eps, gate, x_scale, drop, p, rng, site)
     yc, hc = (d.y_dtype, d.y_layout), (d.h_dtype, d.h_layout)
     if want is None:
-        given = (True, True, weight is not None, bias is not None, gate is not None, x_scale is not None)
-        want = tuple(n for n, g in zip(GRADS, given) if g)
+        wants = (True, True, weight is not None, bias is not None, gate is not None, x_scale is not None)
     else:
-        _wanted(want, GRADS)
-        if "dgate" in want and gate is None:
+        wants = _wanted(want, GRADS)
+        if wants[4] and gate is None:
             raise ValueError("dgate needs a gate")
-        if d.norm == 0 and ("dweight" in want or "dbias" in want):
+        if d.norm == 0 and (wants[2] or wants[3]):
             raise ValueError("dweight and dbias need a norm (kind)")
-    if "dx_scale" in want:
+    if wants[5]:
         if x is None:
             raise ValueError("dx_scale needs x")
         if _act("x", x, dout) != yc:
             raise ValueError("x must have dout's type and memory order")
-    alias = "dx" in want and dx is None and x_scale is None
-    if "dx" not in want:
+    alias = wants[0] and dx is None and x_scale is None
+    if not wants[0]:
         dx = None
     elif dx is not None:
         if _act("dx", dx, dout) != yc:
             raise ValueError("dx must have dout's type and memory order")
     elif not alias:
         dx = torch.empty_like(dout)
-    if "dh" not in want:
+    if not wants[1]:
         dh = None
     elif dh is None:
         dh = torch.empty_like(h)
     elif _act("dh", dh, h) != hc:
         raise ValueError("dh must have h's type and memory order")
-    C = dout.shape[1]
-    dweight, dbias = (_grad(n in want, (C,), dout) for n in ("dweight", "dbias"))
-    dgate = _grad("dgate" in want, gate.shape if gate is not None else (), dout)
-    dx_scale = _grad("dx_scale" in want, (C,), dout)
+    dweight, dbias, dgate, dx_scale = (_grad(w, t, dout) for w, t in zip(wants[2:], (weight, bias, gate, x_scale)))
     wp, wn, ws = _workspace(d, dout, ws)
     _b._check(_b.load_library().wtconv_residual_bwd(
         ctypes.byref(d), _b._ptr(x) if dx_scale is not None else 0, h.data_ptr(), dout.data_ptr(), _b._ptr(weight),
