@@ -121,10 +121,18 @@ def layout_of(act: torch.Tensor) -> int:
     raise ValueError("activations must be contiguous in NCHW or channels-last order")
 
 
+def _check_i32(*values: int) -> None:
+    """The descriptors hold sizes in 32 bits, and ctypes cuts what does not fit without an error."""
+    if any(not -(1 << 31) <= v < 1 << 31 for v in values):
+        raise ValueError(f"sizes must be below 2^31; got {', '.join(map(str, values))}")
+
+
 def _desc(act: torch.Tensor, levels: int, k_base: int, k_level: int) -> WTConvDesc:
     B, C, H, W = act.shape
+    levels, k_base, k_level = int(levels), int(k_base), int(k_level)
+    _check_i32(B, C, H, W, levels, k_base, k_level)
     dt = {torch.float32: WTCONV_F32, torch.bfloat16: WTCONV_BF16}.get(act.dtype, -1)
-    return WTConvDesc(B, C, H, W, int(levels), int(k_base), int(k_level), dt, layout_of(act))
+    return WTConvDesc(B, C, H, W, levels, k_base, k_level, dt, layout_of(act))
 
 
 def _same_layout(a: torch.Tensor, b: torch.Tensor) -> None:

@@ -98,6 +98,8 @@ def _enter(fn, act, stream, tensors, *args, **kw):
 
 def _desc(act, h_code, y_code, norm=0, eps=1e-6, gate=0, drop=0, p=0.0, site=0):
     B, C, H, W = act.shape
+    if (B | C | H | W) >> 31:   # the quick test first
+        _b._check_i32(B, C, H, W)
     if not 0 <= site < 1 << 31:
         raise ValueError("site must be in 0..2^31-1")
     return _b.WTConvBlockDesc(B, C, H, W, *h_code, *y_code, norm, eps, gate, drop, p, site)
