@@ -77,8 +77,10 @@ typedef enum {
     WTCONV_ERR_INVALID_ARG = 1,        /* null pointer, overlap, bad dtype or
                                           layout, B < 0, C, H or W < 1 */
     WTCONV_ERR_UNSUPPORTED_SHAPE = 2,  /* even or unsupported k, L out of
-                                          range, H*W above 2^30, or 2^32 and
-                                          more dropout groups */
+                                          range, H*W above 2^30 (block
+                                          operators: or C), B*C above
+                                          2^31 - 1, or 2^32 and more dropout
+                                          groups */
     WTCONV_ERR_WORKSPACE = 3,          /* ws too small or misaligned */
     WTCONV_ERR_LAUNCH = 4,             /* the HIP runtime rejected a launch */
     WTCONV_ERR_SCRATCH_LIMIT = 5       /* wtconv_bwd_weight_noalloc: the call needs
@@ -293,8 +295,9 @@ wtconv_status_t wtconv_naive_bwd_weight(const wtconv_desc_t *desc, const void *x
  *
  * Pointers need the alignment of their element type only; outputs must not
  * overlap inputs or each other, and backward calls that may run at the same
- * time need workspaces of their own (two captured graphs, too). B = 0 writes nothing but zero parameter
- * gradients. Gradients of parameters are summed in a fixed order (bitwise
+ * time need workspaces of their own (two captured graphs, too). B = 0 writes
+ * nothing but zero parameter gradients. C and H*W go up to 2^30, B*C to
+ * 2^31 - 1. Gradients of parameters are summed in a fixed order (bitwise
  * reproducible) in fp32. A channels-last side with one pixel per sample (or
  * with one channel) has the same memory order as a planar one.
  * ------------------------------------------------------------------------ */

@@ -1,4 +1,7 @@
 """What the block operators and the layer refuse before anything is launched (CPU)."""
+import ctypes
+import os
+
 import pytest
 import torch
 
@@ -41,3 +44,45 @@ def test_levels_and_kernels_past_32_bits_are_refused(levels, k_base, k_level, mo
     for fn in (wt.wtconv_workspace_size, wt.wtconv_route):
         with pytest.raises(ValueError, match="2\\^31"):
             fn(x, levels, k_base, k_level, wt.OP_FWD)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(wt._LIB_PATH):
+        pytest.skip("libwtconv.so not built")
+    return wt.load_library()
+
+
+def _d(**kw):
+    d = dict(B=1, C=16, H=1, W=1, h_dtype=1, h_layout=1, y_dtype=1, y_layout=1, norm=2, eps=1e-6, gate=0, drop=0,
+             p=0.0, site=0)
+    d.update(kw)
+    return ctypes.byref(wt.WTConvBlockDesc(**d))
+
+
+P = [ctypes.c_void_p((i + 1) << 40) for i in range(8)]   # never dereferenced: validation fails first
+
+
+@pytest.mark.parametrize("h_layout,drop", [(1, 0), (0, 0), (1, 1), (1, 2)])
+@pytest.mark.parametrize("C", [(1 << 30) + 1, (1 << 31) - 257, (1 << 31) - 256, (1 << 31) - 8, (1 << 31) - 1])
+def test_channels_past_2_30_are_refused(lib, C, h_layout, drop):
+    """The kernels step over channels in 32-bit numbers, by as much as a workgroup at once."""
+    d = _d(C=C, h_layout=h_layout, drop=drop, p=0.5)
+    assert lib.wtconv_block_workspace_size(d) == ctypes.c_size_t(-1).value
+    assert lib.wtconv_block_route(d) == -1
+    assert lib.wtconv_residual_fwd(d, P[0], P[1], None, None, None, None, P[2], P[3], None) == 2
+    assert lib.wtconv_residual_bwd(d, None, P[0], P[1], None, None, None, None, P[2], None, P[3], None, None, None,
+                                   None, P[4], 1 << 39, None) == 2
+    if drop:
+        assert lib.wtconv_dropout(_d(C=C, norm=0, h_layout=h_layout, drop=drop, p=0.5), P[0], P[2], P[3], None) == 2
+    else:
+        assert lib.wtconv_norm_fwd(d, P[0], None, None, P[1], None) == 2
+        assert lib.wtconv_norm_bwd(d, P[0], P[1], None, P[2], None, None, P[4], 1 << 39, None) == 2
+
+
+def test_channels_up_to_2_30_are_taken(lib):
+    for kw in (dict(), dict(h_layout=0, H=2), dict(drop=1, p=0.5), dict(B=1, gate=2)):
+        d = _d(C=1 << 30, **kw)
+        assert lib.wtconv_block_route(d) == 0
+        # partial sums of every wanted gradient, a slot of C numbers each at least
+        assert 1 << 32 <= lib.wtconv_block_workspace_size(d) < 1 << 40

@@ -479,7 +479,7 @@ const char* wtconv_status_string(wtconv_status_t s) {
     switch (s) {
     case WTCONV_OK: return "WTCONV_OK";
     case WTCONV_ERR_INVALID_ARG: return "WTCONV_ERR_INVALID_ARG: null, misaligned or overlapping pointer, or bad size, dtype or layout";
-    case WTCONV_ERR_UNSUPPORTED_SHAPE: return "WTCONV_ERR_UNSUPPORTED_SHAPE: unsupported kernel size or levels, a plane above 2^30 elements, or 2^32 and more dropout groups";
+    case WTCONV_ERR_UNSUPPORTED_SHAPE: return "WTCONV_ERR_UNSUPPORTED_SHAPE: unsupported kernel size or levels, a plane (block operators: or a row) above 2^30 elements, B*C above 2^31-1, or 2^32 and more dropout groups";
     case WTCONV_ERR_WORKSPACE: return "WTCONV_ERR_WORKSPACE: workspace missing, too small or not 256-byte aligned";
     case WTCONV_ERR_LAUNCH: return "WTCONV_ERR_LAUNCH: the HIP runtime rejected a kernel launch";
     case WTCONV_ERR_SCRATCH_LIMIT:

@@ -29,7 +29,9 @@ wtconv_status_t check_desc(const wtconv_block_desc_t* d) {
     if (d->gate < WTCONV_GATE_NONE || d->gate > WTCONV_GATE_SAMPLE) return WTCONV_ERR_INVALID_ARG;
     if (d->drop < WTCONV_DROP_NONE || d->drop > WTCONV_DROP_SAMPLE) return WTCONV_ERR_INVALID_ARG;
     if (d->drop != WTCONV_DROP_NONE && (!(d->p >= 0. && d->p <= 1.) || d->site < 0)) return WTCONV_ERR_INVALID_ARG;
-    if ((int64_t)d->H * d->W > (1ll << 30) || (int64_t)d->B * d->C > (1ll << 31) - 1)
+    // the kernels count a plane's pixels and a row's channels in 32 bits, and
+    // step past the end by up to a workgroup's share
+    if (d->C > 1 << 30 || (int64_t)d->H * d->W > (1ll << 30) || (int64_t)d->B * d->C > (1ll << 31) - 1)
         return WTCONV_ERR_UNSUPPORTED_SHAPE;
     // 2^61 elements fit every product of sizes in 64 bits; a device holds far fewer
     if (d->drop == WTCONV_DROP_ELEMENT) {
