@@ -86,3 +86,21 @@ def test_channels_up_to_2_30_are_taken(lib):
         assert lib.wtconv_block_route(d) == 0
         # partial sums of every wanted gradient, a slot of C numbers each at least
         assert 1 << 32 <= lib.wtconv_block_workspace_size(d) < 1 << 40
+
+
+@pytest.mark.parametrize("kw,status", [(dict(kind="layer", eps=0.0), 1), (dict(kind="rms", eps=float("nan")), 1),
+                                       (dict(drop="element", p=1.5), 1), (dict(drop="sample", p=-0.5), 1)])
+def test_backward_calls_name_the_argument_that_is_wrong(lib, kw, status, monkeypatch):
+    """A bad eps or p is an invalid argument in a backward call too (which asks for its workspace first), as it is
+    forwards; the check is the library's own, on host memory that no kernel sees."""
+    monkeypatch.setattr(bb, "_on_gpu", lambda *a, **k: None)
+    monkeypatch.setattr(bb, "_elsewhere", lambda *a: False)
+    monkeypatch.setattr(bb, "_stream", lambda act: 0)
+    x, h, rng = torch.zeros(2, 16, 4, 4), torch.zeros(2, 16, 4, 4), torch.zeros(2, dtype=torch.int64)
+    calls = [lambda: bb.wtconv_residual_fwd(x, h, rng=rng, **kw), lambda: bb.wtconv_residual_bwd(x, h, rng=rng, **kw)]
+    if "drop" not in kw:
+        calls += [lambda: bb.wtconv_norm_fwd(x, **kw), lambda: bb.wtconv_norm_bwd(x, h, **kw)]
+    for call in calls:
+        with pytest.raises(wt.WTConvError) as e:
+            call()
+        assert e.value.status == status

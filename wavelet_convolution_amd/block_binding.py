@@ -131,16 +131,19 @@ def _workspace(desc, act, ws):
     """(pointer, bytes) of the workspace, and the tensor that holds it."""
     if ws is not None:
         return _b._ws_ptr(ws), _b._ws_bytes(ws), ws
-    n = _ws_size(desc)
-    if n == 0:
+    n = _b.load_library().wtconv_block_workspace_size(ctypes.byref(desc))
+    if n == 0 or n == _NO_SIZE:   # no size: the call itself says what is wrong
         return 0, 0, None
     ws = act.new_empty(n + 256, dtype=torch.uint8)
     return _b._ws_ptr(ws), n, ws
 
 
+_NO_SIZE = ctypes.c_size_t(-1).value
+
+
 def _ws_size(desc) -> int:
     n = _b.load_library().wtconv_block_workspace_size(ctypes.byref(desc))
-    if n == ctypes.c_size_t(-1).value:
+    if n == _NO_SIZE:
         raise _b.WTConvError(2, _b.wtconv_status_string(2))
     return int(n)
 
