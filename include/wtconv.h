@@ -298,8 +298,10 @@ wtconv_status_t wtconv_naive_bwd_weight(const wtconv_desc_t *desc, const void *x
  * time need workspaces of their own (two captured graphs, too). B = 0 writes
  * nothing but zero parameter gradients. C and H*W go up to 2^30, B*C to
  * 2^31 - 1. Gradients of parameters are summed in a fixed order (bitwise
- * reproducible) in fp32. A channels-last side with one pixel per sample (or
- * with one channel) has the same memory order as a planar one.
+ * reproducible) in fp32; where dout has an infinity, dgate with a bias may be
+ * NaN in that channel (it is made of two sums). A channels-last side with one
+ * pixel per sample (or with one channel) has the same memory order as a planar
+ * one.
  * ------------------------------------------------------------------------ */
 typedef enum { WTCONV_NORM_NONE = 0, WTCONV_NORM_LAYER = 1, WTCONV_NORM_RMS = 2 } wtconv_norm_t;
 typedef enum {

@@ -928,3 +928,24 @@ def test_long_offsets_backward(order):
     for name, t in zip(("dweight", "dbias", "dgate", "dx_scale"), grads):
         if t is not None:
             check(name, t, ref.grads[name], ref.bounds[name])
+
+
+@on_gpu
+@pytest.mark.parametrize("order", ORDERS)
+@pytest.mark.parametrize("shape", [(3, 24, 5, 7), (1030, 16, 3, 5), (2, 5, 3, 3), (4, 1030, 1, 6), (6, 40, 1, 1)],
+                         ids=_shape_id)
+def test_an_infinite_gradient_stays_infinite(shape, order):
+    """Without a bias the gate's gradient sum dout D(v) is infinite, with the sign of that one product, in the
+    channel where one dout is infinite, and the other channels' are as they were."""
+    d = _make(shape, "bf16", "f32", *order, seed=16)
+    b, c, i, j = shape[0] - 1, shape[1] // 2, shape[2] - 1, 0
+    inf = d["dy"].clone()
+    inf[b, c, i, j] = float("inf")
+    for kind, gate in itertools.product(("none", "layer", "rms"), ("gate_c", "gate_s")):
+        opts = dict(kind=kind, gate=d[gate], weight=None if kind == "none" else d["weight"], want=("dh", "dgate"))
+        plain, got = (bb.wtconv_residual_bwd(dy, d["h"], **opts)[2][2].cpu() for dy in (d["dy"], inf))
+        t = bb.wtconv_residual_fwd(torch.zeros_like(d["x"]), d["h"], kind=kind, weight=opts["weight"])[b, c, i, j]
+        at = (c,) if gate == "gate_c" else (b, c)
+        assert float(t) != 0 and float(got[at]) == float("inf") * float(t), (kind, gate, float(got[at]), float(t))
+        got[at] = plain[at]
+        assert torch.equal(got, plain)

@@ -60,7 +60,10 @@ __global__ __launch_bounds__(threads_of(L)) void k_rows_bwd(BlockArgs a, Partiti
             for (int q = 0; q < PER; ++q) {
                 const int e = threadIdx.x + q * T;
                 if (e >= a.C) continue;
-                if (X && dgp) dgp[e] = a.keep * ((a.w ? a.w[e] : 1.f) * t1[q] + (a.b ? a.b[e] : 0.f) * t0[q]);
+                if (X && dgp) {   // without a bias no 0 times S0: where dout is infinite that is no 0
+                    const float w = a.w ? a.w[e] : 1.f;
+                    dgp[e] = a.keep * (a.b ? w * t1[q] + a.b[e] * t0[q] : w * t1[q]);
+                }
                 const float g = X ? (gate ? gate[e] : 1.f) * a.keep : 1.f;
                 if (by_sample) {
                     acc[e] += g * t1[q];
@@ -79,7 +82,8 @@ __global__ __launch_bounds__(threads_of(L)) void k_rows_bwd(BlockArgs a, Partiti
                     at.param(a.w, v, 1.f, p);
                     at.param(a.b, v, 0.f, q);
 #pragma unroll
-                    for (int i = 0; i < CG; ++i) p[i] = a.keep * (p[i] * s1[v][i] + q[i] * s0[v][i]);
+                    for (int i = 0; i < CG; ++i)
+                        p[i] = a.keep * (a.b ? p[i] * s1[v][i] + q[i] * s0[v][i] : p[i] * s1[v][i]);
                     at.store(dgp, p, v);
                 }
                 float g[CG];

@@ -271,7 +271,8 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
         load_param(gate, ch.c, 1.f, g);
 #pragma unroll
         for (int i = 0; i < CG; ++i) {
-            w[i] = a.keep * fmaf(w[i], s1[i], bb[i] * s0[i]);
+            // without a bias no 0 times S0: where dout is infinite that is no 0
+            w[i] = a.keep * (a.b ? fmaf(w[i], s1[i], bb[i] * s0[i]) : w[i] * s1[i]);
             s1[i] *= g[i] * a.keep;
             s0[i] *= g[i] * a.keep;
         }
