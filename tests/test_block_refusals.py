@@ -104,3 +104,46 @@ def test_backward_calls_name_the_argument_that_is_wrong(lib, kw, status, monkeyp
         with pytest.raises(wt.WTConvError) as e:
             call()
         assert e.value.status == status
+
+
+class _Copies(torch.utils._python_dispatch.TorchDispatchMode):
+    """Counts the tensors made of as many elements as a gradient has."""
+    def __init__(self, n):
+        super().__init__()
+        self.n, self.made = n, []
+
+    def __torch_dispatch__(self, fn, types, args=(), kwargs=None):
+        out = fn(*args, **(kwargs or {}))
+        if fn._schema.name in ("aten::clone", "aten::empty", "aten::empty_like", "aten::new_empty") \
+                and out.numel() == self.n:
+            self.made.append(fn._schema.name)
+        return out
+
+
+@pytest.mark.parametrize("channels_last", [False, True])
+def test_a_strided_gradient_is_copied_once(channels_last, monkeypatch):
+    """The residual's backward pass copies an expanded or strided dout into the stream's order, and copies nothing
+    more; one in either order is taken as it is (the call to the library is replaced)."""
+    from wavelet_convolution_amd import block as blk
+    got = []
+    monkeypatch.setattr(bb, "wtconv_residual_bwd",
+                        lambda dout, h, **kw: got.append(dout) or (dout, h, (None,) * 4))
+    order = torch.channels_last if channels_last else torch.contiguous_format
+    h = torch.zeros(2, 8, 4, 6)
+
+    class Ctx:
+        saved_tensors = (None, h, None, None, None, None, None)
+        needs_input_grad = (True, True) + (False,) * 10
+        opts = {}
+
+    Ctx.order = order
+    wide = torch.randn(2, 8, 4, 12)
+    for dout, copies in ((torch.ones(()).expand(2, 8, 4, 6), 1), (wide[..., ::2], 1), (h.clone(), 0),
+                         (torch.randn(2, 8, 4, 6).contiguous(memory_format=torch.channels_last), 0)):
+        got.clear()
+        with _Copies(h.numel()) as c:
+            blk.BlockResidualFunction.backward(Ctx, dout)
+        assert torch.equal(got[0], dout) and (got[0] is dout) == (copies == 0)
+        assert len(c.made) == copies, c.made
+        if copies:
+            assert got[0].is_contiguous(memory_format=order)

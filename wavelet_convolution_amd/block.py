@@ -40,9 +40,14 @@ def _gpu(*ts) -> None:
                                f"{t.device} - there is no CPU implementation")
 
 
+def _is_dense(t: torch.Tensor) -> bool:
+    """Whether t is planar or channels last."""
+    return t.is_contiguous() or (t.dim() == 4 and t.is_contiguous(memory_format=torch.channels_last))
+
+
 def _dense(t: torch.Tensor, like: torch.Tensor | None = None) -> torch.Tensor:
     """t itself where it is planar or channels last, else a copy in the memory order of `like`."""
-    if t.is_contiguous() or (t.dim() == 4 and t.is_contiguous(memory_format=torch.channels_last)):
+    if _is_dense(t):
         return t
     cl = like is not None and _b.layout_of(like) == _b.WTCONV_NHWC
     return t.contiguous(memory_format=torch.channels_last if cl else torch.contiguous_format)
@@ -90,7 +95,7 @@ class BlockResidualFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dout):
         x, h, weight, bias, gate, x_scale, rng = ctx.saved_tensors
-        if x is not None or _dense(dout) is not dout:
+        if x is not None or not _is_dense(dout):
             dout = dout.contiguous(memory_format=ctx.order)   # as x, which is read beside it
         want = _names(ctx, ((0, "dx"), (1, "dh"), (2, "dweight"), (3, "dbias"), (4, "dgate"), (5, "dx_scale")))
         if not want:
