@@ -143,7 +143,6 @@ typedef uint32_t words4 __attribute__((ext_vector_type(4)));
 typedef uint32_t words2 __attribute__((ext_vector_type(2)));
 typedef words4 words4_any __attribute__((aligned(2)));
 typedef words2 words2_any __attribute__((aligned(2)));
-typedef uint32_t word_any __attribute__((aligned(2)));
 
 template <typename T, int N>
 struct Vec {
@@ -164,13 +163,11 @@ struct Vec {
                 w[i + 2] = q.z;
                 w[i + 3] = q.w;
             }
-        } else if constexpr (WORDS == 2) {
+        } else {
+            static_assert(WORDS == 2, "");
             const words2 q = *(const words2_any*)p;
             w[0] = q.x;
             w[1] = q.y;
-        } else {
-            static_assert(WORDS == 1, "");
-            w[0] = *(const word_any*)p;
         }
     }
     // the first n elements, zeros past them
@@ -210,11 +207,9 @@ __device__ __forceinline__ void store_vec(T* __restrict__ p, const float (&v)[N]
     if constexpr (WORDS % 4 == 0) {
 #pragma unroll
         for (int i = 0; i < WORDS; i += 4) *(words4_any*)((char*)p + 4 * i) = words4{w[i], w[i + 1], w[i + 2], w[i + 3]};
-    } else if constexpr (WORDS == 2) {
-        *(words2_any*)p = words2{w[0], w[1]};
     } else {
-        static_assert(WORDS == 1, "");
-        *(word_any*)p = w[0];
+        static_assert(WORDS == 2, "");
+        *(words2_any*)p = words2{w[0], w[1]};
     }
 }
 // The first n of them.
@@ -311,17 +306,18 @@ __device__ __forceinline__ void store_patch(T* __restrict__ p, uint32_t off, siz
 // of a word.
 template <int PV>
 struct Drops {
-    uint32_t w[(PV + 3) / 4];
+    static_assert(PV % 4 == 0, "");
+    uint32_t w[PV / 4];
     template <bool ODD>
     __device__ __forceinline__ void draw(const BlockArgs& a, uint32_t row, int c) {
         const Philox gen(a.rng, a.site);
         const uint32_t G = (uint32_t)cdiv(a.C, CG);
         uint32_t g = row * G;   // fewer than 2^32 groups in all
 #pragma unroll
-        for (int k = 0; k < (PV + 3) / 4; ++k) {
+        for (int k = 0; k < PV / 4; ++k) {
             uint32_t m = 0;
 #pragma unroll 2
-            for (int j = 0; j < 4 && j < PV; ++j, g += G) m = m << 8 | drop_bits_at(gen, g, c, ODD, a.thr);
+            for (int j = 0; j < 4; ++j, g += G) m = m << 8 | drop_bits_at(gen, g, c, ODD, a.thr);
             w[k] = m;
         }
     }
@@ -332,7 +328,7 @@ struct Drops {
     __device__ __forceinline__ uint32_t spread(int i, int j) const {
         return (uint32_t)((int32_t)(w[j / 4] << (31 - bit(i, j))) >> 31);
     }
-    static constexpr int bit(int i, int j) { return 8 * ((PV < 4 ? PV : 4) - 1 - j % 4) + 7 - i; }
+    static constexpr int bit(int i, int j) { return 8 * (3 - j % 4) + 7 - i; }
 };
 
 }  // namespace wtc
