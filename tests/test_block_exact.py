@@ -157,3 +157,27 @@ def test_the_norm_of_this_data_is_the_data():
             if t.dtype == torch.float32:
                 assert torch.equal(t * (var + 1.0).rsqrt(), h)
         assert torch.equal(h.to(torch.bfloat16).float(), h)
+
+
+@on_gpu
+@pytest.mark.parametrize("C", [1, 3, 7, 8, 32])
+def test_sums_over_many_rows_are_short_chains(C):
+    """One dout of 2^24 before many of 1: an fp32 sum of 2^24 and 1 stays at 2^24, so a chain of n additions after
+    the large one loses n. Additions that any term passes, at the most: a row of its lane, 32 of the groups of a
+    workgroup and 4 that join them; in the second stage one slot a lane, 4 over lanes and 16 wavefronts: 58, each of
+    them off by half a step of a number up to 2^24 + n < 2^25, 2^-24 of it: 1.002 for these 19,650 rows."""
+    n = 19650
+    shape = (1, C, 1, n)
+    dy = torch.ones(shape, device="cuda")
+    dy[..., 0] = 2.0 ** 24
+    one = torch.ones(shape, device="cuda")
+    dy, one = _order(dy, 1), _order(one, 1)
+    want = 2.0 ** 24 + (n - 1)
+    xs = torch.ones(C, device="cuda")
+    for gate in (torch.ones(C, device="cuda"), torch.ones(1, C, device="cuda")):
+        print(f"[chains] {C} {tuple(gate.shape)}", flush=True)
+        _, _, (_, _, dgate, dxs) = bb.wtconv_residual_bwd(dy, one, x=one, gate=gate, x_scale=xs)
+        _, _, (_, dbias, _, _) = bb.wtconv_residual_bwd(dy, one, gate=gate, kind="rms", bias=torch.zeros(C, device="cuda"))
+        for name, t in (("dgate", dgate), ("dx_scale", dxs), ("dbias", dbias)):
+            off = (t.double().cpu() - want).abs().max()
+            assert float(off) <= 58 * 1.002, (name, float(off))

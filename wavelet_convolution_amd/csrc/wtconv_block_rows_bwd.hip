@@ -30,8 +30,10 @@ __global__ __launch_bounds__(threads_of(L)) void k_rows_bwd(BlockArgs a, Partiti
     }
     float* slot = slots + (size_t)blockIdx.x * (pt.nsum + pt.partials) * a.C;
     // A sum over the workgroup's rows, channel by channel. NG > 1: the groups'
-    // sums meet in LDS, and channel e is then thread e % T's.
-    constexpr int PER = NG > 1 ? cdiv(W, T) : 1;
+    // sums meet in LDS, and channel e is then thread e % T's, in CH chains that
+    // join pairwise: one chain over the 512 groups of narrow rows lost up to
+    // nine bits (and took longer).
+    constexpr int PER = NG > 1 ? cdiv(W, T) : 1, CH = NG < 16 ? NG : 16;
     auto joined = [&](const float (&s)[NV][CG], float (&t)[PER]) {
         __syncthreads();
 #pragma unroll
@@ -42,11 +44,17 @@ __global__ __launch_bounds__(threads_of(L)) void k_rows_bwd(BlockArgs a, Partiti
         __syncthreads();
 #pragma unroll
         for (int q = 0; q < PER; ++q) {
-            t[q] = 0.f;
+            float p[CH] = {};
             const int e = threadIdx.x + q * T;
             if (e < a.C)
-#pragma unroll 4
-                for (int g = 0; g < NG; ++g) t[q] += join[g * W + e];
+                for (int g = 0; g < NG; g += CH)
+#pragma unroll
+                    for (int k = 0; k < CH; ++k) p[k] += join[(g + k) * W + e];
+#pragma unroll
+            for (int n = CH / 2; n > 0; n /= 2)
+#pragma unroll
+                for (int k = 0; k < n; ++k) p[k] += p[k + n];
+            t[q] = p[0];
         }
     };
     // What a gate's rows give: dg, and parts of dw and db, which add up in LDS
