@@ -147,3 +147,14 @@ def test_a_strided_gradient_is_copied_once(channels_last, monkeypatch):
         assert len(c.made) == copies, c.made
         if copies:
             assert got[0].is_contiguous(memory_format=order)
+
+
+def test_a_workspace_that_is_no_block_of_memory_is_refused():
+    """An expanded or strided tensor counts more bytes than it owns, or leaves gaps."""
+    few = torch.zeros(1, dtype=torch.uint8)
+    for ws in (few.expand(1 << 20), torch.zeros(64, 64).t()[:, :3]):
+        with pytest.raises(ValueError, match="ws must be contiguous"):
+            wt._ws_bytes(ws)
+        with pytest.raises(ValueError, match="ws must be contiguous"):
+            bb._workspace(None, few, ws)
+    assert 64 * 64 * 4 - 256 < wt._ws_bytes(torch.zeros(64, 64)) <= 64 * 64 * 4

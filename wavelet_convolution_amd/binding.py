@@ -234,6 +234,8 @@ def _ws_bytes(ws: torch.Tensor | None) -> int:
     """Usable bytes of a workspace tensor after aligning its start to 256."""
     if ws is None:
         return 0
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous: its bytes are counted from its elements")
     return max(0, ws.numel() * ws.element_size() - (_ws_ptr(ws) - ws.data_ptr()))
 
 
