@@ -130,7 +130,8 @@ def _check_i32(*values: int) -> None:
 def _desc(act: torch.Tensor, levels: int, k_base: int, k_level: int) -> WTConvDesc:
     B, C, H, W = act.shape
     levels, k_base, k_level = int(levels), int(k_base), int(k_level)
-    _check_i32(B, C, H, W, levels, k_base, k_level)
+    if (B | C | H | W | levels | k_base | k_level) >> 31:   # the quick test first
+        _check_i32(B, C, H, W, levels, k_base, k_level)
     dt = {torch.float32: WTCONV_F32, torch.bfloat16: WTCONV_BF16}.get(act.dtype, -1)
     return WTConvDesc(B, C, H, W, levels, k_base, k_level, dt, layout_of(act))
 
