@@ -9,10 +9,10 @@ nn.Modules over the C-ABI entry points.
 Tensors are [B, C, H, W] in planar or channels-last memory order (a linear
 layer's [B, H, W, C] rows are ``rows.permute(0, 3, 1, 2)``; tokens [B, S, C]
 are H = 1, W = S), fp32 or bf16; parameters are fp32. The backward passes keep
-the inputs only: row statistics and dropout masks are computed again. Every
-step of the computation runs in libwtconv.so. Tensors must be on the GPU:
-there is no CPU path. A second derivative
-raises an error.
+inputs only (the residual's h always, its x for the gradient of an x_scale):
+row statistics and dropout masks are computed again. Every step of the
+computation runs in libwtconv.so. Tensors must be on the GPU: there is no CPU
+path. A second derivative raises an error.
 
 Dropout reads its seed and offset from a tensor on the GPU (`dropout_rng`).
 One tensor serves a whole model, each use with a site number of its own; the

@@ -69,7 +69,7 @@ struct BlockArgs {
 struct Partition {
     long long tiles;    // all tiles
     long long tps;      // tiles per sample (samples count only with a gate per sample: else one)
-    int wgs;            // as many as are resident at once, at most one a tile
+    int wgs;            // workgroups: at most one a tile; each kernel's rule is at its partition
     int nsum;           // channel sums a slot holds
     int partials;       // 0, or 2: partial gate gradients per slot
     __host__ __device__ long long begin(long long wg) const { return wg * tiles / wgs; }

@@ -21,10 +21,12 @@ namespace {
 
 // One tile a workgroup where the card takes them in two rounds, else as many
 // workgroups as it holds at once (256 CUs, three wavefronts a SIMD at the
-// kernels' registers), each with an even share: residual backward
-// 64x96x56x56, 1,600 tiles: 58.3 us at a tile each, 61.7 at 1,024 workgroups,
-// 79.5 at 1,280; 32x128x128x128, 8,192 tiles: 162 us at 1,536 (the card's fill
-// there), 170 at 1,280, 174 at 2,048, 178 at a tile each.
+// kernels' registers), each with an even share. Residual backward (layer
+// norm, gate per channel, element dropout, residual scale, bf16) 64x96x56x56,
+// 1,600 tiles of three wavefronts: 56.8 us at a tile each, 61.5 at 1,024
+// workgroups (the card's fill), 76.3 at 1,280; 32x128x128x128, 4,096 tiles of
+// four: 163 us at 768 (the fill), 178 at 640, 180 at 1,280, 157 at 2,048 and
+// 158 at a tile each, for more partial sums to keep and add.
 Partition tile_partition(const BlockArgs& a, const TileShape& t) {
     Partition p{};
     const bool by_sample = a.dg && a.gate_mode == GATE_SAMPLE;
@@ -44,9 +46,9 @@ size_t tile_bwd_bytes(const BlockArgs& a, const TileShape& t) {
 
 // Whether pieces of a plane are no whole 128-byte lines: neighbouring tiles,
 // that share the lines between them, then stay on one XCD (32x128x100x100 norm
-// forward 33.5 against 42.3 us, 64x384x14x14 8.6 against 10.9). Where no line
-// is shared that order only spreads the traffic less evenly (32x128x128x128
-// residual forward 88.6 against 81.7 us).
+// forward 32.1 against 37.1 us, 64x384x14x14 residual forward 9.6 against
+// 12.7). Where no line is shared that order only spreads the traffic less
+// evenly (32x128x128x128 residual forward 89.1 against 81.5 us).
 bool shares_lines(const BlockArgs& a, int h_bf16, int y_bf16, const TileShape& t) {
     auto cut = [&](int bf16) { return (size_t)a.HW * (bf16 ? 2 : 4) % 128 != 0 || t.px * (bf16 ? 2 : 4) % 128 != 0; };
     return (!a.h_cl && cut(h_bf16)) || (!a.y_cl && cut(y_bf16));

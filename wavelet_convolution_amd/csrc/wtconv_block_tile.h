@@ -344,7 +344,9 @@ __global__ __launch_bounds__(MAXT) void k_tile_bwd(BlockArgs a, Partition pt, Su
             }
         }
         // over pixels, for the channels' gradients, and over channels, for the
-        // norm's, without what a neighbour has; z = h r + c
+        // norm's, without what a neighbour has; z = h r + c, one instruction an
+        // element: c's rounding moves z by half a step of mean r, which is what
+        // the rounding of the mean itself does
         float ms[2][PV] = {}, c[PV];
 #pragma unroll
         for (int j = 0; j < PV; ++j) c[j] = -mean[j] * r[j];
@@ -447,22 +449,25 @@ struct TileShape {
     int tps;              // tiles of a sample
 };
 // Channel lanes: the choice among 4, 8 and 16 with the fewest wavefronts over
-// a sample (idle lanes past C and past the plane cost as much as busy ones).
-// Sixteen leave 64-byte pieces of a plane and many workgroups of few
-// wavefronts, so they need a twentieth fewer (64x384x14x14: 28.0 us backward
-// against 29.4 with eight; 32x128x100x100 at the same number: 167 against
-// 139). Between four and eight at about the same number (one in 64), four have
-// a plane's pieces longer and eight fewer wavefronts to a barrier: eight
-// forwards (32x128x127x125 52 us against 59), four backwards where that is
-// three or four wavefronts (207 against 252, 32x128x100x100 125 against 136;
-// 64x64x64x64, two: 54.5 against 50.9).
+// a sample (idle lanes past C and past the plane cost as much as busy ones:
+// 64x768x7x7 norm 6.2 us forward and 13.1 backward with sixteen, 25.6 and 72.7
+// with eight). Sixteen leave 64-byte pieces of a plane and many workgroups of
+// few wavefronts, so they need a twentieth fewer (32x128x100x100 residual
+// backward at the same number 154 us against 135; 64x384x14x14 at an eighth
+// fewer: norm 8.5 against 8.8 forwards, 17.7 against 16.5 backwards). Between
+// four and eight at about the same number (one in 64), four have a plane's
+// pieces longer and eight fewer wavefronts to a barrier: eight forwards (norm
+// 32x128x127x125 57 us against 62, 128x128 57.0 against 56.5; residuals there
+// 87 against 85 and 81 against 76), four backwards where that is three or four
+// wavefronts (residual 208 against 251, 32x128x100x100 124 against 135;
+// 64x64x64x64, two: 54.6 against 50.9).
 //
 // Pixels of a lane: 16 bytes of a plane in bf16 (a tile's fixed costs are
-// spread over twice the elements of 8-byte lanes: residual forward
-// 32x128x128x128 81 against 106 us, its backward 162 against 201), unless
-// that leaves less than a wavefront a SIMD, which is all latency (64x768x7x7
-// residual backward 28.2 us with eight pixels, 21.3 with four); 4 in fp32, and
-// where more than eight wavefronts share the registers.
+// spread over twice the elements of 8-byte lanes: 32x128x128x128 residual
+// forward 81 against 100 us, its backward 163 against 174, the norm's 98
+// against 103), unless that leaves less than a wavefront a SIMD, which is all
+// latency (64x768x7x7 residual backward 26.0 us with eight pixels, 20.9 with
+// four); 4 in fp32, and where more than eight wavefronts share the registers.
 //
 // cl = 0: fewer channels or pixels than a lane's, more channels than sixteen
 // wavefronts hold, a sample of 2^30 elements, or 2^30 tiles.
