@@ -449,18 +449,17 @@ struct TileShape {
     int tps;              // tiles of a sample
 };
 // Channel lanes: the choice among 4, 8 and 16 with the fewest wavefronts over
-// a sample (idle lanes past C and past the plane cost as much as busy ones:
-// 64x768x7x7 norm 6.2 us forward and 13.1 backward with sixteen, 25.6 and 72.7
-// with eight). Sixteen leave 64-byte pieces of a plane and many workgroups of
-// few wavefronts, so they need a twentieth fewer (32x128x100x100 residual
-// backward at the same number 154 us against 135; 64x384x14x14 at an eighth
-// fewer: norm 8.5 against 8.8 forwards, 17.7 against 16.5 backwards). Between
-// four and eight at about the same number (one in 64), four have a plane's
-// pieces longer and eight fewer wavefronts to a barrier: eight forwards (norm
-// 32x128x127x125 57 us against 62, 128x128 57.0 against 56.5; residuals there
-// 87 against 85 and 81 against 76), four backwards where that is three or four
-// wavefronts (residual 208 against 251, 32x128x100x100 124 against 135;
-// 64x64x64x64, two: 54.6 against 50.9).
+// a sample (idle lanes past C and past the plane cost as much as busy ones).
+// Sixteen leave 64-byte pieces of a plane and many workgroups of few
+// wavefronts, so they need a twentieth fewer (32x128x100x100 residual backward
+// at the same number 154 us against 135; 64x384x14x14 at an eighth fewer: norm
+// 8.5 against 8.8 forwards, 17.7 against 16.5 backwards). Between four and
+// eight at about the same number (one in 64), four have a plane's pieces longer
+// and eight fewer wavefronts to a barrier: eight forwards (norm 32x128x127x125
+// 57 us against 62, 128x128 57.0 against 56.5; residuals there 87 against 85
+// and 81 against 76), four backwards where that is three or four wavefronts
+// (residual 208 against 251, 32x128x100x100 124 against 135; 64x64x64x64, two:
+// 54.6 against 50.9).
 //
 // Pixels of a lane: 16 bytes of a plane in bf16 (a tile's fixed costs are
 // spread over twice the elements of 8-byte lanes: 32x128x128x128 residual
