@@ -367,10 +367,147 @@ wtconv_status_t wtconv_residual_bwd(const wtconv_block_desc_t *desc, const void 
 wtconv_status_t wtconv_dropout(const wtconv_block_desc_t *desc, const void *x, const uint64_t *rng, void *y,
                                void *stream);
 
+/* ------------------------------------------------------------------------
+ * Expert rows: the rows of a block whose MLP is a set of experts, to their
+ * experts and back. Row n (a pixel or token of c channels) has k slots
+ * n * k + i, each with the number of an expert; a slot whose number is not
+ * in 0..experts-1 goes to no expert (padding, a row over a capacity).
+ *
+ *   sort   order, place, offsets: the slots sorted by expert, those of one
+ *          expert in their own order, those of none last. order[p] is the
+ *          slot at place p, place[slot] its place, and expert e's places are
+ *          offsets[e] .. offsets[e + 1] - 1 (offsets[experts]: how many
+ *          slots have an expert)
+ *   rows   xs[place[n][i]] = x[n]                      (none: a row of zeros)
+ *   sum    y[n] = sum_i weight[n][i] * ys[place[n][i]]     (without the none)
+ *
+ * and their gradients: rows backward dx[n] = sum_i dxs[place[n][i]] without
+ * the none; sum backward dys[place[n][i]] = weight[n][i] * dy[n] (none:
+ * zeros) and dweight[n][i] = <dy[n], ys[place[n][i]]> (none: 0). A row of xs,
+ * ys or dxs that belongs to no expert is not read, whatever it holds.
+ *
+ * x, y, dx, dy are [n][c], xs, ys, dxs, dys [n * k][c], contiguous, of type
+ * `dtype`; order [n * k], place [n][k], offsets [experts + 1] are int32,
+ * weight and dweight [n][k] fp32. Sums over i run in order in fp32 and are
+ * rounded once. A place outside 0..n*k-1 counts as none; where places are no
+ * permutation, rows of xs and dys that no place names are not written.
+ * Pointers need the alignment of their element type only; outputs must not
+ * overlap inputs or each other. n = 0 writes zero offsets and nothing else.
+ * ------------------------------------------------------------------------ */
+typedef enum { WTCONV_I32 = 0, WTCONV_I64 = 1 } wtconv_index_t;
+
+typedef struct {
+    int64_t n;         /* rows; n * k up to 2^31 - 1 */
+    int32_t k;         /* slots of a row, 1..1024 */
+    int32_t experts;   /* 1..1024 */
+    int32_t c;         /* channels, 1..2^30 (the sort does not look at it) */
+    int32_t dtype;     /* wtconv_dtype_t of the rows (the sort does not look at it) */
+} wtconv_expert_desc_t;
+
+/* Device workspace of wtconv_expert_sort (256-byte aligned; 0 for few
+   slots, ws may then be NULL), or (size_t)-1 if the descriptor is invalid.
+   The other calls need none. Calls that may run at the same time need
+   workspaces of their own (two captured graphs, too). */
+size_t wtconv_expert_workspace_size(const wtconv_expert_desc_t *desc);
+
+/* expert: [n][k] int32 or int64 (id_type, a wtconv_index_t). */
+wtconv_status_t wtconv_expert_sort(const wtconv_expert_desc_t *desc, const void *expert, int32_t id_type,
+                                   int32_t *order, int32_t *place, int32_t *offsets, void *ws,
+                                   size_t ws_bytes, void *stream);
+wtconv_status_t wtconv_expert_rows_fwd(const wtconv_expert_desc_t *desc, const void *x, const int32_t *place,
+                                       const int32_t *offsets, void *xs, void *stream);
+wtconv_status_t wtconv_expert_rows_bwd(const wtconv_expert_desc_t *desc, const void *dxs, const int32_t *place,
+                                       const int32_t *offsets, void *dx, void *stream);
+wtconv_status_t wtconv_expert_sum_fwd(const wtconv_expert_desc_t *desc, const void *ys, const float *weight,
+                                      const int32_t *place, const int32_t *offsets, void *y, void *stream);
+/* dys or dweight may be NULL: not computed (ys is read for dweight only,
+   weight for dys only; what is not read may be NULL). */
+wtconv_status_t wtconv_expert_sum_bwd(const wtconv_expert_desc_t *desc, const void *dy, const void *ys,
+                                      const float *weight, const int32_t *place, const int32_t *offsets,
+                                      void *dys, float *dweight, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The optimizer's step over many tensors at once: the gradients' norm, and
+ * AdamW with its states in 32 or in 8 bits. Tensor i has counts[i] elements
+ * (contiguous, aligned to the element). The pointers of one call go into the
+ * kernels' arguments: nothing is kept, and a captured graph holds them.
+ *
+ * Norm: out[0] = sqrt(sum of all squares), summed in 64 bits in a fixed
+ * order (bitwise reproducible); out[1] = min(1, max_norm / (norm + 1e-6)),
+ * and NaN where the norm is not finite. step (may be NULL) is increased by
+ * one where it is.
+ *
+ * AdamW, with t = *step (1 for the first step; less counts as 1), f = *factor
+ * (NULL: 1), r = lr[i] * *lr_factor (NULL: 1):
+ *     g' = f g,  m = b1 m + (1 - b1) g',  v = b2 v + (1 - b2) g'^2
+ *     p  = p - r wd[i] p - r (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
+ * Where f is not finite nothing is changed: out[1] of the norm as the factor
+ * clips the gradients, and skips a step whose gradients have an infinity or
+ * a NaN. All arithmetic is fp32.
+ *
+ * The states of all tensors stand in one buffer: tensor i's begin at element
+ * 256 * sum_{j < i} ceil(counts[j] / 256). What stands between a tensor's last
+ * element and the next multiple of 256 is not looked at (with 8 bits it may
+ * be written with zeros). state_bits = 32: m and v are fp32. state_bits = 8:
+ * m and v are e4m3 bytes that hold m and sqrt(v) in units of a block of 256
+ * elements, scales[block] = {max |m|, max sqrt(v)} / 448 (fp32 pairs; first
+ * moments of a block whose largest is below 2^-100 are held as zero, and a
+ * root that is not zero as 2^-9 units at least, so that no parameter is
+ * divided by a root that was lost). The step itself uses m and v before
+ * that rounding, which is to the nearest value, or, with rng (two 64-bit
+ * integers {seed, offset} on the device, as for dropout), to the value below
+ * or above it with the probabilities that make the mean right: |q| becomes
+ * floor(|q| / s + (u + 1/2) / 65536) s with s the distance of e4m3 numbers at
+ * q and u the low (m) or high (v) 16 bits of word e % 4 of Philox4x32-10
+ * with counter (e / 4, site + i, offset low, offset high) and key (seed low,
+ * seed high), for element e of tensor i. A moving average changes by less
+ * than half a step of 8 bits in most steps: rounded to nearest it then stays
+ * where it is.
+ *
+ * Parameters are fp32 or bf16. With master (bf16 parameters only) the step
+ * works on fp32 copies of them, laid out as the states, and writes both;
+ * without it a bf16 parameter is widened, changed and rounded to nearest.
+ * grads[i] = NULL leaves tensor i and its states as they are. No tensor may
+ * stand twice in a call or overlap another one.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    int32_t p_dtype, g_dtype;   /* wtconv_dtype_t of all parameters, all gradients */
+    int32_t state_bits;         /* 32 or 8 */
+    int32_t site;               /* 0..2^31-1, read with rng: tensor i uses site + i (below 2^31) */
+    double beta1, beta2;        /* 0 <= beta < 1 */
+    double eps;                 /* FLT_MIN at least, finite */
+} wtconv_adamw_desc_t;
+
+#define WTCONV_ADAMW_BLOCK 256   /* elements that share a scale, and the states' alignment */
+
+/* Elements of the states' buffers (and of master) for n tensors of these
+   counts, or -1 where a count is not in 0..2^34 or the sum exceeds 2^39. */
+int64_t wtconv_adamw_state_count(const int64_t *counts, int32_t n);
+
+/* Host arrays of n entries: params, grads, counts (0..2^34 each), lr,
+   weight_decay (finite); all other pointers are device memory. m, v and
+   master are aligned to 16 bytes, scales to 8. */
+wtconv_status_t wtconv_adamw_step(const wtconv_adamw_desc_t *desc, int32_t n, void *const *params,
+                                  const void *const *grads, const int64_t *counts, const float *lr,
+                                  const float *weight_decay, void *m, void *v, float *scales, float *master,
+                                  const int64_t *step, const float *factor, const float *lr_factor,
+                                  const uint64_t *rng, void *stream);
+
+/* Device workspace of wtconv_grad_norm for n tensors (8-byte aligned), or
+   (size_t)-1 if n < 0. */
+size_t wtconv_grad_norm_workspace_size(int32_t n);
+
+/* dtypes: a wtconv_dtype_t for each gradient (host array, as grads and
+   counts); max_norm > 0, infinity for no clipping. out: two fp32 numbers. A
+   NULL gradient counts nothing. */
+wtconv_status_t wtconv_grad_norm(int32_t n, const void *const *grads, const int64_t *counts,
+                                 const int32_t *dtypes, double max_norm, int64_t *step, float *out, void *ws,
+                                 size_t ws_bytes, void *stream);
+
 /* Static description of a status code. */
 const char *wtconv_status_string(wtconv_status_t status);
 
-/* Library version, e.g. "0.4.0". */
+/* Library version, e.g. "0.5.0". */
 const char *wtconv_version(void);
 
 /* Measurement probes (not operations of the layer). They measure on the

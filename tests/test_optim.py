@@ -1,0 +1,522 @@
+"""The optimizer's step: the gradients' norm and AdamW over many tensors,
+against the definition in 64 bits (tests/_step_ref.py)."""
+import copy
+import math
+
+import pytest
+import torch
+
+from tests._step_ref import BLOCK, Step, U, places
+from wavelet_convolution_amd import AdamW, block_residual, channel_norm, dropout_rng, expert_rows, expert_sort, expert_sum
+from wavelet_convolution_amd import optim_binding as ob
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="no GPU")]
+DEV = "cuda"
+F32, BF16 = torch.float32, torch.bfloat16
+
+# around a vector of four, a block of 256, a workgroup's 4,096; odd shapes, nothing
+SHAPES = [(1,), (0,), (3,), (4, 1), (5,), (255,), (16, 16), (257,), (97, 5, 5), (64, 64), (4097,), (2, 0, 3), (3, 97, 4, 5, 5),
+          (1021, 33)]
+
+
+class Call:
+    """A call's tensors, filled from a seed."""
+
+    def __init__(self, shapes=SHAPES, p=F32, g=F32, master=False, bits=32, seed=0, t=7, random=False, fresh=False,
+                 unaligned=False, missing=(), factor=0.7, lr_factor=None, width=1e-3, **opts):
+        gen = torch.Generator(DEV).manual_seed(seed)
+
+        def randn(*shape):
+            return torch.randn(*shape, generator=gen, device=DEV)
+
+        def place(x):
+            if not unaligned:
+                return x
+            y = torch.empty(x.numel() + 1, dtype=x.dtype, device=DEV)[1:].view(x.shape)
+            return y.copy_(x)
+
+        self.params = [place((0.05 * randn(*s)).to(p)) for s in shapes]
+        self.grads = [None if i in missing else place((width * torch.exp(randn(*s)) * randn(*s)).to(g))
+                      for i, s in enumerate(shapes)]
+        n = ob.wtconv_adamw_state_count(self.params)
+        m, root = (0.3 * width * randn(n)) * (not fresh), (width * (0.5 + torch.rand(n, generator=gen, device=DEV))) * (not fresh)
+        self.scales = None
+        if bits == 8:
+            both = torch.stack((m, root)).view(2, -1, BLOCK)
+            self.scales = (both.abs().amax(-1) / 448).t().contiguous()
+            unit = torch.where(self.scales > 0, self.scales, 1.0)
+            m, v = ((both[i] / unit[:, i:i + 1]).view(-1).to(torch.float8_e4m3fn) for i in range(2))
+        else:
+            v = root ** 2
+        self.m, self.v, self.master = m, v, None
+        if master:
+            self.master = 0.05 * randn(n)
+            for q, at in zip(self.params, places(self.params)):
+                self.master[at] += q.reshape(-1).float()
+        self.step = torch.full((1,), t, dtype=torch.int64, device=DEV)
+        self.opts = dict(lr=1e-3, weight_decay=0.05, scales=self.scales, master=self.master,
+                         factor=None if factor is None else torch.full((1,), factor, device=DEV),
+                         lr_factor=None if lr_factor is None else torch.full((1,), lr_factor, device=DEV),
+                         rng=torch.tensor([seed + 2 ** 40, seed + 2 ** 33], device=DEV) if random else None, site=5 if random else 0)
+        self.opts.update(opts)
+
+    def args(self):
+        return self.params, self.grads, self.m, self.v, self.step
+
+    def run(self, **kw):
+        ob.wtconv_adamw_step(*self.args(), **self.opts, **kw)
+
+    def check(self, **kw):
+        want = Step(*self.args(), **self.opts)
+        self.run(**kw)
+        torch.cuda.synchronize()
+        want.check()
+
+    def tensors(self):
+        return [t for t in (*self.params, self.m, self.v, self.scales, self.master) if t is not None]
+
+    def bits(self):
+        return [t.clone().view(-1).view(torch.uint8) for t in self.tensors()]
+
+
+KINDS = [(F32, F32, False), (F32, BF16, False), (BF16, BF16, True), (BF16, F32, True), (BF16, BF16, False), (BF16, F32, False)]
+STATES = [(32, False), (8, False), (8, True)]
+
+
+@pytest.mark.parametrize("bits,random", STATES)
+@pytest.mark.parametrize("p,g,master", KINDS)
+def test_step(p, g, master, bits, random):
+    Call(p=p, g=g, master=master, bits=bits, random=random).check()
+
+
+@pytest.mark.parametrize("bits,random", STATES)
+@pytest.mark.parametrize("p,g,master", KINDS)
+def test_step_on_pointers_aligned_to_the_element_only(p, g, master, bits, random):
+    Call(p=p, g=g, master=master, bits=bits, random=random, seed=1, unaligned=True).check()
+
+
+@pytest.mark.parametrize("bits,random", STATES)
+@pytest.mark.parametrize("t", [-3, 0, 1, 2, 1000, 10 ** 6, 2 ** 40])
+def test_first_and_late_steps(t, bits, random):
+    """States of zeros at the first step; a count below 1 is 1."""
+    Call(bits=bits, random=random, seed=2, t=t, fresh=t <= 1).check()
+
+
+@pytest.mark.parametrize("bits,random", STATES)
+def test_several_steps(bits, random):
+    c = Call(bits=bits, random=random, fresh=True, t=1, seed=3)
+    for i in range(6):
+        c.check()
+        c.step += 1
+        if random:
+            c.opts["rng"][1] += 1
+        for j, g in enumerate(c.grads):
+            g.copy_(torch.randn(g.shape, device=DEV) * 1e-3 * (i + 1))
+
+
+@pytest.mark.parametrize("bits,random", STATES)
+def test_more_tensors_than_a_launch_takes(bits, random):
+    """200 tensors, rates and decays of their own, some without a gradient (runs of them too)."""
+    shapes = [((i * 37) % 600 + 1,) for i in range(200)]
+    Call(shapes, bits=bits, random=random, seed=4, missing=(0, 5, 79, 80, 81, *range(150, 180), 199),
+         lr=torch.linspace(0, 1e-2, 200), weight_decay=[0.1 * (i % 3) for i in range(200)], lr_factor=0.25).check()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_large_tensor(bits):
+    """Several rounds of workgroups over the card, beside small tensors."""
+    Call([(7,), (5_000_011,), (300,)], p=BF16, g=BF16, master=True, bits=bits, random=bits == 8, seed=5).check()
+
+
+def test_betas_and_eps():
+    for betas, eps in (((0.0, 0.0), 1e-8), ((0.0, 0.99), 1e-3), ((0.95, 0.0), 1e-6), ((0.5, 0.9999), 1.0)):
+        for bits in (32, 8):
+            Call(bits=bits, betas=betas, eps=eps, seed=6, t=3).check()
+
+
+@pytest.mark.parametrize("bits,random", STATES)
+@pytest.mark.parametrize("factor", [float("nan"), float("inf"), -float("inf")])
+def test_a_factor_that_is_not_finite_changes_nothing(factor, bits, random):
+    c = Call(bits=bits, random=random, factor=factor, seed=7)
+    c.grads[3][0] = float("nan")
+    before = c.bits()
+    c.run()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(before, c.bits()))
+
+
+@pytest.mark.parametrize("bits,random", STATES)
+def test_zero_gradients(bits, random):
+    """From zero states nothing but the decay changes a parameter, and states stay zero."""
+    c = Call(bits=bits, random=random, fresh=True, t=1, seed=8)
+    for g in c.grads:
+        g.zero_()
+    old = [p.clone() for p in c.params]
+    c.check()
+    assert not c.m.float().any() and not c.v.float().any()
+    for a, b in zip(c.params, old):
+        assert ((a.double() - b.double() * (1 - 1e-3 * 0.05)).abs() <= 4 * U * b.abs()).all()
+
+
+def test_small_roots_are_not_lost():
+    """Elements far below their block's largest: the root stays above zero, so a step without a gradient is bounded."""
+    for random in (False, True):
+        c = Call([(256,)], bits=8, random=random, fresh=True, t=1, seed=9, factor=None, weight_decay=0.0)
+        g = torch.full((256,), 1e-12, device=DEV)
+        g[0] = 1.0
+        c.grads = [g]
+        c.check()
+        assert (c.v.float() > 0).all()
+        old = c.params[0].clone()
+        c.grads = [torch.zeros(256, device=DEV)]
+        c.step += 1
+        c.check()
+        # |m| / root is at most that of one gradient alone, sqrt of its corrections apart
+        assert (c.params[0] - old).abs().max() <= 1e-3 * 1.5
+
+
+def test_moments_too_small_for_their_units():
+    c = Call([(512,)], bits=8, fresh=True, t=1, seed=10, factor=None)
+    g = torch.full((512,), 1e-38, device=DEV)
+    g[256:] = 1e-20
+    c.grads = [g]
+    c.run()
+    torch.cuda.synchronize()
+    assert not c.m[:256].float().any() and float(c.scales[0, 0]) == 0
+    assert all(torch.isfinite(t.float()).all() for t in c.tensors())
+
+
+def test_stochastic_rounding_has_the_right_mean():
+    """One step from states of one value: of n elements a share of the root's fraction is rounded up, to the next value,
+    within six standard deviations."""
+    n = 1 << 16
+    c = Call([(n,)], bits=8, random=True, fresh=True, t=5, seed=11, factor=None)
+    c.m.zero_(), c.v.copy_(torch.full((n,), 16.0, device=DEV).to(torch.float8_e4m3fn))
+    c.scales[:, 0], c.scales[:, 1] = 0, 1e-4
+    g = torch.full((n,), 2e-3, device=DEV)
+    g[::BLOCK] = 0.2   # the block's largest
+    c.grads = [g]
+    c.check()
+    unit = float(c.scales[0, 1])
+    q = math.sqrt(0.999 * 1.6e-3 ** 2 + 1e-3 * 2e-3 ** 2) / unit
+    step = 2.0 ** (math.floor(math.log2(q)) - 3)
+    up = q / step - math.floor(q / step)
+    rest = torch.ones(n, dtype=torch.bool, device=DEV)
+    rest[::BLOCK] = False
+    held = c.v.float()[rest]
+    assert set(held.unique().tolist()) == {math.floor(q / step) * step, (math.floor(q / step) + 1) * step}
+    share = float((held > q).float().mean())
+    assert abs(share - up) <= 6 * math.sqrt(up * (1 - up) / len(held))
+
+
+def test_a_step_again_is_the_same_bits():
+    for bits, random in STATES:
+        a, b = (Call(bits=bits, random=random, seed=12) for _ in range(2))
+        a.run(), b.run()
+        assert all(torch.equal(x, y) for x, y in zip(a.bits(), b.bits()))
+
+
+# ------------------------------------------------------------------- norm
+
+def check_norm(grads, max_norm=1.0, **kw):
+    want = math.sqrt(sum(float((g.double() ** 2).sum()) for g in grads if g is not None))
+    out = ob.wtconv_grad_norm(grads, max_norm, **kw)
+    factor = min(1.0, max_norm / (want + 1e-6))
+    # sums in 64 bits, rounded once
+    assert abs(float(out[0]) - want) <= 1.001 * U * want and abs(float(out[1]) - factor) <= 1.001 * U * factor
+    return out
+
+
+@pytest.mark.parametrize("shapes", [[(1,)], [(3,), (0,), (8,)], SHAPES, [((i * 91) % 3000,) for i in range(400)],
+                                    [(20_000_003,)], [(17,)] * 161, [(8192,), (8193,), (2048 * 8192 + 5,)]])
+def test_norm(shapes):
+    g = torch.Generator(DEV).manual_seed(0)
+    grads = [torch.randn(s, generator=g, device=DEV).to(F32 if i % 3 else BF16) for i, s in enumerate(shapes)]
+    a = check_norm(grads)
+    assert torch.equal(a, check_norm(grads))
+    check_norm([x.bfloat16() for x in grads], 1e9)
+    check_norm([None, *grads, None], math.inf)
+
+
+def test_norm_of_far_values():
+    for x in (1e-30, 1e-22, 1e18, 1e25):   # squares that 32 bits do not hold
+        check_norm([torch.full((1000,), x, device=DEV), torch.full((9,), x, device=DEV).bfloat16()])
+    assert ob.wtconv_grad_norm([torch.zeros(100, device=DEV)], 0.5).tolist() == [0.0, 1.0]
+    assert ob.wtconv_grad_norm([torch.zeros(0, device=DEV)], 0.5).tolist() == [0.0, 1.0]
+
+
+def test_norm_of_pointers_aligned_to_the_element_only():
+    for t in (F32, BF16):
+        check_norm([torch.randn(70_001, device=DEV).to(t)[1:], torch.randn(12, device=DEV).to(t)[3:]])
+
+
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_norm_that_is_not_finite_is_not_counted(bad):
+    step = torch.full((1,), 4, dtype=torch.int64, device=DEV)
+    grads = [torch.randn(5000, device=DEV), torch.randn(77, device=DEV).bfloat16()]
+    check_norm(grads, step=step)
+    assert int(step) == 5
+    grads[1][50] = bad
+    out = ob.wtconv_grad_norm(grads, 1.0, step=step)
+    assert int(step) == 5 and not math.isfinite(float(out[0])) and math.isnan(float(out[1]))
+
+
+def test_norm_into_given_tensors():
+    out, ws = torch.empty(2, device=DEV), torch.full((1 << 16,), 255, dtype=torch.uint8, device=DEV)
+    assert check_norm([torch.randn(999, device=DEV)], out=out, ws=ws) is out
+
+
+# ------------------------------------------------------- streams and graphs
+
+def test_on_another_stream():
+    s = torch.cuda.Stream()
+    c = Call(bits=8, seed=13)
+    torch.cuda.synchronize()
+    want = Step(*c.args(), **c.opts)
+    norm = ob.wtconv_grad_norm(c.grads, 1.0, stream=s)
+    c.run(stream=s)
+    s.synchronize()
+    want.check()
+    assert torch.equal(norm, ob.wtconv_grad_norm(c.grads, 1.0))
+
+
+@pytest.mark.parametrize("bits,random", STATES)
+def test_captured_and_replayed(bits, random):
+    """Norm and step in a graph: new gradients, counts, rates and random numbers are read at each replay."""
+    shapes = [(300,), (40, 41), (9000,)] + [(50,)] * 100
+    a, b = (Call(shapes, bits=bits, random=random, seed=14, t=0, lr_factor=1.0, factor=None) for _ in range(2))
+
+    def step(c):
+        norm = ob.wtconv_grad_norm(c.grads, 0.01, step=c.step)
+        ob.wtconv_adamw_step(*c.args(), **{**c.opts, "factor": norm[1:]})
+        return norm
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step(a)
+    torch.cuda.current_stream().wait_stream(s)
+    step(b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step(a)
+    for i in range(4):
+        for x, y in zip(a.grads, b.grads):
+            x.copy_(torch.randn(x.shape, device=DEV) * 1e-3)
+            y.copy_(x)
+        if i == 2:
+            a.grads[1][3, 4] = b.grads[1][3, 4] = float("inf")   # skipped
+        for c in (a, b):
+            c.opts["lr_factor"].fill_(0.5 ** i)
+            if random:
+                c.opts["rng"][1] += 1
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(torch.nan_to_num(held, 7), torch.nan_to_num(step(b), 7))
+        assert int(a.step) == int(b.step) == (2 + i if i < 2 else 1 + i)
+        assert all(torch.equal(x, y) for x, y in zip(a.bits(), b.bits()))
+
+
+# --------------------------------------------------------------- optimizer
+
+def net(dtype=F32, seed=0):
+    torch.manual_seed(seed)
+    return torch.nn.Sequential(torch.nn.Linear(13, 37), torch.nn.GELU(), torch.nn.Linear(37, 5)).to(DEV, dtype)
+
+
+def data(i, dtype=F32):
+    g = torch.Generator(DEV).manual_seed(100 + i)
+    return torch.randn(64, 13, generator=g, device=DEV).to(dtype), torch.randn(64, 5, generator=g, device=DEV).to(dtype)
+
+
+def gradients(model, i):
+    x, y = data(i, next(model.parameters()).dtype)
+    model.zero_grad()
+    ((model(x) - y) ** 2).mean().backward()
+
+
+def test_optimizer_follows_torch():
+    """The same updates as torch's own AdamW in 64 bits on the same gradients, two groups, clipped."""
+    a = net()
+    b = copy.deepcopy(a).double()
+    groups = lambda m: [dict(params=[m[0].weight, m[2].weight], weight_decay=0.1),  # noqa: E731
+                        dict(params=[m[0].bias, m[2].bias], weight_decay=0.0, lr=3e-3)]
+    mine = AdamW(groups(a), lr=1e-2, eps=1e-6, betas=(0.8, 0.95), max_norm=0.05)
+    other = torch.optim.AdamW(groups(b), lr=1e-2, eps=1e-6, betas=(0.8, 0.95))
+    for i in range(20):
+        gradients(a, i)
+        for p, q in zip(a.parameters(), b.parameters()):
+            q.grad = p.grad.double()
+        torch.nn.utils.clip_grad_norm_(list(b.parameters()), 0.05)
+        mine.step()
+        other.step()
+        for p, q in zip(a.parameters(), b.parameters()):
+            # a step adds a few half steps of the parameter and 30 of the update (below 5 rates)
+            assert (p.double() - q).abs().max() <= (i + 1) * U * (6 * q.abs().max() + 30 * 5e-2)
+    assert int(mine._step) == 20
+
+
+@pytest.mark.parametrize("dtype,master", [(F32, True), (BF16, True), (BF16, False)])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_optimizer_state_round_trip(dtype, master, bits):
+    """A run that is saved, loaded into a new optimizer and gone on with is the same run, bit for bit."""
+    a = net(dtype)
+    kw = dict(lr=1e-2, state_bits=bits, master=master, max_norm=1.0)
+    mine = AdamW(a.parameters(), **kw)
+    for i in range(3):
+        gradients(a, i)
+        mine.step()
+    b = copy.deepcopy(a)
+    saved = copy.deepcopy(mine.state_dict())
+    theirs = AdamW(b.parameters(), **{**kw, "lr": 1.0})
+    theirs.load_state_dict(saved)
+    assert theirs.param_groups[0]["lr"] == 1e-2
+    for i in range(3, 6):
+        for m, o in ((a, mine), (b, theirs)):
+            gradients(m, i)
+            o.step()
+        assert all(torch.equal(p, q) for p, q in zip(a.parameters(), b.parameters()))
+    with pytest.raises(ValueError):
+        AdamW(b.parameters(), **{**kw, "state_bits": 40 - bits}).load_state_dict(saved)
+    with pytest.raises(ValueError):
+        AdamW(list(b.parameters())[:2], **kw).load_state_dict(saved)
+
+
+def test_optimizer_skips_steps_that_are_not_finite():
+    a = net()
+    o = AdamW(a.parameters(), state_bits=8, max_norm=math.inf)
+    gradients(a, 0)
+    o.step()
+    old = [p.clone() for p in a.parameters()]
+    gradients(a, 1)
+    a[0].bias.grad[2] = float("nan")
+    o.step()
+    assert all(torch.equal(p, q) for p, q in zip(a.parameters(), old)) and int(o._step) == 1
+    assert math.isnan(float(o.last_norm[1]))
+    gradients(a, 1)
+    o.step()
+    assert int(o._step) == 2 and not torch.equal(a[0].bias, old[1])
+
+
+def test_optimizer_with_missing_and_strided_gradients():
+    a = net()
+    o = AdamW(a.parameters(), lr=0.1)
+    gradients(a, 0)
+    a[2].weight.grad = None
+    a[0].weight.grad = a[0].weight.grad.t().contiguous().t()   # another memory order
+    old = a[2].weight.clone()
+    b = copy.deepcopy(a)
+    b[0].weight.grad = a[0].weight.grad.contiguous()
+    b[0].bias.grad, b[2].bias.grad = a[0].bias.grad, a[2].bias.grad
+    o.step()
+    AdamW(b.parameters(), lr=0.1).step()
+    assert torch.equal(a[2].weight, old) and torch.equal(a[0].weight, b[0].weight)
+    with pytest.raises(RuntimeError):
+        o.add_param_group(dict(params=[torch.nn.Parameter(torch.zeros(3, device=DEV))]))
+
+
+def test_a_change_in_place_is_seen_by_autograd():
+    """A graph that needs the old parameter raises an error after the step."""
+    a = net()
+    o = AdamW(a.parameters())
+    gradients(a, 0)
+    x, _ = data(1)
+    y = a(x.requires_grad_())
+    o.step()
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.sum().backward()
+
+
+def test_refusals_on_the_gpu():
+    c = Call([(40,), (5, 7)])
+    p, g, m, v, t = c.args()
+    kw = dict(c.opts)
+
+    def call(p=p, g=g, m=m, v=v, t=t, **more):
+        ob.wtconv_adamw_step(p, g, m, v, t, **{**kw, **more})
+
+    big = torch.zeros(600, device=DEV)
+    bad = [dict(p=[]), dict(g=g[:1]), dict(p=[p[0], p[1].bfloat16()]), dict(g=[g[0], g[1].bfloat16()]),
+           dict(p=[p[0], p[1].double()], g=[g[0], g[1]]), dict(g=[g[0], g[1].t()]), dict(g=[g[0], g[1].reshape(7, 5)]),
+           dict(p=[p[0], p[1].t()], g=[g[0], g[1].t().contiguous()]), dict(g=[g[0], g[1].cpu()]), dict(p=[p[0], p[1].cpu()]),
+           dict(m=m[:256]), dict(m=m.double()), dict(v=big), dict(m=m.to(torch.float8_e4m3fn)), dict(t=None),
+           dict(t=t.int()), dict(t=torch.ones(2, dtype=torch.int64, device=DEV)), dict(scales=torch.zeros(2, 2, device=DEV)),
+           dict(master=m), dict(rng=torch.zeros(2, dtype=torch.int64, device=DEV)), dict(lr=[1e-3]), dict(lr=torch.ones(3)),
+           dict(weight_decay=torch.ones(2, device=DEV)), dict(factor=torch.ones(2, device=DEV)), dict(site=-1),
+           dict(factor=torch.ones(1, device=DEV).double()), dict(lr_factor=torch.ones(1)), dict(p=[p[0], "x"]), dict(site=1 << 31)]
+    for i, kws in enumerate(bad):
+        with pytest.raises(ValueError):
+            call(**kws)
+            pytest.fail(f"case {i}")
+    for kws in (dict(p=[p[0], p[0]], g=[g[0], g[0]], m=m, v=v), dict(lr=float("nan")), dict(eps=0.0), dict(betas=(1.0, 0.9)),
+                dict(v=m), dict(g=[p[0], g[1]])):
+        with pytest.raises(RuntimeError):   # the library's own checks
+            call(**kws)
+    for i, args in enumerate(([], [torch.zeros(3)], [torch.zeros(3, device=DEV, dtype=torch.float16)],
+                              [torch.zeros(4, 4, device=DEV).t()[:2]])):
+        with pytest.raises(ValueError):
+            ob.wtconv_grad_norm(args, 1.0)
+    for kws in (dict(max_norm=0.0), dict(max_norm=float("nan")), dict(step=torch.zeros(1, device=DEV)),
+                dict(out=torch.zeros(3, device=DEV))):
+        with pytest.raises(ValueError):
+            ob.wtconv_grad_norm(g, **kws)
+
+
+# ------------------------------------------------------ as they are used together
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_block_with_experts_is_trained(bits):
+    """Norm, experts, residual, backward pass, norm of the gradients and step: the gradients are those of the plain
+    64-bit form, the step is the definition's."""
+    B, H, W, C, E, K = 2, 5, 3, 24, 4, 2
+    g = torch.Generator(DEV).manual_seed(0)
+    p = {n: torch.nn.Parameter(0.3 * torch.randn(s, generator=g, device=DEV)) for n, s in
+         dict(router=(E, C), up=(E, 2 * C, C), down=(E, C, 2 * C), gate=(C,), weight=(C,), bias=(C,)).items()}
+    x = torch.randn(B, C, H, W, generator=g, device=DEV)
+    dy = torch.randn(B, C, H, W, generator=g, device=DEV)
+
+    def block(p, x, plain, expert=None):
+        if plain:
+            z = (x - x.mean(1, keepdim=True)) / (x.var(1, correction=0, keepdim=True) + 1e-6).sqrt()
+            u = (z * p["weight"].view(-1, 1, 1) + p["bias"].view(-1, 1, 1)).permute(0, 2, 3, 1)
+        else:
+            u = channel_norm(x, p["weight"], p["bias"], channels_last=True).permute(0, 2, 3, 1)
+        logits = u @ p["router"].t()
+        if expert is None:
+            expert = logits.topk(K, -1)[1]
+        w = torch.softmax(logits.gather(-1, expert), -1)
+        if plain:
+            # every expert on every row, and the chosen ones of them
+            each = torch.stack([torch.tanh(u @ p["up"][e].t()) @ p["down"][e].t() for e in range(E)], -2)
+            h = (each.gather(-2, expert.unsqueeze(-1).expand(*expert.shape, C)) * w.unsqueeze(-1)).sum(-2)
+            return x + p["gate"].view(-1, 1, 1) * h.permute(0, 3, 1, 2), expert
+        route = expert_sort(expert, E)
+        rows = expert_rows(u, route)
+        ends = route.offsets.tolist()
+        ys = torch.cat([torch.tanh(rows[a:b] @ p["up"][e].t()) @ p["down"][e].t()
+                        for e, (a, b) in enumerate(zip(ends, ends[1:]))])
+        h = expert_sum(ys, w, route).permute(0, 3, 1, 2)
+        return block_residual(x, h, gate=p["gate"]), expert
+
+    o = AdamW(p.values(), lr=1e-2, state_bits=bits, max_norm=1.0, rng=dropout_rng(3) if bits == 8 else None, site=50)
+    for i in range(4):
+        o.zero_grad()
+        y, expert = block(p, x, False)
+        y.backward(dy)
+        q = {n: t.detach().double().requires_grad_() for n, t in p.items()}
+        z, _ = block(q, x.double(), True, expert)
+        z.backward(dy.double())
+        assert (y.double() - z).abs().max() <= 1e-5 * z.abs().max()
+        for n in p:   # sums of hundreds of fp32 terms
+            assert (p[n].grad.double() - q[n].grad).abs().max() <= 2e-5 * q[n].grad.abs().max(), n
+        if i:
+            b = o._buffers[0]
+            factor = ob.wtconv_grad_norm([t.grad for t in p.values()], 1.0)[1:]
+            want = Step(list(p.values()), [t.grad for t in p.values()], b["m"], b["v"], int(o._step) + 1, lr=1e-2,
+                        weight_decay=1e-2, scales=b.get("scales"), factor=factor, rng=o.rng, site=50)
+            o.step()
+            want.check()
+        else:
+            o.step()
+        if o.rng is not None:
+            o.rng[1] += 1

@@ -25,8 +25,15 @@ _BLOCK_BINDING_NAMES = (
 _BLOCK_NAMES = ("ChannelNorm2d", "BlockResidual2d", "CounterDropout", "channel_norm", "block_residual",
                 "counter_dropout", "dropout_rng")
 
+# rows to their experts and back, and the optimizer's step over many tensors
+_EXPERT_BINDING_NAMES = ("wtconv_expert_sort", "wtconv_expert_rows_fwd", "wtconv_expert_rows_bwd",
+                         "wtconv_expert_sum_fwd", "wtconv_expert_sum_bwd")
+_EXPERT_NAMES = ("ExpertRoute", "expert_sort", "expert_rows", "expert_sum")
+_OPTIM_BINDING_NAMES = ("wtconv_adamw_step", "wtconv_adamw_state_count", "wtconv_grad_norm")
+_OPTIM_NAMES = ("AdamW",)
+
 __all__ = ["CONFIGS", "WorkloadConfig", "get_config", *_BINDING_NAMES, *_MODULE_NAMES, *_BLOCK_BINDING_NAMES,
-           *_BLOCK_NAMES]
+           *_BLOCK_NAMES, *_EXPERT_BINDING_NAMES, *_EXPERT_NAMES, *_OPTIM_BINDING_NAMES, *_OPTIM_NAMES]
 
 
 def __getattr__(name):
@@ -44,4 +51,16 @@ def __getattr__(name):
     if name in _BLOCK_NAMES:
         from . import block
         return getattr(block, name)
+    if name in _EXPERT_BINDING_NAMES:
+        from . import expert_binding
+        return getattr(expert_binding, name)
+    if name in _EXPERT_NAMES:
+        from . import experts
+        return getattr(experts, name)
+    if name in _OPTIM_BINDING_NAMES:
+        from . import optim_binding
+        return getattr(optim_binding, name)
+    if name in _OPTIM_NAMES:
+        from . import optim
+        return getattr(optim, name)
     raise AttributeError(name)

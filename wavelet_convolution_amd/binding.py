@@ -45,6 +45,17 @@ class WTConvBlockDesc(ctypes.Structure):
                 ("site", ctypes.c_int32)]
 
 
+class WTConvExpertDesc(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("k", ctypes.c_int32), ("experts", ctypes.c_int32), ("c", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class WTConvAdamWDesc(ctypes.Structure):
+    _fields_ = [("p_dtype", ctypes.c_int32), ("g_dtype", ctypes.c_int32), ("state_bits", ctypes.c_int32),
+                ("site", ctypes.c_int32), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double)]
+
+
 _V = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _P = ctypes.POINTER(WTConvDesc)
@@ -95,6 +106,23 @@ def load_library() -> ctypes.CDLL:
                 fn = getattr(lib, name)
                 fn.argtypes = [_PB] + [_V] * n + [_SZ, _V]
                 fn.restype = ctypes.c_int
+            _PE = ctypes.POINTER(WTConvExpertDesc)
+            lib.wtconv_expert_workspace_size.argtypes = [_PE]
+            lib.wtconv_expert_workspace_size.restype = _SZ
+            lib.wtconv_expert_sort.argtypes = [_PE, _V, ctypes.c_int32, _V, _V, _V, _V, _SZ, _V]
+            lib.wtconv_expert_sort.restype = ctypes.c_int
+            for name, n in (("rows_fwd", 5), ("rows_bwd", 5), ("sum_fwd", 6), ("sum_bwd", 8)):
+                fn = getattr(lib, "wtconv_expert_" + name)
+                fn.argtypes = [_PE] + [_V] * n
+                fn.restype = ctypes.c_int
+            lib.wtconv_adamw_state_count.argtypes = [_V, ctypes.c_int32]
+            lib.wtconv_adamw_state_count.restype = ctypes.c_int64
+            lib.wtconv_adamw_step.argtypes = [ctypes.POINTER(WTConvAdamWDesc), ctypes.c_int32] + [_V] * 14
+            lib.wtconv_adamw_step.restype = ctypes.c_int
+            lib.wtconv_grad_norm_workspace_size.argtypes = [ctypes.c_int32]
+            lib.wtconv_grad_norm_workspace_size.restype = _SZ
+            lib.wtconv_grad_norm.argtypes = [ctypes.c_int32, _V, _V, _V, ctypes.c_double, _V, _V, _V, _SZ, _V]
+            lib.wtconv_grad_norm.restype = ctypes.c_int
             lib.wtconv_status_string.argtypes = [ctypes.c_int]
             lib.wtconv_status_string.restype = ctypes.c_char_p
             lib.wtconv_version.restype = ctypes.c_char_p

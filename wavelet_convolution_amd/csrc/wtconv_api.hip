@@ -489,6 +489,6 @@ const char* wtconv_status_string(wtconv_status_t s) {
     }
 }
 
-const char* wtconv_version(void) { return "0.4.0"; }
+const char* wtconv_version(void) { return "0.5.0"; }
 
 }  // extern "C"

@@ -8,12 +8,15 @@
 
 #include "../../include/wtconv.h"
 #include "wtconv_block.h"
+#include "wtconv_buffers.h"
 
 namespace {
 
-bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+using wtc::aligned;
+using wtc::buffers_ok;
+using wtc::done;
+using wtc::elem_bytes;
 
-size_t elem_bytes(int dtype) { return dtype == WTCONV_BF16 ? 2 : 4; }
 size_t act_count(const wtconv_block_desc_t* d) { return (size_t)d->B * d->C * d->H * d->W; }
 
 wtconv_status_t check_desc(const wtconv_block_desc_t* d) {
@@ -68,31 +71,6 @@ wtc::BlockArgs args_of(const wtconv_block_desc_t* d) {
     return a;
 }
 
-struct Buf {
-    const void* p;
-    size_t bytes, align;
-};
-
-// No output overlaps an input or another output; everything is aligned to
-// its element type. Absent buffers are null.
-template <int NI, int NO>
-bool buffers_ok(const Buf (&in)[NI], const Buf (&out)[NO]) {
-    auto hit = [](const Buf& a, const Buf& b) {
-        const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
-        return a.p && b.p && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
-    };
-    for (const Buf& b : in)
-        if (!aligned(b.p, b.align)) return false;
-    for (int i = 0; i < NO; ++i) {
-        if (!aligned(out[i].p, out[i].align)) return false;
-        for (const Buf& b : in)
-            if (hit(out[i], b)) return false;
-        for (int j = 0; j < i; ++j)
-            if (hit(out[i], out[j])) return false;
-    }
-    return true;
-}
-
 // Everything that a backward call could be asked for: the workspace holds
 // the sums of all of them.
 size_t workspace(const wtconv_block_desc_t* d) {
@@ -108,8 +86,6 @@ bool ws_ok(const wtconv_block_desc_t* d, const void* ws, size_t ws_bytes) {
     const size_t need = workspace(d);
     return need == 0 || (ws && aligned(ws, 256) && ws_bytes >= need);
 }
-
-wtconv_status_t done(hipError_t err) { return err == hipSuccess ? WTCONV_OK : WTCONV_ERR_LAUNCH; }
 
 }  // namespace
 

@@ -1,0 +1,249 @@
+// Rows to their experts and back. Every kernel goes by rows n: what a row has
+// in [N][C] is read or written once, and its K rows among the sorted ones are
+// reached through place[n][k] (4 bytes a slot against 2 C), whichever side is
+// read. Memory is the bound in each.
+#include "wtconv_block_device.h"
+#include "wtconv_experts.h"
+
+namespace wtc {
+namespace {
+
+constexpr int T = 256;
+
+// A slot's row among the sorted ones: whether there is one (a place that is no
+// place would be out of bounds), and whether it belongs to an expert.
+struct Slot {
+    uint32_t at;
+    bool is, live;
+};
+__device__ __forceinline__ Slot slot_of(uint32_t at, uint32_t S, uint32_t kept) {
+    return {at, at < S, at < S && at < kept};
+}
+__device__ __forceinline__ uint32_t kept_of(const ExpertArgs& a) {
+    const int n = a.offsets[a.E];
+    return n > 0 ? (uint32_t)n : 0u;
+}
+
+// A thread takes eight channels of a row (one vector; where C is no multiple
+// of eight the last one moves back to end with the row and stores its
+// neighbour's values once more), and KK slots at a time, whose reads are in
+// flight together.
+template <typename X, int OP, int KK, bool PART>
+__device__ __forceinline__ void expert_move_wg(const ExpertArgs& a, uint32_t G, uint64_t wg, uint32_t S, uint32_t kept) {
+    const uint64_t first = wg * T, row0 = first / G;   // scalar
+    const uint32_t t = (uint32_t)(first - row0 * G) + threadIdx.x, down = t / G;
+    const uint64_t row = row0 + down;
+    if (row >= (uint64_t)a.N) return;
+    const uint32_t c = PART ? 0 : min((t - down * G) * CG, (uint32_t)a.C - CG);
+    const int* place = a.place + row * a.K;
+    const float* w = a.w + row * a.K;
+    auto load = [&](Vec<X, CG>& v, const X* p) {
+        if constexpr (PART)
+            v.load_part(p, a.C);
+        else
+            v.load(p + c);
+    };
+    auto store = [&](X* p, const float (&v)[CG]) {
+        if constexpr (PART)
+            store_part<X, CG>(p, v, a.C);
+        else
+            store_vec<X, CG>(p + c, v);
+    };
+    Vec<X, CG> x;
+    float sum[CG] = {};
+    if constexpr (OP == ROWS_FWD) load(x, (const X*)a.rows + row * a.C);
+    for (int k = 0; k < a.K; k += KK) {
+        Slot s[KK];
+        Vec<X, CG> q[KK];
+        float f[KK];
+#pragma unroll
+        for (int i = 0; i < KK; ++i) s[i] = slot_of(k + i < a.K ? (uint32_t)place[k + i] : ~0u, S, kept);
+        if constexpr (OP == ROWS_FWD) {
+#pragma unroll
+            for (int i = 0; i < KK; ++i) {
+                float o[CG];
+#pragma unroll
+                for (int j = 0; j < CG; ++j) o[j] = s[i].live ? x[j] : 0.f;
+                if (s[i].is) store((X*)a.to_sorted + (size_t)s[i].at * a.C, o);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < KK; ++i) {
+                q[i].zero();
+                f[i] = 1.f;
+                if (s[i].live) {
+                    load(q[i], (const X*)a.sorted + (size_t)s[i].at * a.C);
+                    if constexpr (OP == SUM_FWD) f[i] = w[k + i];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < KK; ++i)
+#pragma unroll
+                for (int j = 0; j < CG; ++j) sum[j] = fmaf(f[i], q[i][j], sum[j]);
+        }
+    }
+    if constexpr (OP != ROWS_FWD) store((X*)a.to_rows + row * a.C, sum);
+}
+
+template <typename X, int OP, int KK, bool PART>
+__global__ __launch_bounds__(T) void k_expert_move(ExpertArgs a, uint32_t G, uint64_t wgs) {
+    const uint32_t S = (uint32_t)(a.N * a.K), kept = kept_of(a);
+    for (uint64_t wg = blockIdx.x; wg < wgs; wg += gridDim.x) expert_move_wg<X, OP, KK, PART>(a, G, wg, S, kept);
+}
+
+// A grid of at most 2^31 lanes takes any number of pieces.
+unsigned grid_of(uint64_t wgs) { return (unsigned)(wgs < 1u << 23 ? wgs : 1u << 23); }
+
+template <typename X, int OP, int KK>
+hipError_t move_launch(const ExpertArgs& a, hipStream_t s) {
+    const uint32_t G = (uint32_t)cdiv(a.C, CG);
+    const uint64_t wgs = ((uint64_t)a.N * G + T - 1) / T;
+    if (a.C < CG)
+        hipLaunchKernelGGL((k_expert_move<X, OP, KK, true>), dim3(grid_of(wgs)), dim3(T), 0, s, a, G, wgs);
+    else
+        hipLaunchKernelGGL((k_expert_move<X, OP, KK, false>), dim3(grid_of(wgs)), dim3(T), 0, s, a, G, wgs);
+    return hipGetLastError();
+}
+
+template <typename X, int OP>
+hipError_t move_by_k(const ExpertArgs& a, hipStream_t s) {
+    if (a.K == 1) return move_launch<X, OP, 1>(a, s);
+    if (a.K == 2) return move_launch<X, OP, 2>(a, s);
+    return move_launch<X, OP, 4>(a, s);
+}
+
+template <typename X>
+hipError_t move_by_op(const ExpertArgs& a, int op, hipStream_t s) {
+    if (op == ROWS_FWD) return move_by_k<X, ROWS_FWD>(a, s);
+    if (op == ROWS_BWD) return move_by_k<X, ROWS_BWD>(a, s);
+    return move_by_k<X, SUM_FWD>(a, s);
+}
+
+// The sum's gradients: L lanes hold a row, UN vectors of it at a time, read dy
+// once and each of its K rows of ys, write w dy in their places, and sum up
+// <dy, ys>, of which a vector that moved back counts the channels of its own.
+constexpr int UN = 3;
+template <typename X, int L, int KK, bool PART>
+__device__ __forceinline__ void expert_sum_bwd_wg(const ExpertArgs& a, uint32_t G, uint64_t wg, uint32_t S,
+                                                  uint32_t kept) {
+    const uint64_t row = (wg * T + threadIdx.x) / L;
+    const uint32_t lane = threadIdx.x % L;
+    const bool in = row < (uint64_t)a.N;
+    const X* dy = (const X*)a.rows + row * a.C;
+    const int* place = a.place + row * a.K;
+    for (int k = 0; k < a.K; k += KK) {
+        Slot s[KK];
+        float w[KK], dot[KK];
+#pragma unroll
+        for (int i = 0; i < KK; ++i) {
+            s[i] = slot_of(in && k + i < a.K ? (uint32_t)place[k + i] : ~0u, S, kept);
+            w[i] = s[i].live && a.to_sorted ? a.w[row * a.K + k + i] : 0.f;
+            dot[i] = 0.f;
+        }
+        for (uint32_t v0 = lane; v0 < G; v0 += UN * L) {
+            Vec<X, CG> d[UN], y[UN][KK];
+            uint32_t c[UN], shared[UN];
+#pragma unroll
+            for (int u = 0; u < UN; ++u) {
+                const uint32_t first = (v0 + u * L) * CG;
+                const bool on = in && first < (uint32_t)a.C;
+                c[u] = PART ? 0 : min(first, (uint32_t)a.C - CG);
+                shared[u] = on ? first - c[u] : CG;   // off: counts nothing
+                d[u].zero();
+                if (on) {
+                    if constexpr (PART)
+                        d[u].load_part(dy, a.C);
+                    else
+                        d[u].load(dy + c[u]);
+                }
+#pragma unroll
+                for (int i = 0; i < KK; ++i) {
+                    y[u][i].zero();
+                    if (on && s[i].live && a.dw) {
+                        const X* ys = (const X*)a.sorted + (size_t)s[i].at * a.C;
+                        if constexpr (PART)
+                            y[u][i].load_part(ys, a.C);
+                        else
+                            y[u][i].load(ys + c[u]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < UN; ++u) {
+#pragma unroll
+                for (int i = 0; i < KK; ++i) {
+                    float o[CG];
+#pragma unroll
+                    for (int j = 0; j < CG; ++j) {
+                        o[j] = s[i].live ? w[i] * d[u][j] : 0.f;
+                        dot[i] = fmaf(d[u][j], (uint32_t)j < shared[u] || !s[i].live ? 0.f : y[u][i][j], dot[i]);
+                    }
+                    if (shared[u] < CG && s[i].is && a.to_sorted) {
+                        X* out = (X*)a.to_sorted + (size_t)s[i].at * a.C;
+                        if constexpr (PART)
+                            store_part<X, CG>(out, o, a.C);
+                        else
+                            store_vec<X, CG>(out + c[u], o);
+                    }
+                }
+            }
+        }
+        if (a.dw) {
+#pragma unroll
+            for (int i = 0; i < KK; ++i) {
+                const float sum = lane_sum<L>(dot[i]);
+                if (lane == 0 && in && k + i < a.K) a.dw[row * a.K + k + i] = sum;
+            }
+        }
+    }
+}
+
+template <typename X, int L, int KK, bool PART>
+__global__ __launch_bounds__(T) void k_expert_sum_bwd(ExpertArgs a, uint32_t G, uint64_t wgs) {
+    const uint32_t S = (uint32_t)(a.N * a.K), kept = kept_of(a);
+    for (uint64_t wg = blockIdx.x; wg < wgs; wg += gridDim.x) expert_sum_bwd_wg<X, L, KK, PART>(a, G, wg, S, kept);
+}
+
+template <typename X, int L, int KK>
+hipError_t sum_bwd_launch(const ExpertArgs& a, hipStream_t s) {
+    const uint32_t G = (uint32_t)cdiv(a.C, CG);
+    const uint64_t wgs = ((uint64_t)a.N * L + T - 1) / T;
+    if constexpr (L == 4) {
+        if (a.C < CG) {
+            hipLaunchKernelGGL((k_expert_sum_bwd<X, L, KK, true>), dim3(grid_of(wgs)), dim3(T), 0, s, a, G, wgs);
+            return hipGetLastError();
+        }
+    }
+    hipLaunchKernelGGL((k_expert_sum_bwd<X, L, KK, false>), dim3(grid_of(wgs)), dim3(T), 0, s, a, G, wgs);
+    return hipGetLastError();
+}
+
+// The fewest lanes that hold a row in one round of UN vectors each.
+template <typename X, int KK>
+hipError_t sum_bwd_by_row(const ExpertArgs& a, hipStream_t s) {
+    const int G = cdiv(a.C, CG);
+    if (G <= 4 * UN) return sum_bwd_launch<X, 4, KK>(a, s);
+    if (G <= 8 * UN) return sum_bwd_launch<X, 8, KK>(a, s);
+    if (G <= 16 * UN) return sum_bwd_launch<X, 16, KK>(a, s);
+    if (G <= 32 * UN) return sum_bwd_launch<X, 32, KK>(a, s);
+    return sum_bwd_launch<X, 64, KK>(a, s);
+}
+
+template <typename X>
+hipError_t sum_bwd_by_k(const ExpertArgs& a, hipStream_t s) {
+    if (a.K == 1) return sum_bwd_by_row<X, 1>(a, s);
+    if (a.K == 2) return sum_bwd_by_row<X, 2>(a, s);
+    return sum_bwd_by_row<X, 4>(a, s);
+}
+
+}  // namespace
+
+hipError_t expert_move(const ExpertArgs& a, int op, int bf16, hipStream_t s) {
+    return bf16 ? move_by_op<bf16_t>(a, op, s) : move_by_op<float>(a, op, s);
+}
+
+hipError_t expert_sum_bwd(const ExpertArgs& a, int bf16, hipStream_t s) {
+    return bf16 ? sum_bwd_by_k<bf16_t>(a, s) : sum_bwd_by_k<float>(a, s);
+}
+
+}  // namespace wtc

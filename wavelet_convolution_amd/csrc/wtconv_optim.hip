@@ -1,0 +1,304 @@
+// AdamW and the gradients' norm over many tensors. Memory is the bound: every
+// element of a parameter, its gradient and its states is read once and
+// written once.
+#include "wtconv_block_device.h"
+#include "wtconv_optim.h"
+
+namespace wtc {
+namespace {
+
+constexpr int T = 256;
+
+// The tensor of a workgroup: the last one whose first workgroup is not behind
+// it. All lanes look at a first workgroup each, and a ballot counts.
+template <class A>
+__device__ __forceinline__ int tensor_of(const A& a, uint32_t wg) {
+    const int lane = threadIdx.x % 64;
+    int n = 0;
+    for (int i = 0; i < a.n; i += 64) n += (int)__popcll(__ballot(i + lane < a.n && a.t[min(i + lane, a.n - 1)].wg <= wg));
+    return __builtin_amdgcn_readfirstlane(n - 1);
+}
+
+// Largest of 64 lanes, for values that are not negative: as whole numbers,
+// where a NaN is the largest.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0u, v, CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float wave_max(float f) {
+    uint32_t v = __float_as_uint(f);
+    v = dpp_max<0xB1>(v);
+    v = dpp_max<0x4E>(v);
+    v = dpp_max<0x141>(v);
+    v = dpp_max<0x140>(v);
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = max(r[0], r[1]);
+    const auto q = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return __uint_as_float(max(q[0], q[1]));
+}
+
+// Four e4m3 numbers from |q| <= 448 (a little more by rounding), to nearest.
+__device__ __forceinline__ uint32_t e4m3_near(const float (&q)[4]) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true);
+}
+// One, up or down by 16 bits u. Times 2^-120 a float has e4m3's exponent (its
+// subnormals too) and 20 bits more of fraction: the carry of the random bits
+// out of those 20 rounds up.
+__device__ __forceinline__ uint32_t e4m3_random(float q, uint32_t u) {
+    float f = fabsf(q);
+    f = f > 448.f ? 448.f : f;   // a NaN stays
+    const uint32_t code = min((__float_as_uint(f * 0x1p-120f) + (u << 4) + 8) >> 20, 0x7fu);
+    return code | (__float_as_uint(q) >> 24 & 0x80u);
+}
+__device__ __forceinline__ void widen_e4m3(uint32_t w, float unit, float (&o)[4]) {
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+    o[0] = lo[0] * unit;
+    o[1] = lo[1] * unit;
+    o[2] = hi[0] * unit;
+    o[3] = hi[1] * unit;
+}
+
+// A lane takes four consecutive elements, a wavefront a block of 256 at a
+// time, UN of them in flight.
+constexpr int UN = 2;
+
+template <typename P, typename G, bool MASTER, int MODE>
+__global__ __launch_bounds__(T) void k_adamw(AdamArgs a) {
+    const float f = a.factor ? *a.factor : 1.f;
+    if (!(fabsf(f) < INFINITY)) return;
+    const AdamTensor& t = a.t[tensor_of(a, blockIdx.x)];
+    const uint64_t count = t.count, piece = (uint64_t)(blockIdx.x - t.wg) * ADAM_PIECE;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+    // 1 - beta^t as -(e^(t log beta) - 1): no difference of near numbers
+    const float steps = (float)max(1ll, *a.step), c1 = -expm1f(steps * a.log1), c2 = -expm1f(steps * a.log2);
+    const float lr = a.lr_factor ? t.lr * *a.lr_factor : t.lr;
+    const float decay = 1.f - lr * t.wd, rate = lr / c1, root_scale = 1.f / sqrtf(c2);
+    for (uint32_t b0 = wave; b0 < ADAM_PIECE / OB; b0 += UN * T / 64) {
+        Vec<P, 4> pv[UN];
+        Vec<float, 4> xv[UN], mv[UN], vv[UN];
+        Vec<G, 4> gv[UN];
+        uint32_t m8[UN], v8[UN];
+        float2 unit[UN];
+        uint64_t e[UN];
+        size_t s[UN];
+        int n[UN];
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            const uint64_t first = piece + (uint64_t)(b0 + u * T / 64) * OB;
+            e[u] = first + 4 * lane;
+            n[u] = e[u] >= count ? 0 : count - e[u] < 4 ? (int)(count - e[u]) : 4;
+            const size_t block = t.block + first / OB;
+            s[u] = block * OB + 4 * lane;
+            if (n[u] == 4) {
+                gv[u].load((const G*)t.g + e[u]);
+                if constexpr (!MASTER) pv[u].load((const P*)t.p + e[u]);
+            } else {
+                gv[u].load_part((const G*)t.g + e[u], n[u]);
+                if constexpr (!MASTER) pv[u].load_part((const P*)t.p + e[u], n[u]);
+            }
+            const bool in = first < count;   // the whole block is there
+            m8[u] = v8[u] = 0;
+            unit[u] = make_float2(0.f, 0.f);
+            mv[u].zero();
+            vv[u].zero();
+            xv[u].zero();
+            if (in) {
+                if constexpr (MASTER) xv[u].load(a.master + s[u]);
+                if constexpr (MODE == STATES_32) {
+                    mv[u].load((const float*)a.m + s[u]);
+                    vv[u].load((const float*)a.v + s[u]);
+                } else {
+                    m8[u] = *(const uint32_t*)((const char*)a.m + s[u]);
+                    v8[u] = *(const uint32_t*)((const char*)a.v + s[u]);
+                    unit[u] = ((const float2*)a.scales)[block];
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            if (e[u] - 4 * lane >= count) continue;   // the wavefront's
+            float m[4], v[4], x[4], root[4];
+            if constexpr (MODE == STATES_32) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) m[i] = mv[u][i], v[i] = vv[u][i];
+            } else {
+                widen_e4m3(m8[u], unit[u].x, m);
+                widen_e4m3(v8[u], unit[u].y, v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[i] *= v[i];
+                    if (i >= n[u]) m[i] = v[i] = 0.f;   // past the tensor's end
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float g = gv[u][i] * f;
+                if constexpr (MASTER)
+                    x[i] = xv[u][i];
+                else
+                    x[i] = pv[u][i];
+                m[i] = fmaf(a.b1, m[i], a.a1 * g);
+                v[i] = fmaf(a.b2, v[i], a.a2 * g * g);
+                root[i] = sqrtf(v[i]);
+                x[i] = fmaf(-rate * m[i], __builtin_amdgcn_rcpf(fmaf(root[i], root_scale, a.eps)), x[i] * decay);
+            }
+            if (n[u] == 4) {
+                store_vec<P, 4>((P*)t.p + e[u], x);
+                if constexpr (MASTER) store_vec<float, 4>(a.master + s[u], x);
+            } else {
+                store_part<P, 4>((P*)t.p + e[u], x, n[u]);
+                if constexpr (MASTER) store_part<float, 4>(a.master + s[u], x, n[u]);
+            }
+            if constexpr (MODE == STATES_32) {
+                if (n[u] == 4) {
+                    store_vec<float, 4>((float*)a.m + s[u], m);
+                    store_vec<float, 4>((float*)a.v + s[u], v);
+                } else {
+                    store_part<float, 4>((float*)a.m + s[u], m, n[u]);
+                    store_part<float, 4>((float*)a.v + s[u], v, n[u]);
+                }
+            } else {
+                float top = 0.f, most = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // as whole numbers, as in the wavefront's
+                    top = __uint_as_float(max(__float_as_uint(top), __float_as_uint(fabsf(m[i]))));
+                    most = __uint_as_float(max(__float_as_uint(most), __float_as_uint(root[i])));
+                }
+                top = wave_max(top);
+                most = wave_max(most);
+                // a moment below 2^-100 is none; a root is above 2^-75 or zero
+                const float per_m = top < 0x1p-100f ? 0.f : 448.f / top, per_v = most > 0.f ? 448.f / most : most;
+                float q[4], r[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    q[i] = m[i] * per_m;
+                    r[i] = root[i] * per_v;
+                    if (root[i] > 0.f) r[i] = r[i] < 0x1p-9f ? 0x1p-9f : r[i];
+                }
+                uint32_t cm, cv;
+                if constexpr (MODE == STATES_8) {
+                    cm = e4m3_near(q);
+                    cv = e4m3_near(r);
+                } else {
+                    const uint4 bits = Philox(a.rng, t.site)((uint32_t)(e[u] / 4));
+                    const uint32_t w[4] = {bits.x, bits.y, bits.z, bits.w};
+                    cm = cv = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        cm |= e4m3_random(q[i], w[i] & 0xffffu) << (8 * i);
+                        cv |= e4m3_random(r[i], w[i] >> 16) << (8 * i);
+                    }
+                }
+                *(uint32_t*)((char*)a.m + s[u]) = cm;
+                *(uint32_t*)((char*)a.v + s[u]) = cv;
+                if (lane == 0)
+                    ((float2*)a.scales)[s[u] / OB] = make_float2(top < 0x1p-100f ? 0.f : top * (1.f / 448.f),
+                                                                 most * (1.f / 448.f));
+            }
+        }
+    }
+}
+
+template <typename P, typename G, bool MASTER>
+hipError_t adamw_by_mode(const AdamArgs& a, uint32_t wgs, int mode, hipStream_t s) {
+    if (mode == STATES_32)
+        hipLaunchKernelGGL((k_adamw<P, G, MASTER, STATES_32>), dim3(wgs), dim3(T), 0, s, a);
+    else if (mode == STATES_8)
+        hipLaunchKernelGGL((k_adamw<P, G, MASTER, STATES_8>), dim3(wgs), dim3(T), 0, s, a);
+    else
+        hipLaunchKernelGGL((k_adamw<P, G, MASTER, STATES_8_RANDOM>), dim3(wgs), dim3(T), 0, s, a);
+    return hipGetLastError();
+}
+template <typename G>
+hipError_t adamw_by_param(const AdamArgs& a, uint32_t wgs, int p_bf16, int mode, hipStream_t s) {
+    if (!p_bf16) return adamw_by_mode<float, G, false>(a, wgs, mode, s);
+    return a.master ? adamw_by_mode<bf16_t, G, true>(a, wgs, mode, s) : adamw_by_mode<bf16_t, G, false>(a, wgs, mode, s);
+}
+
+// Squares are summed in 64 bits: in 32 those of gradients above 2^64 or below
+// 2^-75 would be lost. A widening and a product of 64 bits an element are a
+// quarter of the time that memory takes for bf16.
+template <typename G>
+__device__ __forceinline__ double squares(const G* __restrict__ g, uint64_t n) {
+    constexpr int N = 8, UV = 4;
+    double sum[2] = {0., 0.};
+    const uint64_t vecs = n / N;
+    uint64_t i = threadIdx.x;
+    for (; i + (UV - 1) * T < vecs; i += UV * T) {
+        Vec<G, N> v[UV];
+#pragma unroll
+        for (int u = 0; u < UV; ++u) v[u].load(g + (i + u * T) * N);
+#pragma unroll
+        for (int u = 0; u < UV; ++u)
+#pragma unroll
+            for (int k = 0; k < N; ++k) sum[k % 2] = fma((double)v[u][k], (double)v[u][k], sum[k % 2]);
+    }
+    for (; i < vecs; i += T) {
+        Vec<G, N> v;
+        v.load(g + i * N);
+#pragma unroll
+        for (int k = 0; k < N; ++k) sum[k % 2] = fma((double)v[k], (double)v[k], sum[k % 2]);
+    }
+    if (const uint64_t k = vecs * N + threadIdx.x; k < n) {
+        const double x = widen(g[k]);
+        sum[0] = fma(x, x, sum[0]);
+    }
+    return sum[0] + sum[1];
+}
+
+// Sum over a workgroup of N lanes in a fixed order, in lane 0.
+template <int N>
+__device__ __forceinline__ double wg_sum(double v) {
+    __shared__ double part[N / 64];
+#pragma unroll
+    for (int d = 32; d >= 1; d /= 2) v += __shfl_xor(v, d);
+    if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = v;
+    __syncthreads();
+    v = 0.;
+    if (threadIdx.x == 0)
+        for (int w = 0; w < N / 64; ++w) v += part[w];
+    return v;
+}
+
+__global__ __launch_bounds__(T) void k_norm(NormArgs a) {
+    const NormTensor& t = a.t[tensor_of(a, blockIdx.x)];
+    const uint64_t at = (uint64_t)(blockIdx.x - t.wg) * a.piece, n = min(a.piece, t.count - at);
+    const double sum = wg_sum<T>(t.bf16 ? squares((const bf16_t*)t.g + at, n) : squares((const float*)t.g + at, n));
+    if (threadIdx.x == 0) a.sums[blockIdx.x] = sum;
+}
+
+constexpr int TF = 1024;
+__global__ __launch_bounds__(TF) void k_norm_finish(const double* sums, uint32_t n, double max_norm, long long* step,
+                                                    float* out) {
+    double sum = 0.;
+#pragma unroll 4
+    for (uint32_t i = threadIdx.x; i < n; i += TF) sum += sums[i];
+    sum = wg_sum<TF>(sum);
+    if (threadIdx.x == 0) {
+        const double norm = sqrt(sum);
+        const bool finite = norm < (double)INFINITY;
+        out[0] = (float)norm;
+        out[1] = finite ? (float)fmin(1., max_norm / (norm + 1e-6)) : NAN;
+        if (step && finite) ++*step;
+    }
+}
+
+}  // namespace
+
+hipError_t adamw_launch(const AdamArgs& a, uint32_t wgs, int p_bf16, int g_bf16, int mode, hipStream_t s) {
+    return g_bf16 ? adamw_by_param<bf16_t>(a, wgs, p_bf16, mode, s) : adamw_by_param<float>(a, wgs, p_bf16, mode, s);
+}
+
+hipError_t norm_launch(const NormArgs& a, uint32_t wgs, hipStream_t s) {
+    hipLaunchKernelGGL(k_norm, dim3(wgs), dim3(T), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t norm_finish(const double* sums, uint32_t n, double max_norm, long long* step, float* out, hipStream_t s) {
+    hipLaunchKernelGGL(k_norm_finish, dim3(1), dim3(TF), 0, s, sums, n, max_norm, step, out);
+    return hipGetLastError();
+}
+
+}  // namespace wtc

@@ -1,0 +1,154 @@
+"""AdamW for PyTorch over the C-ABI entry points: every parameter of a group in
+one call, states in 32 or in 8 bits, the gradients' clipping and the step's
+number on the GPU.
+
+    optim = AdamW(model.parameters(), lr=1e-3, weight_decay=0.05, state_bits=8, max_norm=1.0)
+    loss.backward()
+    optim.step()
+
+The update is that of torch.optim.AdamW with the bias corrections of one step
+count for all parameters. Parameters are fp32, or bf16 with fp32 master copies
+(master=False: without). Tensors must be on the GPU: there is no CPU path.
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+from . import optim_binding as _ob
+
+
+class AdamW(torch.optim.Optimizer):
+    """Parameter groups may set lr, betas, eps and weight_decay of their own.
+
+    state_bits: 32 or 8 (a block of 256 elements shares a scale; the first
+    moment and the second one's root are e4m3 numbers). rng: an int64
+    {seed, offset} on the GPU (`dropout_rng`), for stochastic rounding of 8-bit
+    states; parameter i (counted over all groups) uses the generator's site
+    `site + i`, and the caller changes the offset once per step. max_norm:
+    gradients are scaled down to this norm over all of them, and a step whose
+    gradients are not finite changes nothing and is not counted (inf: no
+    clipping, but such steps are skipped; None: neither, and no norm is
+    computed). `last_norm` is the last step's {norm, factor} on the GPU.
+
+    The states of a group's parameters stand in one buffer each. A parameter
+    without a gradient is left as it is in that step. step() makes no copy to
+    the host and waits for nothing, so it can be captured into a graph after a
+    first step (a graph keeps lr and the other numbers of its capture, but for
+    `lr_factor`, an optional fp32 number on the GPU that lr is multiplied by).
+    A group's states are made at its first step."""
+
+    def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 1e-2,
+                 state_bits: int = 32, master: bool = True, max_norm=None, rng=None, site: int = 0, lr_factor=None):
+        if not (0 <= lr < math.inf and 0 <= weight_decay < math.inf and eps > 0
+                and all(0 <= b < 1 for b in betas) and state_bits in (8, 32)):
+            raise ValueError("lr >= 0, weight_decay >= 0, eps > 0, betas in [0, 1) and state_bits 8 or 32 are required")
+        if max_norm is not None and not max_norm > 0:
+            raise ValueError(f"max_norm must be above 0, or None; got {max_norm}")
+        if rng is not None and state_bits != 8:
+            raise ValueError("rng is for states in 8 bits")
+        self.state_bits, self.master, self.max_norm = state_bits, master, max_norm
+        self.rng, self.site, self.lr_factor = rng, site, lr_factor
+        self.last_norm = self._step = None
+        self._buffers = []   # of each group: None, or a dict of its states
+        super().__init__(params, dict(lr=lr, betas=tuple(betas), eps=eps, weight_decay=weight_decay))
+
+    def __getstate__(self):
+        own = ("state_bits", "master", "max_norm", "rng", "site", "lr_factor", "last_norm", "_step", "_buffers")
+        return {**super().__getstate__(), **{k: self.__dict__[k] for k in own}}
+
+    def add_param_group(self, group):
+        if self._step is not None:
+            raise RuntimeError("parameter groups are added before the first step: all share its count")
+        super().add_param_group(group)
+        params = self.param_groups[-1]["params"]
+        first = self.param_groups[0]["params"][0]
+        if any(p.dtype not in (torch.float32, torch.bfloat16) or p.dtype != params[0].dtype for p in params):
+            self.param_groups.pop()
+            raise ValueError("the parameters of a group must be all float32 or all bfloat16")
+        if any(p.device != first.device for p in params):
+            self.param_groups.pop()
+            raise ValueError("all parameters must be on one device")
+        self._buffers.append(None)
+
+    def _make(self, params) -> dict:
+        n, dev = _ob.wtconv_adamw_state_count(params), params[0].device
+        eight = self.state_bits == 8
+        kind = torch.float8_e4m3fn if eight else torch.float32
+        b = {"m": torch.zeros(n, dtype=kind, device=dev), "v": torch.zeros(n, dtype=kind, device=dev)}
+        if eight:
+            b["scales"] = torch.zeros(n // _ob.BLOCK, 2, device=dev)
+        if self.master and params[0].dtype == torch.bfloat16:
+            b["master"] = torch.zeros(n, device=dev)
+            for p, (at, count) in zip(params, _places(params)):
+                b["master"][at:at + count].copy_(p.detach().reshape(-1))
+        return b
+
+    @torch.no_grad()
+    def step(self, closure=None):
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        groups = [(g, [p.grad if p.grad is None else p.grad.contiguous() for p in g["params"]])
+                  for g in self.param_groups]
+        grads = [t for _, ts in groups for t in ts if t is not None]
+        if not grads:
+            return loss
+        for i, (g, _) in enumerate(groups):
+            if self._buffers[i] is None:
+                self._buffers[i] = self._make(g["params"])
+        if self._step is None:
+            self._step = torch.zeros(1, dtype=torch.int64, device=grads[0].device)
+        if self.max_norm is None:
+            self._step += 1
+            factor = None
+        else:
+            self.last_norm = _ob.wtconv_grad_norm(grads, self.max_norm, step=self._step)
+            factor = self.last_norm[1:]
+        site = self.site
+        for (g, ts), b in zip(groups, self._buffers):
+            if any(t is not None for t in ts):
+                _ob.wtconv_adamw_step(g["params"], ts, step=self._step, lr=g["lr"], weight_decay=g["weight_decay"],
+                                      betas=g["betas"], eps=g["eps"], factor=factor, lr_factor=self.lr_factor,
+                                      rng=self.rng, site=site, **b)
+            site += len(ts)
+        return loss
+
+    def state_dict(self) -> dict:
+        """{"state": {"step", "buffers"}, "param_groups"}: the states' buffers as they are (a group's are None before
+        its first step), not a state for each parameter."""
+        groups = super().state_dict()["param_groups"]
+        return {"state": {"step": self._step, "buffers": [b and dict(b) for b in self._buffers]},
+                "param_groups": groups}
+
+    @torch.no_grad()
+    def load_state_dict(self, state_dict) -> None:
+        state, groups = state_dict["state"], state_dict["param_groups"]
+        if len(groups) != len(self.param_groups) or any(
+                len(a["params"]) != len(b["params"]) for a, b in zip(groups, self.param_groups)):
+            raise ValueError("the state has other parameter groups than this optimizer")
+        new = []
+        for b, g in zip(state["buffers"], self.param_groups):
+            if b is None:
+                new.append(None)
+                continue
+            like = self._make(g["params"])
+            if like.keys() != b.keys() or any(like[k].shape != t.shape or like[k].dtype != t.dtype
+                                              for k, t in b.items()):
+                raise ValueError("the state is of other parameters, or of other state_bits or master copies")
+            new.append({k: like[k].copy_(t) for k, t in b.items()})
+        self._buffers = new
+        dev = self.param_groups[0]["params"][0].device
+        self._step = None if state["step"] is None else state["step"].to(dev, copy=True)
+        for mine, other in zip(self.param_groups, groups):
+            mine.update({k: v for k, v in other.items() if k != "params"})
+
+
+def _places(params):
+    """(first element, elements) of each tensor in the states' buffers."""
+    at = 0
+    for p in params:
+        yield at, p.numel()
+        at += -(-p.numel() // _ob.BLOCK) * _ob.BLOCK
