@@ -130,6 +130,23 @@ def load_library() -> ctypes.CDLL:
     return _lib
 
 
+_native = None
+
+
+def load_native():
+    """The module that marshals the expert rows' and the optimizer's calls (after libwtconv.so, which it links)."""
+    global _native
+    if _native is None:
+        load_library()
+        try:
+            from . import _native as m
+        except ImportError as e:
+            raise ImportError(f"{e}: build it with `python -m wavelet_convolution_amd.build` (there is no "
+                              "fallback)") from e
+        _native = m
+    return _native
+
+
 def wtconv_status_string(status: int) -> str:
     return load_library().wtconv_status_string(int(status)).decode()
 

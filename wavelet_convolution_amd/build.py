@@ -1,4 +1,5 @@
-"""Build libwtconv.so (HIP, gfx950) in-tree with hipcc.
+"""Build libwtconv.so (HIP, gfx950) in-tree with hipcc, and _native.so (host
+C++ against the installed torch) beside it with g++.
 
     python -m wavelet_convolution_amd.build
 
@@ -19,6 +20,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libwtconv.so")
+NATIVE = os.path.join(PKG, "_native.so")   # the Python side of some entry points, against the installed torch
 SOURCES = ["wtconv_fused.hip", "wtconv_tiled.hip", "wtconv_bwdw.hip", "wtconv_naive.hip", "wtconv_api.hip",
            "wtconv_peaks.hip", "wtconv_layout.hip", "wtconv_dw.hip", "wtconv_bwd1.hip",
            "wtconv_block_api.hip", "wtconv_block.hip", "wtconv_block_generic.hip", "wtconv_block_rows_fwd.hip", "wtconv_block_rows_bwd.hip",
@@ -67,6 +69,23 @@ def _compile(src: str, incremental: bool = False) -> str:
     return obj
 
 
+def _build_native() -> None:
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    tmp = NATIVE + ".tmp%d" % os.getpid()
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-I{sysconfig.get_paths()['include']}", f"-I{base}/include", f"-I{base}/include/torch/csrc/api/include",
+           os.path.join(CSRC, "wtconv_native.cpp"), "-o", tmp, f"-L{base}/lib", "-ltorch_python", "-ltorch_cpu",
+           "-lc10", f"-L{PKG}", "-l:libwtconv.so", "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on wtconv_native.cpp:\n{res.stderr}")
+    os.replace(tmp, NATIVE)
+
+
 def build(verbose: bool = False, incremental: bool = False) -> str:
     """Compile every HIP source and link libwtconv.so; return its path.
     With incremental=True (a development aid, off by default), translation
@@ -81,8 +100,9 @@ def build(verbose: bool = False, incremental: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stderr}")
     os.replace(tmp, LIB)
+    _build_native()
     if verbose:
-        print(f"built {LIB}")
+        print(f"built {LIB}\nbuilt {NATIVE}")
     return LIB
 
 
