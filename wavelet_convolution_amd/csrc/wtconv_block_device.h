@@ -182,6 +182,27 @@ struct Vec {
                     w[i / 2] |= (uint32_t)p[i] << (16 * (i % 2));
             }
     }
+    // as they are, without a rounding
+    __device__ __forceinline__ void store(T* __restrict__ p) const {
+        if constexpr (WORDS % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < WORDS; i += 4)
+                *(words4_any*)((char*)p + 4 * i) = words4{w[i], w[i + 1], w[i + 2], w[i + 3]};
+        } else {
+            static_assert(WORDS == 2, "");
+            *(words2_any*)p = words2{w[0], w[1]};
+        }
+    }
+    __device__ __forceinline__ void store_part(T* __restrict__ p, int n) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < n) {
+                if constexpr (sizeof(T) == 4)
+                    p[i] = __uint_as_float(w[i]);
+                else
+                    p[i] = (T)(w[i / 2] >> (16 * (i % 2)));
+            }
+    }
     __device__ __forceinline__ void renew() {
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) asm volatile("" : "+v"(w[i]));

@@ -27,68 +27,71 @@ __device__ __forceinline__ uint32_t kept_of(const ExpertArgs& a) {
 // A thread takes eight channels of a row (one vector; where C is no multiple
 // of eight the last one moves back to end with the row and stores its
 // neighbour's values once more), and KK slots at a time, whose reads are in
-// flight together.
-template <typename X, int OP, int KK, bool PART>
-__device__ __forceinline__ void expert_move_wg(const ExpertArgs& a, uint32_t G, uint64_t wg, uint32_t S, uint32_t kept) {
-    const uint64_t first = wg * T, row0 = first / G;   // scalar
-    const uint32_t t = (uint32_t)(first - row0 * G) + threadIdx.x, down = t / G;
-    const uint64_t row = row0 + down;
-    if (row >= (uint64_t)a.N) return;
-    const uint32_t c = PART ? 0 : min((t - down * G) * CG, (uint32_t)a.C - CG);
-    const int* place = a.place + row * a.K;
-    const float* w = a.w + row * a.K;
-    auto load = [&](Vec<X, CG>& v, const X* p) {
-        if constexpr (PART)
-            v.load_part(p, a.C);
-        else
-            v.load(p + c);
-    };
-    auto store = [&](X* p, const float (&v)[CG]) {
-        if constexpr (PART)
-            store_part<X, CG>(p, v, a.C);
-        else
-            store_vec<X, CG>(p + c, v);
-    };
-    Vec<X, CG> x;
-    float sum[CG] = {};
-    if constexpr (OP == ROWS_FWD) load(x, (const X*)a.rows + row * a.C);
-    for (int k = 0; k < a.K; k += KK) {
-        Slot s[KK];
-        Vec<X, CG> q[KK];
-        float f[KK];
-#pragma unroll
-        for (int i = 0; i < KK; ++i) s[i] = slot_of(k + i < a.K ? (uint32_t)place[k + i] : ~0u, S, kept);
-        if constexpr (OP == ROWS_FWD) {
-#pragma unroll
-            for (int i = 0; i < KK; ++i) {
-                float o[CG];
-#pragma unroll
-                for (int j = 0; j < CG; ++j) o[j] = s[i].live ? x[j] : 0.f;
-                if (s[i].is) store((X*)a.to_sorted + (size_t)s[i].at * a.C, o);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < KK; ++i) {
-                q[i].zero();
-                f[i] = 1.f;
-                if (s[i].live) {
-                    load(q[i], (const X*)a.sorted + (size_t)s[i].at * a.C);
-                    if constexpr (OP == SUM_FWD) f[i] = w[k + i];
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < KK; ++i)
-#pragma unroll
-                for (int j = 0; j < CG; ++j) sum[j] = fmaf(f[i], q[i][j], sum[j]);
-        }
-    }
-    if constexpr (OP != ROWS_FWD) store((X*)a.to_rows + row * a.C, sum);
-}
-
+// flight together. More vectors a thread were slower: 401,408 slots of 96 bf16
+// channels, weighted sum 23.1 us, 24.2 with two and 26.7 with four.
 template <typename X, int OP, int KK, bool PART>
 __global__ __launch_bounds__(T) void k_expert_move(ExpertArgs a, uint32_t G, uint64_t wgs) {
     const uint32_t S = (uint32_t)(a.N * a.K), kept = kept_of(a);
-    for (uint64_t wg = blockIdx.x; wg < wgs; wg += gridDim.x) expert_move_wg<X, OP, KK, PART>(a, G, wg, S, kept);
+    for (uint64_t wg = blockIdx.x; wg < wgs; wg += gridDim.x) {
+        const uint64_t first = wg * T, row0 = first / G;   // scalar
+        const uint32_t t = (uint32_t)(first - row0 * G) + threadIdx.x, down = t / G;
+        const uint64_t row = row0 + down;
+        if (row >= (uint64_t)a.N) return;
+        const uint32_t c = PART ? 0 : min((t - down * G) * CG, (uint32_t)a.C - CG);
+        auto load = [&](Vec<X, CG>& v, const void* rows, uint64_t at) {
+            const X* p = (const X*)rows + at * a.C;
+            if constexpr (PART)
+                v.load_part(p, a.C);
+            else
+                v.load(p + c);
+        };
+        Vec<X, CG> x;
+        float sum[CG] = {};
+        if constexpr (OP == ROWS_FWD) load(x, a.rows, row);
+        for (int k = 0; k < a.K; k += KK) {
+            Slot s[KK];
+            float w[KK];
+#pragma unroll
+            for (int i = 0; i < KK; ++i) {
+                const bool is = k + i < a.K;
+                s[i] = slot_of(is ? (uint32_t)a.place[row * a.K + k + i] : ~0u, S, kept);
+                if constexpr (OP == SUM_FWD) w[i] = is ? a.w[row * a.K + k + i] : 0.f;
+            }
+            if constexpr (OP == ROWS_FWD) {
+#pragma unroll
+                for (int i = 0; i < KK; ++i) {
+                    if (!s[i].is) continue;
+                    Vec<X, CG> o = x;
+                    if (!s[i].live) o.zero();
+                    X* p = (X*)a.to_sorted + (size_t)s[i].at * a.C;
+                    if constexpr (PART)
+                        o.store_part(p, a.C);
+                    else
+                        o.store(p + c);
+                }
+            } else {
+                Vec<X, CG> q[KK];
+#pragma unroll
+                for (int i = 0; i < KK; ++i) {
+                    q[i].zero();
+                    if (s[i].live) load(q[i], a.sorted, s[i].at);
+                }
+#pragma unroll
+                for (int i = 0; i < KK; ++i) {
+                    const float f = OP == ROWS_BWD ? 1.f : s[i].live ? w[i] : 0.f;
+#pragma unroll
+                    for (int j = 0; j < CG; ++j) sum[j] = fmaf(f, q[i][j], sum[j]);
+                }
+            }
+        }
+        if constexpr (OP != ROWS_FWD) {
+            X* p = (X*)a.to_rows + row * a.C;
+            if constexpr (PART)
+                store_part<X, CG>(p, sum, a.C);
+            else
+                store_vec<X, CG>(p + c, sum);
+        }
+    }
 }
 
 // A grid of at most 2^31 lanes takes any number of pieces.

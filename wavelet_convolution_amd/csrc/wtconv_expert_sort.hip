@@ -4,6 +4,11 @@
 // once more, 64 slots at a time; slots of one expert among the 64 are found
 // by a ballot over each bit of the expert's number, so that a slot's rank is
 // a population count and no atomic decides an order.
+//
+// What bounds it is the length of that chain, not memory: one workgroup sorts
+// few slots alone (SORT_ALONE); else a first launch counts parts of 2,048 slots
+// and each part's workgroup sums up the counts of all (SORT_SUMS), or, where
+// those are many, a launch in between makes running sums of them (SORT_SCAN).
 #include "wtconv_experts.h"
 
 namespace wtc {
@@ -11,9 +16,11 @@ namespace {
 
 constexpr int T = 1024, WAVES = T / 64;
 
-// One workgroup sorts this many slots by itself; more of them are cut into
-// parts, whose counts a first launch leaves in the workspace.
-constexpr uint32_t ALONE = 8192;
+// Groups of 64 slots whose experts a wavefront holds in registers from its
+// count to its walk; runs of more read them again.
+constexpr int HELD = 4;
+
+enum { SORT_ALONE = 0, SORT_SUMS = 1, SORT_SCAN = 2 };
 
 // The slot's expert; E where it has none.
 template <typename I>
@@ -22,94 +29,164 @@ __device__ __forceinline__ int key_of(const SortArgs& a, uint32_t slot) {
     return e >= 0 && e < (I)a.E ? (int)e : a.E;
 }
 
-// f(first slot of 64, how many) over wavefront w's run of the slots
-// [begin, end): whole groups of 64, each a wavefront's at once.
-template <class F>
-__device__ __forceinline__ void each_group(uint32_t begin, uint32_t end, int w, F&& f) {
-    const uint32_t groups = (end - begin + 63) / 64, per = (groups + WAVES - 1) / WAVES;
-    const uint32_t first = min(groups, w * per), last = min(groups, first + per);
-    for (uint32_t g = first; g < last; ++g) f(begin + g * 64, min(64u, end - begin - g * 64));
-}
+// Wavefront w's run of the slots [begin, end): groups of 64, the last one of
+// all perhaps of fewer.
+struct Run {
+    uint32_t first, last, end;   // slots: of the first group, past the last group, past the last slot
+    int waves;                   // wavefronts that have a group
+    __device__ __forceinline__ Run(uint32_t begin, uint32_t stop, uint32_t w) : end(stop) {
+        const uint32_t groups = (stop - begin + 63) / 64, per = (groups + WAVES - 1) / WAVES;
+        first = begin + min(groups, w * per) * 64;
+        last = begin + min(groups, w * per + per) * 64;
+        waves = per ? (int)((groups + per - 1) / per) : 0;
+    }
+};
 
-// cnt[w][e]: the slots of expert e in wavefront w's run.
+// The experts of a run, a group after the other: held, or read at each use.
+template <typename I, bool ALL>
+struct Keys {
+    int held[ALL ? HELD : 1];
+    __device__ __forceinline__ void load(const SortArgs& a, const Run& r, uint32_t lane) {
+        if constexpr (ALL) {
+#pragma unroll
+            for (int g = 0; g < HELD; ++g) {
+                const uint32_t slot = r.first + g * 64 + lane;
+                held[g] = r.first + g * 64 < r.last && slot < r.end ? key_of<I>(a, slot) : -1;
+            }
+        }
+    }
+    // f(first slot of the group, this lane's expert, or -1 past the end)
+    template <class F>
+    __device__ __forceinline__ void each(const SortArgs& a, const Run& r, uint32_t lane, F&& f) const {
+        if constexpr (ALL) {
+#pragma unroll
+            for (int g = 0; g < HELD; ++g)
+                if (r.first + g * 64 < r.last) f(r.first + g * 64, held[g]);
+        } else {
+            for (uint32_t at = r.first; at < r.last; at += 64)
+                f(at, at + lane < r.end ? key_of<I>(a, at + lane) : -1);
+        }
+    }
+};
+
+// By parts, or by experts where k_sort_scan goes over an expert's parts.
 template <typename I>
-__device__ __forceinline__ void count_runs(const SortArgs& a, uint32_t begin, uint32_t end, int* cnt) {
-    const int n = a.E + 1, w = threadIdx.x / 64, lane = threadIdx.x % 64;
-    for (int i = threadIdx.x; i < WAVES * n; i += T) cnt[i] = 0;
+__global__ __launch_bounds__(T) void k_sort_count(SortArgs a, bool by_expert) {
+    __shared__ int cnt[MAX_EXPERTS + 1];
+    const uint32_t w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+    const uint32_t begin = min(a.S, blockIdx.x * a.per), end = min(a.S, begin + a.per);   // the last parts may be empty
+    const int n = a.E + 1;
+    for (int e = threadIdx.x; e < n; e += T) cnt[e] = 0;
     __syncthreads();
-    each_group(begin, end, w, [&](uint32_t at, uint32_t len) {
-        if ((uint32_t)lane < len) atomicAdd(&cnt[w * n + key_of<I>(a, at + lane)], 1);   // counts: any order
+    Keys<I, false>().each(a, Run(begin, end, w), lane, [&](uint32_t, int e) {
+        if (e >= 0) atomicAdd(&cnt[e], 1);   // counts: any order
     });
     __syncthreads();
+    for (int e = threadIdx.x; e < n; e += T)
+        a.counts[by_expert ? (size_t)e * a.parts + blockIdx.x : (size_t)blockIdx.x * n + e] = cnt[e];
 }
 
-template <typename I>
-__global__ __launch_bounds__(T) void k_sort_count(SortArgs a) {
-    __shared__ int cnt[WAVES * (MAX_EXPERTS + 1)];
-    const uint32_t begin = min(a.S, blockIdx.x * a.per);   // the last parts may be empty
-    count_runs<I>(a, begin, min(a.S, begin + a.per), cnt);
-    const int n = a.E + 1;
-    for (int e = threadIdx.x; e < n; e += T) {
-        int sum = 0;
+__device__ __forceinline__ int wave_before(int v, int lane) {   // of the lanes before
+    int up = v;
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) sum += cnt[w * n + e];
-        a.counts[(size_t)blockIdx.x * n + e] = sum;
+    for (int d = 1; d < 64; d *= 2) {
+        const int o = __shfl_up(up, d);
+        up += lane >= d ? o : 0;
     }
+    return up - v;
 }
 
-template <typename I>
-__global__ __launch_bounds__(T) void k_sort_place(SortArgs a) {
-    __shared__ int cnt[WAVES * (MAX_EXPERTS + 1)];
-    __shared__ int all[MAX_EXPERTS + 1], before[MAX_EXPERTS + 1];   // of all parts; of those before this one
-    const int n = a.E + 1, w = threadIdx.x / 64, lane = threadIdx.x % 64;
-    const uint32_t part = blockIdx.x, begin = min(a.S, part * a.per), end = min(a.S, begin + a.per);
-    for (int e = threadIdx.x; e < n; e += T) all[e] = before[e] = 0;
-    count_runs<I>(a, begin, end, cnt);   // with barriers
-    if (a.parts == 1) {
-        for (int e = threadIdx.x; e < n; e += T) {
-            int sum = 0;
+// Running sums of one expert's counts over the parts, in their place, and their
+// total behind all counts: a workgroup an expert.
+__global__ __launch_bounds__(T) void k_sort_scan(SortArgs a) {
+    __shared__ int of[WAVES];
+    const int w = threadIdx.x / 64, lane = threadIdx.x % 64, n = a.E + 1;
+    int* counts = a.counts + (size_t)blockIdx.x * a.parts;
+    int done = 0;
+    for (int p0 = 0; p0 < a.parts; p0 += T) {
+        const int p = p0 + (int)threadIdx.x, c = p < a.parts ? counts[p] : 0, before = wave_before(c, lane);
+        if (lane == 63) of[w] = before + c;
+        __syncthreads();
+        int at = done;
 #pragma unroll
-            for (int k = 0; k < WAVES; ++k) sum += cnt[k * n + e];
-            all[e] = sum;
+        for (int k = 0; k < WAVES; ++k) {
+            at += k < w ? of[k] : 0;
+            done += of[k];
         }
-    } else {
-        // a thread sums one expert's counts of every `slices`-th part
-        const int wide = n > T / 2 ? T : 1 << (32 - __clz(n - 1)), slices = T / wide;
-        for (int e = threadIdx.x % wide; e < n; e += wide) {
-            int sum = 0, mine = 0;
+        if (p < a.parts) counts[p] = at + before;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) a.counts[(size_t)n * a.parts + blockIdx.x] = done;
+}
+
+template <typename I, bool ALL, int MODE>
+__global__ __launch_bounds__(T) void k_sort_place(SortArgs a) {
+    __shared__ int cnt[WAVES * (MAX_EXPERTS + 1)];                  // a wavefront's slots of an expert; then its next place
+    __shared__ int all[MAX_EXPERTS + 1], before[MAX_EXPERTS + 1];   // of all parts; of those before this one
+    const uint32_t w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+    const int n = a.E + 1;
+    const uint32_t part = blockIdx.x, begin = min(a.S, part * a.per), end = min(a.S, begin + a.per);
+    const Run run(begin, end, w);
+    Keys<I, ALL> keys;
+    keys.load(a, run, lane);
+    // a thread sums up one expert's counts in every `slices`-th part
+    const int wide = n > T / 2 ? T : 1 << (32 - __clz(n - 1)), mine = threadIdx.x % wide;
+    int sum[2] = {0, 0}, less[2] = {0, 0};   // two experts where there is one more than threads
+    if constexpr (MODE == SORT_SUMS) {
 #pragma unroll 8
-            for (int p = threadIdx.x / wide; p < a.parts; p += slices) {
-                const int c = a.counts[(size_t)p * n + e];
-                sum += c;
-                mine += p < (int)part ? c : 0;
-            }
-            if (slices == 1) {
-                all[e] = sum;
-                before[e] = mine;
-            } else {   // whole numbers: any order
-                atomicAdd(&all[e], sum);
-                atomicAdd(&before[e], mine);
-            }
+        for (int p = threadIdx.x / wide; p < a.parts; p += T / wide) {
+            const int c = mine < n ? a.counts[(size_t)p * n + mine] : 0;
+            sum[0] += c;
+            less[0] += p < (int)part ? c : 0;
         }
+        if (mine + T < n)
+            for (int p = 0; p < a.parts; ++p) {
+                const int c = a.counts[(size_t)p * n + mine + T];
+                sum[1] += c;
+                less[1] += p < (int)part ? c : 0;
+            }
+        for (int e = threadIdx.x; e < n; e += T) all[e] = before[e] = 0;
+    }
+    if constexpr (MODE == SORT_SCAN) {
+        for (int e = threadIdx.x; e < n; e += T) {
+            all[e] = a.counts[(size_t)n * a.parts + e];
+            before[e] = a.counts[(size_t)e * a.parts + part];
+        }
+    }
+    for (int i = threadIdx.x; i < run.waves * n; i += T) cnt[i] = 0;
+    __syncthreads();
+    keys.each(a, run, lane, [&](uint32_t, int e) {
+        if (e >= 0) atomicAdd(&cnt[w * n + e], 1);   // counts, here and below: any order
+    });
+    if constexpr (MODE == SORT_SUMS) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (const int e = mine + i * T; e < n) {
+                atomicAdd(&all[e], sum[i]);
+                atomicAdd(&before[e], less[i]);
+            }
     }
     __syncthreads();
+    if constexpr (MODE == SORT_ALONE) {
+        for (int e = threadIdx.x; e < n; e += T) {
+            int c = 0;
+            for (int k = 0; k < run.waves; ++k) c += cnt[k * n + e];
+            all[e] = c;
+            before[e] = 0;
+        }
+        __syncthreads();
+    }
     // each expert's first place: the sums before it, 64 runs of experts in a
     // wavefront's lanes
     if (w == 0) {
-        const int per = (n + 63) / 64, first = min(n, lane * per), last = min(n, first + per);
-        int sum = 0;
-        for (int e = first; e < last; ++e) sum += all[e];
-        int up = sum;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int o = __shfl_up(up, d);
-            up += lane >= d ? o : 0;
-        }
-        int at = up - sum;
+        const int per = (n + 63) / 64, first = min(n, (int)lane * per), last = min(n, first + per);
+        int c = 0;
+        for (int e = first; e < last; ++e) c += all[e];
+        int at = wave_before(c, (int)lane);
         for (int e = first; e < last; ++e) {
-            const int c = all[e];
+            const int here = all[e];
             all[e] = at;
-            at += c;
+            at += here;
         }
     }
     __syncthreads();
@@ -117,8 +194,7 @@ __global__ __launch_bounds__(T) void k_sort_place(SortArgs a) {
     for (int e = threadIdx.x; e < n; e += T) {
         if (part == 0) a.offsets[e] = all[e];
         int at = all[e] + before[e];
-#pragma unroll
-        for (int k = 0; k < WAVES; ++k) {
+        for (int k = 0; k < run.waves; ++k) {
             const int c = cnt[k * n + e];
             cnt[k * n + e] = at;
             at += c;
@@ -126,9 +202,8 @@ __global__ __launch_bounds__(T) void k_sort_place(SortArgs a) {
     }
     __syncthreads();
     const int bits = 32 - __clz(a.E);   // of the numbers 0..E
-    each_group(begin, end, w, [&](uint32_t at, uint32_t len) {
-        const bool on = (uint32_t)lane < len;
-        const int e = on ? key_of<I>(a, at + lane) : 0;
+    keys.each(a, run, lane, [&](uint32_t at, int e) {
+        const bool on = e >= 0;
         uint64_t same = __ballot(on);
         for (int b = 0; b < bits; ++b) {
             const uint64_t set = __ballot(e >> b & 1);
@@ -150,41 +225,59 @@ __global__ __launch_bounds__(T) void k_sort_place(SortArgs a) {
     });
 }
 
-// Slots go to as many workgroups as leave each 2,048 of them (two groups a
-// wavefront), but to fewer where many experts would make the counts that
-// every workgroup reads long.
-int parts_of(long long S, int E) {
-    if (S <= ALONE) return 1;
-    long long most = 65536 / (E + 1);
-    most = most < 32 ? 32 : most > 256 ? 256 : most;
-    const long long p = (S + 2047) / 2048;
-    return (int)(p < most ? p : most);
+// How S slots of E experts are sorted, in how many parts. Alone up to what the
+// wavefronts of a workgroup hold: 4,096 slots of 64 experts 6.4 us against 7.3
+// in two parts, 8,192 in two rounds 10.7 against 7.4.
+struct Plan {
+    int mode, parts;
+    uint32_t per;
+};
+// The sums in each part's workgroup cost parts * (E + 1) reads there, the
+// running sums a launch: 401,408 slots of 64 experts (196 parts) 10.5 us against
+// 12.0, of 256 experts 16.0 against 13.7; 131,072 of 1,024 22.1 against 17.9.
+Plan plan_of(long long S, int E) {
+    constexpr long long ALONE = WAVES * 64 * HELD, PART = 2048, MOST = 4096, SUMS = 32768;
+    if (S <= ALONE) return {SORT_ALONE, 1, (uint32_t)S};
+    const long long parts = (S + PART - 1) / PART < MOST ? (S + PART - 1) / PART : MOST;
+    const long long per = ((S + parts - 1) / parts + 63) / 64 * 64;   // the last parts may be short or empty
+    return {parts * (E + 1) <= SUMS ? SORT_SUMS : SORT_SCAN, (int)parts, (uint32_t)per};
+}
+
+template <typename I, bool ALL>
+void place(const SortArgs& a, int mode, hipStream_t s) {
+    if (mode == SORT_ALONE)
+        hipLaunchKernelGGL((k_sort_place<I, true, SORT_ALONE>), dim3(1), dim3(T), 0, s, a);
+    else if (mode == SORT_SUMS)
+        hipLaunchKernelGGL((k_sort_place<I, true, SORT_SUMS>), dim3(a.parts), dim3(T), 0, s, a);
+    else
+        hipLaunchKernelGGL((k_sort_place<I, ALL, SORT_SCAN>), dim3(a.parts), dim3(T), 0, s, a);
+}
+
+template <typename I>
+hipError_t sort(const SortArgs& a, int mode, hipStream_t s) {
+    if (mode != SORT_ALONE) {
+        hipLaunchKernelGGL(k_sort_count<I>, dim3(a.parts), dim3(T), 0, s, a, mode == SORT_SCAN);
+        if (mode == SORT_SCAN) hipLaunchKernelGGL(k_sort_scan, dim3(a.E + 1), dim3(T), 0, s, a);
+    }
+    if (a.per <= WAVES * 64 * HELD)
+        place<I, true>(a, mode, s);
+    else
+        place<I, false>(a, mode, s);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 size_t expert_sort_bytes(long long S, int E) {
-    const int parts = parts_of(S, E);
-    return parts == 1 ? 0 : (size_t)parts * (E + 1) * sizeof(int);
+    const Plan p = plan_of(S, E);
+    return p.mode == SORT_ALONE ? 0 : (size_t)(p.parts + 1) * (E + 1) * sizeof(int);
 }
 
 hipError_t expert_sort(SortArgs a, int id64, hipStream_t s) {
-    a.parts = parts_of(a.S, a.E);
-    a.per = (uint32_t)(((long long)a.S + a.parts - 1) / a.parts);
-    a.per = (a.per + 63) / 64 * 64;
-    if (a.parts > 1) {
-        if (id64)
-            hipLaunchKernelGGL(k_sort_count<int64_t>, dim3(a.parts), dim3(T), 0, s, a);
-        else
-            hipLaunchKernelGGL(k_sort_count<int32_t>, dim3(a.parts), dim3(T), 0, s, a);
-        const hipError_t err = hipGetLastError();
-        if (err != hipSuccess) return err;
-    }
-    if (id64)
-        hipLaunchKernelGGL(k_sort_place<int64_t>, dim3(a.parts), dim3(T), 0, s, a);
-    else
-        hipLaunchKernelGGL(k_sort_place<int32_t>, dim3(a.parts), dim3(T), 0, s, a);
-    return hipGetLastError();
+    const Plan p = plan_of(a.S, a.E);
+    a.parts = p.parts;
+    a.per = p.per;
+    return id64 ? sort<int64_t>(a, p.mode, s) : sort<int32_t>(a, p.mode, s);
 }
 
 }  // namespace wtc

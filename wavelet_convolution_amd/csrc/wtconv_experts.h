@@ -32,7 +32,7 @@ struct SortArgs {
     int* order;            // [S]
     int* place;            // [S]
     int* offsets;          // [E + 1]
-    int* counts;           // [parts][E + 1]: the workspace
+    int* counts;           // of each part and expert, then totals: the workspace
     uint32_t S;
     int E, parts;
     uint32_t per;          // slots of a part

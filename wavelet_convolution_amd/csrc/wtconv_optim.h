@@ -14,20 +14,22 @@
 
 namespace wtc {
 
-constexpr int OB = 256;            // elements of a block of the states
-constexpr int ADAM_PIECE = 4096;   // elements of a workgroup
+constexpr int OB = 256;   // elements of a block of the states
+constexpr int ADAM_PIECE = 1024;   // elements of a workgroup
 
+// A tensor of a launch in 32 bytes: 330 tensors are three launches instead of
+// five at 48. What few tensors have of their own (rate and decay) is in a
+// short table beside.
 struct AdamTensor {
     void* p;
     const void* g;
-    uint64_t count;
+    uint32_t last;    // count - 1, its low 32 bits
     uint32_t block;   // the tensor's first block in the states
     uint32_t wg;      // its first workgroup
-    float lr, wd;
-    uint32_t site;
-    uint32_t pad;
+    uint32_t more;    // its number in the call, its rates', and the two high bits of count - 1
 };
-constexpr int ADAM_TENSORS = 80;
+constexpr int ADAM_TENSORS = 119, ADAM_RATES = 16;
+constexpr uint32_t ADAM_NUMBERS = 1u << 26;   // tensors of a call
 
 struct AdamArgs {
     void *m, *v;
@@ -37,7 +39,9 @@ struct AdamArgs {
     const unsigned long long* rng;
     float b1, b2, a1, a2;              // betas, 1 - betas
     float log1, log2, eps;             // log(beta)
-    int n;
+    uint32_t site;
+    int n, rates;
+    float lr[ADAM_RATES], wd[ADAM_RATES];
     AdamTensor t[ADAM_TENSORS];
 };
 static_assert(sizeof(AdamArgs) <= 4096, "");
@@ -45,13 +49,13 @@ static_assert(sizeof(AdamArgs) <= 4096, "");
 enum { STATES_32 = 0, STATES_8 = 1, STATES_8_RANDOM = 2 };
 hipError_t adamw_launch(const AdamArgs& a, uint32_t wgs, int p_bf16, int g_bf16, int mode, hipStream_t s);
 
+// A gradient of a launch in 12 bytes, so that one launch takes hundreds: its
+// address (48 bits; even, so bit 0 says bf16), count - 1 (34 bits) and first
+// workgroup (the 14 high bits of the last word).
 struct NormTensor {
-    const void* g;
-    uint64_t count;
-    uint32_t wg;
-    uint32_t bf16;
+    uint32_t w[3];
 };
-constexpr int NORM_TENSORS = 160;
+constexpr int NORM_TENSORS = 339;
 
 struct NormArgs {
     double* sums;       // a sum a workgroup
@@ -61,7 +65,12 @@ struct NormArgs {
 };
 static_assert(sizeof(NormArgs) <= 4096, "");
 
-constexpr uint32_t NORM_WGS = 2048;   // most sums of a launch, besides one more a tensor
+// Most sums of a launch, besides one more a tensor: fewer workgroups in all than
+// the card holds at once (256 CUs, eight of four wavefronts each), as the few
+// that would come after took as long as the others. 34 M bf16 elements in 330
+// tensors: 18.7 us with 1,536, 21.0 with 2,048, 22.5 with 8,192.
+constexpr uint32_t NORM_WGS = 1536;
+static_assert(NORM_WGS + NORM_TENSORS < 1u << 14, "");
 hipError_t norm_launch(const NormArgs& a, uint32_t wgs, hipStream_t s);
 hipError_t norm_finish(const double* sums, uint32_t n, double max_norm, long long* step, float* out, hipStream_t s);
 

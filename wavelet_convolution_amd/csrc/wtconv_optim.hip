@@ -11,11 +11,18 @@ constexpr int T = 256;
 
 // The tensor of a workgroup: the last one whose first workgroup is not behind
 // it. All lanes look at a first workgroup each, and a ballot counts.
-template <class A>
+__device__ __forceinline__ uint32_t first_wg(const AdamTensor& t) { return t.wg; }
+__device__ __forceinline__ uint32_t first_wg(const NormTensor& t) { return t.w[2] >> 18; }
+template <int MOST, class A>
 __device__ __forceinline__ int tensor_of(const A& a, uint32_t wg) {
+    constexpr int N = (MOST + 63) / 64;   // loads that are in flight together
     const int lane = threadIdx.x % 64;
+    uint32_t at[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) at[i] = i * 64 < a.n ? first_wg(a.t[min(i * 64 + lane, a.n - 1)]) : 0;
     int n = 0;
-    for (int i = 0; i < a.n; i += 64) n += (int)__popcll(__ballot(i + lane < a.n && a.t[min(i + lane, a.n - 1)].wg <= wg));
+#pragma unroll
+    for (int i = 0; i < N; ++i) n += (int)__popcll(__ballot(i * 64 + lane < a.n && at[i] <= wg));
     return __builtin_amdgcn_readfirstlane(n - 1);
 }
 
@@ -59,156 +66,141 @@ __device__ __forceinline__ void widen_e4m3(uint32_t w, float unit, float (&o)[4]
     o[3] = hi[1] * unit;
 }
 
-// A lane takes four consecutive elements, a wavefront a block of 256 at a
-// time, UN of them in flight.
-constexpr int UN = 2;
-
+// A wavefront takes one block of 256 elements, a lane four of them, and ends:
+// the next one's loads are on their way while it computes, with more of them in
+// flight than a loop over blocks keeps.
 template <typename P, typename G, bool MASTER, int MODE>
-__global__ __launch_bounds__(T) void k_adamw(AdamArgs a) {
+__global__ __launch_bounds__(T) void k_adamw(AdamArgs a, uint32_t wgs) {
     const float f = a.factor ? *a.factor : 1.f;
     if (!(fabsf(f) < INFINITY)) return;
-    const AdamTensor& t = a.t[tensor_of(a, blockIdx.x)];
-    const uint64_t count = t.count, piece = (uint64_t)(blockIdx.x - t.wg) * ADAM_PIECE;
+    const uint32_t wg = blockIdx.y * gridDim.x + blockIdx.x;
+    if (wg >= wgs) return;
+    const AdamTensor& t = a.t[tensor_of<ADAM_TENSORS>(a, wg)];
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+    const uint64_t count = ((uint64_t)(t.more >> 30) << 32 | t.last) + 1,
+                   first = (uint64_t)(wg - t.wg) * ADAM_PIECE + wave * OB;
+    if (first >= count) return;
+    const uint32_t number = t.more & (ADAM_NUMBERS - 1), of = t.more >> 26 & (ADAM_RATES - 1);
+    // a lane's n elements of the tensor from e on, and its place in the states
+    const uint64_t e = first + 4 * lane;
+    const int n = e >= count ? 0 : count - e < 4 ? (int)(count - e) : 4;
+    const size_t block = t.block + first / OB, s = block * OB + 4 * lane;
+    Vec<P, 4> pv;
+    Vec<float, 4> xv, mv, vv;
+    Vec<G, 4> gv;
+    uint32_t m8 = 0, v8 = 0;
+    float2 unit = make_float2(0.f, 0.f);
+    if (n == 4) {
+        gv.load((const G*)t.g + e);
+        if constexpr (!MASTER) pv.load((const P*)t.p + e);
+    } else {
+        gv.load_part((const G*)t.g + e, n);
+        if constexpr (!MASTER) pv.load_part((const P*)t.p + e, n);
+    }
+    if constexpr (MASTER) xv.load(a.master + s);
+    if constexpr (MODE == STATES_32) {
+        mv.load((const float*)a.m + s);
+        vv.load((const float*)a.v + s);
+    } else {
+        m8 = *(const uint32_t*)((const char*)a.m + s);
+        v8 = *(const uint32_t*)((const char*)a.v + s);
+        unit = ((const float2*)a.scales)[block];
+    }
     // 1 - beta^t as -(e^(t log beta) - 1): no difference of near numbers
     const float steps = (float)max(1ll, *a.step), c1 = -expm1f(steps * a.log1), c2 = -expm1f(steps * a.log2);
-    const float lr = a.lr_factor ? t.lr * *a.lr_factor : t.lr;
-    const float decay = 1.f - lr * t.wd, rate = lr / c1, root_scale = 1.f / sqrtf(c2);
-    for (uint32_t b0 = wave; b0 < ADAM_PIECE / OB; b0 += UN * T / 64) {
-        Vec<P, 4> pv[UN];
-        Vec<float, 4> xv[UN], mv[UN], vv[UN];
-        Vec<G, 4> gv[UN];
-        uint32_t m8[UN], v8[UN];
-        float2 unit[UN];
-        uint64_t e[UN];
-        size_t s[UN];
-        int n[UN];
+    const float lr = a.lr_factor ? a.lr[of] * *a.lr_factor : a.lr[of];
+    const float decay = 1.f - lr * a.wd[of], rate = lr / c1, root_scale = 1.f / sqrtf(c2);
+    float m[4], v[4], x[4], root[4];
+    if constexpr (MODE == STATES_32) {
 #pragma unroll
-        for (int u = 0; u < UN; ++u) {
-            const uint64_t first = piece + (uint64_t)(b0 + u * T / 64) * OB;
-            e[u] = first + 4 * lane;
-            n[u] = e[u] >= count ? 0 : count - e[u] < 4 ? (int)(count - e[u]) : 4;
-            const size_t block = t.block + first / OB;
-            s[u] = block * OB + 4 * lane;
-            if (n[u] == 4) {
-                gv[u].load((const G*)t.g + e[u]);
-                if constexpr (!MASTER) pv[u].load((const P*)t.p + e[u]);
-            } else {
-                gv[u].load_part((const G*)t.g + e[u], n[u]);
-                if constexpr (!MASTER) pv[u].load_part((const P*)t.p + e[u], n[u]);
-            }
-            const bool in = first < count;   // the whole block is there
-            m8[u] = v8[u] = 0;
-            unit[u] = make_float2(0.f, 0.f);
-            mv[u].zero();
-            vv[u].zero();
-            xv[u].zero();
-            if (in) {
-                if constexpr (MASTER) xv[u].load(a.master + s[u]);
-                if constexpr (MODE == STATES_32) {
-                    mv[u].load((const float*)a.m + s[u]);
-                    vv[u].load((const float*)a.v + s[u]);
-                } else {
-                    m8[u] = *(const uint32_t*)((const char*)a.m + s[u]);
-                    v8[u] = *(const uint32_t*)((const char*)a.v + s[u]);
-                    unit[u] = ((const float2*)a.scales)[block];
-                }
-            }
+        for (int i = 0; i < 4; ++i) m[i] = mv[i], v[i] = vv[i];
+    } else {
+        widen_e4m3(m8, unit.x, m);
+        widen_e4m3(v8, unit.y, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] *= v[i];
+            if (i >= n) m[i] = v[i] = 0.f;   // past the tensor's end
         }
+    }
 #pragma unroll
-        for (int u = 0; u < UN; ++u) {
-            if (e[u] - 4 * lane >= count) continue;   // the wavefront's
-            float m[4], v[4], x[4], root[4];
-            if constexpr (MODE == STATES_32) {
+    for (int i = 0; i < 4; ++i) {
+        const float g = gv[i] * f;
+        if constexpr (MASTER)
+            x[i] = xv[i];
+        else
+            x[i] = pv[i];
+        m[i] = fmaf(a.b1, m[i], a.a1 * g);
+        v[i] = fmaf(a.b2, v[i], a.a2 * g * g);
+        root[i] = sqrtf(v[i]);
+        x[i] = fmaf(-rate * m[i], __builtin_amdgcn_rcpf(fmaf(root[i], root_scale, a.eps)), x[i] * decay);
+    }
+    if (n == 4) {
+        store_vec<P, 4>((P*)t.p + e, x);
+        if constexpr (MASTER) store_vec<float, 4>(a.master + s, x);
+    } else {
+        store_part<P, 4>((P*)t.p + e, x, n);
+        if constexpr (MASTER) store_part<float, 4>(a.master + s, x, n);
+    }
+    if constexpr (MODE == STATES_32) {
+        if (n == 4) {
+            store_vec<float, 4>((float*)a.m + s, m);
+            store_vec<float, 4>((float*)a.v + s, v);
+        } else {
+            store_part<float, 4>((float*)a.m + s, m, n);
+            store_part<float, 4>((float*)a.v + s, v, n);
+        }
+    } else {
+        float top = 0.f, most = 0.f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) m[i] = mv[u][i], v[i] = vv[u][i];
-            } else {
-                widen_e4m3(m8[u], unit[u].x, m);
-                widen_e4m3(v8[u], unit[u].y, v);
+        for (int i = 0; i < 4; ++i) {
+            // as whole numbers, as in the wavefront's
+            top = __uint_as_float(max(__float_as_uint(top), __float_as_uint(fabsf(m[i]))));
+            most = __uint_as_float(max(__float_as_uint(most), __float_as_uint(root[i])));
+        }
+        top = wave_max(top);
+        most = wave_max(most);
+        // a moment below 2^-100 is none; a root is above 2^-75 or zero
+        const float per_m = top < 0x1p-100f ? 0.f : 448.f / top, per_v = most > 0.f ? 448.f / most : most;
+        float q[4], r[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    v[i] *= v[i];
-                    if (i >= n[u]) m[i] = v[i] = 0.f;   // past the tensor's end
-                }
-            }
+        for (int i = 0; i < 4; ++i) {
+            q[i] = m[i] * per_m;
+            r[i] = root[i] * per_v;
+            if (root[i] > 0.f) r[i] = r[i] < 0x1p-9f ? 0x1p-9f : r[i];
+        }
+        uint32_t cm, cv;
+        if constexpr (MODE == STATES_8) {
+            cm = e4m3_near(q);
+            cv = e4m3_near(r);
+        } else {
+            const uint4 bits = Philox(a.rng, a.site + number)((uint32_t)(e / 4));
+            const uint32_t w[4] = {bits.x, bits.y, bits.z, bits.w};
+            cm = cv = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float g = gv[u][i] * f;
-                if constexpr (MASTER)
-                    x[i] = xv[u][i];
-                else
-                    x[i] = pv[u][i];
-                m[i] = fmaf(a.b1, m[i], a.a1 * g);
-                v[i] = fmaf(a.b2, v[i], a.a2 * g * g);
-                root[i] = sqrtf(v[i]);
-                x[i] = fmaf(-rate * m[i], __builtin_amdgcn_rcpf(fmaf(root[i], root_scale, a.eps)), x[i] * decay);
-            }
-            if (n[u] == 4) {
-                store_vec<P, 4>((P*)t.p + e[u], x);
-                if constexpr (MASTER) store_vec<float, 4>(a.master + s[u], x);
-            } else {
-                store_part<P, 4>((P*)t.p + e[u], x, n[u]);
-                if constexpr (MASTER) store_part<float, 4>(a.master + s[u], x, n[u]);
-            }
-            if constexpr (MODE == STATES_32) {
-                if (n[u] == 4) {
-                    store_vec<float, 4>((float*)a.m + s[u], m);
-                    store_vec<float, 4>((float*)a.v + s[u], v);
-                } else {
-                    store_part<float, 4>((float*)a.m + s[u], m, n[u]);
-                    store_part<float, 4>((float*)a.v + s[u], v, n[u]);
-                }
-            } else {
-                float top = 0.f, most = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // as whole numbers, as in the wavefront's
-                    top = __uint_as_float(max(__float_as_uint(top), __float_as_uint(fabsf(m[i]))));
-                    most = __uint_as_float(max(__float_as_uint(most), __float_as_uint(root[i])));
-                }
-                top = wave_max(top);
-                most = wave_max(most);
-                // a moment below 2^-100 is none; a root is above 2^-75 or zero
-                const float per_m = top < 0x1p-100f ? 0.f : 448.f / top, per_v = most > 0.f ? 448.f / most : most;
-                float q[4], r[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    q[i] = m[i] * per_m;
-                    r[i] = root[i] * per_v;
-                    if (root[i] > 0.f) r[i] = r[i] < 0x1p-9f ? 0x1p-9f : r[i];
-                }
-                uint32_t cm, cv;
-                if constexpr (MODE == STATES_8) {
-                    cm = e4m3_near(q);
-                    cv = e4m3_near(r);
-                } else {
-                    const uint4 bits = Philox(a.rng, t.site)((uint32_t)(e[u] / 4));
-                    const uint32_t w[4] = {bits.x, bits.y, bits.z, bits.w};
-                    cm = cv = 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        cm |= e4m3_random(q[i], w[i] & 0xffffu) << (8 * i);
-                        cv |= e4m3_random(r[i], w[i] >> 16) << (8 * i);
-                    }
-                }
-                *(uint32_t*)((char*)a.m + s[u]) = cm;
-                *(uint32_t*)((char*)a.v + s[u]) = cv;
-                if (lane == 0)
-                    ((float2*)a.scales)[s[u] / OB] = make_float2(top < 0x1p-100f ? 0.f : top * (1.f / 448.f),
-                                                                 most * (1.f / 448.f));
+                cm |= e4m3_random(q[i], w[i] & 0xffffu) << (8 * i);
+                cv |= e4m3_random(r[i], w[i] >> 16) << (8 * i);
             }
         }
+        *(uint32_t*)((char*)a.m + s) = cm;
+        *(uint32_t*)((char*)a.v + s) = cv;
+        if (lane == 0)
+            ((float2*)a.scales)[block] = make_float2(top < 0x1p-100f ? 0.f : top * (1.f / 448.f), most * (1.f / 448.f));
     }
 }
 
 template <typename P, typename G, bool MASTER>
 hipError_t adamw_by_mode(const AdamArgs& a, uint32_t wgs, int mode, hipStream_t s) {
+    // a grid's side has fewer than 2^32 lanes
+    const uint32_t x = wgs < 1u << 20 ? wgs : 1u << 20;
+    const dim3 grid(x, (wgs + x - 1) / x);
     if (mode == STATES_32)
-        hipLaunchKernelGGL((k_adamw<P, G, MASTER, STATES_32>), dim3(wgs), dim3(T), 0, s, a);
+        hipLaunchKernelGGL((k_adamw<P, G, MASTER, STATES_32>), grid, dim3(T), 0, s, a, wgs);
     else if (mode == STATES_8)
-        hipLaunchKernelGGL((k_adamw<P, G, MASTER, STATES_8>), dim3(wgs), dim3(T), 0, s, a);
+        hipLaunchKernelGGL((k_adamw<P, G, MASTER, STATES_8>), grid, dim3(T), 0, s, a, wgs);
     else
-        hipLaunchKernelGGL((k_adamw<P, G, MASTER, STATES_8_RANDOM>), dim3(wgs), dim3(T), 0, s, a);
+        hipLaunchKernelGGL((k_adamw<P, G, MASTER, STATES_8_RANDOM>), grid, dim3(T), 0, s, a, wgs);
     return hipGetLastError();
 }
 template <typename G>
@@ -218,28 +210,35 @@ hipError_t adamw_by_param(const AdamArgs& a, uint32_t wgs, int p_bf16, int mode,
 }
 
 // Squares are summed in 64 bits: in 32 those of gradients above 2^64 or below
-// 2^-75 would be lost. A widening and a product of 64 bits an element are a
-// quarter of the time that memory takes for bf16.
+// 2^-75 would be lost. It costs no time: with fp32 products and sums 34 M bf16
+// elements took as long (19.4 us against 19.6). The next vectors are loaded
+// while these are summed.
 template <typename G>
 __device__ __forceinline__ double squares(const G* __restrict__ g, uint64_t n) {
-    constexpr int N = 8, UV = 4;
+    constexpr int N = 8, UV = 2;
     double sum[2] = {0., 0.};
     const uint64_t vecs = n / N;
-    uint64_t i = threadIdx.x;
-    for (; i + (UV - 1) * T < vecs; i += UV * T) {
-        Vec<G, N> v[UV];
+    Vec<G, N> v[UV], next[UV];
+    auto load = [&](Vec<G, N>(&q)[UV], uint64_t first) {
 #pragma unroll
-        for (int u = 0; u < UV; ++u) v[u].load(g + (i + u * T) * N);
+        for (int u = 0; u < UV; ++u) {
+            q[u].zero();
+            if (first + u * T < vecs) q[u].load(g + (first + u * T) * N);
+        }
+    };
+    load(v, threadIdx.x);
+    for (uint64_t first = threadIdx.x; first < vecs;) {
+        first += UV * T;
+        load(next, first);
 #pragma unroll
         for (int u = 0; u < UV; ++u)
 #pragma unroll
-            for (int k = 0; k < N; ++k) sum[k % 2] = fma((double)v[u][k], (double)v[u][k], sum[k % 2]);
-    }
-    for (; i < vecs; i += T) {
-        Vec<G, N> v;
-        v.load(g + i * N);
+            for (int k = 0; k < N; ++k) {
+                const double x = v[u][k];
+                sum[k % 2] = fma(x, x, sum[k % 2]);
+            }
 #pragma unroll
-        for (int k = 0; k < N; ++k) sum[k % 2] = fma((double)v[k], (double)v[k], sum[k % 2]);
+        for (int u = 0; u < UV; ++u) v[u] = next[u];
     }
     if (const uint64_t k = vecs * N + threadIdx.x; k < n) {
         const double x = widen(g[k]);
@@ -263,9 +262,12 @@ __device__ __forceinline__ double wg_sum(double v) {
 }
 
 __global__ __launch_bounds__(T) void k_norm(NormArgs a) {
-    const NormTensor& t = a.t[tensor_of(a, blockIdx.x)];
-    const uint64_t at = (uint64_t)(blockIdx.x - t.wg) * a.piece, n = min(a.piece, t.count - at);
-    const double sum = wg_sum<T>(t.bf16 ? squares((const bf16_t*)t.g + at, n) : squares((const float*)t.g + at, n));
+    const NormTensor& t = a.t[tensor_of<NORM_TENSORS>(a, blockIdx.x)];
+    const uint64_t address = (uint64_t)(t.w[1] & 0xffffu) << 32 | t.w[0],
+                   count = ((uint64_t)(t.w[2] & 0x3ffffu) << 16 | t.w[1] >> 16) + 1,
+                   at = (uint64_t)(blockIdx.x - first_wg(t)) * a.piece, n = min(a.piece, count - at);
+    const double sum = wg_sum<T>(address & 1 ? squares((const bf16_t*)(address - 1) + at, n)
+                                              : squares((const float*)address + at, n));
     if (threadIdx.x == 0) a.sums[blockIdx.x] = sum;
 }
 

@@ -79,6 +79,7 @@ wtconv_status_t wtconv_adamw_step(const wtconv_adamw_desc_t* d, int32_t n, void*
     if (!((float)d->eps >= FLT_MIN && isfinite((float)d->eps))) return WTCONV_ERR_INVALID_ARG;
     const bool eight = d->state_bits == 8, bf16 = d->p_dtype == WTCONV_BF16;
     if (rng && (!eight || d->site < 0 || n > (1ll << 31) - d->site)) return WTCONV_ERR_INVALID_ARG;
+    if (n > (int32_t)wtc::ADAM_NUMBERS) return WTCONV_ERR_UNSUPPORTED_SHAPE;
     if (n == 0) return WTCONV_OK;
     if (!params || !grads || !counts || !lr || !weight_decay || !step) return WTCONV_ERR_INVALID_ARG;
     const int64_t all = state_count(counts, n);
@@ -125,6 +126,7 @@ wtconv_status_t wtconv_adamw_step(const wtconv_adamw_desc_t* d, int32_t n, void*
     a.log1 = (float)log(d->beta1);   // minus infinity for 0
     a.log2 = (float)log(d->beta2);
     a.eps = (float)d->eps;
+    a.site = (uint32_t)d->site;
     const int mode = !eight ? wtc::STATES_32 : rng ? wtc::STATES_8_RANDOM : wtc::STATES_8;
     uint32_t wgs = 0;
     int64_t block = 0;
@@ -132,18 +134,32 @@ wtconv_status_t wtconv_adamw_step(const wtconv_adamw_desc_t* d, int32_t n, void*
         const hipError_t err = a.n ? wtc::adamw_launch(a, wgs, bf16, d->g_dtype == WTCONV_BF16, mode,
                                                        (hipStream_t)stream)
                                    : hipSuccess;
-        a.n = 0;
+        a.n = a.rates = 0;
         wgs = 0;
         return err;
     };
+    // the place of a tensor's rates in the launch's table; its length where there is no room
+    auto rates_of = [&](int i) {
+        for (int r = a.rates - 1; r >= 0; --r)
+            if (a.lr[r] == lr[i] && a.wd[r] == weight_decay[i]) return r;
+        if (a.rates < wtc::ADAM_RATES) {
+            a.lr[a.rates] = lr[i];
+            a.wd[a.rates] = weight_decay[i];
+            return a.rates++;
+        }
+        return wtc::ADAM_RATES;
+    };
     for (int i = 0; i < n; ++i) {
         if (grads[i] && counts[i] > 0) {
-            const uint32_t more = (uint32_t)((counts[i] + wtc::ADAM_PIECE - 1) / wtc::ADAM_PIECE);   // 2^22 at most
-            // a grid has fewer than 2^32 lanes
-            if (a.n == wtc::ADAM_TENSORS || wgs + more > 1u << 23)
+            const uint32_t more = (uint32_t)((counts[i] + wtc::ADAM_PIECE - 1) / wtc::ADAM_PIECE);   // 2^24 at most
+            int r = rates_of(i);
+            if (a.n == wtc::ADAM_TENSORS || wgs + more > 1u << 30 || r == wtc::ADAM_RATES) {
                 if (const hipError_t err = flush(); err != hipSuccess) return done(err);
-            a.t[a.n++] = {params[i], grads[i], (uint64_t)counts[i], (uint32_t)block, wgs, lr[i], weight_decay[i],
-                          (uint32_t)d->site + (uint32_t)i, 0};
+                r = rates_of(i);
+            }
+            const uint64_t last = (uint64_t)counts[i] - 1;
+            a.t[a.n++] = {params[i], grads[i], (uint32_t)last, (uint32_t)block, wgs,
+                          (uint32_t)i | (uint32_t)r << 26 | (uint32_t)(last >> 32) << 30};
             wgs += more;
         }
         block += blocks_of(counts[i]);
@@ -174,7 +190,7 @@ wtconv_status_t wtconv_grad_norm(int32_t n, const void* const* grads, const int6
         if (!grads[i] || counts[i] == 0) continue;
         const size_t e = elem_bytes(dtypes[i]);
         const uint64_t bytes = (uint64_t)counts[i] * e;
-        if (!aligned(grads[i], e) || hit(grads[i], bytes, out, 8) || hit(grads[i], bytes, step, 8) ||
+        if (!aligned(grads[i], e) || (uint64_t)(uintptr_t)grads[i] >> 48 || hit(grads[i], bytes, out, 8) || hit(grads[i], bytes, step, 8) ||
             hit(grads[i], bytes, ws, need))
             return WTCONV_ERR_INVALID_ARG;
     }
@@ -195,7 +211,10 @@ wtconv_status_t wtconv_grad_norm(int32_t n, const void* const* grads, const int6
         a.n = 0;
         for (; first < at; ++first)
             if (grads[first] && counts[first] > 0) {
-                a.t[a.n++] = {grads[first], (uint64_t)counts[first], wgs, dtypes[first] == WTCONV_BF16};
+                const uint64_t g = (uintptr_t)grads[first] | (dtypes[first] == WTCONV_BF16),
+                               last = (uint64_t)counts[first] - 1;
+                a.t[a.n++] = {{(uint32_t)g, (uint32_t)(g >> 32) | (uint32_t)last << 16,
+                               (uint32_t)(last >> 16) | wgs << 18}};
                 wgs += (uint32_t)(((uint64_t)counts[first] + a.piece - 1) / a.piece);
             }
         if (a.n == 0) continue;
