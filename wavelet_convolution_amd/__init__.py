@@ -36,31 +36,19 @@ __all__ = ["CONFIGS", "WorkloadConfig", "get_config", *_BINDING_NAMES, *_MODULE_
            *_BLOCK_NAMES, *_EXPERT_BINDING_NAMES, *_EXPERT_NAMES, *_OPTIM_BINDING_NAMES, *_OPTIM_NAMES]
 
 
+# the module of each name: imported on first use, so that CPU-only code
+# (configs, inputs, the I/O model) never needs the HIP runtime
+_HOMES = {name: home for home, names in (
+    ("binding", _BINDING_NAMES), ("module", _MODULE_NAMES), ("block_binding", _BLOCK_BINDING_NAMES),
+    ("block", _BLOCK_NAMES), ("expert_binding", _EXPERT_BINDING_NAMES), ("experts", _EXPERT_NAMES),
+    ("optim_binding", _OPTIM_BINDING_NAMES), ("optim", _OPTIM_NAMES)) for name in names}
+
+
 def __getattr__(name):
-    # the binding is imported on first use so that CPU-only code (configs,
-    # inputs, the I/O model) never needs the HIP runtime
-    if name in _BINDING_NAMES:
-        from . import binding
-        return getattr(binding, name)
-    if name in _MODULE_NAMES:
-        from . import module
-        return getattr(module, name)
-    if name in _BLOCK_BINDING_NAMES:
-        from . import block_binding
-        return getattr(block_binding, name)
-    if name in _BLOCK_NAMES:
-        from . import block
-        return getattr(block, name)
-    if name in _EXPERT_BINDING_NAMES:
-        from . import expert_binding
-        return getattr(expert_binding, name)
-    if name in _EXPERT_NAMES:
-        from . import experts
-        return getattr(experts, name)
-    if name in _OPTIM_BINDING_NAMES:
-        from . import optim_binding
-        return getattr(optim_binding, name)
-    if name in _OPTIM_NAMES:
-        from . import optim
-        return getattr(optim, name)
-    raise AttributeError(name)
+    home = _HOMES.get(name)
+    if home is None:
+        raise AttributeError(name)
+    import importlib
+    # kept: the next use does not come here
+    value = globals()[name] = getattr(importlib.import_module(f".{home}", __name__), name)
+    return value

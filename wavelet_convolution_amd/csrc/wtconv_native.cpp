@@ -4,14 +4,17 @@
 // parameters is walked here because an attribute of a tensor costs Python 50
 // to 100 ns: 330 gradients were 150 us that way, ten times the norm's own time.
 //
-// Every function takes positional arguments and the raw stream last; the
-// tensors' device is the current one. What a caller got wrong is a ValueError,
-// what the library refuses is its status' WTConvError.
+// Every function takes positional arguments and enqueues on the current stream
+// of the tensors' device, which has to be the current one: where it is not, the
+// answer is NotImplemented, and the caller comes back from there. What a caller
+// got wrong is a ValueError, what the library refuses is its status' WTConvError.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/hip/HIPFunctions.h>
+#include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <sstream>
@@ -25,7 +28,8 @@ namespace {
 struct Refused : std::runtime_error {
     using std::runtime_error::runtime_error;
 };
-struct Raised {};   // Python's error is set
+struct Raised {};      // Python's error is set
+struct Elsewhere {};   // another device is the current one
 
 template <class... A>
 [[noreturn]] void refuse(const A&... parts) {
@@ -40,6 +44,8 @@ PyObject* guarded(F&& f) {
     try {
         return f();
     } catch (const Raised&) {
+    } catch (const Elsewhere&) {
+        Py_RETURN_NOTIMPLEMENTED;
     } catch (const Refused& e) {
         PyErr_SetString(PyExc_ValueError, e.what());
     } catch (const std::exception& e) {
@@ -111,7 +117,11 @@ double real(PyObject* o) {
     if (v == -1. && PyErr_Occurred()) throw Raised();
     return v;
 }
-void* stream_of(PyObject* o) { return (void*)(uintptr_t)PyLong_AsUnsignedLongLong(o); }
+// The current stream of the call's device, which is the current device.
+void* stream_of(const at::Tensor& t) {
+    if (t.get_device() != c10::hip::current_device()) throw Elsewhere();
+    return (void*)c10::hip::getCurrentHIPStream(t.get_device()).stream();
+}
 
 // A workspace: the caller's, from its next multiple of 256 bytes on, or a new one.
 struct Workspace {
@@ -160,10 +170,11 @@ PyObject* tuple_of(std::initializer_list<const at::Tensor*> ts) {
     return r;
 }
 
-// expert, experts, order, place, offsets, ws, stream
+// expert, experts, order, place, offsets, ws
 PyObject* expert_sort(PyObject*, PyObject* const* a, Py_ssize_t) {
     return guarded([&] {
         const at::Tensor& e = tensor("expert", a[0]);
+        void* const stream = stream_of(e);
         const bool wide = e.scalar_type() == at::kLong;
         if ((!wide && e.scalar_type() != at::kInt) || e.dim() < 2 || !e.is_contiguous())
             refuse("expert must be a contiguous int32 or int64 tensor [..., K]; got ", e.sizes(), " ", e.scalar_type(),
@@ -180,7 +191,7 @@ PyObject* expert_sort(PyObject*, PyObject* const* a, Py_ssize_t) {
         const Workspace ws(a[5], need, e);
         check_status(wtconv_expert_sort(&d, e.const_data_ptr(), wide ? WTCONV_I64 : WTCONV_I32,
                                         order.mutable_data_ptr<int32_t>(), place.mutable_data_ptr<int32_t>(),
-                                        offsets.mutable_data_ptr<int32_t>(), ws.p, ws.bytes, stream_of(a[6])));
+                                        offsets.mutable_data_ptr<int32_t>(), ws.p, ws.bytes, stream));
         return tuple_of({&order, &place, &offsets});
     });
 }
@@ -225,51 +236,55 @@ std::vector<int64_t> token_shape(const at::Tensor& place, int64_t c) {
     return s;
 }
 
-// x, place, offsets, xs, stream
+// x, place, offsets, xs
 PyObject* expert_rows_fwd(PyObject*, PyObject* const* a, Py_ssize_t) {
     return guarded([&] {
         const at::Tensor& x = rows_arg("x", a[0]);
+        void* const stream = stream_of(x);
         const Route r = route(a[1], a[2], x);
         check_token_rows("x", x, r.place);
         const at::Tensor xs = output("xs", a[3], x, x.scalar_type(), {r.place.numel(), x.size(-1)});
         check_status(wtconv_expert_rows_fwd(&r.d, x.const_data_ptr(), r.at, r.ends, xs.mutable_data_ptr(),
-                                            stream_of(a[4])));
+                                            stream));
         return THPVariable_Wrap(xs);
     });
 }
 
-// dxs, place, offsets, dx, stream
+// dxs, place, offsets, dx
 PyObject* expert_rows_bwd(PyObject*, PyObject* const* a, Py_ssize_t) {
     return guarded([&] {
         const at::Tensor& dxs = rows_arg("dxs", a[0]);
+        void* const stream = stream_of(dxs);
         const Route r = route(a[1], a[2], dxs);
         check_sorted_rows("dxs", dxs, r.place);
         const at::Tensor dx = output("dx", a[3], dxs, dxs.scalar_type(), token_shape(r.place, dxs.size(-1)));
         check_status(wtconv_expert_rows_bwd(&r.d, dxs.const_data_ptr(), r.at, r.ends, dx.mutable_data_ptr(),
-                                            stream_of(a[4])));
+                                            stream));
         return THPVariable_Wrap(dx);
     });
 }
 
-// ys, weight, place, offsets, y, stream
+// ys, weight, place, offsets, y
 PyObject* expert_sum_fwd(PyObject*, PyObject* const* a, Py_ssize_t) {
     return guarded([&] {
         const at::Tensor& ys = rows_arg("ys", a[0]);
+        void* const stream = stream_of(ys);
         const Route r = route(a[2], a[3], ys);
         check_sorted_rows("ys", ys, r.place);
         const at::Tensor& w = tensor("weight", a[1], &ys);
         check_dense("weight", w, at::kFloat, r.place.sizes());
         const at::Tensor y = output("y", a[4], ys, ys.scalar_type(), token_shape(r.place, ys.size(-1)));
         check_status(wtconv_expert_sum_fwd(&r.d, ys.const_data_ptr(), w.const_data_ptr<float>(), r.at, r.ends,
-                                           y.mutable_data_ptr(), stream_of(a[5])));
+                                           y.mutable_data_ptr(), stream));
         return THPVariable_Wrap(y);
     });
 }
 
-// dy, ys, weight, place, offsets, want dys, want dweight, dys, dweight, stream
+// dy, ys, weight, place, offsets, want dys, want dweight, dys, dweight
 PyObject* expert_sum_bwd(PyObject*, PyObject* const* a, Py_ssize_t) {
     return guarded([&] {
         const at::Tensor& dy = rows_arg("dy", a[0]);
+        void* const stream = stream_of(dy);
         const Route r = route(a[3], a[4], dy);
         check_token_rows("dy", dy, r.place);
         const at::Tensor& ys = tensor("ys", a[1], &dy);
@@ -281,7 +296,7 @@ PyObject* expert_sum_bwd(PyObject*, PyObject* const* a, Py_ssize_t) {
         if (a[6] == Py_True) dw = output("dweight", a[8], dy, at::kFloat, r.place.sizes());
         check_status(wtconv_expert_sum_bwd(&r.d, dy.const_data_ptr(), ys.const_data_ptr(), w.const_data_ptr<float>(),
                                            r.at, r.ends, dys.defined() ? dys.mutable_data_ptr() : nullptr,
-                                           dw.defined() ? dw.mutable_data_ptr<float>() : nullptr, stream_of(a[9])));
+                                           dw.defined() ? dw.mutable_data_ptr<float>() : nullptr, stream));
         return tuple_of({&dys, &dw});
     });
 }
@@ -350,7 +365,7 @@ PyObject* adamw_state_count(PyObject*, PyObject* const* a, Py_ssize_t) {
     });
 }
 
-// params, grads, m, v, step, lr, weight_decay, beta1, beta2, eps, scales, master, factor, lr_factor, rng, site, stream
+// params, grads, m, v, step, lr, weight_decay, beta1, beta2, eps, scales, master, factor, lr_factor, rng, site
 PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t) {
     return guarded([&]() -> PyObject* {
         const Items params("params", a[0]), grads("grads", a[1]);
@@ -380,6 +395,7 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t) {
                 refuse("gradients must have their parameters' shapes; got ", u.sizes(), " for ", t.sizes());
             g[i] = u.const_data_ptr();
         }
+        void* const stream = stream_of(*like);
         const int64_t all = wtconv_adamw_state_count(counts.data(), n);
         if (all < 0) check_status(WTCONV_ERR_UNSUPPORTED_SHAPE);
         const bool eight = a[10] != Py_None;
@@ -417,7 +433,7 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t) {
                                     real(a[8]), real(a[9])};
         check_status(wtconv_adamw_step(&d, n, p.data(), g.data(), counts.data(), lr, wd, m.mutable_data_ptr(),
                                        v.mutable_data_ptr(), scales, master, (const int64_t*)step,
-                                       (const float*)factor, (const float*)lr_factor, rng, stream_of(a[16])));
+                                       (const float*)factor, (const float*)lr_factor, rng, stream));
         // autograd's own record of changes in place, as torch's operations keep it
         for (int32_t i = 0; i < n; ++i) {
             const at::Tensor& t = THPVariable_Unpack(params.o[i]);
@@ -427,7 +443,7 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t) {
     });
 }
 
-// grads, max_norm, step, out, ws, stream
+// grads, max_norm, step, out, ws
 PyObject* grad_norm(PyObject*, PyObject* const* a, Py_ssize_t) {
     return guarded([&] {
         const Items grads("grads", a[0]);
@@ -445,13 +461,14 @@ PyObject* grad_norm(PyObject*, PyObject* const* a, Py_ssize_t) {
             g[n++] = t.const_data_ptr();
         }
         if (n == 0) refuse("at least one gradient is required");
+        void* const stream = stream_of(*like);
         const double most = real(a[1]);
         if (!(most > 0)) refuse("max_norm must be above 0 (infinity: no clipping); got ", most);
         const at::Tensor out = output("out", a[3], *like, at::kFloat, {2});
         const void* step = scalar("step", a[2], at::kLong, *like);
         const Workspace ws(a[4], wtconv_grad_norm_workspace_size(n), *like);
         check_status(wtconv_grad_norm(n, g.data(), counts.data(), types.data(), most, (int64_t*)step,
-                                      out.mutable_data_ptr<float>(), ws.p, ws.bytes, stream_of(a[5])));
+                                      out.mutable_data_ptr<float>(), ws.p, ws.bytes, stream));
         return THPVariable_Wrap(out);
     });
 }
@@ -472,14 +489,14 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef methods[] = {
-    method<expert_sort, 7>("expert_sort"),
-    method<expert_rows_fwd, 5>("expert_rows_fwd"),
-    method<expert_rows_bwd, 5>("expert_rows_bwd"),
-    method<expert_sum_fwd, 6>("expert_sum_fwd"),
-    method<expert_sum_bwd, 10>("expert_sum_bwd"),
+    method<expert_sort, 6>("expert_sort"),
+    method<expert_rows_fwd, 4>("expert_rows_fwd"),
+    method<expert_rows_bwd, 4>("expert_rows_bwd"),
+    method<expert_sum_fwd, 5>("expert_sum_fwd"),
+    method<expert_sum_bwd, 9>("expert_sum_bwd"),
     method<adamw_state_count, 1>("adamw_state_count"),
-    method<adamw_step, 17>("adamw_step"),
-    method<grad_norm, 6>("grad_norm"),
+    method<adamw_step, 16>("adamw_step"),
+    method<grad_norm, 5>("grad_norm"),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

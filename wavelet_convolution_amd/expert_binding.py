@@ -10,17 +10,8 @@ on which outputs are then allocated too). There is no fallback.
 """
 from __future__ import annotations
 
-import torch
-
 from . import binding as _b
-from .block_binding import _elsewhere, _enter, _stream, _wanted
-
-
-def _first(name: str, t) -> None:
-    """The tensor whose device the call runs on."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda):
-        raise ValueError(f"{name} must be a GPU tensor, got one on "
-                         f"{t.device if isinstance(t, torch.Tensor) else type(t).__name__}")
+from .block_binding import _elsewhere, _enter, _wanted
 
 
 def wtconv_expert_sort(expert, experts: int, *, order=None, place=None, offsets=None, ws=None, stream=None):
@@ -28,46 +19,50 @@ def wtconv_expert_sort(expert, experts: int, *, order=None, place=None, offsets=
     0..experts-1 is no expert): order [N * K] lists the slots (row * K + k) sorted by expert, each expert's in their
     own order and those of none last, place (expert's shape) is each slot's place in it, and expert e's places are
     offsets[e] .. offsets[e + 1] - 1 (offsets[1:] are the ends that a grouped product takes)."""
-    _first("expert", expert)
-    if _elsewhere(expert, stream):
-        return _enter(wtconv_expert_sort, expert, stream, (expert, order, place, offsets, ws), expert, experts,
-                      order=order, place=place, offsets=offsets, ws=ws)
-    return _b.load_native().expert_sort(expert, experts, order, place, offsets, ws, _stream(expert))
+    if stream is None or not _elsewhere(expert, stream):
+        r = _b.load_native().expert_sort(expert, experts, order, place, offsets, ws)
+        if r is not NotImplemented:
+            return r
+    return _enter(wtconv_expert_sort, expert, stream, (expert, order, place, offsets, ws), expert, experts,
+                  order=order, place=place, offsets=offsets, ws=ws)
 
 
 def wtconv_expert_rows_fwd(x, place, offsets, *, xs=None, stream=None):
     """xs [N * K, C]: row place[n, k] is row n of x [..., C]; rows of slots without an expert are zeros."""
-    _first("x", x)
-    if _elsewhere(x, stream):
-        return _enter(wtconv_expert_rows_fwd, x, stream, (x, place, offsets, xs), x, place, offsets, xs=xs)
-    return _b.load_native().expert_rows_fwd(x, place, offsets, xs, _stream(x))
+    if stream is None or not _elsewhere(x, stream):
+        r = _b.load_native().expert_rows_fwd(x, place, offsets, xs)
+        if r is not NotImplemented:
+            return r
+    return _enter(wtconv_expert_rows_fwd, x, stream, (x, place, offsets, xs), x, place, offsets, xs=xs)
 
 
 def wtconv_expert_rows_bwd(dxs, place, offsets, *, dx=None, stream=None):
     """dx [..., C] of wtconv_expert_rows_fwd: the sum of each row's slots' rows of dxs [N * K, C]."""
-    _first("dxs", dxs)
-    if _elsewhere(dxs, stream):
-        return _enter(wtconv_expert_rows_bwd, dxs, stream, (dxs, place, offsets, dx), dxs, place, offsets, dx=dx)
-    return _b.load_native().expert_rows_bwd(dxs, place, offsets, dx, _stream(dxs))
+    if stream is None or not _elsewhere(dxs, stream):
+        r = _b.load_native().expert_rows_bwd(dxs, place, offsets, dx)
+        if r is not NotImplemented:
+            return r
+    return _enter(wtconv_expert_rows_bwd, dxs, stream, (dxs, place, offsets, dx), dxs, place, offsets, dx=dx)
 
 
 def wtconv_expert_sum_fwd(ys, weight, place, offsets, *, y=None, stream=None):
     """y [..., C]: the sum over each row's slots of weight (place's shape, fp32) times the slot's row of ys
     [N * K, C]. Slots without an expert count nothing, whatever their weight and their row of ys hold."""
-    _first("ys", ys)
-    if _elsewhere(ys, stream):
-        return _enter(wtconv_expert_sum_fwd, ys, stream, (ys, weight, place, offsets, y), ys, weight, place, offsets,
-                      y=y)
-    return _b.load_native().expert_sum_fwd(ys, weight, place, offsets, y, _stream(ys))
+    if stream is None or not _elsewhere(ys, stream):
+        r = _b.load_native().expert_sum_fwd(ys, weight, place, offsets, y)
+        if r is not NotImplemented:
+            return r
+    return _enter(wtconv_expert_sum_fwd, ys, stream, (ys, weight, place, offsets, y), ys, weight, place, offsets, y=y)
 
 
 def wtconv_expert_sum_bwd(dy, ys, weight, place, offsets, *, want=("dys", "dweight"), dys=None, dweight=None,
                           stream=None):
     """(dys, dweight) of wtconv_expert_sum_fwd: rows weight * dy for the slots, zeros for those without an expert,
     and the products <dy, ys>. `want`: the names of the gradients to compute; the others are None."""
-    _first("dy", dy)
-    if _elsewhere(dy, stream):
-        return _enter(wtconv_expert_sum_bwd, dy, stream, (dy, ys, weight, place, offsets, dys, dweight), dy, ys,
-                      weight, place, offsets, want=want, dys=dys, dweight=dweight)
     wants = _wanted(want, ("dys", "dweight"))
-    return _b.load_native().expert_sum_bwd(dy, ys, weight, place, offsets, *wants, dys, dweight, _stream(dy))
+    if stream is None or not _elsewhere(dy, stream):
+        r = _b.load_native().expert_sum_bwd(dy, ys, weight, place, offsets, *wants, dys, dweight)
+        if r is not NotImplemented:
+            return r
+    return _enter(wtconv_expert_sum_bwd, dy, stream, (dy, ys, weight, place, offsets, dys, dweight), dy, ys, weight,
+                  place, offsets, want=want, dys=dys, dweight=dweight)

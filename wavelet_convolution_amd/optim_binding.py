@@ -14,8 +14,7 @@ from __future__ import annotations
 import math
 
 from . import binding as _b
-from .block_binding import _elsewhere, _enter, _stream
-from .expert_binding import _first
+from .block_binding import _elsewhere, _enter
 
 BLOCK = 256
 
@@ -38,17 +37,13 @@ def wtconv_adamw_step(params, grads, m, v, step, *, lr, weight_decay, betas=(0.9
     copies of bf16 parameters, laid out as the states. rng (int64 {seed, offset} on the GPU): states in 8 bits are
     rounded stochastically; tensor i uses the generator's site + i."""
     params, grads = list(params), list(grads)
-    if not params:
-        raise ValueError("one parameter at least is required")
-    _first("params", params[0])
-    if _elsewhere(params[0], stream):
-        held = (params, grads, m, v, step, scales, master, factor, lr_factor, rng)
-        return _enter(wtconv_adamw_step, params[0], stream, held, params, grads, m, v, step, lr=lr,
-                      weight_decay=weight_decay, betas=betas, eps=eps, scales=scales, master=master, factor=factor,
-                      lr_factor=lr_factor, rng=rng, site=site)
-    b1, b2 = betas
-    _b.load_native().adamw_step(params, grads, m, v, step, lr, weight_decay, b1, b2, eps, scales, master, factor,
-                                lr_factor, rng, site, _stream(params[0]))
+    if stream is None or not params or not _elsewhere(params[0], stream):
+        if _b.load_native().adamw_step(params, grads, m, v, step, lr, weight_decay, *betas, eps, scales, master,
+                                       factor, lr_factor, rng, site) is not NotImplemented:
+            return
+    held = (params, grads, m, v, step, scales, master, factor, lr_factor, rng)
+    _enter(wtconv_adamw_step, params[0], stream, held, params, grads, m, v, step, lr=lr, weight_decay=weight_decay,
+           betas=betas, eps=eps, scales=scales, master=master, factor=factor, lr_factor=lr_factor, rng=rng, site=site)
 
 
 def wtconv_grad_norm(grads, max_norm: float = math.inf, *, step=None, out=None, ws=None, stream=None):
@@ -57,10 +52,8 @@ def wtconv_grad_norm(grads, max_norm: float = math.inf, *, step=None, out=None, 
     one where it is finite. ws: a workspace (allocated if None)."""
     grads = list(grads)
     first = next((t for t in grads if t is not None), None)
-    if first is None:
-        raise ValueError("at least one gradient is required")
-    _first("grads", first)
-    if _elsewhere(first, stream):
-        return _enter(wtconv_grad_norm, first, stream, (grads, step, out, ws), grads, max_norm, step=step, out=out,
-                      ws=ws)
-    return _b.load_native().grad_norm(grads, max_norm, step, out, ws, _stream(first))
+    if stream is None or first is None or not _elsewhere(first, stream):
+        r = _b.load_native().grad_norm(grads, max_norm, step, out, ws)
+        if r is not NotImplemented:
+            return r
+    return _enter(wtconv_grad_norm, first, stream, (grads, step, out, ws), grads, max_norm, step=step, out=out, ws=ws)
