@@ -173,6 +173,32 @@ def test_infinities_and_nan_stay_in_their_rows():
 
 
 @pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("C", [5, 8, 21, 97, 200])
+def test_infinities_do_not_reach_other_sums(C, t):
+    """An infinity in dy or ys gives infinite products in its own slots, none in slots without an expert, and no NaN
+    where a row's vectors overlap."""
+    N, K, E = 70, 2, 4
+    place, offsets, x, ys, w, dy = routed(N, K, E, C, t)
+    live = live_of(place, offsets).view(N, K)
+    ys[torch.arange(N * K, device=DEV) < offsets[-1]] = 1
+    dy.fill_(1)
+    one = int(live.all(1).nonzero()[0])
+    for j in range(C):
+        for row in (0, one, int((~live).any(1).nonzero()[0])):
+            bad = dy.clone()
+            bad[row, j] = float("inf")
+            dys, dw = eb.wtconv_expert_sum_bwd(bad, ys, w, place, offsets)
+            want = torch.where(live, float(C), 0.0)
+            want[row] = torch.where(live[row], float("inf"), 0.0)
+            assert torch.equal(dw, want), (C, j, row)
+        bad = ys.clone()
+        bad[place[one, 0].long(), j] = float("inf")
+        want = torch.where(live, float(C), 0.0)
+        want[one, 0] = float("inf")
+        assert torch.equal(eb.wtconv_expert_sum_bwd(dy, bad, w, place, offsets)[1], want), (C, j)
+
+
+@pytest.mark.parametrize("t", TYPES)
 def test_pointers_aligned_to_the_element_only(t):
     place, offsets, x, ys, w, dy = routed(90, 2, 4, 33, t)
 

@@ -203,6 +203,11 @@ struct Vec {
                     p[i] = (T)(w[i / 2] >> (16 * (i % 2)));
             }
     }
+    // zeros otherwise, whatever was loaded
+    __device__ __forceinline__ void keep_if(bool yes) {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] = yes ? w[i] : 0u;
+    }
     __device__ __forceinline__ void renew() {
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) asm volatile("" : "+v"(w[i]));

@@ -73,8 +73,8 @@ __global__ __launch_bounds__(T) void k_expert_move(ExpertArgs a, uint32_t G, uin
                 Vec<X, CG> q[KK];
 #pragma unroll
                 for (int i = 0; i < KK; ++i) {
-                    q[i].zero();
-                    if (s[i].live) load(q[i], a.sorted, s[i].at);
+                    load(q[i], a.sorted, s[i].live ? s[i].at : 0);
+                    q[i].keep_if(s[i].live);
                 }
 #pragma unroll
                 for (int i = 0; i < KK; ++i) {
@@ -122,18 +122,26 @@ hipError_t move_by_op(const ExpertArgs& a, int op, hipStream_t s) {
     return move_by_k<X, SUM_FWD>(a, s);
 }
 
-// The sum's gradients: L lanes hold a row, UN vectors of it at a time, read dy
-// once and each of its K rows of ys, write w dy in their places, and sum up
-// <dy, ys>, of which a vector that moved back counts the channels of its own.
-constexpr int UN = 3;
+// The sum's gradients: L lanes hold a row, a vector each (rows of more than 64
+// vectors in rounds), read dy once and each of its K rows of ys, write w dy in
+// their places, and sum up <dy, ys>, of which a vector that moved back counts
+// the channels of its own. Fewer lanes with three vectors each were slower
+// (401,408 slots of 96 bf16 channels 47.5 us against 42.3; 25,088 of 384 the
+// same 11.5).
 template <typename X, int L, int KK, bool PART>
 __device__ __forceinline__ void expert_sum_bwd_wg(const ExpertArgs& a, uint32_t G, uint64_t wg, uint32_t S,
                                                   uint32_t kept) {
     const uint64_t row = (wg * T + threadIdx.x) / L;
     const uint32_t lane = threadIdx.x % L;
     const bool in = row < (uint64_t)a.N;
-    const X* dy = (const X*)a.rows + row * a.C;
+    const X* dy = (const X*)a.rows + (in ? row * a.C : 0);
     const int* place = a.place + row * a.K;
+    auto load = [&](Vec<X, CG>& v, const X* p, uint32_t c) {
+        if constexpr (PART)
+            v.load_part(p, a.C);
+        else
+            v.load(p + c);
+    };
     for (int k = 0; k < a.K; k += KK) {
         Slot s[KK];
         float w[KK], dot[KK];
@@ -143,51 +151,28 @@ __device__ __forceinline__ void expert_sum_bwd_wg(const ExpertArgs& a, uint32_t 
             w[i] = s[i].live && a.to_sorted ? a.w[row * a.K + k + i] : 0.f;
             dot[i] = 0.f;
         }
-        for (uint32_t v0 = lane; v0 < G; v0 += UN * L) {
-            Vec<X, CG> d[UN], y[UN][KK];
-            uint32_t c[UN], shared[UN];
+        for (uint32_t v = lane; v < G; v += L) {
+            const uint32_t c = PART ? 0 : min(v * CG, (uint32_t)a.C - CG), shared = v * CG - c;
+            Vec<X, CG> d, y[KK];
+            load(d, dy, c);
 #pragma unroll
-            for (int u = 0; u < UN; ++u) {
-                const uint32_t first = (v0 + u * L) * CG;
-                const bool on = in && first < (uint32_t)a.C;
-                c[u] = PART ? 0 : min(first, (uint32_t)a.C - CG);
-                shared[u] = on ? first - c[u] : CG;   // off: counts nothing
-                d[u].zero();
-                if (on) {
+            for (int i = 0; i < KK; ++i)
+                if (a.dw) load(y[i], (const X*)a.sorted + (s[i].live ? (size_t)s[i].at * a.C : 0), c);
+#pragma unroll
+            for (int i = 0; i < KK; ++i) {
+                float o[CG];
+#pragma unroll
+                for (int j = 0; j < CG; ++j) {
+                    o[j] = s[i].live ? w[i] * d[j] : 0.f;
+                    const float more = fmaf(d[j], y[i][j], dot[i]);
+                    dot[i] = (uint32_t)j < shared || !s[i].live ? dot[i] : more;
+                }
+                if (s[i].is && a.to_sorted) {
+                    X* out = (X*)a.to_sorted + (size_t)s[i].at * a.C;
                     if constexpr (PART)
-                        d[u].load_part(dy, a.C);
+                        store_part<X, CG>(out, o, a.C);
                     else
-                        d[u].load(dy + c[u]);
-                }
-#pragma unroll
-                for (int i = 0; i < KK; ++i) {
-                    y[u][i].zero();
-                    if (on && s[i].live && a.dw) {
-                        const X* ys = (const X*)a.sorted + (size_t)s[i].at * a.C;
-                        if constexpr (PART)
-                            y[u][i].load_part(ys, a.C);
-                        else
-                            y[u][i].load(ys + c[u]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < UN; ++u) {
-#pragma unroll
-                for (int i = 0; i < KK; ++i) {
-                    float o[CG];
-#pragma unroll
-                    for (int j = 0; j < CG; ++j) {
-                        o[j] = s[i].live ? w[i] * d[u][j] : 0.f;
-                        dot[i] = fmaf(d[u][j], (uint32_t)j < shared[u] || !s[i].live ? 0.f : y[u][i][j], dot[i]);
-                    }
-                    if (shared[u] < CG && s[i].is && a.to_sorted) {
-                        X* out = (X*)a.to_sorted + (size_t)s[i].at * a.C;
-                        if constexpr (PART)
-                            store_part<X, CG>(out, o, a.C);
-                        else
-                            store_vec<X, CG>(out + c[u], o);
-                    }
+                        store_vec<X, CG>(out + c, o);
                 }
             }
         }
@@ -221,14 +206,14 @@ hipError_t sum_bwd_launch(const ExpertArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// The fewest lanes that hold a row in one round of UN vectors each.
+// The fewest lanes that hold a row.
 template <typename X, int KK>
 hipError_t sum_bwd_by_row(const ExpertArgs& a, hipStream_t s) {
     const int G = cdiv(a.C, CG);
-    if (G <= 4 * UN) return sum_bwd_launch<X, 4, KK>(a, s);
-    if (G <= 8 * UN) return sum_bwd_launch<X, 8, KK>(a, s);
-    if (G <= 16 * UN) return sum_bwd_launch<X, 16, KK>(a, s);
-    if (G <= 32 * UN) return sum_bwd_launch<X, 32, KK>(a, s);
+    if (G <= 4) return sum_bwd_launch<X, 4, KK>(a, s);
+    if (G <= 8) return sum_bwd_launch<X, 8, KK>(a, s);
+    if (G <= 16) return sum_bwd_launch<X, 16, KK>(a, s);
+    if (G <= 32) return sum_bwd_launch<X, 32, KK>(a, s);
     return sum_bwd_launch<X, 64, KK>(a, s);
 }
 
