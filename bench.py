@@ -315,11 +315,14 @@ def block_context(torch, wt, cfg, steps: int):
     residual in the place of torch's (`wtconv_own_norm_residual`), and as it is
     trained, with dropout on the hidden rows, a layer scale and whole samples
     dropped: torch's operators (`wtconv_train`) and this library's
-    (`wtconv_train_own`)."""
+    (`wtconv_train_own`). The same two with the optimizer's step, gradients
+    clipped to their norm and AdamW on all parameters: torch's
+    (`wtconv_train_step`) and this library's (`wtconv_train_step_own`)."""
     import torch.nn.functional as F
 
     from wavelet_convolution_amd.block import block_residual, channel_norm, counter_dropout, dropout_rng
     from wavelet_convolution_amd.module import wtconv
+    from wavelet_convolution_amd.optim import AdamW
 
     dev = torch.device("cuda:0")
     dt = torch.bfloat16 if cfg.dtype == "bf16" else torch.float32
@@ -382,6 +385,23 @@ def block_context(torch, wt, cfg, steps: int):
     blocks["wtconv_own_norm_residual"] = lambda x: own_block(x, False)
     blocks["wtconv_train"] = torch_train_block
     blocks["wtconv_train_own"] = lambda x: own_block(x, True)
+    blocks["wtconv_train_step"] = torch_train_block
+    blocks["wtconv_train_step_own"] = lambda x: own_block(x, True)
+
+    shared = [wt_wb, wt_wl, wt_sc, w1, b1, w2, b2, gamma]
+    torch_params, own_params = [*shared, ln_w, ln_b], [*shared, own_w, own_b]
+    torch_optim = torch.optim.AdamW(torch_params, lr=1e-6, fused=True)
+    own_optim = AdamW([dict(params=[p for p in own_params if p.dtype == d]) for d in {torch.float32, dt}], lr=1e-6,
+                      max_norm=1.0)
+
+    def optim_step(name):
+        if name == "wtconv_train_step":
+            torch.nn.utils.clip_grad_norm_(torch_params, 1.0)
+            torch_optim.step()
+            torch_optim.zero_grad()
+        elif name == "wtconv_train_step_own":
+            own_optim.step()
+            own_optim.zero_grad()
 
     out = {"what": f"ConvNeXt-style block (mixer, LayerNorm, {C}->{4 * C}->{C} MLP with GELU, residual), "
                    f"{B}x{C}x{H}x{W} {cfg.dtype}, forward + backward", "steps": steps}
@@ -389,9 +409,13 @@ def block_context(torch, wt, cfg, steps: int):
         def step(i, run=run):
             x = xs[i % nsets]
             run(x).backward(gs[i % nsets])
-            if name == "wtconv_train_own":
+            if name.endswith("own") and "train" in name:
                 rng[1] += 1
+            optim_step(name)
 
+        if "step" in name:
+            torch_optim.zero_grad()
+            own_optim.zero_grad()
         for i in range(2):
             step(i)
         torch.cuda.synchronize()
@@ -404,6 +428,8 @@ def block_context(torch, wt, cfg, steps: int):
     out["own_norm_residual_over_torch"] = round(out["wtconv_own_norm_residual_ms_per_step"] / out["wtconv_ms_per_step"],
                                                 3)
     out["train_own_over_torch"] = round(out["wtconv_train_own_ms_per_step"] / out["wtconv_train_ms_per_step"], 3)
+    out["train_step_own_over_torch"] = round(
+        out["wtconv_train_step_own_ms_per_step"] / out["wtconv_train_step_ms_per_step"], 3)
     out["wtconv_over_this_library_L0"] = round(out["wtconv_ms_per_step"] / out["this_library_L0_ms_per_step"], 3)
     del xs, gs
     torch.cuda.empty_cache()

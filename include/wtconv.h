@@ -80,7 +80,9 @@ typedef enum {
                                           range, H*W above 2^30 (block
                                           operators: or C), B*C above
                                           2^31 - 1, or 2^32 and more dropout
-                                          groups */
+                                          groups; expert rows and the
+                                          optimizer: sizes past those of
+                                          their descriptors */
     WTCONV_ERR_WORKSPACE = 3,          /* ws too small or misaligned */
     WTCONV_ERR_LAUNCH = 4,             /* the HIP runtime rejected a launch */
     WTCONV_ERR_SCRATCH_LIMIT = 5       /* wtconv_bwd_weight_noalloc: the call needs
@@ -443,7 +445,8 @@ wtconv_status_t wtconv_expert_sum_bwd(const wtconv_expert_desc_t *desc, const vo
  *     p  = p - r wd[i] p - r (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
  * Where f is not finite nothing is changed: out[1] of the norm as the factor
  * clips the gradients, and skips a step whose gradients have an infinity or
- * a NaN. All arithmetic is fp32.
+ * a NaN. (With another factor such a gradient makes its element not finite,
+ * with states in 8 bits its whole block.) All arithmetic is fp32.
  *
  * The states of all tensors stand in one buffer: tensor i's begin at element
  * 256 * sum_{j < i} ceil(counts[j] / 256). What stands between a tensor's last
@@ -499,7 +502,8 @@ size_t wtconv_grad_norm_workspace_size(int32_t n);
 
 /* dtypes: a wtconv_dtype_t for each gradient (host array, as grads and
    counts); max_norm > 0, infinity for no clipping. out: two fp32 numbers. A
-   NULL gradient counts nothing. */
+   NULL gradient counts nothing. Gradients are at addresses below 2^48, as
+   the GPU's are. */
 wtconv_status_t wtconv_grad_norm(int32_t n, const void *const *grads, const int64_t *counts,
                                  const int32_t *dtypes, double max_norm, int64_t *step, float *out, void *ws,
                                  size_t ws_bytes, void *stream);

@@ -123,6 +123,13 @@ def test_more_tensors_than_a_launch_takes(bits, random):
 
 
 @pytest.mark.parametrize("bits", [32, 8])
+def test_rates_of_every_tensor(bits):
+    """As many rates as tensors: more than a launch's table holds."""
+    n = 50
+    Call([(130,)] * n, bits=bits, seed=15, lr=[1e-3 * (1 + i) for i in range(n)], weight_decay=torch.linspace(0, 1, n)).check()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
 def test_large_tensor(bits):
     """Several rounds of workgroups over the card, beside small tensors."""
     Call([(7,), (5_000_011,), (300,)], p=BF16, g=BF16, master=True, bits=bits, random=bits == 8, seed=5).check()
@@ -380,6 +387,60 @@ def test_optimizer_state_round_trip(dtype, master, bits):
         AdamW(b.parameters(), **{**kw, "state_bits": 40 - bits}).load_state_dict(saved)
     with pytest.raises(ValueError):
         AdamW(list(b.parameters())[:2], **kw).load_state_dict(saved)
+
+
+def test_optimizer_copies_and_files(tmp_path):
+    """A copied optimizer goes on by itself; a state goes through a file that is read without executing anything."""
+    a = net()
+    o = AdamW(a.parameters(), state_bits=8, max_norm=1.0)
+    gradients(a, 0)
+    o.step()
+    b, p = copy.deepcopy((a, o))
+    assert p._buffers[0]["m"].data_ptr() != o._buffers[0]["m"].data_ptr() and p.max_norm == 1.0
+    torch.save(o.state_dict(), tmp_path / "state.pt")
+    c = copy.deepcopy(a)
+    q = AdamW(c.parameters(), state_bits=8, max_norm=1.0)
+    q.load_state_dict(torch.load(tmp_path / "state.pt", weights_only=True))
+    for m, r in ((a, o), (b, p), (c, q)):
+        gradients(m, 1)
+        r.step()
+    for x, y, z in zip(a.parameters(), b.parameters(), c.parameters()):
+        assert torch.equal(x, y) and torch.equal(x, z)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_optimizer_captured(bits):
+    """A whole training step in a graph, against the same steps outside of one."""
+    a, b = net(), net()
+    rng = [dropout_rng(1) if bits == 8 else None for _ in range(2)]
+    o, p = (AdamW(m.parameters(), lr=1e-2, state_bits=bits, max_norm=0.1, rng=r) for m, r in zip((a, b), rng))
+    x, y = data(0)
+
+    def step(m, opt):
+        for w, g in zip(m.parameters(), torch.autograd.grad(((m(x) - y) ** 2).mean(), list(m.parameters()))):
+            w.grad = g
+        opt.step()
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step(a, o)
+    torch.cuda.current_stream().wait_stream(s)
+    step(b, p)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(a, o)
+    for i in range(1, 5):
+        for t, n in zip((x, y), data(i)):
+            t.copy_(n)
+        for r in rng:
+            if r is not None:
+                r[1] += 1
+        graph.replay()
+        torch.cuda.synchronize()
+        step(b, p)
+        assert int(o._step) == int(p._step) == i + 1
+        assert all(torch.equal(u, v) for u, v in zip(a.parameters(), b.parameters()))
 
 
 def test_optimizer_skips_steps_that_are_not_finite():

@@ -177,7 +177,7 @@ def test_bad_norms(lib):
                        (dict(grads=((1 << 40) + 2, 2 << 40)), 1), (dict(grads=(1 << 40, (2 << 40) + 1)), 1),
                        (dict(step=(5 << 40) + 4), 1), (dict(counts=(-1, 5)), 2), (dict(counts=(1, (1 << 34) + 1)), 2),
                        (dict(ws=None), 3), (dict(bytes_=need - 1), 3), (dict(ws=(4 << 40) + 4), 3), (dict(out=1 << 40), 1),
-                       (dict(step=1 << 40), 1), (dict(ws=1 << 40), 1), (dict(step=3 << 40), 1), (dict(out=(4 << 40) + 8), 1)):
+                       (dict(step=1 << 40), 1), (dict(ws=1 << 40), 1), (dict(grads=(1 << 48, 2 << 40)), 1), (dict(step=3 << 40), 1), (dict(out=(4 << 40) + 8), 1)):
         assert norm(**kw) == status, kw
     assert lib.wtconv_grad_norm(1, None, None, None, 1.0, None, P[0], P[1], 1 << 20, None) == 1
 

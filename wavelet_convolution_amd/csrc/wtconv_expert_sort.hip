@@ -9,6 +9,8 @@
 // few slots alone (SORT_ALONE); else a first launch counts parts of 2,048 slots
 // and each part's workgroup sums up the counts of all (SORT_SUMS), or, where
 // those are many, a launch in between makes running sums of them (SORT_SCAN).
+// 16 experts: 2 slots 3.7 us, 4,096 6.3, 401,408 10.3 us (their 6.4 MB take 1.2);
+// 64 experts: 8.4 M slots 76 us, 1.8 TB/s.
 #include "wtconv_experts.h"
 
 namespace wtc {

@@ -44,7 +44,7 @@ struct AdamArgs {
     float lr[ADAM_RATES], wd[ADAM_RATES];
     AdamTensor t[ADAM_TENSORS];
 };
-static_assert(sizeof(AdamArgs) <= 4096, "");
+static_assert(sizeof(AdamArgs) + 8 <= 4096, "");   // and the number of workgroups
 
 enum { STATES_32 = 0, STATES_8 = 1, STATES_8_RANDOM = 2 };
 hipError_t adamw_launch(const AdamArgs& a, uint32_t wgs, int p_bf16, int g_bf16, int mode, hipStream_t s);

@@ -1,6 +1,9 @@
 // AdamW and the gradients' norm over many tensors. Memory is the bound: every
 // element of a parameter, its gradient and its states is read once and
-// written once.
+// written once (copy rate of the card 5.2 TB/s). AdamW: 34.6 M bf16 parameters
+// in 330 tensors with fp32 master copies, 28 bytes an element, 190 us, 5.1 TB/s;
+// 76 M with states in 8 bits, 16 bytes an element, 233 us, 5.2 TB/s. Norm: 34.6 M
+// bf16 elements 18.8 us, of which 6 are the latency of its two launches.
 #include "wtconv_block_device.h"
 #include "wtconv_optim.h"
 
@@ -68,7 +71,9 @@ __device__ __forceinline__ void widen_e4m3(uint32_t w, float unit, float (&o)[4]
 
 // A wavefront takes one block of 256 elements, a lane four of them, and ends:
 // the next one's loads are on their way while it computes, with more of them in
-// flight than a loop over blocks keeps.
+// flight than a loop over blocks keeps (four blocks a wavefront, two at a time:
+// 219 us for 190, with states in 8 bits 250 for 233; streaming stores change
+// neither).
 template <typename P, typename G, bool MASTER, int MODE>
 __global__ __launch_bounds__(T) void k_adamw(AdamArgs a, uint32_t wgs) {
     const float f = a.factor ? *a.factor : 1.f;
@@ -275,8 +280,10 @@ constexpr int TF = 1024;
 __global__ __launch_bounds__(TF) void k_norm_finish(const double* sums, uint32_t n, double max_norm, long long* step,
                                                     float* out) {
     double sum = 0.;
-#pragma unroll 4
-    for (uint32_t i = threadIdx.x; i < n; i += TF) sum += sums[i];
+    for (uint32_t i = threadIdx.x; i < n; i += 2 * TF) {   // both in flight: a launch leaves fewer than 2 TF
+        const double a = sums[i], b = i + TF < n ? sums[i + TF] : 0.;
+        sum += a + b;
+    }
     sum = wg_sum<TF>(sum);
     if (threadIdx.x == 0) {
         const double norm = sqrt(sum);
