@@ -408,6 +408,39 @@ def test_optimizer_copies_and_files(tmp_path):
         assert torch.equal(x, y) and torch.equal(x, z)
 
 
+def test_master_copies_are_made_again():
+    a = net(BF16)
+    o = AdamW(a.parameters(), lr=1e-2)
+    gradients(a, 0)
+    o.step()
+    other = net(BF16, seed=1)
+    a.load_state_dict(other.state_dict())
+    o.renew_master()
+    for p, q in zip(a.parameters(), other.parameters()):
+        p.grad = torch.zeros_like(p)
+        q.grad = torch.zeros_like(q)
+    o.param_groups[0]["lr"] = 0.0
+    o.step()
+    assert all(torch.equal(p, q) for p, q in zip(a.parameters(), other.parameters()))
+
+
+def test_optimizer_groups_of_other_bits():
+    """Large matrices in 8 bits, small vectors in 32: each group as an optimizer of its own."""
+    a = net()
+    b = copy.deepcopy(a)
+    groups = lambda m: [dict(params=[m[0].weight, m[2].weight]), dict(params=[m[0].bias, m[2].bias], state_bits=32)]  # noqa: E731
+    o = AdamW(groups(a), lr=1e-2, state_bits=8, rng=dropout_rng(4), site=9)
+    p = [AdamW([groups(b)[0]], lr=1e-2, state_bits=8, rng=dropout_rng(4), site=9), AdamW([groups(b)[1]], lr=1e-2)]
+    assert [x["state_bits"] for x in o.param_groups] == [8, 32]
+    for i in range(3):
+        for m, opts in ((a, [o]), (b, p)):
+            gradients(m, i)
+            for x in opts:
+                x.step()
+    assert [t.dtype for t in (o._buffers[0]["m"], o._buffers[1]["m"])] == [torch.float8_e4m3fn, F32]
+    assert all(torch.equal(x, y) for x, y in zip(a.parameters(), b.parameters()))
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_optimizer_captured(bits):
     """A whole training step in a graph, against the same steps outside of one."""

@@ -20,7 +20,8 @@ from . import optim_binding as _ob
 
 
 class AdamW(torch.optim.Optimizer):
-    """Parameter groups may set lr, betas, eps and weight_decay of their own.
+    """Parameter groups may set lr, betas, eps, weight_decay and state_bits of
+    their own.
 
     state_bits: 32 or 8 (a block of 256 elements shares a scale; the first
     moment and the second one's root are e4m3 numbers). rng: an int64
@@ -37,53 +38,63 @@ class AdamW(torch.optim.Optimizer):
     the host and waits for nothing, so it can be captured into a graph after a
     first step (a graph keeps lr and the other numbers of its capture, but for
     `lr_factor`, an optional fp32 number on the GPU that lr is multiplied by).
-    A group's states are made at its first step."""
+    A group's states are made at its first step, master copies from the
+    parameters as they are then: call `renew_master` after changing bf16
+    parameters in another way, or the next step goes on from the copies."""
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 1e-2,
                  state_bits: int = 32, master: bool = True, max_norm=None, rng=None, site: int = 0, lr_factor=None):
-        if not (0 <= lr < math.inf and 0 <= weight_decay < math.inf and eps > 0
-                and all(0 <= b < 1 for b in betas) and state_bits in (8, 32)):
-            raise ValueError("lr >= 0, weight_decay >= 0, eps > 0, betas in [0, 1) and state_bits 8 or 32 are required")
         if max_norm is not None and not max_norm > 0:
             raise ValueError(f"max_norm must be above 0, or None; got {max_norm}")
-        if rng is not None and state_bits != 8:
-            raise ValueError("rng is for states in 8 bits")
-        self.state_bits, self.master, self.max_norm = state_bits, master, max_norm
+        self.master, self.max_norm = master, max_norm
         self.rng, self.site, self.lr_factor = rng, site, lr_factor
         self.last_norm = self._step = None
         self._buffers = []   # of each group: None, or a dict of its states
-        super().__init__(params, dict(lr=lr, betas=tuple(betas), eps=eps, weight_decay=weight_decay))
+        super().__init__(params, dict(lr=lr, betas=tuple(betas), eps=eps, weight_decay=weight_decay,
+                                      state_bits=state_bits))
+        if rng is not None and all(g["state_bits"] != 8 for g in self.param_groups):
+            raise ValueError("rng is for states in 8 bits")
 
     def __getstate__(self):
-        own = ("state_bits", "master", "max_norm", "rng", "site", "lr_factor", "last_norm", "_step", "_buffers")
+        own = ("master", "max_norm", "rng", "site", "lr_factor", "last_norm", "_step", "_buffers")
         return {**super().__getstate__(), **{k: self.__dict__[k] for k in own}}
 
     def add_param_group(self, group):
         if self._step is not None:
             raise RuntimeError("parameter groups are added before the first step: all share its count")
         super().add_param_group(group)
-        params = self.param_groups[-1]["params"]
-        first = self.param_groups[0]["params"][0]
-        if any(p.dtype not in (torch.float32, torch.bfloat16) or p.dtype != params[0].dtype for p in params):
+        g, first = self.param_groups[-1], self.param_groups[0]["params"][0]
+        why = None
+        if any(p.dtype not in (torch.float32, torch.bfloat16) or p.dtype != g["params"][0].dtype for p in g["params"]):
+            why = "the parameters of a group must be all float32 or all bfloat16"
+        elif any(p.device != first.device for p in g["params"]):
+            why = "all parameters must be on one device"
+        elif not (0 <= g["lr"] < math.inf and 0 <= g["weight_decay"] < math.inf and g["eps"] > 0
+                  and all(0 <= b < 1 for b in g["betas"]) and g["state_bits"] in (8, 32)):
+            why = "lr >= 0, weight_decay >= 0, eps > 0, betas in [0, 1) and state_bits 8 or 32 are required"
+        if why:
             self.param_groups.pop()
-            raise ValueError("the parameters of a group must be all float32 or all bfloat16")
-        if any(p.device != first.device for p in params):
-            self.param_groups.pop()
-            raise ValueError("all parameters must be on one device")
+            raise ValueError(why)
         self._buffers.append(None)
 
-    def _make(self, params) -> dict:
+    def _make(self, group) -> dict:
+        params, eight = group["params"], group["state_bits"] == 8
         n, dev = _ob.wtconv_adamw_state_count(params), params[0].device
-        eight = self.state_bits == 8
         kind = torch.float8_e4m3fn if eight else torch.float32
         b = {"m": torch.zeros(n, dtype=kind, device=dev), "v": torch.zeros(n, dtype=kind, device=dev)}
         if eight:
             b["scales"] = torch.zeros(n // _ob.BLOCK, 2, device=dev)
         if self.master and params[0].dtype == torch.bfloat16:
             b["master"] = torch.zeros(n, device=dev)
-            for p, (at, count) in zip(params, _places(params)):
-                b["master"][at:at + count].copy_(p.detach().reshape(-1))
+            _copy(params, b["master"])
         return b
+
+    @torch.no_grad()
+    def renew_master(self) -> None:
+        """The master copies made again from the parameters."""
+        for g, b in zip(self.param_groups, self._buffers):
+            if b and "master" in b:
+                _copy(g["params"], b["master"])
 
     @torch.no_grad()
     def step(self, closure=None):
@@ -98,7 +109,7 @@ class AdamW(torch.optim.Optimizer):
             return loss
         for i, (g, _) in enumerate(groups):
             if self._buffers[i] is None:
-                self._buffers[i] = self._make(g["params"])
+                self._buffers[i] = self._make(g)
         if self._step is None:
             self._step = torch.zeros(1, dtype=torch.int64, device=grads[0].device)
         if self.max_norm is None:
@@ -112,7 +123,7 @@ class AdamW(torch.optim.Optimizer):
             if any(t is not None for t in ts):
                 _ob.wtconv_adamw_step(g["params"], ts, step=self._step, lr=g["lr"], weight_decay=g["weight_decay"],
                                       betas=g["betas"], eps=g["eps"], factor=factor, lr_factor=self.lr_factor,
-                                      rng=self.rng, site=site, **b)
+                                      rng=self.rng if g["state_bits"] == 8 else None, site=site, **b)
             site += len(ts)
         return loss
 
@@ -134,7 +145,7 @@ class AdamW(torch.optim.Optimizer):
             if b is None:
                 new.append(None)
                 continue
-            like = self._make(g["params"])
+            like = self._make(g)
             if like.keys() != b.keys() or any(like[k].shape != t.shape or like[k].dtype != t.dtype
                                               for k, t in b.items()):
                 raise ValueError("the state is of other parameters, or of other state_bits or master copies")
@@ -146,9 +157,9 @@ class AdamW(torch.optim.Optimizer):
             mine.update({k: v for k, v in other.items() if k != "params"})
 
 
-def _places(params):
-    """(first element, elements) of each tensor in the states' buffers."""
+def _copy(params, master) -> None:
+    """fp32 copies of the parameters, each at its place in the states' layout."""
     at = 0
     for p in params:
-        yield at, p.numel()
+        master[at:at + p.numel()].copy_(p.detach().reshape(-1))
         at += -(-p.numel() // _ob.BLOCK) * _ob.BLOCK
