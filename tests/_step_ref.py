@@ -164,15 +164,16 @@ class Step:
             em = U * 1.01 * ((1 + more) * (b1 * m0).abs() + 3 * ((1 - b1) * g).abs() + m.abs()) + 1e-44
             ev = U * 1.01 * ((1 + 3 * more) * (b2 * v0) + 6 * (1 - b2) * g * g + v) + 1e-44
             root, den = v.sqrt(), (v / c2).sqrt() + self.eps
-            # the root to half a step of its own; where v is (near) zero, by the square root of v's error
-            eroot = torch.minimum(ev / root.clamp(min=1e-300), (2 * ev).sqrt()) + U * 1.01 * root
+            # the root to one step of its own; where v is (near) zero, by the square root of v's error
+            eroot = torch.minimum(ev / root.clamp(min=1e-300), (2 * ev).sqrt()) + 2 * U * 1.01 * root
             rate = self.lr[i] / c1
             old = (self.old["master"][at] if self.now["master"] is not None
                    else self.old_params[i].reshape(-1)).double()
             update = rate * m / den
             want = old * (1 - self.lr[i] * self.wd[i]) - update
-            # 1 - b^t to five half steps (the logarithm, its product with t, the exponential to one step); its root, its
-            # reciprocal; the sum; the reciprocal to one step; the rate and its two products
+            # in half steps: 1 - b^t 5 (the logarithm and its product with t 2 at most, as |x e^x| < 1 - e^x for x < 0;
+            # the series or the power 3); its reciprocal root 4.5; the rate 12 (its factor, that root twice, two
+            # products); the denominator 5.5, its reciprocal 2, two products: 21.5 of the update
             ep = U * 1.01 * (4 * old.abs() + 24 * update.abs() + want.abs()) + rate * em / den \
                 + update.abs() * (eroot / c2 ** 0.5 / den) + 1e-44
             left = self.now["master"][at] if self.now["master"] is not None else p.detach().reshape(-1)

@@ -35,8 +35,7 @@ template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
     return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0u, v, CTRL, 0xf, 0xf, true));
 }
-__device__ __forceinline__ float wave_max(float f) {
-    uint32_t v = __float_as_uint(f);
+__device__ __forceinline__ float wave_max(uint32_t v) {
     v = dpp_max<0xB1>(v);
     v = dpp_max<0x4E>(v);
     v = dpp_max<0x141>(v);
@@ -69,6 +68,32 @@ __device__ __forceinline__ void widen_e4m3(uint32_t w, float unit, float (&o)[4]
     o[3] = hi[1] * unit;
 }
 
+// 1 - e^x for x <= 0: the series of e^x - 1 down to -1 (its next term is 2^-25 of
+// the sum), so that no near numbers are subtracted; below, the power itself.
+__device__ __forceinline__ float one_less_exp(float x) {
+    constexpr float inv[] = {1.f, 1.f / 2, 1.f / 6, 1.f / 24, 1.f / 120, 1.f / 720, 1.f / 5040, 1.f / 40320, 1.f / 362880,
+                             1.f / 3628800, 1.f / 39916800};
+    float s = inv[10];
+#pragma unroll
+    for (int k = 9; k >= 0; --k) s = fmaf(s, x, inv[k]);
+    return x > -1.f ? -x * s : 1.f - __builtin_amdgcn_exp2f(x * 1.44269504f);
+}
+
+// The square root to one step, by the hardware's instruction where it has the
+// range (a denormal would be zero there, and a moment divided by eps alone).
+__device__ __forceinline__ void roots(const float (&v)[4], float (&root)[4]) {
+    uint32_t low = ~0u;   // of those that are not zero
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        root[i] = __builtin_amdgcn_sqrtf(v[i]);
+        low = min(low, __float_as_uint(v[i]) - 1);
+    }
+    if (low < __float_as_uint(0x1p-100f)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) root[i] = sqrtf(v[i]);
+    }
+}
+
 // A wavefront takes one block of 256 elements, a lane four of them, and ends:
 // the next one's loads are on their way while it computes, with more of them in
 // flight than a loop over blocks keeps (four blocks a wavefront, two at a time:
@@ -87,20 +112,23 @@ __global__ __launch_bounds__(T) void k_adamw(AdamArgs a, uint32_t wgs) {
     if (first >= count) return;
     const uint32_t number = t.more & (ADAM_NUMBERS - 1), of = t.more >> 26 & (ADAM_RATES - 1);
     // a lane's n elements of the tensor from e on, and its place in the states
+    const bool full = count - first >= OB;   // the same for every lane
     const uint64_t e = first + 4 * lane;
-    const int n = e >= count ? 0 : count - e < 4 ? (int)(count - e) : 4;
+    const int n = full ? 4 : e >= count ? 0 : count - e < 4 ? (int)(count - e) : 4;
     const size_t block = t.block + first / OB, s = block * OB + 4 * lane;
+    P* const param = (P*)t.p + first;
+    const G* const grad = (const G*)t.g + first;
     Vec<P, 4> pv;
     Vec<float, 4> xv, mv, vv;
     Vec<G, 4> gv;
     uint32_t m8 = 0, v8 = 0;
     float2 unit = make_float2(0.f, 0.f);
-    if (n == 4) {
-        gv.load((const G*)t.g + e);
-        if constexpr (!MASTER) pv.load((const P*)t.p + e);
+    if (full) {
+        gv.load(grad + 4 * lane);
+        if constexpr (!MASTER) pv.load(param + 4 * lane);
     } else {
-        gv.load_part((const G*)t.g + e, n);
-        if constexpr (!MASTER) pv.load_part((const P*)t.p + e, n);
+        gv.load_part(grad + 4 * lane, n);
+        if constexpr (!MASTER) pv.load_part(param + 4 * lane, n);
     }
     if constexpr (MASTER) xv.load(a.master + s);
     if constexpr (MODE == STATES_32) {
@@ -111,10 +139,13 @@ __global__ __launch_bounds__(T) void k_adamw(AdamArgs a, uint32_t wgs) {
         v8 = *(const uint32_t*)((const char*)a.v + s);
         unit = ((const float2*)a.scales)[block];
     }
-    // 1 - beta^t as -(e^(t log beta) - 1): no difference of near numbers
-    const float steps = (float)max(1ll, *a.step), c1 = -expm1f(steps * a.log1), c2 = -expm1f(steps * a.log2);
+    // 1 / sqrt(1 - beta^t) of the first beta in the lower lanes, of the second
+    // in the upper ones
+    const float half = __builtin_amdgcn_rsqf(one_less_exp((float)max(1ll, *a.step) * (lane < 32 ? a.log1 : a.log2)));
+    const float half1 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(half), 0)),
+                root_scale = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(half), 32));
     const float lr = a.lr_factor ? a.lr[of] * *a.lr_factor : a.lr[of];
-    const float decay = 1.f - lr * a.wd[of], rate = lr / c1, root_scale = 1.f / sqrtf(c2);
+    const float decay = 1.f - lr * a.wd[of], rate = lr * half1 * half1;
     float m[4], v[4], x[4], root[4];
     if constexpr (MODE == STATES_32) {
 #pragma unroll
@@ -123,32 +154,37 @@ __global__ __launch_bounds__(T) void k_adamw(AdamArgs a, uint32_t wgs) {
         widen_e4m3(m8, unit.x, m);
         widen_e4m3(v8, unit.y, v);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] *= v[i];
-            if (i >= n) m[i] = v[i] = 0.f;   // past the tensor's end
+        for (int i = 0; i < 4; ++i) v[i] *= v[i];
+        if (!full) {   // nothing past the tensor's end
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i >= n) m[i] = v[i] = 0.f;
         }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float g = gv[i] * f;
+        m[i] = fmaf(a.b1, m[i], a.a1 * g);
+        v[i] = fmaf(a.b2, v[i], a.a2 * g * g);
+    }
+    roots(v, root);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
         if constexpr (MASTER)
             x[i] = xv[i];
         else
             x[i] = pv[i];
-        m[i] = fmaf(a.b1, m[i], a.a1 * g);
-        v[i] = fmaf(a.b2, v[i], a.a2 * g * g);
-        root[i] = sqrtf(v[i]);
         x[i] = fmaf(-rate * m[i], __builtin_amdgcn_rcpf(fmaf(root[i], root_scale, a.eps)), x[i] * decay);
     }
-    if (n == 4) {
-        store_vec<P, 4>((P*)t.p + e, x);
+    if (full) {
+        store_vec<P, 4>(param + 4 * lane, x);
         if constexpr (MASTER) store_vec<float, 4>(a.master + s, x);
     } else {
-        store_part<P, 4>((P*)t.p + e, x, n);
+        store_part<P, 4>(param + 4 * lane, x, n);
         if constexpr (MASTER) store_part<float, 4>(a.master + s, x, n);
     }
     if constexpr (MODE == STATES_32) {
-        if (n == 4) {
+        if (full) {
             store_vec<float, 4>((float*)a.m + s, m);
             store_vec<float, 4>((float*)a.v + s, v);
         } else {
@@ -156,23 +192,25 @@ __global__ __launch_bounds__(T) void k_adamw(AdamArgs a, uint32_t wgs) {
             store_part<float, 4>((float*)a.v + s, v, n);
         }
     } else {
-        float top = 0.f, most = 0.f;
+        uint32_t top = 0, most = 0;   // as whole numbers, as in the wavefront's
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            // as whole numbers, as in the wavefront's
-            top = __uint_as_float(max(__float_as_uint(top), __float_as_uint(fabsf(m[i]))));
-            most = __uint_as_float(max(__float_as_uint(most), __float_as_uint(root[i])));
+            top = max(top, __float_as_uint(m[i]) & 0x7fffffffu);
+            most = max(most, __float_as_uint(root[i]));
         }
-        top = wave_max(top);
-        most = wave_max(most);
         // a moment below 2^-100 is none; a root is above 2^-75 or zero
-        const float per_m = top < 0x1p-100f ? 0.f : 448.f / top, per_v = most > 0.f ? 448.f / most : most;
+        float um = wave_max(top), uv = wave_max(most);
+        um = um < 0x1p-100f ? 0.f : um * (1.f / 448.f);
+        uv *= 1.f / 448.f;
+        const float per_m = um == 0.f ? 0.f : __builtin_amdgcn_rcpf(um), per_v = uv == 0.f ? 0.f : __builtin_amdgcn_rcpf(uv);
         float q[4], r[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             q[i] = m[i] * per_m;
+            // 2^-9 at least, but for zero: a root times 2^100 is more than that
             r[i] = root[i] * per_v;
-            if (root[i] > 0.f) r[i] = r[i] < 0x1p-9f ? 0x1p-9f : r[i];
+            const float least = fminf(root[i] * 0x1p100f, 0x1p-9f);
+            r[i] = r[i] < least ? least : r[i];
         }
         uint32_t cm, cv;
         if constexpr (MODE == STATES_8) {
@@ -190,8 +228,7 @@ __global__ __launch_bounds__(T) void k_adamw(AdamArgs a, uint32_t wgs) {
         }
         *(uint32_t*)((char*)a.m + s) = cm;
         *(uint32_t*)((char*)a.v + s) = cv;
-        if (lane == 0)
-            ((float2*)a.scales)[block] = make_float2(top < 0x1p-100f ? 0.f : top * (1.f / 448.f), most * (1.f / 448.f));
+        if (lane == 0) ((float2*)a.scales)[block] = make_float2(um, uv);
     }
 }
 
