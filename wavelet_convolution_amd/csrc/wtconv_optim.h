@@ -15,7 +15,6 @@
 namespace wtc {
 
 constexpr int OB = 256;   // elements of a block of the states
-constexpr int ADAM_PIECE = 1024;   // elements of a workgroup
 
 // A tensor of a launch in 32 bytes: 330 tensors are three launches instead of
 // five at 48. What few tensors have of their own (rate and decay) is in a
@@ -47,6 +46,9 @@ struct AdamArgs {
 static_assert(sizeof(AdamArgs) + 8 <= 4096, "");   // and the number of workgroups
 
 enum { STATES_32 = 0, STATES_8 = 1, STATES_8_RANDOM = 2 };
+// Blocks of a wavefront, of which a workgroup has four, and elements of a workgroup.
+constexpr int adam_blocks(bool p_bf16, bool master, int mode) { return p_bf16 && !master && mode != STATES_32 ? 2 : 1; }
+constexpr int adam_piece(bool p_bf16, bool master, int mode) { return 4 * OB * adam_blocks(p_bf16, master, mode); }
 hipError_t adamw_launch(const AdamArgs& a, uint32_t wgs, int p_bf16, int g_bf16, int mode, hipStream_t s);
 
 // A gradient of a launch in 12 bytes, so that one launch takes hundreds: its

@@ -98,7 +98,10 @@ __device__ __forceinline__ void roots(const float (&v)[4], float (&root)[4]) {
 // the next one's loads are on their way while it computes, with more of them in
 // flight than a loop over blocks keeps (four blocks a wavefront, two at a time:
 // 219 us for 190, with states in 8 bits 250 for 233; streaming stores change
-// neither).
+// neither). It takes two where an element is only ten or twelve bytes and its
+// instructions are the bound, one after the other: 33 M bf16 parameters without
+// master copies, states in 8 bits, 67 us for 77, with random rounding 84 for 91;
+// fp32 parameters 107 for 99.
 template <typename P, typename G, bool MASTER, int MODE>
 __global__ __launch_bounds__(T) void k_adamw(AdamArgs a, uint32_t wgs) {
     const float f = a.factor ? *a.factor : 1.f;
@@ -107,128 +110,136 @@ __global__ __launch_bounds__(T) void k_adamw(AdamArgs a, uint32_t wgs) {
     if (wg >= wgs) return;
     const AdamTensor& t = a.t[tensor_of<ADAM_TENSORS>(a, wg)];
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
-    const uint64_t count = ((uint64_t)(t.more >> 30) << 32 | t.last) + 1,
-                   first = (uint64_t)(wg - t.wg) * ADAM_PIECE + wave * OB;
-    if (first >= count) return;
+    constexpr int BLOCKS = adam_blocks(sizeof(P) == 2, MASTER, MODE);
+    const uint64_t count = ((uint64_t)(t.more >> 30) << 32 | t.last) + 1;
     const uint32_t number = t.more & (ADAM_NUMBERS - 1), of = t.more >> 26 & (ADAM_RATES - 1);
-    // a lane's n elements of the tensor from e on, and its place in the states
-    const bool full = count - first >= OB;   // the same for every lane
-    const uint64_t e = first + 4 * lane;
-    const int n = full ? 4 : e >= count ? 0 : count - e < 4 ? (int)(count - e) : 4;
-    const size_t block = t.block + first / OB, s = block * OB + 4 * lane;
-    P* const param = (P*)t.p + first;
-    const G* const grad = (const G*)t.g + first;
-    Vec<P, 4> pv;
-    Vec<float, 4> xv, mv, vv;
-    Vec<G, 4> gv;
-    uint32_t m8 = 0, v8 = 0;
-    float2 unit = make_float2(0.f, 0.f);
-    if (full) {
-        gv.load(grad + 4 * lane);
-        if constexpr (!MASTER) pv.load(param + 4 * lane);
-    } else {
-        gv.load_part(grad + 4 * lane, n);
-        if constexpr (!MASTER) pv.load_part(param + 4 * lane, n);
-    }
-    if constexpr (MASTER) xv.load(a.master + s);
-    if constexpr (MODE == STATES_32) {
-        mv.load((const float*)a.m + s);
-        vv.load((const float*)a.v + s);
-    } else {
-        m8 = *(const uint32_t*)((const char*)a.m + s);
-        v8 = *(const uint32_t*)((const char*)a.v + s);
-        unit = ((const float2*)a.scales)[block];
-    }
-    // 1 / sqrt(1 - beta^t) of the first beta in the lower lanes, of the second
-    // in the upper ones
-    const float half = __builtin_amdgcn_rsqf(one_less_exp((float)max(1ll, *a.step) * (lane < 32 ? a.log1 : a.log2)));
-    const float half1 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(half), 0)),
-                root_scale = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(half), 32));
-    const float lr = a.lr_factor ? a.lr[of] * *a.lr_factor : a.lr[of];
-    const float decay = 1.f - lr * a.wd[of], rate = lr * half1 * half1;
-    float m[4], v[4], x[4], root[4];
-    if constexpr (MODE == STATES_32) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m[i] = mv[i], v[i] = vv[i];
-    } else {
-        widen_e4m3(m8, unit.x, m);
-        widen_e4m3(v8, unit.y, v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] *= v[i];
-        if (!full) {   // nothing past the tensor's end
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i >= n) m[i] = v[i] = 0.f;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float g = gv[i] * f;
-        m[i] = fmaf(a.b1, m[i], a.a1 * g);
-        v[i] = fmaf(a.b2, v[i], a.a2 * g * g);
-    }
-    roots(v, root);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (MASTER)
-            x[i] = xv[i];
-        else
-            x[i] = pv[i];
-        x[i] = fmaf(-rate * m[i], __builtin_amdgcn_rcpf(fmaf(root[i], root_scale, a.eps)), x[i] * decay);
-    }
-    if (full) {
-        store_vec<P, 4>(param + 4 * lane, x);
-        if constexpr (MASTER) store_vec<float, 4>(a.master + s, x);
-    } else {
-        store_part<P, 4>(param + 4 * lane, x, n);
-        if constexpr (MASTER) store_part<float, 4>(a.master + s, x, n);
-    }
-    if constexpr (MODE == STATES_32) {
+    float rate = 0.f, root_scale = 0.f, decay = 0.f;
+#pragma unroll 1
+    for (int b = 0; b < BLOCKS; ++b) {
+        const uint64_t first = ((uint64_t)(wg - t.wg) * (T / 64) * BLOCKS + b * (T / 64) + wave) * OB;
+        if (first >= count) return;
+        // a lane's n elements of the tensor from e on, and its place in the states
+        const bool full = count - first >= OB;   // the same for every lane
+        const uint64_t e = first + 4 * lane;
+        const int n = full ? 4 : e >= count ? 0 : count - e < 4 ? (int)(count - e) : 4;
+        const size_t block = t.block + first / OB, s = block * OB + 4 * lane;
+        P* const param = (P*)t.p + first;
+        const G* const grad = (const G*)t.g + first;
+        Vec<P, 4> pv;
+        Vec<float, 4> xv, mv, vv;
+        Vec<G, 4> gv;
+        uint32_t m8 = 0, v8 = 0;
+        float2 unit = make_float2(0.f, 0.f);
         if (full) {
-            store_vec<float, 4>((float*)a.m + s, m);
-            store_vec<float, 4>((float*)a.v + s, v);
+            gv.load(grad + 4 * lane);
+            if constexpr (!MASTER) pv.load(param + 4 * lane);
         } else {
-            store_part<float, 4>((float*)a.m + s, m, n);
-            store_part<float, 4>((float*)a.v + s, v, n);
+            gv.load_part(grad + 4 * lane, n);
+            if constexpr (!MASTER) pv.load_part(param + 4 * lane, n);
         }
-    } else {
-        uint32_t top = 0, most = 0;   // as whole numbers, as in the wavefront's
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            top = max(top, __float_as_uint(m[i]) & 0x7fffffffu);
-            most = max(most, __float_as_uint(root[i]));
-        }
-        // a moment below 2^-100 is none; a root is above 2^-75 or zero
-        float um = wave_max(top), uv = wave_max(most);
-        um = um < 0x1p-100f ? 0.f : um * (1.f / 448.f);
-        uv *= 1.f / 448.f;
-        const float per_m = um == 0.f ? 0.f : __builtin_amdgcn_rcpf(um), per_v = uv == 0.f ? 0.f : __builtin_amdgcn_rcpf(uv);
-        float q[4], r[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            q[i] = m[i] * per_m;
-            // 2^-9 at least, but for zero: a root times 2^100 is more than that
-            r[i] = root[i] * per_v;
-            const float least = fminf(root[i] * 0x1p100f, 0x1p-9f);
-            r[i] = r[i] < least ? least : r[i];
-        }
-        uint32_t cm, cv;
-        if constexpr (MODE == STATES_8) {
-            cm = e4m3_near(q);
-            cv = e4m3_near(r);
+        if constexpr (MASTER) xv.load(a.master + s);
+        if constexpr (MODE == STATES_32) {
+            mv.load((const float*)a.m + s);
+            vv.load((const float*)a.v + s);
         } else {
-            const uint4 bits = Philox(a.rng, a.site + number)((uint32_t)(e / 4));
-            const uint32_t w[4] = {bits.x, bits.y, bits.z, bits.w};
-            cm = cv = 0;
+            m8 = *(const uint32_t*)((const char*)a.m + s);
+            v8 = *(const uint32_t*)((const char*)a.v + s);
+            unit = ((const float2*)a.scales)[block];
+        }
+        if (b == 0) {
+            // 1 / sqrt(1 - beta^t) of the first beta in the lower lanes, of the
+            // second in the upper ones
+            const float half = __builtin_amdgcn_rsqf(one_less_exp((float)max(1ll, *a.step) * (lane < 32 ? a.log1 : a.log2)));
+            const float half1 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(half), 0));
+            root_scale = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(half), 32));
+            const float lr = a.lr_factor ? a.lr[of] * *a.lr_factor : a.lr[of];
+            decay = 1.f - lr * a.wd[of];
+            rate = lr * half1 * half1;
+        }
+        float m[4], v[4], x[4], root[4];
+        if constexpr (MODE == STATES_32) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                cm |= e4m3_random(q[i], w[i] & 0xffffu) << (8 * i);
-                cv |= e4m3_random(r[i], w[i] >> 16) << (8 * i);
+            for (int i = 0; i < 4; ++i) m[i] = mv[i], v[i] = vv[i];
+        } else {
+            widen_e4m3(m8, unit.x, m);
+            widen_e4m3(v8, unit.y, v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] *= v[i];
+            if (!full) {   // nothing past the tensor's end
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i >= n) m[i] = v[i] = 0.f;
             }
         }
-        *(uint32_t*)((char*)a.m + s) = cm;
-        *(uint32_t*)((char*)a.v + s) = cv;
-        if (lane == 0) ((float2*)a.scales)[block] = make_float2(um, uv);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float g = gv[i] * f;
+            m[i] = fmaf(a.b1, m[i], a.a1 * g);
+            v[i] = fmaf(a.b2, v[i], a.a2 * g * g);
+        }
+        roots(v, root);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (MASTER)
+                x[i] = xv[i];
+            else
+                x[i] = pv[i];
+            x[i] = fmaf(-rate * m[i], __builtin_amdgcn_rcpf(fmaf(root[i], root_scale, a.eps)), x[i] * decay);
+        }
+        if (full) {
+            store_vec<P, 4>(param + 4 * lane, x);
+            if constexpr (MASTER) store_vec<float, 4>(a.master + s, x);
+        } else {
+            store_part<P, 4>(param + 4 * lane, x, n);
+            if constexpr (MASTER) store_part<float, 4>(a.master + s, x, n);
+        }
+        if constexpr (MODE == STATES_32) {
+            if (full) {
+                store_vec<float, 4>((float*)a.m + s, m);
+                store_vec<float, 4>((float*)a.v + s, v);
+            } else {
+                store_part<float, 4>((float*)a.m + s, m, n);
+                store_part<float, 4>((float*)a.v + s, v, n);
+            }
+        } else {
+            uint32_t top = 0, most = 0;   // as whole numbers, as in the wavefront's
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                top = max(top, __float_as_uint(m[i]) & 0x7fffffffu);
+                most = max(most, __float_as_uint(root[i]));
+            }
+            // a moment below 2^-100 is none; a root is above 2^-75 or zero
+            float um = wave_max(top), uv = wave_max(most);
+            um = um < 0x1p-100f ? 0.f : um * (1.f / 448.f);
+            uv *= 1.f / 448.f;
+            const float per_m = um == 0.f ? 0.f : __builtin_amdgcn_rcpf(um), per_v = uv == 0.f ? 0.f : __builtin_amdgcn_rcpf(uv);
+            float q[4], r[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                q[i] = m[i] * per_m;
+                // 2^-9 at least, but for zero: a root times 2^100 is more than that
+                r[i] = root[i] * per_v;
+                const float least = fminf(root[i] * 0x1p100f, 0x1p-9f);
+                r[i] = r[i] < least ? least : r[i];
+            }
+            uint32_t cm, cv;
+            if constexpr (MODE == STATES_8) {
+                cm = e4m3_near(q);
+                cv = e4m3_near(r);
+            } else {
+                const uint4 bits = Philox(a.rng, a.site + number)((uint32_t)(e / 4));
+                const uint32_t w[4] = {bits.x, bits.y, bits.z, bits.w};
+                cm = cv = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    cm |= e4m3_random(q[i], w[i] & 0xffffu) << (8 * i);
+                    cv |= e4m3_random(r[i], w[i] >> 16) << (8 * i);
+                }
+            }
+            *(uint32_t*)((char*)a.m + s) = cm;
+            *(uint32_t*)((char*)a.v + s) = cv;
+            if (lane == 0) ((float2*)a.scales)[block] = make_float2(um, uv);
+        }
     }
 }
 

@@ -128,6 +128,7 @@ wtconv_status_t wtconv_adamw_step(const wtconv_adamw_desc_t* d, int32_t n, void*
     a.eps = (float)d->eps;
     a.site = (uint32_t)d->site;
     const int mode = !eight ? wtc::STATES_32 : rng ? wtc::STATES_8_RANDOM : wtc::STATES_8;
+    const int piece = wtc::adam_piece(bf16, master != nullptr, mode);
     uint32_t wgs = 0;
     int64_t block = 0;
     auto flush = [&]() {
@@ -151,7 +152,7 @@ wtconv_status_t wtconv_adamw_step(const wtconv_adamw_desc_t* d, int32_t n, void*
     };
     for (int i = 0; i < n; ++i) {
         if (grads[i] && counts[i] > 0) {
-            const uint32_t more = (uint32_t)((counts[i] + wtc::ADAM_PIECE - 1) / wtc::ADAM_PIECE);   // 2^24 at most
+            const uint32_t more = (uint32_t)((counts[i] + piece - 1) / piece);   // 2^24 at most
             int r = rates_of(i);
             if (a.n == wtc::ADAM_TENSORS || wgs + more > 1u << 30 || r == wtc::ADAM_RATES) {
                 if (const hipError_t err = flush(); err != hipSuccess) return done(err);
