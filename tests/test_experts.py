@@ -253,6 +253,19 @@ def test_gradients_through_autograd():
         assert (a.double() - b).abs().max() <= 2e-5 * b.abs().max()
 
 
+def test_any_memory_order_through_autograd():
+    """Planar activations, transposed weights and experts, an expanded gradient."""
+    B, C, H, W, K, E = 2, 12, 3, 5, 2, 4
+    e = ids(K, B * H * W, E, dropped=0.0).view(K, B, H, W).permute(1, 2, 3, 0)
+    x = torch.randn(B, C, H, W, device=DEV, requires_grad=True)
+    w = torch.rand(K, B, H, W, device=DEV, requires_grad=True)
+    route = ex.expert_sort(e, E)
+    y = ex.expert_sum(ex.expert_rows(x.permute(0, 2, 3, 1), route), w.permute(1, 2, 3, 0), route)
+    dx, dw = torch.autograd.grad(y.sum(), (x, w))
+    assert (dx - w.sum(0).unsqueeze(1)).abs().max() <= 1e-6
+    assert (dw - x.sum(1).unsqueeze(0)).abs().max() <= C * 1e-6
+
+
 def test_gradients_against_differences():
     """rows and sum are linear in each argument: central differences with powers of two are exact up to rounding."""
     place, offsets, x, ys, w, dy = routed(40, 3, 4, 12, torch.float32, dropped=0.0)
@@ -301,6 +314,29 @@ def test_on_another_stream():
     same(got, sort_ref(e, 16))
     assert torch.equal(xs, rows_ref(x, place, offsets)[0])
     near(y, *sum_ref(ys, w, place, offsets))
+
+
+def test_calls_at_once():
+    """Sorts (with workspaces of their own) and sums on two streams at the same time."""
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    es = [ids(200_000, 2, 16 + i, seed=i) for i in range(2)]
+    sets = [routed(20_000, 2, 8, 96, torch.bfloat16, seed=i) for i in range(2)]
+    want = [eb.wtconv_expert_sum_bwd(s[5], s[3], s[4], s[0], s[1]) for s in sets]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            place, offsets, x, ys, w, dy = sets[i]
+            got.append((i, eb.wtconv_expert_sort(es[i], 16 + i, stream=s),
+                        eb.wtconv_expert_sum_bwd(dy, ys, w, place, offsets, stream=s)))
+    torch.cuda.synchronize()
+    first = [next(g[1] for g in got if g[0] == i) for i in range(2)]
+    for i in range(2):
+        same(first[i], sort_ref(es[i], 16 + i))
+    for i, a, b in got:
+        assert all(torch.equal(x, y) for x, y in zip(a, first[i]))
+        # bit for bit, NaN of slots that are not read apart
+        assert all(torch.equal(x.nan_to_num(), y.nan_to_num()) for x, y in zip(b, want[i]))
 
 
 @pytest.mark.parametrize("N", [200, 6000])   # one workgroup, and parts with a workspace

@@ -287,6 +287,27 @@ def test_on_another_stream():
     assert torch.equal(norm, ob.wtconv_grad_norm(c.grads, 1.0))
 
 
+def test_calls_at_once():
+    """Steps and norms of other tensors on two streams at the same time."""
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    calls = [Call([(3_000_001,), (77,)], bits=8, random=True, seed=20 + i) for i in range(2)]
+    alone = [Call([(3_000_001,), (77,)], bits=8, random=True, seed=20 + i) for i in range(2)]
+    for _ in range(5):
+        for c in alone:
+            c.run()
+    norms = [ob.wtconv_grad_norm(c.grads) for c in alone]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for c, s in zip(calls, streams):
+            c.run(stream=s)
+            got.append(ob.wtconv_grad_norm(c.grads, stream=s))
+    torch.cuda.synchronize()
+    for c, d in zip(calls, alone):
+        assert all(torch.equal(x, y) for x, y in zip(c.bits(), d.bits()))
+    assert all(torch.equal(g, norms[i % 2]) for i, g in enumerate(got))
+
+
 @pytest.mark.parametrize("bits,random", STATES)
 def test_captured_and_replayed(bits, random):
     """Norm and step in a graph: new gradients, counts, rates and random numbers are read at each replay."""
