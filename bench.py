@@ -317,10 +317,15 @@ def block_context(torch, wt, cfg, steps: int):
     dropped: torch's operators (`wtconv_train`) and this library's
     (`wtconv_train_own`). The same two with the optimizer's step, gradients
     clipped to their norm and AdamW on all parameters: torch's
-    (`wtconv_train_step`) and this library's (`wtconv_train_step_own`)."""
+    (`wtconv_train_step`) and this library's (`wtconv_train_step_own`). Last,
+    the block with eight experts of two chosen for each pixel in the place of
+    its MLP (the experts' products one after the other, library products in
+    both): rows sent to their experts and back by torch's sort and indexing
+    (`wtconv_experts`) and by this library's (`wtconv_experts_own`)."""
     import torch.nn.functional as F
 
     from wavelet_convolution_amd.block import block_residual, channel_norm, counter_dropout, dropout_rng
+    from wavelet_convolution_amd.experts import expert_rows, expert_sort, expert_sum
     from wavelet_convolution_amd.module import wtconv
     from wavelet_convolution_amd.optim import AdamW
 
@@ -388,6 +393,33 @@ def block_context(torch, wt, cfg, steps: int):
     blocks["wtconv_train_step"] = torch_train_block
     blocks["wtconv_train_step_own"] = lambda x: own_block(x, True)
 
+    E, K = 8, 2
+    router, up, down = param(E, C, std=0.1), param(E, 4 * C, C), param(E, C, 4 * C)
+
+    def expert_block(x, own):
+        rows = channel_norm(wtconv(x, wt_wb, wt_wl, wt_sc), own_w, own_b, channels_last=True)
+        rows = rows.permute(0, 2, 3, 1).reshape(-1, C)
+        top, expert = F.linear(rows, router).float().topk(K, 1)
+        weight = torch.softmax(top, 1)
+        if own:
+            route = expert_sort(expert, E)
+            xs, ends = expert_rows(rows, route), route.offsets.tolist()
+        else:
+            order = torch.sort(expert.view(-1), stable=True)[1]
+            source = order // K
+            xs = rows[source]
+            ends = [0, *torch.bincount(expert.view(-1), minlength=E).cumsum(0).tolist()]
+        ys = torch.cat([F.linear(F.gelu(F.linear(xs[a:b], up[e])), down[e])
+                        for e, (a, b) in enumerate(zip(ends, ends[1:]))])
+        if own:
+            h = expert_sum(ys, weight, route)
+        else:
+            h = torch.zeros_like(rows).index_add(0, source, ys * weight.view(-1)[order].unsqueeze(1).to(dt))
+        return block_residual(x, h.view(B, H, W, C).permute(0, 3, 1, 2))
+
+    blocks["wtconv_experts"] = lambda x: expert_block(x, False)
+    blocks["wtconv_experts_own"] = lambda x: expert_block(x, True)
+
     shared = [wt_wb, wt_wl, wt_sc, w1, b1, w2, b2, gamma]
     torch_params, own_params = [*shared, ln_w, ln_b], [*shared, own_w, own_b]
     torch_optim = torch.optim.AdamW(torch_params, lr=1e-6, fused=True)
@@ -409,7 +441,7 @@ def block_context(torch, wt, cfg, steps: int):
         def step(i, run=run):
             x = xs[i % nsets]
             run(x).backward(gs[i % nsets])
-            if name.endswith("own") and "train" in name:
+            if "train" in name and name.endswith("own"):
                 rng[1] += 1
             optim_step(name)
 
@@ -430,6 +462,7 @@ def block_context(torch, wt, cfg, steps: int):
     out["train_own_over_torch"] = round(out["wtconv_train_own_ms_per_step"] / out["wtconv_train_ms_per_step"], 3)
     out["train_step_own_over_torch"] = round(
         out["wtconv_train_step_own_ms_per_step"] / out["wtconv_train_step_ms_per_step"], 3)
+    out["experts_own_over_torch"] = round(out["wtconv_experts_own_ms_per_step"] / out["wtconv_experts_ms_per_step"], 3)
     out["wtconv_over_this_library_L0"] = round(out["wtconv_ms_per_step"] / out["this_library_L0_ms_per_step"], 3)
     del xs, gs
     torch.cuda.empty_cache()
