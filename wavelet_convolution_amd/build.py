@@ -80,7 +80,8 @@ def _build_native() -> None:
            "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-isystem", os.path.join(os.path.dirname(_hipcc()), "../include"),
            f"-I{sysconfig.get_paths()['include']}", f"-I{base}/include", f"-I{base}/include/torch/csrc/api/include",
            os.path.join(CSRC, "wtconv_native.cpp"), "-o", tmp, f"-L{base}/lib", "-ltorch_python", "-ltorch_cpu",
-           "-lc10", "-lc10_hip", f"-L{PKG}", "-l:libwtconv.so", "-Wl,-rpath,$ORIGIN"]
+           "-lc10", "-lc10_hip", "-ltorch_hip",
+           f"-L{PKG}", "-l:libwtconv.so", "-Wl,-rpath,$ORIGIN"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"g++ failed on wtconv_native.cpp:\n{res.stderr}")

@@ -12,7 +12,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -123,6 +123,11 @@ void* stream_of(const at::Tensor& t) {
     return (void*)c10::hip::getCurrentHIPStream(t.get_device()).stream();
 }
 
+// New memory on a tensor's device: what torch.empty does behind its dispatch.
+at::Tensor fresh(const at::Tensor& like, at::IntArrayRef shape, at::ScalarType type) {
+    return at::Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
+}
+
 // A workspace: the caller's, from its next multiple of 256 bytes on, or a new one.
 struct Workspace {
     at::Tensor held;
@@ -133,7 +138,7 @@ struct Workspace {
             held = tensor("ws", given, &like);
             if (!held.is_contiguous()) refuse("ws must be contiguous: its bytes are counted from its elements");
         } else if (need) {
-            held = at::empty({(int64_t)need + 256}, like.options().dtype(at::kByte));
+            held = fresh(like, {(int64_t)need + 256}, at::kByte);
         } else {
             return;
         }
@@ -147,7 +152,7 @@ struct Workspace {
 // An output to write: the one given, checked, or a new one.
 at::Tensor output(const char* name, PyObject* given, const at::Tensor& like, at::ScalarType type,
                   at::IntArrayRef shape) {
-    if (given == Py_None) return at::empty(shape, like.options().dtype(type));
+    if (given == Py_None) return fresh(like, shape, type);
     const at::Tensor& t = tensor(name, given, &like);
     check_dense(name, t, type, shape);
     return t;

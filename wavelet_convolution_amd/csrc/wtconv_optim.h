@@ -27,10 +27,12 @@ struct AdamTensor {
     uint32_t wg;      // its first workgroup
     uint32_t more;    // its number in the call, its rates', and the two high bits of count - 1
 };
-constexpr int ADAM_TENSORS = 119, ADAM_RATES = 16;
+// Tensors of a launch; a launch of few has a short table of its own, as 4 KB of
+// arguments take the host 1 us more than a hundred bytes (3.5 us against 2.5).
+constexpr int ADAM_TENSORS = 119, ADAM_FEW = 16, ADAM_RATES = 16;
 constexpr uint32_t ADAM_NUMBERS = 1u << 26;   // tensors of a call
 
-struct AdamArgs {
+struct AdamHead {
     void *m, *v;
     float *scales, *master;
     const long long* step;
@@ -41,8 +43,13 @@ struct AdamArgs {
     uint32_t site;
     int n, rates;
     float lr[ADAM_RATES], wd[ADAM_RATES];
-    AdamTensor t[ADAM_TENSORS];
 };
+template <int N>
+struct AdamTable : AdamHead {
+    static constexpr int MOST = N;
+    AdamTensor t[N];
+};
+typedef AdamTable<ADAM_TENSORS> AdamArgs;
 static_assert(sizeof(AdamArgs) + 8 <= 4096, "");   // and the number of workgroups
 
 enum { STATES_32 = 0, STATES_8 = 1, STATES_8_RANDOM = 2 };
@@ -57,14 +64,19 @@ hipError_t adamw_launch(const AdamArgs& a, uint32_t wgs, int p_bf16, int g_bf16,
 struct NormTensor {
     uint32_t w[3];
 };
-constexpr int NORM_TENSORS = 339;
+constexpr int NORM_TENSORS = 339, NORM_FEW = 40;
 
-struct NormArgs {
+struct NormHead {
     double* sums;       // a sum a workgroup
     uint64_t piece;     // elements of a workgroup
     int n, pad;
-    NormTensor t[NORM_TENSORS];
 };
+template <int N>
+struct NormTable : NormHead {
+    static constexpr int MOST = N;
+    NormTensor t[N];
+};
+typedef NormTable<NORM_TENSORS> NormArgs;
 static_assert(sizeof(NormArgs) <= 4096, "");
 
 // Most sums of a launch, besides one more a tensor: fewer workgroups in all than

@@ -16,9 +16,9 @@ constexpr int T = 256;
 // it. All lanes look at a first workgroup each, and a ballot counts.
 __device__ __forceinline__ uint32_t first_wg(const AdamTensor& t) { return t.wg; }
 __device__ __forceinline__ uint32_t first_wg(const NormTensor& t) { return t.w[2] >> 18; }
-template <int MOST, class A>
+template <class A>
 __device__ __forceinline__ int tensor_of(const A& a, uint32_t wg) {
-    constexpr int N = (MOST + 63) / 64;   // loads that are in flight together
+    constexpr int N = (A::MOST + 63) / 64;   // loads that are in flight together
     const int lane = threadIdx.x % 64;
     uint32_t at[N];
 #pragma unroll
@@ -102,13 +102,13 @@ __device__ __forceinline__ void roots(const float (&v)[4], float (&root)[4]) {
 // instructions are the bound, one after the other: 33 M bf16 parameters without
 // master copies, states in 8 bits, 67 us for 77, with random rounding 84 for 91;
 // fp32 parameters 107 for 99.
-template <typename P, typename G, bool MASTER, int MODE>
-__global__ __launch_bounds__(T) void k_adamw(AdamArgs a, uint32_t wgs) {
+template <typename P, typename G, bool MASTER, int MODE, int TENSORS>
+__global__ __launch_bounds__(T) void k_adamw(AdamTable<TENSORS> a, uint32_t wgs) {
     const float f = a.factor ? *a.factor : 1.f;
     if (!(fabsf(f) < INFINITY)) return;
     const uint32_t wg = blockIdx.y * gridDim.x + blockIdx.x;
     if (wg >= wgs) return;
-    const AdamTensor& t = a.t[tensor_of<ADAM_TENSORS>(a, wg)];
+    const AdamTensor& t = a.t[tensor_of(a, wg)];
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
     constexpr int BLOCKS = adam_blocks(sizeof(P) == 2, MASTER, MODE);
     const uint64_t count = ((uint64_t)(t.more >> 30) << 32 | t.last) + 1;
@@ -243,18 +243,32 @@ __global__ __launch_bounds__(T) void k_adamw(AdamArgs a, uint32_t wgs) {
     }
 }
 
-template <typename P, typename G, bool MASTER>
-hipError_t adamw_by_mode(const AdamArgs& a, uint32_t wgs, int mode, hipStream_t s) {
+// The same arguments with a shorter table.
+template <class Head, class Table, class A>
+Table shorter(const A& a) {
+    Table b;
+    (Head&)b = a;
+    for (int i = 0; i < a.n; ++i) b.t[i] = a.t[i];
+    return b;
+}
+
+template <typename P, typename G, bool MASTER, int MODE>
+hipError_t adamw_by_count(const AdamArgs& a, uint32_t wgs, hipStream_t s) {
     // a grid's side has fewer than 2^32 lanes
     const uint32_t x = wgs < 1u << 20 ? wgs : 1u << 20;
     const dim3 grid(x, (wgs + x - 1) / x);
-    if (mode == STATES_32)
-        hipLaunchKernelGGL((k_adamw<P, G, MASTER, STATES_32>), grid, dim3(T), 0, s, a, wgs);
-    else if (mode == STATES_8)
-        hipLaunchKernelGGL((k_adamw<P, G, MASTER, STATES_8>), grid, dim3(T), 0, s, a, wgs);
+    if (a.n <= ADAM_FEW)
+        hipLaunchKernelGGL((k_adamw<P, G, MASTER, MODE, ADAM_FEW>), grid, dim3(T), 0, s,
+                           (shorter<AdamHead, AdamTable<ADAM_FEW>>(a)), wgs);
     else
-        hipLaunchKernelGGL((k_adamw<P, G, MASTER, STATES_8_RANDOM>), grid, dim3(T), 0, s, a, wgs);
+        hipLaunchKernelGGL((k_adamw<P, G, MASTER, MODE, ADAM_TENSORS>), grid, dim3(T), 0, s, a, wgs);
     return hipGetLastError();
+}
+template <typename P, typename G, bool MASTER>
+hipError_t adamw_by_mode(const AdamArgs& a, uint32_t wgs, int mode, hipStream_t s) {
+    if (mode == STATES_32) return adamw_by_count<P, G, MASTER, STATES_32>(a, wgs, s);
+    return mode == STATES_8 ? adamw_by_count<P, G, MASTER, STATES_8>(a, wgs, s)
+                            : adamw_by_count<P, G, MASTER, STATES_8_RANDOM>(a, wgs, s);
 }
 template <typename G>
 hipError_t adamw_by_param(const AdamArgs& a, uint32_t wgs, int p_bf16, int mode, hipStream_t s) {
@@ -314,8 +328,9 @@ __device__ __forceinline__ double wg_sum(double v) {
     return v;
 }
 
-__global__ __launch_bounds__(T) void k_norm(NormArgs a) {
-    const NormTensor& t = a.t[tensor_of<NORM_TENSORS>(a, blockIdx.x)];
+template <int TENSORS>
+__global__ __launch_bounds__(T) void k_norm(NormTable<TENSORS> a) {
+    const NormTensor& t = a.t[tensor_of(a, blockIdx.x)];
     const uint64_t address = (uint64_t)(t.w[1] & 0xffffu) << 32 | t.w[0],
                    count = ((uint64_t)(t.w[2] & 0x3ffffu) << 16 | t.w[1] >> 16) + 1,
                    at = (uint64_t)(blockIdx.x - first_wg(t)) * a.piece, n = min(a.piece, count - at);
@@ -349,7 +364,10 @@ hipError_t adamw_launch(const AdamArgs& a, uint32_t wgs, int p_bf16, int g_bf16,
 }
 
 hipError_t norm_launch(const NormArgs& a, uint32_t wgs, hipStream_t s) {
-    hipLaunchKernelGGL(k_norm, dim3(wgs), dim3(T), 0, s, a);
+    if (a.n <= NORM_FEW)
+        hipLaunchKernelGGL(k_norm<NORM_FEW>, dim3(wgs), dim3(T), 0, s, (shorter<NormHead, NormTable<NORM_FEW>>(a)));
+    else
+        hipLaunchKernelGGL(k_norm<NORM_TENSORS>, dim3(wgs), dim3(T), 0, s, a);
     return hipGetLastError();
 }
 
