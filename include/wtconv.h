@@ -385,8 +385,8 @@ wtconv_status_t wtconv_dropout(const wtconv_block_desc_t *desc, const void *x, c
  *
  * and their gradients: rows backward dx[n] = sum_i dxs[place[n][i]] without
  * the none; sum backward dys[place[n][i]] = weight[n][i] * dy[n] (none:
- * zeros) and dweight[n][i] = <dy[n], ys[place[n][i]]> (none: 0). A row of xs,
- * ys or dxs that belongs to no expert is not read, whatever it holds.
+ * zeros) and dweight[n][i] = <dy[n], ys[place[n][i]]> (none: 0). What a row
+ * of ys or dxs that belongs to no expert holds reaches no result.
  *
  * x, y, dx, dy are [n][c], xs, ys, dxs, dys [n * k][c], contiguous, of type
  * `dtype`; order [n * k], place [n][k], offsets [experts + 1] are int32,

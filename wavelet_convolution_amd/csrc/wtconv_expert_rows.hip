@@ -111,6 +111,7 @@ hipError_t move_launch(const ExpertArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Slots at a time: see sum_bwd_by_k.
 template <typename X, int OP>
 hipError_t move_by_k(const ExpertArgs& a, hipStream_t s) {
     if (a.K == 1) return move_launch<X, OP, 1>(a, s);
@@ -220,6 +221,10 @@ hipError_t sum_bwd_by_row(const ExpertArgs& a, hipStream_t s) {
     return sum_bwd_launch<X, 64, KK>(a, s);
 }
 
+// As many slots at a time as a row has, four at most: room for more is masked
+// work (200,704 rows of 96 bf16 channels with one slot 26.4 us, 30.6 with room
+// for two and 35.4 for four, with two slots 41.9 and 49.2; the weighted sum 15.8,
+// 16.1 and 16.5).
 template <typename X>
 hipError_t sum_bwd_by_k(const ExpertArgs& a, hipStream_t s) {
     if (a.K == 1) return sum_bwd_by_row<X, 1>(a, s);
