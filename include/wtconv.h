@@ -496,9 +496,10 @@ wtconv_status_t wtconv_adamw_step(const wtconv_adamw_desc_t *desc, int32_t n, vo
                                   const int64_t *step, const float *factor, const float *lr_factor,
                                   const uint64_t *rng, void *stream);
 
-/* Device workspace of wtconv_grad_norm for n tensors (8-byte aligned), or
-   (size_t)-1 if n < 0. */
-size_t wtconv_grad_norm_workspace_size(int32_t n);
+/* Device workspace of wtconv_grad_norm for n tensors of these counts (8-byte
+   aligned; 0 for few elements, ws may then be NULL), or (size_t)-1 where a
+   count is not in 0..2^34, their sum exceeds 2^39 or n < 0. */
+size_t wtconv_grad_norm_workspace_size(const int64_t *counts, int32_t n);
 
 /* dtypes: a wtconv_dtype_t for each gradient (host array, as grads and
    counts); max_norm > 0, infinity for no clipping. out: two fp32 numbers. A

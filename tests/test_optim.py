@@ -235,7 +235,9 @@ def check_norm(grads, max_norm=1.0, **kw):
 
 
 @pytest.mark.parametrize("shapes", [[(1,)], [(3,), (0,), (8,)], SHAPES, [((i * 91) % 3000,) for i in range(400)],
-                                    [(20_000_003,)], [(17,)] * 161, [(8192,), (8193,), (2048 * 8192 + 5,)]])
+                                    [(20_000_003,)], [(17,)] * 161, [(8192,), (8193,), (2048 * 8192 + 5,)],
+                                    [(2048,)] * 64, [(2047,), (131_072 - 2048,)], [(2049,)] * 32, [(2049,)] * 33, [(1,)] * 64,
+                                    [(1,)] * 65, [(40_000,)] * 40, [(40_000,)] * 41])
 def test_norm(shapes):
     g = torch.Generator(DEV).manual_seed(0)
     grads = [torch.randn(s, generator=g, device=DEV).to(F32 if i % 3 else BF16) for i, s in enumerate(shapes)]

@@ -162,11 +162,16 @@ def test_state_count(lib):
 
 
 def test_bad_norms(lib):
-    need = lib.wtconv_grad_norm_workspace_size(2)
-    assert 0 < need < 1 << 16 and lib.wtconv_grad_norm_workspace_size(-1) == NONE
-    assert lib.wtconv_grad_norm_workspace_size(1000) >= 8 * 1000
+    def size(*counts):
+        return lib.wtconv_grad_norm_workspace_size((ctypes.c_int64 * len(counts))(*counts), len(counts))
 
-    def norm(counts=(100, 50), grads=(1 << 40, 2 << 40), dtypes=(0, 1), max_norm=1.0, step=None, out=3 << 40, ws=4 << 40,
+    need = size(200_000, 50)
+    assert 0 < need < 1 << 16 and lib.wtconv_grad_norm_workspace_size(None, -1) == NONE
+    assert size() == size(100, 0, 2048) == size(*[1] * 64) == 0 < size(*[1] * 65)
+    assert size(-1) == size((1 << 34) + 1) == lib.wtconv_grad_norm_workspace_size(None, 2) == NONE
+    assert size(*[10_000] * 1000) >= 8 * 1000
+
+    def norm(counts=(200_000, 50), grads=(1 << 40, 2 << 40), dtypes=(0, 1), max_norm=1.0, step=None, out=3 << 40, ws=4 << 40,
              bytes_=need, n=None):
         k = len(counts)
         return lib.wtconv_grad_norm(k if n is None else n, (ctypes.c_void_p * k)(*grads), (ctypes.c_int64 * k)(*counts),

@@ -471,7 +471,9 @@ PyObject* grad_norm(PyObject*, PyObject* const* a, Py_ssize_t) {
         if (!(most > 0)) refuse("max_norm must be above 0 (infinity: no clipping); got ", most);
         const at::Tensor out = output("out", a[3], *like, at::kFloat, {2});
         const void* step = scalar("step", a[2], at::kLong, *like);
-        const Workspace ws(a[4], wtconv_grad_norm_workspace_size(n), *like);
+        const size_t need = wtconv_grad_norm_workspace_size(counts.data(), n);
+        if (need == (size_t)-1) check_status(WTCONV_ERR_UNSUPPORTED_SHAPE);
+        const Workspace ws(a[4], need, *like);
         check_status(wtconv_grad_norm(n, g.data(), counts.data(), types.data(), most, (int64_t*)step,
                                       out.mutable_data_ptr<float>(), ws.p, ws.bytes, stream));
         return THPVariable_Wrap(out);

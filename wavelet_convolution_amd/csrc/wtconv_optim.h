@@ -85,6 +85,10 @@ static_assert(sizeof(NormArgs) <= 4096, "");
 // tensors: 18.7 us with 1,536, 21.0 with 2,048, 22.5 with 8,192.
 constexpr uint32_t NORM_WGS = 1536;
 static_assert(NORM_WGS + NORM_TENSORS < 1u << 14, "");
+// Up to so many pieces of so many elements are one workgroup's: its table has an
+// entry a piece, as above without a first workgroup.
+constexpr int NORM_PIECES = 64, NORM_PIECE = 2048;
+hipError_t norm_alone(const NormTable<NORM_PIECES>& a, double max_norm, long long* step, float* out, hipStream_t s);
 hipError_t norm_launch(const NormArgs& a, uint32_t wgs, hipStream_t s);
 hipError_t norm_finish(const double* sums, uint32_t n, double max_norm, long long* step, float* out, hipStream_t s);
 

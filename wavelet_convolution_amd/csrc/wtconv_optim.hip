@@ -340,6 +340,15 @@ __global__ __launch_bounds__(T) void k_norm(NormTable<TENSORS> a) {
 }
 
 constexpr int TF = 1024;
+// The sum is the first lane's.
+__device__ __forceinline__ void norm_out(double sum, double max_norm, long long* step, float* out) {
+    if (threadIdx.x > 0) return;
+    const double norm = sqrt(sum);
+    const bool finite = norm < (double)INFINITY;
+    out[0] = (float)norm;
+    out[1] = finite ? (float)fmin(1., max_norm / (norm + 1e-6)) : NAN;
+    if (step && finite) ++*step;
+}
 __global__ __launch_bounds__(TF) void k_norm_finish(const double* sums, uint32_t n, double max_norm, long long* step,
                                                     float* out) {
     double sum = 0.;
@@ -347,14 +356,54 @@ __global__ __launch_bounds__(TF) void k_norm_finish(const double* sums, uint32_t
         const double a = sums[i], b = i + TF < n ? sums[i + TF] : 0.;
         sum += a + b;
     }
-    sum = wg_sum<TF>(sum);
-    if (threadIdx.x == 0) {
-        const double norm = sqrt(sum);
-        const bool finite = norm < (double)INFINITY;
-        out[0] = (float)norm;
-        out[1] = finite ? (float)fmin(1., max_norm / (norm + 1e-6)) : NAN;
-        if (step && finite) ++*step;
+    norm_out(wg_sum<TF>(sum), max_norm, step, out);
+}
+
+// Few elements: one workgroup takes all pieces, each an entry of the table (no
+// search), a wavefront one after the other, and finishes; the next entry is read
+// while the present one's loads are in flight. One launch instead of two: a call
+// takes 4.5 us instead of 6.9 for 10 x 2,000 fp32 elements, 5.8 instead of 6.8
+// for 107,000; 131,072 are the same.
+template <typename G>
+__device__ __forceinline__ void add_piece(double (&sum)[2], const NormTensor& now, NormTensor& next, const NormTensor* after,
+                                          uint32_t lane) {
+    constexpr int N = 8, UV = NORM_PIECE / (64 * N);
+    const G* g = (const G*)(((uint64_t)(now.w[1] & 0xffffu) << 32 | now.w[0]) & ~1ull);
+    const uint32_t n = (now.w[1] >> 16) + 1;
+    Vec<G, N> v[UV];
+#pragma unroll
+    for (int u = 0; u < UV; ++u) {
+        const uint32_t at = (u * 64 + lane) * N;
+        if (at + N <= n) {
+            v[u].load(g + at);
+        } else {
+            v[u].zero();
+            if (at < n) v[u].load_part(g + at, (int)(n - at));
+        }
     }
+    next = *after;
+#pragma unroll
+    for (int u = 0; u < UV; ++u)
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const double x = v[u][k];
+            sum[k % 2] = fma(x, x, sum[k % 2]);
+        }
+}
+__global__ __launch_bounds__(TF) void k_norm_alone(NormTable<NORM_PIECES> a, double max_norm, long long* step, float* out) {
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, n = (uint32_t)a.n;
+    double sum[2] = {0., 0.};
+    NormTensor next = a.t[wave];
+    for (uint32_t p = wave; p < n;) {
+        const NormTensor now = next;
+        p += TF / 64;
+        const NormTensor* after = &a.t[min(p, (uint32_t)NORM_PIECES - 1)];
+        if (now.w[0] & 1)
+            add_piece<bf16_t>(sum, now, next, after, lane);
+        else
+            add_piece<float>(sum, now, next, after, lane);
+    }
+    norm_out(wg_sum<TF>(sum[0] + sum[1]), max_norm, step, out);
 }
 
 }  // namespace
@@ -368,6 +417,11 @@ hipError_t norm_launch(const NormArgs& a, uint32_t wgs, hipStream_t s) {
         hipLaunchKernelGGL(k_norm<NORM_FEW>, dim3(wgs), dim3(T), 0, s, (shorter<NormHead, NormTable<NORM_FEW>>(a)));
     else
         hipLaunchKernelGGL(k_norm<NORM_TENSORS>, dim3(wgs), dim3(T), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t norm_alone(const NormTable<NORM_PIECES>& a, double max_norm, long long* step, float* out, hipStream_t s) {
+    hipLaunchKernelGGL(k_norm_alone, dim3(1), dim3(TF), 0, s, a, max_norm, step, out);
     return hipGetLastError();
 }
 

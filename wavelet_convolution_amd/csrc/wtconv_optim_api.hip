@@ -168,8 +168,12 @@ wtconv_status_t wtconv_adamw_step(const wtconv_adamw_desc_t* d, int32_t n, void*
     return done(flush());
 }
 
-size_t wtconv_grad_norm_workspace_size(int32_t n) {
-    if (n < 0) return (size_t)-1;
+size_t wtconv_grad_norm_workspace_size(const int64_t* counts, int32_t n) {
+    if (state_count(counts, n) < 0) return (size_t)-1;
+    // few elements: pieces of them in one launch, whichever gradients are missing
+    int64_t pieces = 0;
+    for (int i = 0; i < n && pieces <= wtc::NORM_PIECES; ++i) pieces += (counts[i] + wtc::NORM_PIECE - 1) / wtc::NORM_PIECE;
+    if (pieces <= wtc::NORM_PIECES) return 0;
     const size_t launches = ((size_t)n + wtc::NORM_TENSORS - 1) / wtc::NORM_TENSORS;
     return (launches * wtc::NORM_WGS + n) * sizeof(double);
 }
@@ -179,8 +183,8 @@ wtconv_status_t wtconv_grad_norm(int32_t n, const void* const* grads, const int6
     if (n < 0 || !out || !(max_norm > 0.)) return WTCONV_ERR_INVALID_ARG;
     if (n > 0 && (!grads || !counts || !dtypes)) return WTCONV_ERR_INVALID_ARG;
     if (!aligned(out, 4) || !aligned(step, 8)) return WTCONV_ERR_INVALID_ARG;
-    if (state_count(counts, n) < 0) return WTCONV_ERR_UNSUPPORTED_SHAPE;
-    const size_t need = wtconv_grad_norm_workspace_size(n);
+    const size_t need = wtconv_grad_norm_workspace_size(counts, n);
+    if (need == (size_t)-1) return WTCONV_ERR_UNSUPPORTED_SHAPE;
     if (need && (!ws || !aligned(ws, 8) || ws_bytes < need)) return WTCONV_ERR_WORKSPACE;
     auto hit = [](const void* p, uint64_t np, const void* q, uint64_t nq) {
         return p && q && (uintptr_t)p < (uintptr_t)q + nq && (uintptr_t)q < (uintptr_t)p + np;
@@ -194,6 +198,16 @@ wtconv_status_t wtconv_grad_norm(int32_t n, const void* const* grads, const int6
         if (!aligned(grads[i], e) || (uint64_t)(uintptr_t)grads[i] >> 48 || hit(grads[i], bytes, out, 8) || hit(grads[i], bytes, step, 8) ||
             hit(grads[i], bytes, ws, need))
             return WTCONV_ERR_INVALID_ARG;
+    }
+    if (need == 0) {
+        wtc::NormTable<wtc::NORM_PIECES> few = {};
+        for (int i = 0; i < n; ++i)
+            for (int64_t at = 0; grads[i] && at < counts[i]; at += wtc::NORM_PIECE) {
+                const uint64_t g = ((uintptr_t)grads[i] + at * elem_bytes(dtypes[i])) | (dtypes[i] == WTCONV_BF16);
+                const uint32_t last = (uint32_t)std::min<int64_t>(wtc::NORM_PIECE, counts[i] - at) - 1;
+                few.t[few.n++] = {{(uint32_t)g, (uint32_t)(g >> 32) | last << 16, 0}};
+            }
+        return done(wtc::norm_alone(few, max_norm, (long long*)step, out, (hipStream_t)stream));
     }
     double* sums = (double*)ws;
     for (int at = 0; at < n;) {
