@@ -465,6 +465,20 @@ def test_optimizer_groups_of_other_bits():
 
 
 @pytest.mark.parametrize("bits", [32, 8])
+def test_optimizer_groups_without_parameters(bits):
+    """As when a list of parameters is split by a rule that holds for none or for all of them."""
+    a, b = net(), net()
+    mine = AdamW([dict(params=[]), dict(params=a.parameters()), dict(params=[], lr=0.5)], state_bits=bits, max_norm=1.0)
+    plain = AdamW(b.parameters(), state_bits=bits, max_norm=1.0)
+    for i in range(2):
+        for m, o in ((a, mine), (b, plain)):
+            gradients(m, i)
+            o.step()
+        mine.load_state_dict(copy.deepcopy(mine.state_dict()))
+    assert all(torch.equal(p, q) for p, q in zip(a.parameters(), b.parameters()))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
 def test_optimizer_captured(bits):
     """A whole training step in a graph, against the same steps outside of one."""
     a, b = net(), net()

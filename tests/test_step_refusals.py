@@ -203,3 +203,13 @@ def test_optimizer_arguments():
     w.grad = torch.zeros(4)
     with pytest.raises((ValueError, RuntimeError)):
         o.step()   # not on the GPU
+
+
+def test_optimizer_groups_without_parameters():
+    w = torch.nn.Parameter(torch.zeros(4))
+    for groups in ([[w], []], [[], [w]], [[]]):
+        o = op.AdamW([dict(params=g) for g in groups])
+        assert o.step() is None
+        o.load_state_dict(o.state_dict())
+    with pytest.raises(ValueError):
+        op.AdamW([dict(params=[]), dict(params=[w]), dict(params=[torch.nn.Parameter(torch.zeros(4, device="meta"))])])

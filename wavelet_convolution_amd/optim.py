@@ -63,11 +63,11 @@ class AdamW(torch.optim.Optimizer):
         if self._step is not None:
             raise RuntimeError("parameter groups are added before the first step: all share its count")
         super().add_param_group(group)
-        g, first = self.param_groups[-1], self.param_groups[0]["params"][0]
+        g, params = self.param_groups[-1], self._params()
         why = None
         if any(p.dtype not in (torch.float32, torch.bfloat16) or p.dtype != g["params"][0].dtype for p in g["params"]):
             why = "the parameters of a group must be all float32 or all bfloat16"
-        elif any(p.device != first.device for p in g["params"]):
+        elif any(p.device != params[0].device for p in g["params"]):
             why = "all parameters must be on one device"
         elif not (0 <= g["lr"] < math.inf and 0 <= g["weight_decay"] < math.inf and g["eps"] > 0
                   and all(0 <= b < 1 for b in g["betas"]) and g["state_bits"] in (8, 32)):
@@ -77,8 +77,13 @@ class AdamW(torch.optim.Optimizer):
             raise ValueError(why)
         self._buffers.append(None)
 
+    def _params(self) -> list:
+        return [p for g in self.param_groups for p in g["params"]]
+
     def _make(self, group) -> dict:
         params, eight = group["params"], group["state_bits"] == 8
+        if not params:
+            return {}
         n, dev = _ob.wtconv_adamw_state_count(params), params[0].device
         kind = torch.float8_e4m3fn if eight else torch.float32
         b = {"m": torch.zeros(n, dtype=kind, device=dev), "v": torch.zeros(n, dtype=kind, device=dev)}
@@ -151,8 +156,7 @@ class AdamW(torch.optim.Optimizer):
                 raise ValueError("the state is of other parameters, or of other state_bits or master copies")
             new.append({k: like[k].copy_(t) for k, t in b.items()})
         self._buffers = new
-        dev = self.param_groups[0]["params"][0].device
-        self._step = None if state["step"] is None else state["step"].to(dev, copy=True)
+        self._step = None if state["step"] is None else state["step"].to(self._params()[0].device, copy=True)
         for mine, other in zip(self.param_groups, groups):
             mine.update({k: v for k, v in other.items() if k != "params"})
 
