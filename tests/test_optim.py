@@ -513,6 +513,19 @@ def test_optimizer_captured(bits):
         assert all(torch.equal(u, v) for u, v in zip(a.parameters(), b.parameters()))
 
 
+def test_the_first_step_is_not_captured():
+    """A graph would make the states again at every replay."""
+    w = torch.nn.Parameter(torch.ones(300, device=DEV))
+    w.grad = torch.ones_like(w)
+    o = AdamW([w], max_norm=1.0)
+    with pytest.raises(RuntimeError, match="before the capture"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            o.step()
+    assert torch.equal(w.detach(), torch.ones_like(w))
+    o.step()
+    assert int(o.state_dict()["state"]["step"]) == 1
+
+
 def test_optimizer_skips_steps_that_are_not_finite():
     a = net()
     o = AdamW(a.parameters(), state_bits=8, max_norm=math.inf)

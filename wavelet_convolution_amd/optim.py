@@ -112,11 +112,15 @@ class AdamW(torch.optim.Optimizer):
         grads = [t for _, ts in groups for t in ts if t is not None]
         if not grads:
             return loss
-        for i, (g, _) in enumerate(groups):
-            if self._buffers[i] is None:
-                self._buffers[i] = self._make(g)
-        if self._step is None:
-            self._step = torch.zeros(1, dtype=torch.int64, device=grads[0].device)
+        if self._step is None or None in self._buffers:
+            if grads[0].is_cuda and torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("the first step makes the states, which a graph would make again at every replay: "
+                                   "take a step before the capture")
+            for i, (g, _) in enumerate(groups):
+                if self._buffers[i] is None:
+                    self._buffers[i] = self._make(g)
+            if self._step is None:
+                self._step = torch.zeros(1, dtype=torch.int64, device=grads[0].device)
         if self.max_norm is None:
             self._step += 1
             factor = None
