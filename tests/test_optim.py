@@ -513,6 +513,36 @@ def test_optimizer_captured(bits):
         assert all(torch.equal(u, v) for u, v in zip(a.parameters(), b.parameters()))
 
 
+@pytest.mark.parametrize("dtype,bits", [(F32, 32), (F32, 8), (BF16, 32)])
+def test_a_captured_step_goes_on_from_a_loaded_state(dtype, bits):
+    """The graph's buffers are those that the state is loaded into."""
+    a = net(dtype)
+    o = AdamW(a.parameters(), state_bits=bits, max_norm=0.1)
+    for w in a.parameters():
+        w.grad = torch.randn_like(w)
+    o.step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o.step()
+    torch.cuda.synchronize()
+    saved, weights = copy.deepcopy(o.state_dict()), copy.deepcopy(a.state_dict())
+    results = []
+    for _ in range(3):
+        a.load_state_dict(weights)
+        o.load_state_dict(saved)
+        graph.replay()
+        torch.cuda.synchronize()
+        results.append(([w.detach().clone() for w in a.parameters()], copy.deepcopy(o.state_dict()["state"])))
+        graph.replay()   # goes on, and is taken back
+    assert int(results[0][1]["step"]) == 2
+    first = results[0][1]["buffers"][0]
+    for ws, st in results[1:]:
+        assert all(torch.equal(p, q) for p, q in zip(ws, results[0][0]))
+        assert int(st["step"]) == 2 and all(
+            torch.equal(t.view(torch.uint8), first[k].view(torch.uint8)) for k, t in st["buffers"][0].items())
+    assert not any(torch.equal(p, q) for p, q in zip(results[0][0], weights.values()))
+
+
 def test_the_first_step_is_not_captured():
     """A graph would make the states again at every replay."""
     w = torch.nn.Parameter(torch.ones(300, device=DEV))

@@ -145,22 +145,26 @@ class AdamW(torch.optim.Optimizer):
 
     @torch.no_grad()
     def load_state_dict(self, state_dict) -> None:
+        """States are copied into the buffers that are there, so that a captured step goes on with them."""
         state, groups = state_dict["state"], state_dict["param_groups"]
         if len(groups) != len(self.param_groups) or any(
                 len(a["params"]) != len(b["params"]) for a, b in zip(groups, self.param_groups)):
             raise ValueError("the state has other parameter groups than this optimizer")
         new = []
-        for b, g in zip(state["buffers"], self.param_groups):
-            if b is None:
-                new.append(None)
-                continue
-            like = self._make(g)
-            if like.keys() != b.keys() or any(like[k].shape != t.shape or like[k].dtype != t.dtype
-                                              for k, t in b.items()):
+        for b, g, own in zip(state["buffers"], self.param_groups, self._buffers):
+            like = None if b is None else own or self._make(g)
+            if like is not None and (like.keys() != b.keys() or any(
+                    like[k].shape != t.shape or like[k].dtype != t.dtype for k, t in b.items())):
                 raise ValueError("the state is of other parameters, or of other state_bits or master copies")
-            new.append({k: like[k].copy_(t) for k, t in b.items()})
+            new.append(like)
+        for like, b in zip(new, state["buffers"]):
+            for k in like or ():
+                like[k].copy_(b[k])
         self._buffers = new
-        self._step = None if state["step"] is None else state["step"].to(self._params()[0].device, copy=True)
+        if state["step"] is None or self._step is None:
+            self._step = None if state["step"] is None else state["step"].to(self._params()[0].device, copy=True)
+        else:
+            self._step.copy_(state["step"])
         for mine, other in zip(self.param_groups, groups):
             mine.update({k: v for k, v in other.items() if k != "params"})
 
