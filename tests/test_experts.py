@@ -419,3 +419,19 @@ def test_refusals_on_the_gpu():
         with pytest.raises(ValueError):
             call()
             pytest.fail(f"case {i}")
+
+
+def test_no_memory_is_torchs_error():
+    """An output that does not fit raises what torch's own allocations raise."""
+    x, place = torch.zeros(1 << 14, 512, device=DEV), torch.zeros(1 << 14, 64, dtype=torch.int32, device=DEV)
+    offsets = torch.zeros(9, dtype=torch.int32, device=DEV)   # xs takes 2 GiB
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    try:
+        torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + 2 ** 30) / total)
+        with pytest.raises(torch.OutOfMemoryError):
+            eb.wtconv_expert_rows_fwd(x, place, offsets)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert eb.wtconv_expert_rows_fwd(x[:16], place[:16], offsets).shape == (1024, 512)
