@@ -213,3 +213,10 @@ def test_optimizer_groups_without_parameters():
         o.load_state_dict(o.state_dict())
     with pytest.raises(ValueError):
         op.AdamW([dict(params=[]), dict(params=[w]), dict(params=[torch.nn.Parameter(torch.zeros(4, device="meta"))])])
+
+
+def test_optimizer_takes_contiguous_parameters():
+    w = torch.zeros(4, 3, 2, 2).to(memory_format=torch.channels_last)
+    with pytest.raises(ValueError, match="contiguous"):
+        op.AdamW([torch.nn.Parameter(w)])
+    op.AdamW([torch.nn.Parameter(w[:, :, :1, :1].contiguous())])

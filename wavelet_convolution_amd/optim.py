@@ -7,8 +7,9 @@ number on the GPU.
     optim.step()
 
 The update is that of torch.optim.AdamW with the bias corrections of one step
-count for all parameters. Parameters are fp32, or bf16 with fp32 master copies
-(master=False: without). Tensors must be on the GPU: there is no CPU path.
+count for all parameters. Parameters are contiguous, fp32, or bf16 with fp32
+master copies (master=False: without). Tensors must be on the GPU: there is no
+CPU path.
 """
 from __future__ import annotations
 
@@ -69,6 +70,8 @@ class AdamW(torch.optim.Optimizer):
             why = "the parameters of a group must be all float32 or all bfloat16"
         elif any(p.device != params[0].device for p in g["params"]):
             why = "all parameters must be on one device"
+        elif any(not p.is_contiguous() for p in g["params"]):
+            why = "parameters must be contiguous (the states have their elements' order)"
         elif not (0 <= g["lr"] < math.inf and 0 <= g["weight_decay"] < math.inf and g["eps"] > 0
                   and all(0 <= b < 1 for b in g["betas"]) and g["state_bits"] in (8, 32)):
             why = "lr >= 0, weight_decay >= 0, eps > 0, betas in [0, 1) and state_bits 8 or 32 are required"
