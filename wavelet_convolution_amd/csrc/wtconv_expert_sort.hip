@@ -6,11 +6,13 @@
 // a population count and no atomic decides an order.
 //
 // What bounds it is the length of that chain, not memory: one workgroup sorts
-// few slots alone (SORT_ALONE); else a first launch counts parts of 2,048 slots
-// and each part's workgroup sums up the counts of all (SORT_SUMS), or, where
+// few slots alone (SORT_ALONE); else a first launch counts parts of some thousand
+// slots and each part's workgroup sums up the counts of all (SORT_SUMS), or, where
 // those are many, a launch in between makes running sums of them (SORT_SCAN).
-// 16 experts: 2 slots 3.7 us, 4,096 6.3, 401,408 10.3 us (their 6.4 MB take 1.2);
-// 64 experts: 8.4 M slots 76 us, 1.8 TB/s.
+// 16 experts: 2 slots 3.7 us, 4,096 5.9, 401,408 9.9 us (their 6.4 MB take 1.2);
+// 64 experts: 8.4 M slots 65 us, 2.1 TB/s.
+#include <algorithm>
+
 #include "wtconv_experts.h"
 
 namespace wtc {
@@ -233,21 +235,30 @@ __global__ __launch_bounds__(T) void k_sort_place(SortArgs a) {
 }
 
 // How S slots of E experts are sorted, in how many parts. Alone up to what the
-// wavefronts of a workgroup hold: 4,096 slots of 64 experts 6.4 us against 7.3
-// in two parts, 8,192 in two rounds 10.7 against 7.4.
+// wavefronts of a workgroup hold: 4,096 slots of 64 experts 6.1 us against 6.9
+// in parts, 8,192 in two rounds 10.7 against 7.4.
 struct Plan {
     int mode, parts;
     uint32_t per;
 };
-// The sums in each part's workgroup cost parts * (E + 1) reads there, the
-// running sums a launch: 401,408 slots of 64 experts (196 parts) 10.5 us against
-// 12.0, of 256 experts 16.0 against 13.7; 131,072 of 1,024 22.1 against 17.9.
+// Parts of 2,048 slots; of 1,024 where a part's workgroup has few counts to sum
+// up and a CU to itself (65,536 slots of 64 experts 7.8 us against 8.9, of 128
+// experts 8.8 against 8.7), and of 4,096 where the card would not hold all of
+// 2,048 at once (2.1 M slots of 16 experts 17.4 against 22, 1.05 M the same).
+// The sums cost every part's workgroup the counts of all parts, in rows of a power
+// of two, and the running sums a launch: 401,408 slots of 64 experts (196 rows of
+// 128) 11.1 us against 11.7, 262,144 of 128 (128 of 256) 11.5 and 11.7, 300,000 of
+// 128 12.8 and 12.0; with two workgroups a CU 600,000 of 32 (293 of 64) 12.2 and
+// 12.4, of 64 16.2 and 13.3.
 Plan plan_of(long long S, int E) {
-    constexpr long long ALONE = WAVES * 64 * HELD, PART = 2048, MOST = 4096, SUMS = 32768;
+    constexpr long long ALONE = WAVES * 64 * HELD, MOST = 4096;
     if (S <= ALONE) return {SORT_ALONE, 1, (uint32_t)S};
-    const long long parts = (S + PART - 1) / PART < MOST ? (S + PART - 1) / PART : MOST;
+    long long row = 2;
+    while (row < E + 1) row *= 2;
+    auto count = [&](long long part) { return std::min((S + part - 1) / part, MOST); };
+    const long long parts = count(S > 512 * 2048 ? 4096 : S <= 256 * 1024 && count(1024) * row <= 12288 ? 1024 : 2048);
     const long long per = ((S + parts - 1) / parts + 63) / 64 * 64;   // the last parts may be short or empty
-    return {parts * (E + 1) <= SUMS ? SORT_SUMS : SORT_SCAN, (int)parts, (uint32_t)per};
+    return {parts * row <= (parts <= 256 ? 32768 : 20480) ? SORT_SUMS : SORT_SCAN, (int)parts, (uint32_t)per};
 }
 
 template <typename I, bool ALL>
