@@ -44,10 +44,10 @@ def test_sort(N, K, E, dtype):
 
 
 # on both sides of where parts change their size, and counts the way they are summed up
-@pytest.mark.parametrize("N,K,E", [(4096, 1, 1023), (4097, 1, 16), (16_385, 1, 255), (24_577, 1, 256), (262_144, 1, 16),
-                                   (262_145, 1, 16), (131_072, 2, 128), (131_073, 2, 128), (65_537, 1, 1024),
-                                   (1_048_576, 1, 32), (1_048_577, 1, 16), (2_097_153, 1, 3), (2_500_000, 1, 1024),
-                                   (8_388_608, 2, 5), (8_388_609, 2, 5)])
+@pytest.mark.parametrize("N,K,E", [(2048, 2, 63), (2048, 2, 64), (4096, 1, 1023), (4097, 1, 16), (16_385, 1, 255),
+                                   (24_577, 1, 256), (262_144, 1, 16), (262_145, 1, 16), (131_072, 2, 128),
+                                   (131_073, 2, 128), (65_537, 1, 1024), (1_048_576, 1, 32), (1_048_577, 1, 16),
+                                   (2_097_153, 1, 3), (2_500_000, 1, 1024), (8_388_608, 2, 5), (8_388_609, 2, 5)])
 def test_sort_in_parts(N, K, E):
     e = ids(N, K, E, dtype=torch.int32)
     same(eb.wtconv_expert_sort(e, E), sort_ref(e, E))

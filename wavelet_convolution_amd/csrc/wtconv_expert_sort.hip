@@ -9,7 +9,7 @@
 // few slots alone (SORT_ALONE); else a first launch counts parts of some thousand
 // slots and each part's workgroup sums up the counts of all (SORT_SUMS), or, where
 // those are many, a launch in between makes running sums of them (SORT_SCAN).
-// 16 experts: 2 slots 3.7 us, 4,096 5.9, 401,408 9.9 us (their 6.4 MB take 1.2);
+// 16 experts: 2 slots 3.3 us, 4,096 5.5, 401,408 9.9 us (their 6.4 MB take 1.2);
 // 64 experts: 8.4 M slots 65 us, 2.1 TB/s.
 #include <algorithm>
 
@@ -171,40 +171,62 @@ __global__ __launch_bounds__(T) void k_sort_place(SortArgs a) {
             }
     }
     __syncthreads();
-    if constexpr (MODE == SORT_ALONE) {
-        for (int e = threadIdx.x; e < n; e += T) {
+    int* next = cnt + w * n;   // of each expert, the wavefront's next place
+    if (MODE == SORT_ALONE && n <= 64) {
+        // every wavefront for itself, an expert a lane, without the three barriers
+        // below: 256 slots of 16 experts 3.4 us against 4.0, 4,096 5.5 against 5.9;
+        // more experts, and parts' workgroups, were slower
+        next += WAVES * n;
+        const int e = min((int)lane, n - 1);
+        int of_before = 0, of_all = 0;   // of the wavefronts
+        for (int k = 0; k < run.waves; ++k) {
+            const int c = cnt[k * n + e];
+            of_before += k < (int)w ? c : 0;
+            of_all += c;
+        }
+        const int first = wave_before((int)lane < n ? of_all : 0, (int)lane);
+        if ((int)lane < n) {
+            if (w == 0) a.offsets[e] = first;
+            next[e] = first + of_before;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    } else {
+        if constexpr (MODE == SORT_ALONE) {
+            for (int e = threadIdx.x; e < n; e += T) {
+                int c = 0;
+                for (int k = 0; k < run.waves; ++k) c += cnt[k * n + e];
+                all[e] = c;
+                before[e] = 0;
+            }
+            __syncthreads();
+        }
+        // each expert's first place: the sums before it, 64 runs of experts in a
+        // wavefront's lanes
+        if (w == 0) {
+            const int per = (n + 63) / 64, first = min(n, (int)lane * per), last = min(n, first + per);
             int c = 0;
-            for (int k = 0; k < run.waves; ++k) c += cnt[k * n + e];
-            all[e] = c;
-            before[e] = 0;
+            for (int e = first; e < last; ++e) c += all[e];
+            int at = wave_before(c, (int)lane);
+            for (int e = first; e < last; ++e) {
+                const int here = all[e];
+                all[e] = at;
+                at += here;
+            }
+        }
+        __syncthreads();
+        // each wavefront's first place of each expert
+        for (int e = threadIdx.x; e < n; e += T) {
+            if (part == 0) a.offsets[e] = all[e];
+            int at = all[e] + before[e];
+            for (int k = 0; k < run.waves; ++k) {
+                const int c = cnt[k * n + e];
+                cnt[k * n + e] = at;
+                at += c;
+            }
         }
         __syncthreads();
     }
-    // each expert's first place: the sums before it, 64 runs of experts in a
-    // wavefront's lanes
-    if (w == 0) {
-        const int per = (n + 63) / 64, first = min(n, (int)lane * per), last = min(n, first + per);
-        int c = 0;
-        for (int e = first; e < last; ++e) c += all[e];
-        int at = wave_before(c, (int)lane);
-        for (int e = first; e < last; ++e) {
-            const int here = all[e];
-            all[e] = at;
-            at += here;
-        }
-    }
-    __syncthreads();
-    // each wavefront's first place of each expert
-    for (int e = threadIdx.x; e < n; e += T) {
-        if (part == 0) a.offsets[e] = all[e];
-        int at = all[e] + before[e];
-        for (int k = 0; k < run.waves; ++k) {
-            const int c = cnt[k * n + e];
-            cnt[k * n + e] = at;
-            at += c;
-        }
-    }
-    __syncthreads();
     const int bits = 32 - __clz(a.E);   // of the numbers 0..E
     keys.each(a, run, lane, [&](uint32_t at, int e) {
         const bool on = e >= 0;
@@ -221,12 +243,12 @@ __global__ __launch_bounds__(T) void k_sort_place(SortArgs a) {
         }
         const int rank = __builtin_amdgcn_mbcnt_hi(hi, __builtin_amdgcn_mbcnt_lo(lo, 0));
         if (on) {
-            const int first = cnt[w * n + e], p = first + rank;
+            const int first = next[e], p = first + rank;
             a.place[at + lane] = p;
             a.order[p] = (int)(at + lane);
             // one lane of each expert moves its count on, after all have read
             // it: a wavefront's LDS accesses are in order
-            if (rank == 0) cnt[w * n + e] = first + __popc(lo) + __popc(hi);
+            if (rank == 0) next[e] = first + __popc(lo) + __popc(hi);
         }
         // the next group's reads stay behind this one's writes
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
