@@ -53,6 +53,56 @@ def test_sort_in_parts(N, K, E):
     same(eb.wtconv_expert_sort(e, E), sort_ref(e, E))
 
 
+def check_stable(e, E, got):
+    """order, place and offsets are those of a stable sort, by what defines them: places and slots undo each other,
+    experts do not fall along the places, the slots of one rise, and offsets count. In pieces, for many slots."""
+    order, place, offsets = got
+    order, flat, place, S = order.view(-1), e.reshape(-1), place.view(-1), e.numel()
+    count, last = torch.zeros(E + 1, dtype=torch.int64, device=DEV), (-1, -1)
+    for at in range(0, S, 1 << 27):
+        slots = order[at:at + (1 << 27)].long()
+        assert int(slots.min()) >= 0 and int(slots.max()) < S, at
+        assert torch.equal(place[slots].long(), torch.arange(at, at + len(slots), device=DEV)), at
+        key = flat[slots].long()
+        key = torch.where((key < 0) | (key >= E), E, key)
+        assert (int(key[0]), int(slots[0])) > last, at
+        assert ((key[1:] > key[:-1]) | ((key[1:] == key[:-1]) & (slots[1:] > slots[:-1]))).all(), at
+        count += torch.bincount(key, minlength=E + 1)
+        last = int(key[-1]), int(slots[-1])
+    assert torch.equal(offsets[1:].long(), count.cumsum(0)[:E]) and int(offsets[0]) == 0
+
+
+@pytest.mark.parametrize("E", [1, 2, 3, 4, 64])
+@pytest.mark.parametrize("S", [2 ** 24, 2 ** 24 + 1, 100_000_003])
+def test_sort_of_more_slots_than_the_parts_hold(S, E):
+    """From 2^24 slots on a part has more slots than a workgroup's wavefronts hold in registers."""
+    g = torch.Generator(DEV).manual_seed(S + E)
+    e = torch.randint(-1 if E > 1 else 0, E + 1, (S, 1), generator=g, device=DEV, dtype=torch.int32)
+    check_stable(e, E, eb.wtconv_expert_sort(e, E))
+
+
+@pytest.mark.parametrize("E", [3, 1000])
+def test_sort_of_as_many_slots_as_there_are_places(E):
+    S = 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[0] < 64 * 2 ** 30:
+        pytest.skip("needs 64 GiB")
+    e = torch.empty(S, 1, device=DEV, dtype=torch.int32).random_(0, E + 1, generator=torch.Generator(DEV).manual_seed(E))
+    check_stable(e, E, eb.wtconv_expert_sort(e, E))
+
+
+def test_stable_sorts_are_told_from_others():
+    e = ids(5000, 2, 7)
+    order, place, offsets = eb.wtconv_expert_sort(e, 7)
+    check_stable(e, 7, (order, place, offsets))
+    other = order.clone()
+    other[:2] = order[:2].flip(0)   # two slots of one expert
+    turned = torch.empty_like(place.view(-1))
+    turned[other.long()] = torch.arange(len(other), device=DEV, dtype=torch.int32)
+    for bad in ((other, turned, offsets), (order, turned, offsets), (other, place, offsets), (order, place, offsets + 1)):
+        with pytest.raises(AssertionError):
+            check_stable(e, 7, bad)
+
+
 @pytest.mark.parametrize("N", [1, 700, 9000])
 @pytest.mark.parametrize("what", ["one", "last", "none", "far", "in order", "backwards"])
 def test_sort_of_extremes(N, what):

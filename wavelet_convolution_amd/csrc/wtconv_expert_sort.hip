@@ -23,6 +23,7 @@ constexpr int T = 1024, WAVES = T / 64;
 // Groups of 64 slots whose experts a wavefront holds in registers from its
 // count to its walk; runs of more read them again.
 constexpr int HELD = 4;
+constexpr uint32_t MOST_HELD = WAVES * 64 * HELD;   // slots of a workgroup that are all held
 
 enum { SORT_ALONE = 0, SORT_SUMS = 1, SORT_SCAN = 2 };
 
@@ -271,16 +272,19 @@ struct Plan {
 // of two, and the running sums a launch: 401,408 slots of 64 experts (196 rows of
 // 128) 11.1 us against 11.7, 262,144 of 128 (128 of 256) 11.5 and 11.7, 300,000 of
 // 128 12.8 and 12.0; with two workgroups a CU 600,000 of 32 (293 of 64) 12.2 and
-// 12.4, of 64 16.2 and 13.3.
+// 12.4, of 64 16.2 and 13.3. The number of parts is bounded, so beyond 2^24 slots
+// a part has more than its wavefronts hold: those are for the kernel that reads
+// experts again, which goes by running sums.
 Plan plan_of(long long S, int E) {
-    constexpr long long ALONE = WAVES * 64 * HELD, MOST = 4096;
-    if (S <= ALONE) return {SORT_ALONE, 1, (uint32_t)S};
+    constexpr long long MOST = 4096;
+    if (S <= MOST_HELD) return {SORT_ALONE, 1, (uint32_t)S};
     long long row = 2;
     while (row < E + 1) row *= 2;
     auto count = [&](long long part) { return std::min((S + part - 1) / part, MOST); };
     const long long parts = count(S > 512 * 2048 ? 4096 : S <= 256 * 1024 && count(1024) * row <= 12288 ? 1024 : 2048);
     const long long per = ((S + parts - 1) / parts + 63) / 64 * 64;   // the last parts may be short or empty
-    return {parts * row <= (parts <= 256 ? 32768 : 20480) ? SORT_SUMS : SORT_SCAN, (int)parts, (uint32_t)per};
+    const bool sums = per <= MOST_HELD && parts * row <= (parts <= 256 ? 32768 : 20480);
+    return {sums ? SORT_SUMS : SORT_SCAN, (int)parts, (uint32_t)per};
 }
 
 template <typename I, bool ALL>
@@ -295,11 +299,14 @@ void place(const SortArgs& a, int mode, hipStream_t s) {
 
 template <typename I>
 hipError_t sort(const SortArgs& a, int mode, hipStream_t s) {
+    // held slots past the last group would be neither counted nor placed
+    const bool held = a.per <= MOST_HELD;
+    if (!held && mode != SORT_SCAN) return hipErrorInvalidConfiguration;
     if (mode != SORT_ALONE) {
         hipLaunchKernelGGL(k_sort_count<I>, dim3(a.parts), dim3(T), 0, s, a, mode == SORT_SCAN);
         if (mode == SORT_SCAN) hipLaunchKernelGGL(k_sort_scan, dim3(a.E + 1), dim3(T), 0, s, a);
     }
-    if (a.per <= WAVES * 64 * HELD)
+    if (held)
         place<I, true>(a, mode, s);
     else
         place<I, false>(a, mode, s);
