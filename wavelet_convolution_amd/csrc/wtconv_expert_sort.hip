@@ -245,10 +245,13 @@ __global__ __launch_bounds__(T) void k_sort_place(SortArgs a) {
         const int rank = __builtin_amdgcn_mbcnt_hi(hi, __builtin_amdgcn_mbcnt_lo(lo, 0));
         if (on) {
             const int first = next[e], p = first + rank;
+            // one lane of each expert moves its count on, after all have read
+            // it: a wavefront's LDS accesses are in order, and the compiler
+            // keeps the reads before the fence
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
             a.place[at + lane] = p;
             a.order[p] = (int)(at + lane);
-            // one lane of each expert moves its count on, after all have read
-            // it: a wavefront's LDS accesses are in order
             if (rank == 0) next[e] = first + __popc(lo) + __popc(hi);
         }
         // the next group's reads stay behind this one's writes
