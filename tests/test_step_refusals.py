@@ -220,3 +220,47 @@ def test_optimizer_takes_contiguous_parameters():
     with pytest.raises(ValueError, match="contiguous"):
         op.AdamW([torch.nn.Parameter(w)])
     op.AdamW([torch.nn.Parameter(w[:, :, :1, :1].contiguous())])
+
+
+def _made(shapes, dtype=torch.float32, **kw):
+    """An optimizer whose states are there (on the host: no step is taken)."""
+    o = op.AdamW([torch.nn.Parameter(torch.randn(s).to(dtype)) for s in shapes], **kw)
+    o._buffers, o._step = [o._make(g) for g in o.param_groups], torch.full((1,), 3)
+    for t in o._buffers[0].values():
+        t.copy_(torch.rand(t.shape))
+    return o
+
+
+@pytest.mark.parametrize("dtype,bits", [(torch.float32, 32), (torch.float32, 8), (torch.bfloat16, 32)])
+@pytest.mark.parametrize("mine,theirs", [(((256,), (10,)), ((10,), (256,))), (((300, 2), (700,)), ((700,), (300, 2))),
+                                         (((16, 8),), ((8, 16),)), (((100,), (0,)), ((0,), (100,)))])
+def test_a_state_of_other_shapes_is_refused(lib, mine, theirs, dtype, bits):
+    """Buffers of the same size whose tensors stand elsewhere."""
+    saved = _made(mine, dtype, state_bits=bits).state_dict()
+    for o in (_made(theirs, dtype, state_bits=bits),
+              op.AdamW([torch.nn.Parameter(torch.zeros(s, dtype=dtype)) for s in theirs], state_bits=bits)):
+        before = [None if b is None else {k: t.clone() for k, t in b.items()} for b in o._buffers], o._step
+        with pytest.raises(ValueError, match="other parameters"):
+            o.load_state_dict(saved)
+        assert o._step is before[1]
+        assert all(b is a or all(torch.equal(a[k].float(), b[k].float()) for k in a) for a, b in zip(before[0], o._buffers))
+    same = _made(mine, dtype, state_bits=bits)
+    same.load_state_dict(saved)
+    assert all(torch.equal(same._buffers[0][k].float(), t.float()) for k, t in saved["state"]["buffers"][0].items())
+
+
+def test_a_state_without_shapes_is_loaded(lib):
+    """As states were saved that did not hold them."""
+    saved = _made(((7, 3), (300,))).state_dict()
+    del saved["state"]["shapes"]
+    o = _made(((7, 3), (300,)))
+    o.load_state_dict(saved)
+    assert all(torch.equal(o._buffers[0][k], t) for k, t in saved["state"]["buffers"][0].items())
+
+
+def test_a_state_without_buffers_is_loaded_for_any_shapes():
+    """There is nothing in it that belongs to a parameter."""
+    saved = op.AdamW([torch.nn.Parameter(torch.zeros(4, 2))], lr=0.5).state_dict()
+    o = op.AdamW([torch.nn.Parameter(torch.zeros(9))])
+    o.load_state_dict(saved)
+    assert o.param_groups[0]["lr"] == 0.5 and o._buffers == [None]

@@ -83,6 +83,9 @@ class AdamW(torch.optim.Optimizer):
     def _params(self) -> list:
         return [p for g in self.param_groups for p in g["params"]]
 
+    def _shapes(self) -> list:
+        return [[tuple(p.shape) for p in g["params"]] for g in self.param_groups]
+
     def _make(self, group) -> dict:
         params, eight = group["params"], group["state_bits"] == 8
         if not params:
@@ -140,10 +143,11 @@ class AdamW(torch.optim.Optimizer):
         return loss
 
     def state_dict(self) -> dict:
-        """{"state": {"step", "buffers"}, "param_groups"}: the states' buffers as they are (a group's are None before
-        its first step), not a state for each parameter."""
+        """{"state": {"step", "buffers", "shapes"}, "param_groups"}: the states' buffers as they are (a group's are
+        None before its first step), not a state for each parameter, and the parameters' shapes, which say whose."""
         groups = super().state_dict()["param_groups"]
-        return {"state": {"step": self._step, "buffers": [b and dict(b) for b in self._buffers]},
+        return {"state": {"step": self._step, "buffers": [b and dict(b) for b in self._buffers],
+                          "shapes": self._shapes()},
                 "param_groups": groups}
 
     @torch.no_grad()
@@ -154,7 +158,12 @@ class AdamW(torch.optim.Optimizer):
                 len(a["params"]) != len(b["params"]) for a, b in zip(groups, self.param_groups)):
             raise ValueError("the state has other parameter groups than this optimizer")
         new = []
-        for b, g, own in zip(state["buffers"], self.param_groups, self._buffers):
+        shapes = self._shapes()
+        # the sums of two lists of shapes may agree (states saved without shapes: as they come)
+        for b, g, own, here, there in zip(state["buffers"], self.param_groups, self._buffers, shapes,
+                                          state.get("shapes", shapes)):
+            if b is not None and here != [tuple(s) for s in there]:
+                raise ValueError("the state is of other parameters: their shapes differ, or their order")
             like = None if b is None else own or self._make(g)
             if like is not None and (like.keys() != b.keys() or any(
                     like[k].shape != t.shape or like[k].dtype != t.dtype for k, t in b.items())):
