@@ -496,6 +496,15 @@ wtconv_status_t wtconv_adamw_step(const wtconv_adamw_desc_t *desc, int32_t n, vo
                                   const int64_t *step, const float *factor, const float *lr_factor,
                                   const uint64_t *rng, void *stream);
 
+/* What wtconv_adamw_step returns for these arguments where it refuses them,
+   and WTCONV_OK otherwise; launches nothing and makes no device call. For a
+   caller whose step is several calls, all or none of which are to be made. */
+wtconv_status_t wtconv_adamw_check(const wtconv_adamw_desc_t *desc, int32_t n, void *const *params,
+                                   const void *const *grads, const int64_t *counts, const float *lr,
+                                   const float *weight_decay, const void *m, const void *v, const float *scales,
+                                   const float *master, const int64_t *step, const float *factor,
+                                   const float *lr_factor, const uint64_t *rng);
+
 /* Device workspace of wtconv_grad_norm for n tensors of these counts (8-byte
    aligned; 0 for few elements, ws may then be NULL), or (size_t)-1 where a
    count is not in 0..2^34, their sum exceeds 2^39 or n < 0. */

@@ -694,3 +694,81 @@ def test_a_block_with_experts_is_trained(bits):
             o.step()
         if o.rng is not None:
             o.rng[1] += 1
+
+
+# ------------------------------------------------------------ refused steps
+
+def _state(model, o):
+    return ([p.detach().clone() for p in model.parameters()], None if o._step is None else int(o._step),
+            [None if b is None else {k: t.clone() for k, t in b.items()} for b in o._buffers])
+
+
+def _same_state(a, b):
+    return (all(torch.equal(x, y) for x, y in zip(a[0], b[0])) and a[1] == b[1]
+            and all(x is y or all(torch.equal(x[k].view(torch.uint8), y[k].view(torch.uint8)) for k in x)
+                    for x, y in zip(a[2], b[2])))
+
+
+# what is wrong in the second group, or for all: how it comes, and how it goes
+REFUSED = {
+    "rate": (lambda o, q: o.param_groups[1].update(lr=float("nan")), lambda o, q: o.param_groups[1].update(lr=1e-2)),
+    "decay": (lambda o, q: o.param_groups[1].update(weight_decay=math.inf),
+              lambda o, q: o.param_groups[1].update(weight_decay=1e-2)),
+    "eps": (lambda o, q: o.param_groups[1].update(eps=1e-40), lambda o, q: o.param_groups[1].update(eps=1e-8)),
+    "betas": (lambda o, q: o.param_groups[1].update(betas=(0.9, 1.0)),
+              lambda o, q: o.param_groups[1].update(betas=(0.9, 0.999))),
+    "rng": (lambda o, q: setattr(o, "rng", o.rng.repeat(2)), lambda o, q: setattr(o, "rng", o.rng[:2].clone())),
+    "lr_factor": (lambda o, q: setattr(o, "lr_factor", torch.ones(2, device=DEV)), lambda o, q: setattr(o, "lr_factor", None)),
+    "site": (lambda o, q: setattr(o, "site", 2 ** 31 - 1), lambda o, q: setattr(o, "site", 40)),
+    "norm": (lambda o, q: setattr(o, "max_norm", -1.0), lambda o, q: setattr(o, "max_norm", 1.0)),
+    "its own gradient": (lambda o, q: setattr(q, "grad", q.data), lambda o, q: setattr(q, "grad", torch.full_like(q, 0.1))),
+}
+
+
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("what", REFUSED)
+def test_a_refused_step_leaves_everything_as_it_was(what, first):
+    """The count, the states and the groups before the one that is wrong; once it is right the step is the one that
+    an optimizer takes to which that did not happen."""
+    wrong, right = REFUSED[what]
+    models = net(), net()
+    opts = [AdamW([dict(params=[m[0].weight, m[0].bias]), dict(params=[m[2].weight, m[2].bias])], lr=1e-2, state_bits=8,
+                  max_norm=1.0, rng=dropout_rng(5), site=40) for m in models]
+    if not first:
+        for m, o in zip(models, opts):
+            gradients(m, 0)
+            o.step()
+    for m in models:
+        gradients(m, 1)
+        m[2].bias.grad = torch.full_like(m[2].bias, 0.1)
+    (a, b), (o, p) = models, opts
+    before = _state(a, o)
+    wrong(o, a[2].bias)
+    for _ in range(2):
+        with pytest.raises((ValueError, RuntimeError)):
+            o.step()
+        torch.cuda.synchronize()
+        assert _same_state(before, _state(a, o))
+    right(o, a[2].bias)
+    for x in opts:
+        x.step()
+    assert _same_state(_state(a, o), _state(b, p)) and int(o._step) == (1 if first else 2)
+
+
+def test_a_refused_first_step_makes_no_master_copies():
+    """They are made from the parameters as they are at the first step that is taken."""
+    a = net(BF16)
+    o = AdamW(a.parameters(), lr=1e-2)
+    o.param_groups[0]["lr"] = float("inf")
+    gradients(a, 0)
+    with pytest.raises(RuntimeError):
+        o.step()
+    assert o._step is None and o._buffers == [None]
+    b = net(BF16, seed=1)
+    a.load_state_dict(b.state_dict())
+    o.param_groups[0]["lr"] = 1e-2
+    p = AdamW(b.parameters(), lr=1e-2)
+    for m, x in ((a, o), (b, p)):
+        gradients(m, 2)
+        x.step()
+    assert all(torch.equal(u, v) for u, v in zip(a.parameters(), b.parameters()))

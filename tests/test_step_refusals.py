@@ -264,3 +264,13 @@ def test_a_state_without_buffers_is_loaded_for_any_shapes():
     o = op.AdamW([torch.nn.Parameter(torch.zeros(9))])
     o.load_state_dict(saved)
     assert o.param_groups[0]["lr"] == 0.5 and o._buffers == [None]
+
+
+@pytest.mark.parametrize("kw,status", [*test_bad_steps.pytestmark[0].args[1], (dict(), 0), (dict(counts=(0, 0)), 0),
+                                       (dict(state_bits=8, scales=8 << 40, rng=9 << 40, site=(1 << 31) - 2), 0),
+                                       (dict(p_dtype=1, master=8 << 40), 0), (dict(grads=(None, None)), 0)])
+def test_the_check_of_a_step_says_what_the_step_says(lib, kw, status, monkeypatch):
+    """Where it finds nothing, too: nothing is launched."""
+    class Check:
+        wtconv_adamw_step = staticmethod(lambda *a: lib.wtconv_adamw_check(*a[:-1]))
+    assert _adamw(Check, **kw) == status

@@ -29,7 +29,7 @@ _BLOCK_NAMES = ("ChannelNorm2d", "BlockResidual2d", "CounterDropout", "channel_n
 _EXPERT_BINDING_NAMES = ("wtconv_expert_sort", "wtconv_expert_rows_fwd", "wtconv_expert_rows_bwd",
                          "wtconv_expert_sum_fwd", "wtconv_expert_sum_bwd")
 _EXPERT_NAMES = ("ExpertRoute", "expert_sort", "expert_rows", "expert_sum")
-_OPTIM_BINDING_NAMES = ("wtconv_adamw_step", "wtconv_adamw_state_count", "wtconv_grad_norm")
+_OPTIM_BINDING_NAMES = ("wtconv_adamw_step", "wtconv_adamw_check", "wtconv_adamw_state_count", "wtconv_grad_norm")
 _OPTIM_NAMES = ("AdamW",)
 
 __all__ = ["CONFIGS", "WorkloadConfig", "get_config", *_BINDING_NAMES, *_MODULE_NAMES, *_BLOCK_BINDING_NAMES,

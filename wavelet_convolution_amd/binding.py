@@ -119,6 +119,8 @@ def load_library() -> ctypes.CDLL:
             lib.wtconv_adamw_state_count.restype = ctypes.c_int64
             lib.wtconv_adamw_step.argtypes = [ctypes.POINTER(WTConvAdamWDesc), ctypes.c_int32] + [_V] * 14
             lib.wtconv_adamw_step.restype = ctypes.c_int
+            lib.wtconv_adamw_check.argtypes = [ctypes.POINTER(WTConvAdamWDesc), ctypes.c_int32] + [_V] * 13
+            lib.wtconv_adamw_check.restype = ctypes.c_int
             lib.wtconv_grad_norm_workspace_size.argtypes = [_V, ctypes.c_int32]
             lib.wtconv_grad_norm_workspace_size.restype = _SZ
             lib.wtconv_grad_norm.argtypes = [ctypes.c_int32, _V, _V, _V, ctypes.c_double, _V, _V, _V, _SZ, _V]

@@ -378,17 +378,29 @@ PyObject* adamw_state_count(PyObject*, PyObject* const* a, Py_ssize_t) {
     });
 }
 
+// The arguments of a step as the C-ABI takes them, from
 // params, grads, m, v, step, lr, weight_decay, beta1, beta2, eps, scales, master, factor, lr_factor, rng, site
-PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t) {
-    return guarded([&]() -> PyObject* {
-        const Items params("params", a[0]), grads("grads", a[1]);
-        const int32_t n = params.n;
+struct AdamwCall {
+    const Items params, grads;
+    const int32_t n;
+    std::vector<void*> p;
+    std::vector<const void*> g;
+    std::vector<int64_t> counts;
+    const at::Tensor* like = nullptr;
+    void *m, *v;
+    float *scales = nullptr, *master = nullptr;
+    const int64_t* step;
+    const float *factor, *lr_factor, *lr, *wd;
+    const uint64_t* rng = nullptr;
+    std::vector<float> own_lr, own_wd;
+    wtconv_adamw_desc_t d;
+
+    explicit AdamwCall(PyObject* const* a) : params("params", a[0]), grads("grads", a[1]), n(params.n) {
         if (n != grads.n || n == 0)
             refuse("one gradient (or None) a parameter, and one at least, are required; got ", n, " and ", grads.n);
-        std::vector<void*> p(n);
-        std::vector<const void*> g(n);
-        std::vector<int64_t> counts(n);
-        const at::Tensor* like = nullptr;
+        p.resize(n);
+        g.resize(n);
+        counts.resize(n);
         int32_t ptype = -1, gtype = -1;
         for (int32_t i = 0; i < n; ++i) {
             const at::Tensor& t = listed("params", params.o[i], like);
@@ -408,15 +420,15 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t) {
                 refuse("gradients must have their parameters' shapes; got ", u.sizes(), " for ", t.sizes());
             g[i] = u.const_data_ptr();
         }
-        void* const stream = stream_of(*like);
         const int64_t all = wtconv_adamw_state_count(counts.data(), n);
         if (all < 0) check_status(WTCONV_ERR_UNSUPPORTED_SHAPE);
         const bool eight = a[10] != Py_None;
         const at::ScalarType kind = eight ? at::kFloat8_e4m3fn : at::kFloat;
-        const at::Tensor &m = tensor("m", a[2], like), &v = tensor("v", a[3], like);
-        check_buffer("m", m, kind, all);
-        check_buffer("v", v, kind, all);
-        float *scales = nullptr, *master = nullptr;
+        const at::Tensor &m_ = tensor("m", a[2], like), &v_ = tensor("v", a[3], like);
+        check_buffer("m", m_, kind, all);
+        check_buffer("v", v_, kind, all);
+        m = m_.mutable_data_ptr();
+        v = v_.mutable_data_ptr();
         if (eight) {
             const at::Tensor& t = tensor("scales", a[10], like);
             check_buffer("scales", t, at::kFloat, all / WTCONV_ADAMW_BLOCK * 2);
@@ -429,9 +441,9 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t) {
             master = t.mutable_data_ptr<float>();
         }
         if (a[4] == Py_None) refuse("step, one int64 number on the GPU, is required");
-        const void* step = scalar("step", a[4], at::kLong, *like);
-        const void *factor = scalar("factor", a[12], at::kFloat, *like), *lr_factor = scalar("lr_factor", a[13], at::kFloat, *like);
-        const uint64_t* rng = nullptr;
+        step = (const int64_t*)scalar("step", a[4], at::kLong, *like);
+        factor = (const float*)scalar("factor", a[12], at::kFloat, *like);
+        lr_factor = (const float*)scalar("lr_factor", a[13], at::kFloat, *like);
         if (a[14] != Py_None) {
             const at::Tensor& t = tensor("rng", a[14], like);
             if (!eight || t.scalar_type() != at::kLong || t.numel() != 2 || !t.is_contiguous())
@@ -440,17 +452,31 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t) {
         }
         const int64_t site = whole("site", a[15]);
         if (site < 0 || site >= 1ll << 31) refuse("site must be in 0..2^31-1");
-        std::vector<float> own_lr, own_wd;
-        const float *lr = each("lr", a[5], n, own_lr), *wd = each("weight_decay", a[6], n, own_wd);
-        const wtconv_adamw_desc_t d{ptype, gtype < 0 ? WTCONV_F32 : gtype, eight ? 8 : 32, (int32_t)site, real(a[7]),
-                                    real(a[8]), real(a[9])};
-        check_status(wtconv_adamw_step(&d, n, p.data(), g.data(), counts.data(), lr, wd, m.mutable_data_ptr(),
-                                       v.mutable_data_ptr(), scales, master, (const int64_t*)step,
-                                       (const float*)factor, (const float*)lr_factor, rng, stream));
+        lr = each("lr", a[5], n, own_lr);
+        wd = each("weight_decay", a[6], n, own_wd);
+        d = {ptype, gtype < 0 ? WTCONV_F32 : gtype, eight ? 8 : 32, (int32_t)site, real(a[7]), real(a[8]), real(a[9])};
+    }
+};
+
+PyObject* adamw_check(PyObject*, PyObject* const* a, Py_ssize_t) {
+    return guarded([&]() -> PyObject* {
+        const AdamwCall c(a);
+        check_status(wtconv_adamw_check(&c.d, c.n, c.p.data(), c.g.data(), c.counts.data(), c.lr, c.wd, c.m, c.v,
+                                        c.scales, c.master, c.step, c.factor, c.lr_factor, c.rng));
+        Py_RETURN_NONE;
+    });
+}
+
+PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t) {
+    return guarded([&]() -> PyObject* {
+        const AdamwCall c(a);
+        void* const stream = stream_of(*c.like);
+        check_status(wtconv_adamw_step(&c.d, c.n, c.p.data(), c.g.data(), c.counts.data(), c.lr, c.wd, c.m, c.v,
+                                       c.scales, c.master, c.step, c.factor, c.lr_factor, c.rng, stream));
         // autograd's own record of changes in place, as torch's operations keep it
-        for (int32_t i = 0; i < n; ++i) {
-            const at::Tensor& t = THPVariable_Unpack(params.o[i]);
-            if (g[i] && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+        for (int32_t i = 0; i < c.n; ++i) {
+            const at::Tensor& t = THPVariable_Unpack(c.params.o[i]);
+            if (c.g[i] && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
         }
         Py_RETURN_NONE;
     });
@@ -510,6 +536,7 @@ PyMethodDef methods[] = {
     method<expert_sum_fwd, 5>("expert_sum_fwd"),
     method<expert_sum_bwd, 9>("expert_sum_bwd"),
     method<adamw_state_count, 1>("adamw_state_count"),
+    method<adamw_check, 16>("adamw_check"),
     method<adamw_step, 16>("adamw_step"),
     method<grad_norm, 5>("grad_norm"),
     {nullptr, nullptr, 0, nullptr},

@@ -60,17 +60,13 @@ struct Ranges {
 
 bool dtype_ok(int d) { return d == WTCONV_F32 || d == WTCONV_BF16; }
 
-}  // namespace
-
-extern "C" {
-
-int64_t wtconv_adamw_state_count(const int64_t* counts, int32_t n) { return state_count(counts, n); }
-
-wtconv_status_t wtconv_adamw_step(const wtconv_adamw_desc_t* d, int32_t n, void* const* params,
-                                  const void* const* grads, const int64_t* counts, const float* lr,
-                                  const float* weight_decay, void* m, void* v, float* scales, float* master,
-                                  const int64_t* step, const float* factor, const float* lr_factor,
-                                  const uint64_t* rng, void* stream) {
+// Everything that a step refuses; whether it has something to do.
+wtconv_status_t check_adamw(const wtconv_adamw_desc_t* d, int32_t n, void* const* params,
+                            const void* const* grads, const int64_t* counts, const float* lr,
+                            const float* weight_decay, const void* m, const void* v, const float* scales,
+                            const float* master, const int64_t* step, const float* factor, const float* lr_factor,
+                            const uint64_t* rng, bool& work) {
+    work = false;
     if (!d || n < 0) return WTCONV_ERR_INVALID_ARG;
     if (!dtype_ok(d->p_dtype) || !dtype_ok(d->g_dtype)) return WTCONV_ERR_INVALID_ARG;
     if (d->state_bits != 8 && d->state_bits != 32) return WTCONV_ERR_INVALID_ARG;
@@ -109,6 +105,36 @@ wtconv_status_t wtconv_adamw_step(const wtconv_adamw_desc_t* d, int32_t n, void*
     ranges.add(lr_factor, 4, false);
     ranges.add(rng, 16, false);
     if (!disjoint(ranges.r, ranges.n)) return WTCONV_ERR_INVALID_ARG;
+    work = true;
+    return WTCONV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t wtconv_adamw_state_count(const int64_t* counts, int32_t n) { return state_count(counts, n); }
+
+wtconv_status_t wtconv_adamw_check(const wtconv_adamw_desc_t* d, int32_t n, void* const* params,
+                                   const void* const* grads, const int64_t* counts, const float* lr,
+                                   const float* weight_decay, const void* m, const void* v, const float* scales,
+                                   const float* master, const int64_t* step, const float* factor,
+                                   const float* lr_factor, const uint64_t* rng) {
+    bool work;
+    return check_adamw(d, n, params, grads, counts, lr, weight_decay, m, v, scales, master, step, factor, lr_factor,
+                       rng, work);
+}
+
+wtconv_status_t wtconv_adamw_step(const wtconv_adamw_desc_t* d, int32_t n, void* const* params,
+                                  const void* const* grads, const int64_t* counts, const float* lr,
+                                  const float* weight_decay, void* m, void* v, float* scales, float* master,
+                                  const int64_t* step, const float* factor, const float* lr_factor,
+                                  const uint64_t* rng, void* stream) {
+    bool work;
+    const wtconv_status_t st = check_adamw(d, n, params, grads, counts, lr, weight_decay, m, v, scales, master, step,
+                                           factor, lr_factor, rng, work);
+    if (st != WTCONV_OK || !work) return st;
+    const bool eight = d->state_bits == 8, bf16 = d->p_dtype == WTCONV_BF16;
 
     wtc::AdamArgs a = {};
     a.m = m;

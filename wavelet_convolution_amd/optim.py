@@ -35,7 +35,8 @@ class AdamW(torch.optim.Optimizer):
     computed). `last_norm` is the last step's {norm, factor} on the GPU.
 
     The states of a group's parameters stand in one buffer each. A parameter
-    without a gradient is left as it is in that step. step() makes no copy to
+    without a gradient is left as it is in that step, and a step that raises an
+    error for its arguments changes nothing in any group. step() makes no copy to
     the host and waits for nothing, so it can be captured into a graph after a
     first step (a graph keeps lr and the other numbers of its capture, but for
     `lr_factor`, an optional fp32 number on the GPU that lr is multiplied by).
@@ -113,33 +114,41 @@ class AdamW(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
-        groups = [(g, [p.grad if p.grad is None else p.grad.contiguous() for p in g["params"]])
-                  for g in self.param_groups]
-        grads = [t for _, ts in groups for t in ts if t is not None]
+        groups, grads = [], []
+        for g in self.param_groups:
+            ts = [_dense(p.grad) for p in g["params"]]
+            there = [t for t in ts if t is not None]
+            groups.append((g, ts, there))
+            grads += there
         if not grads:
             return loss
-        if self._step is None or None in self._buffers:
+        step, buffers = self._step, self._buffers
+        if step is None or None in buffers:
             if grads[0].is_cuda and torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("the first step makes the states, which a graph would make again at every replay: "
                                    "take a step before the capture")
-            for i, (g, _) in enumerate(groups):
-                if self._buffers[i] is None:
-                    self._buffers[i] = self._make(g)
-            if self._step is None:
-                self._step = torch.zeros(1, dtype=torch.int64, device=grads[0].device)
+            buffers = [self._make(g) if b is None else b for g, b in zip(self.param_groups, buffers)]
+            if step is None:
+                step = torch.zeros(1, dtype=torch.int64, device=grads[0].device)
+        calls, site = [], self.site
+        for (g, ts, there), b in zip(groups, buffers):
+            if there:
+                calls.append(((g["params"], ts), dict(
+                    step=step, lr=g["lr"], weight_decay=g["weight_decay"], betas=g["betas"], eps=g["eps"],
+                    lr_factor=self.lr_factor, rng=self.rng if g["state_bits"] == 8 else None, site=site, **b)))
+            site += len(ts)
+        # a step that is refused leaves the count, the states and every group as they were
+        for lists, kw in calls:
+            _ob.wtconv_adamw_check(*lists, **kw)
         if self.max_norm is None:
-            self._step += 1
+            step += 1
             factor = None
         else:
-            self.last_norm = _ob.wtconv_grad_norm(grads, self.max_norm, step=self._step)
+            self.last_norm = _ob.wtconv_grad_norm(grads, self.max_norm, step=step)
             factor = self.last_norm[1:]
-        site = self.site
-        for (g, ts), b in zip(groups, self._buffers):
-            if any(t is not None for t in ts):
-                _ob.wtconv_adamw_step(g["params"], ts, step=self._step, lr=g["lr"], weight_decay=g["weight_decay"],
-                                      betas=g["betas"], eps=g["eps"], factor=factor, lr_factor=self.lr_factor,
-                                      rng=self.rng if g["state_bits"] == 8 else None, site=site, **b)
-            site += len(ts)
+        self._step, self._buffers = step, buffers
+        for lists, kw in calls:
+            _ob.wtconv_adamw_step(*lists, factor=factor, **kw)
         return loss
 
     def state_dict(self) -> dict:
@@ -179,6 +188,10 @@ class AdamW(torch.optim.Optimizer):
             self._step.copy_(state["step"])
         for mine, other in zip(self.param_groups, groups):
             mine.update({k: v for k, v in other.items() if k != "params"})
+
+
+def _dense(grad):
+    return grad if grad is None or grad.is_contiguous() else grad.contiguous()
 
 
 def _copy(params, master) -> None:

@@ -46,6 +46,13 @@ def wtconv_adamw_step(params, grads, m, v, step, *, lr, weight_decay, betas=(0.9
            betas=betas, eps=eps, scales=scales, master=master, factor=factor, lr_factor=lr_factor, rng=rng, site=site)
 
 
+def wtconv_adamw_check(params, grads, m, v, step, *, lr, weight_decay, betas=(0.9, 0.999), eps: float = 1e-8,
+                       scales=None, master=None, factor=None, lr_factor=None, rng=None, site: int = 0) -> None:
+    """Raises what wtconv_adamw_step would raise for these arguments; makes no device call."""
+    _b.load_native().adamw_check(list(params), list(grads), m, v, step, lr, weight_decay, *betas, eps, scales, master,
+                                 factor, lr_factor, rng, site)
+
+
 def wtconv_grad_norm(grads, max_norm: float = math.inf, *, step=None, out=None, ws=None, stream=None):
     """A tensor of two fp32 numbers: the norm of all gradients (a list of fp32 and bf16 tensors; None counts nothing)
     and min(1, max_norm / (norm + 1e-6)), NaN where the norm is not finite. step: an int64 on the GPU, increased by
