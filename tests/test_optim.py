@@ -772,3 +772,27 @@ def test_a_refused_first_step_makes_no_master_copies():
         gradients(m, 2)
         x.step()
     assert all(torch.equal(u, v) for u, v in zip(a.parameters(), b.parameters()))
+
+
+@pytest.mark.parametrize("kind", ["tensor", "tensor of 64 bits", "numpy"])
+def test_rates_that_are_not_python_s_numbers(kind):
+    """A rate or decay that a scheduler holds as a tensor on the host, or as numpy's number."""
+    import numpy as np
+
+    make = {"tensor": torch.tensor, "tensor of 64 bits": lambda x: torch.tensor([x], dtype=torch.float64),
+            "numpy": np.float32}[kind]
+    models = net(), net()
+    opts = [AdamW(m.parameters(), lr=f(1e-2), weight_decay=f(0.25)) for m, f in zip(models, (make, float))]
+    for i, rate in enumerate((1e-2, 0.5, 0.0)):
+        for m, o, f in zip(models, opts, (make, float)):
+            o.param_groups[0]["lr"] = f(rate)
+            gradients(m, i)
+            o.step()
+        assert all(torch.equal(torch.tensor(float(x.param_groups[0]["lr"])), torch.tensor(rate)) for x in opts)
+        assert all(torch.equal(p, q) for p, q in zip(*(m.parameters() for m in models)))
+    before = _state(models[0], opts[0])
+    opts[0].param_groups[0]["lr"] = torch.ones((), device=DEV)
+    gradients(models[0], 3)
+    with pytest.raises(ValueError, match="lr_factor"):
+        opts[0].step()
+    assert _same_state(before, _state(models[0], opts[0]))

@@ -274,3 +274,27 @@ def test_the_check_of_a_step_says_what_the_step_says(lib, kw, status, monkeypatc
     class Check:
         wtconv_adamw_step = staticmethod(lambda *a: lib.wtconv_adamw_check(*a[:-1]))
     assert _adamw(Check, **kw) == status
+
+
+def test_optimizer_numbers():
+    """What a step would refuse is refused when the group is added, and a refused group is not there afterwards."""
+    w, b = torch.nn.Parameter(torch.zeros(4)), torch.nn.Parameter(torch.zeros(3))
+    good = dict(lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.1)
+    bad = [dict(eps=1e-40), dict(eps=float("inf")), dict(eps=1e39), dict(eps=float("nan")), dict(lr=1e39), dict(lr="fast"),
+           dict(lr=None), dict(lr=torch.ones(2)), dict(weight_decay=float("nan")), dict(weight_decay=1e39),
+           dict(betas=0.9), dict(betas=(0.9,)), dict(betas=(0.9, 0.99, 0.999)), dict(betas=("a", "b")),
+           dict(betas=(0.9, float("nan"))), dict(eps=None), dict(weight_decay=[0.1])]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            op.AdamW([w], **{**good, **kw})
+        o = op.AdamW([w], **good)
+        with pytest.raises(ValueError):
+            o.add_param_group({"params": [b], **good, **kw})
+        assert len(o.param_groups) == len(o._buffers) == 1
+    for kw in (dict(eps=1.18e-38), dict(eps=torch.tensor(1e-6)), dict(lr=torch.tensor(1e-3)), dict(lr=0), dict(betas=[0.0, 0.5]),
+               dict(lr=torch.tensor([1e-3], dtype=torch.float64)), dict(weight_decay=0)):
+        o = op.AdamW([w], **{**good, **kw})
+        o.add_param_group({"params": [b]})
+        assert len(o.param_groups) == len(o._buffers) == 2
+    with pytest.raises(ValueError, match="lr_factor"):   # a rate that is not on the host
+        op.AdamW([w], lr=torch.ones((), device="meta"))

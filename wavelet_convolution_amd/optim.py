@@ -13,6 +13,7 @@ CPU path.
 """
 from __future__ import annotations
 
+import ctypes
 import math
 
 import torch
@@ -52,8 +53,8 @@ class AdamW(torch.optim.Optimizer):
         self.rng, self.site, self.lr_factor = rng, site, lr_factor
         self.last_norm = self._step = None
         self._buffers = []   # of each group: None, or a dict of its states
-        super().__init__(params, dict(lr=lr, betas=tuple(betas), eps=eps, weight_decay=weight_decay,
-                                      state_bits=state_bits))
+        betas = tuple(betas) if hasattr(betas, "__iter__") else betas
+        super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, state_bits=state_bits))
         if rng is not None and all(g["state_bits"] != 8 for g in self.param_groups):
             raise ValueError("rng is for states in 8 bits")
 
@@ -73,9 +74,8 @@ class AdamW(torch.optim.Optimizer):
             why = "all parameters must be on one device"
         elif any(not p.is_contiguous() for p in g["params"]):
             why = "parameters must be contiguous (the states have their elements' order)"
-        elif not (0 <= g["lr"] < math.inf and 0 <= g["weight_decay"] < math.inf and g["eps"] > 0
-                  and all(0 <= b < 1 for b in g["betas"]) and g["state_bits"] in (8, 32)):
-            why = "lr >= 0, weight_decay >= 0, eps > 0, betas in [0, 1) and state_bits 8 or 32 are required"
+        else:
+            why = _wrong_numbers(g)
         if why:
             self.param_groups.pop()
             raise ValueError(why)
@@ -134,8 +134,9 @@ class AdamW(torch.optim.Optimizer):
         for (g, ts, there), b in zip(groups, buffers):
             if there:
                 calls.append(((g["params"], ts), dict(
-                    step=step, lr=g["lr"], weight_decay=g["weight_decay"], betas=g["betas"], eps=g["eps"],
-                    lr_factor=self.lr_factor, rng=self.rng if g["state_bits"] == 8 else None, site=site, **b)))
+                    step=step, lr=_number("lr", g["lr"]), weight_decay=_number("weight_decay", g["weight_decay"]),
+                    betas=g["betas"], eps=g["eps"], lr_factor=self.lr_factor,
+                    rng=self.rng if g["state_bits"] == 8 else None, site=site, **b)))
             site += len(ts)
         # a step that is refused leaves the count, the states and every group as they were
         for lists, kw in calls:
@@ -188,6 +189,30 @@ class AdamW(torch.optim.Optimizer):
             self._step.copy_(state["step"])
         for mine, other in zip(self.param_groups, groups):
             mine.update({k: v for k, v in other.items() if k != "params"})
+
+
+def _number(name: str, v) -> float:
+    if type(v) is float:
+        return v
+    if isinstance(v, torch.Tensor) and v.device.type != "cpu":
+        raise ValueError(f"{name} must be a number on the host (lr_factor scales rates on the GPU)")
+    return float(v)
+
+
+def _wrong_numbers(g):
+    """What is wrong with a group's numbers, as the step sees them (in fp32), or None."""
+    def f32(name):
+        return ctypes.c_float(_number(name, g[name])).value
+
+    try:
+        betas = [float(b) for b in g["betas"]]
+        ok = (0 <= f32("lr") < math.inf and 0 <= f32("weight_decay") < math.inf
+              and torch.finfo(torch.float32).tiny <= f32("eps") < math.inf
+              and len(betas) == 2 and all(0 <= b < 1 for b in betas) and g["state_bits"] in (8, 32))
+    except (TypeError, ValueError, RuntimeError) as e:
+        return f"a group's numbers: {e}"
+    return None if ok else ("lr >= 0, weight_decay >= 0, eps of 2^-126 at least, two betas in [0, 1) and state_bits "
+                            "8 or 32 are required")
 
 
 def _dense(grad):
