@@ -463,7 +463,9 @@ wtconv_status_t wtconv_expert_sum_bwd(const wtconv_expert_desc_t *desc, const vo
  * floor(|q| / s + (u + 1/2) / 65536) s with s the distance of e4m3 numbers at
  * q and u the low (m) or high (v) 16 bits of word e % 4 of Philox4x32-10
  * with counter (e / 4, site + i, offset low, offset high) and key (seed low,
- * seed high), for element e of tensor i. A moving average changes by less
+ * seed high), for element e of tensor i. The bits are those of an element
+ * dropout with the same seed, offset and site: sites site .. site + n - 1 are
+ * for this call alone. A moving average changes by less
  * than half a step of 8 bits in most steps: rounded to nearest it then stays
  * where it is.
  *

@@ -796,3 +796,26 @@ def test_rates_that_are_not_python_s_numbers(kind):
     with pytest.raises(ValueError, match="lr_factor"):
         opts[0].step()
     assert _same_state(before, _state(models[0], opts[0]))
+
+
+def test_rounding_is_not_the_dropouts_bits():
+    """With the rng that the model's dropouts take, at the offset of this step, and no site given."""
+    rng = dropout_rng(3)
+    params = [torch.nn.Parameter(torch.randn(700, device=DEV)) for _ in range(3)]
+    o = AdamW(params, lr=1e-3, state_bits=8, rng=rng)
+    for i in range(2):
+        for q in params:
+            q.grad = torch.randn(700, device=DEV) * 1e-2
+        if i:
+            b, copies = o._buffers[0], [q.detach().clone() for q in params]
+            args = [copies, [q.grad for q in params], b["m"], b["v"], int(o._step) + 1]
+            kw = dict(lr=1e-3, weight_decay=1e-2, scales=b["scales"], rng=rng)
+            want, other = Step(*args, **kw, site=1 << 30), Step(*args, **kw, site=0)
+        o.step()
+        rng[1] += 1
+    rng[1] -= 1
+    for q, c in zip(params, copies):
+        c.copy_(q.detach())
+    want.check()
+    with pytest.raises(AssertionError):
+        other.check()

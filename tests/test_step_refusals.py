@@ -298,3 +298,10 @@ def test_optimizer_numbers():
         assert len(o.param_groups) == len(o._buffers) == 2
     with pytest.raises(ValueError, match="lr_factor"):   # a rate that is not on the host
         op.AdamW([w], lr=torch.ones((), device="meta"))
+
+
+def test_the_optimizer_s_sites_are_not_the_dropouts():
+    """One rng serves a whole model, whose dropouts are numbered from 0 on; sites are below 2^31."""
+    w = [torch.nn.Parameter(torch.zeros(4)) for _ in range(3)]
+    assert op.AdamW(w).site == op.AdamW(w, state_bits=8, rng=torch.zeros(2, dtype=torch.int64)).site == 1 << 30
+    assert op.AdamW(w, site=7).site == 7

@@ -29,7 +29,10 @@ class AdamW(torch.optim.Optimizer):
     moment and the second one's root are e4m3 numbers). rng: an int64
     {seed, offset} on the GPU (`dropout_rng`), for stochastic rounding of 8-bit
     states; parameter i (counted over all groups) uses the generator's site
-    `site + i`, and the caller changes the offset once per step. max_norm:
+    `site + i`, and the caller changes the offset once per step. No other use
+    of the same rng, dropouts among them, may have one of these sites: its bits
+    would be the same (the default is far above a model's dropouts; another
+    optimizer with this rng needs a site of its own). max_norm:
     gradients are scaled down to this norm over all of them, and a step whose
     gradients are not finite changes nothing and is not counted (inf: no
     clipping, but such steps are skipped; None: neither, and no norm is
@@ -46,7 +49,7 @@ class AdamW(torch.optim.Optimizer):
     parameters in another way, or the next step goes on from the copies."""
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 1e-2,
-                 state_bits: int = 32, master: bool = True, max_norm=None, rng=None, site: int = 0, lr_factor=None):
+                 state_bits: int = 32, master: bool = True, max_norm=None, rng=None, site: int = 1 << 30, lr_factor=None):
         if max_norm is not None and not max_norm > 0:
             raise ValueError(f"max_norm must be above 0, or None; got {max_norm}")
         self.master, self.max_norm = master, max_norm

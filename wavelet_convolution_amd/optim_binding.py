@@ -35,7 +35,8 @@ def wtconv_adamw_step(params, grads, m, v, step, *, lr, weight_decay, betas=(0.9
     fp32 number on the GPU that lr is multiplied by. factor: one fp32 number on the GPU that the gradients are
     multiplied by (as wtconv_grad_norm's second result); where it is not finite nothing is changed. master: fp32
     copies of bf16 parameters, laid out as the states. rng (int64 {seed, offset} on the GPU): states in 8 bits are
-    rounded stochastically; tensor i uses the generator's site + i."""
+    rounded stochastically; tensor i uses the generator's site + i, which no dropout or other call with the same rng
+    may use at this offset."""
     params, grads = list(params), list(grads)
     if stream is None or not params or not _elsewhere(params[0], stream):
         if _b.load_native().adamw_step(params, grads, m, v, step, lr, weight_decay, *betas, eps, scales, master,
