@@ -495,3 +495,24 @@ def test_no_memory_is_torchs_error():
     finally:
         torch.cuda.set_per_process_memory_fraction(1.0)
     assert eb.wtconv_expert_rows_fwd(x[:16], place[:16], offsets).shape == (1024, 512)
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("K", [1, 2, 5])
+def test_what_a_sum_s_gradient_does_not_read_may_be_missing(K, t):
+    place, offsets, x, ys, w, dy = routed(90, K, 4, 40, t)
+    dys, dw = eb.wtconv_expert_sum_bwd(dy, ys, w, place, offsets)
+    only = eb.wtconv_expert_sum_bwd(dy, None, w, place, offsets, want=["dys"])
+    assert only[1] is None and torch.equal(only[0], dys)
+    only = eb.wtconv_expert_sum_bwd(dy, ys, None, place, offsets, want=["dweight"])
+    assert only[0] is None and torch.equal(only[1], dw)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    only = eb.wtconv_expert_sum_bwd(dy, ys, None, place, offsets, want=["dweight"], stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(only[1], dw)
+    assert eb.wtconv_expert_sum_bwd(dy, None, None, place, offsets, want=[]) == (None, None)
+    for args, want in (((dy, None, w), ["dweight"]), ((dy, ys, None), ["dys"]), ((dy, None, w), ["dys", "dweight"]),
+                       ((dy, ys, None), ["dys", "dweight"]), ((dy, ys[:1], w), ["dys"]), ((dy, ys, w[:1]), ["dweight"])):
+        with pytest.raises(ValueError):
+            eb.wtconv_expert_sum_bwd(*args, place, offsets, want=want)

@@ -300,15 +300,24 @@ PyObject* expert_sum_bwd(PyObject*, PyObject* const* a, Py_ssize_t) {
         void* const stream = stream_of(dy);
         const Route r = route(a[3], a[4], dy);
         check_token_rows("dy", dy, r.place);
-        const at::Tensor& ys = tensor("ys", a[1], &dy);
-        check_dense("ys", ys, dy.scalar_type(), {r.place.numel(), dy.size(-1)});
-        const at::Tensor& w = tensor("weight", a[2], &dy);
-        check_dense("weight", w, at::kFloat, r.place.sizes());
+        const bool want_dys = a[5] == Py_True, want_dw = a[6] == Py_True;
+        const void* ys_at = nullptr;
+        const float* w_at = nullptr;
+        if (want_dw || a[1] != Py_None) {
+            const at::Tensor& ys = tensor("ys", a[1], &dy);
+            check_dense("ys", ys, dy.scalar_type(), {r.place.numel(), dy.size(-1)});
+            ys_at = ys.const_data_ptr();
+        }
+        if (want_dys || a[2] != Py_None) {
+            const at::Tensor& w = tensor("weight", a[2], &dy);
+            check_dense("weight", w, at::kFloat, r.place.sizes());
+            w_at = w.const_data_ptr<float>();
+        }
         at::Tensor dys, dw;
-        if (a[5] == Py_True) dys = output("dys", a[7], dy, dy.scalar_type(), {r.place.numel(), dy.size(-1)});
-        if (a[6] == Py_True) dw = output("dweight", a[8], dy, at::kFloat, r.place.sizes());
-        check_status(wtconv_expert_sum_bwd(&r.d, dy.const_data_ptr(), ys.const_data_ptr(), w.const_data_ptr<float>(),
-                                           r.at, r.ends, dys.defined() ? dys.mutable_data_ptr() : nullptr,
+        if (want_dys) dys = output("dys", a[7], dy, dy.scalar_type(), {r.place.numel(), dy.size(-1)});
+        if (want_dw) dw = output("dweight", a[8], dy, at::kFloat, r.place.sizes());
+        check_status(wtconv_expert_sum_bwd(&r.d, dy.const_data_ptr(), ys_at, w_at, r.at, r.ends,
+                                           dys.defined() ? dys.mutable_data_ptr() : nullptr,
                                            dw.defined() ? dw.mutable_data_ptr<float>() : nullptr, stream));
         return tuple_of({&dys, &dw});
     });

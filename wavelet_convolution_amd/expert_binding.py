@@ -58,7 +58,8 @@ def wtconv_expert_sum_fwd(ys, weight, place, offsets, *, y=None, stream=None):
 def wtconv_expert_sum_bwd(dy, ys, weight, place, offsets, *, want=("dys", "dweight"), dys=None, dweight=None,
                           stream=None):
     """(dys, dweight) of wtconv_expert_sum_fwd: rows weight * dy for the slots, zeros for those without an expert,
-    and the products <dy, ys>. `want`: the names of the gradients to compute; the others are None."""
+    and the products <dy, ys>. `want`: the names of the gradients to compute; the others are None. ys is read for
+    dweight only and weight for dys only: what is not read may be None."""
     wants = _wanted(want, ("dys", "dweight"))
     if stream is None or not _elsewhere(dy, stream):
         r = _b.load_native().expert_sum_bwd(dy, ys, weight, place, offsets, *wants, dys, dweight)
