@@ -516,3 +516,21 @@ def test_what_a_sum_s_gradient_does_not_read_may_be_missing(K, t):
                        ((dy, ys, None), ["dys", "dweight"]), ((dy, ys[:1], w), ["dys"]), ((dy, ys, w[:1]), ["dweight"])):
         with pytest.raises(ValueError):
             eb.wtconv_expert_sum_bwd(*args, place, offsets, want=want)
+
+
+def test_refusals_on_another_stream():
+    """They are the same as on the current one."""
+    place, offsets, x, ys, w, dy = routed(40, 2, 4, 16, torch.float32)
+    e, s = ids(40, 2, 4), torch.cuda.Stream()
+    for stream in (None, s):
+        for call in (lambda: eb.wtconv_expert_sort(e, 4, place=place.cpu(), stream=stream),
+                     lambda: eb.wtconv_expert_sort("e", 4, stream=stream),
+                     lambda: eb.wtconv_expert_sort(e, 4, ws=[1], stream=stream),
+                     lambda: eb.wtconv_expert_rows_fwd(x, place.cpu(), offsets, stream=stream),
+                     lambda: eb.wtconv_expert_rows_fwd(None, place, offsets, stream=stream),
+                     lambda: eb.wtconv_expert_rows_bwd(ys, place, offsets.cpu(), stream=stream),
+                     lambda: eb.wtconv_expert_sum_fwd(ys, w.cpu(), place, offsets, stream=stream),
+                     lambda: eb.wtconv_expert_sum_bwd(dy, ys.cpu(), w, place, offsets, stream=stream),
+                     lambda: eb.wtconv_expert_sum_bwd(dy.cpu(), ys, w, place, offsets, stream=stream)):
+            with pytest.raises(ValueError):
+                call()

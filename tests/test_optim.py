@@ -819,3 +819,20 @@ def test_rounding_is_not_the_dropouts_bits():
     want.check()
     with pytest.raises(AssertionError):
         other.check()
+
+
+def test_refusals_on_another_stream():
+    """They are the same as on the current one."""
+    c, s = Call([(40,), (5, 7)], bits=8), torch.cuda.Stream()
+    p, g, m, v, t = c.args()
+    for stream in (None, s):
+        for args, kw in (((p, [g[0], g[1].cpu()], m, v, t), {}), ((p, g, m.cpu(), v, t), {}), ((p, g, m, v, t.cpu()), {}),
+                         ((p, g, m, v, t), dict(factor=torch.ones(1))), ((p, g, m, v, t), dict(rng=torch.zeros(2, dtype=torch.int64))),
+                         (([p[0].cpu(), p[1]], g, m, v, t), {}), ((["x", p[1]], g, m, v, t), {}), ((p, ["x", None], m, v, t), {}),
+                         ((p, g, m, v, 3), {}), (([], [], m, v, t), {})):
+            with pytest.raises(ValueError):
+                ob.wtconv_adamw_step(*args, **{**c.opts, **kw}, stream=stream)
+        for args, kw in (([g[0].cpu()], {}), ([g[0], g[1].cpu()], {}), (["x"], {}), ([None], {}), ([g[0]], dict(out=torch.zeros(2))),
+                         ([g[0]], dict(step=torch.zeros(1, dtype=torch.int64))), ([g[0]], dict(ws=5))):
+            with pytest.raises(ValueError):
+                ob.wtconv_grad_norm(args, 1.0, **kw, stream=stream)

@@ -77,6 +77,8 @@ def _elsewhere(act: torch.Tensor, stream) -> bool:
     """Whether the call has to enter another device or stream first."""
     if stream is None:
         return act.device.index != torch.cuda.current_device()
+    if not (isinstance(act, torch.Tensor) and act.is_cuda):
+        return False   # the call itself refuses it
     if stream.device != act.device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {act.device}")
     return stream != torch.cuda.current_stream(act.device)
@@ -84,13 +86,13 @@ def _elsewhere(act: torch.Tensor, stream) -> bool:
 
 def _enter(fn, act, stream, tensors, *args, **kw):
     """fn on act's device and on `stream`: outputs and workspace are allocated there, and the tensors that come
-    from another stream are marked as in use on it."""
+    from another stream are marked as in use on it (what is no GPU tensor is refused by the call itself)."""
     if stream is None:
         with torch.cuda.device(act.device):
             return fn(*args, **kw)
     for t in tensors:
         for u in t if isinstance(t, (tuple, list)) else (t,):
-            if u is not None:
+            if isinstance(u, torch.Tensor) and u.is_cuda:
                 u.record_stream(stream)
     with torch.cuda.stream(stream):
         return fn(*args, **kw)
