@@ -534,3 +534,43 @@ def test_refusals_on_another_stream():
                      lambda: eb.wtconv_expert_sum_bwd(dy.cpu(), ys, w, place, offsets, stream=stream)):
             with pytest.raises(ValueError):
                 call()
+
+
+def test_given_outputs_are_seen_by_autograd():
+    """A graph that needs what stood in a tensor before a call wrote it raises an error, as after torch's own
+    operations in place."""
+    e = ids(60, 2, 4)
+    x = torch.randn(60, 16, device=DEV, requires_grad=True)
+    w = torch.rand(60, 2, device=DEV)
+
+    def graph():
+        route = ex.expert_sort(e, 4)
+        return route, ex.expert_sum(ex.expert_rows(x, route), w, route)
+
+    for name in ("order", "place", "offsets"):
+        route, y = graph()
+        other = ids(60, 2, 4, seed=9)
+        eb.wtconv_expert_sort(other, 4, **{name: getattr(route, name)})
+        if name == "order":   # which no gradient needs
+            y.sum().backward()
+            continue
+        with pytest.raises(RuntimeError, match="inplace"):
+            y.sum().backward()
+    place, offsets, rows, ys, w, dy = routed(30, 2, 4, 16, torch.float32)
+    calls = {"xs": lambda t: eb.wtconv_expert_rows_fwd(rows, place, offsets, xs=t),
+             "dx": lambda t: eb.wtconv_expert_rows_bwd(ys, place, offsets, dx=t),
+             "y": lambda t: eb.wtconv_expert_sum_fwd(ys, w, place, offsets, y=t),
+             "dys": lambda t: eb.wtconv_expert_sum_bwd(dy, ys, w, place, offsets, dys=t),
+             "dweight": lambda t: eb.wtconv_expert_sum_bwd(dy, ys, w, place, offsets, dweight=t)}
+    for name, call in calls.items():
+        t = torch.empty_like({"xs": ys, "dys": ys, "dweight": w}.get(name, rows))
+        before = t._version
+        call(t)
+        assert t._version == before + 1, name
+        with torch.inference_mode():   # which keeps no record
+            call(torch.empty_like(t))
+    wrong = torch.empty(3, device=DEV)
+    for call in calls.values():
+        with pytest.raises(ValueError):
+            call(wrong)
+    assert wrong._version == 0

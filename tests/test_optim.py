@@ -836,3 +836,17 @@ def test_refusals_on_another_stream():
                          ([g[0]], dict(step=torch.zeros(1, dtype=torch.int64))), ([g[0]], dict(ws=5))):
             with pytest.raises(ValueError):
                 ob.wtconv_grad_norm(args, 1.0, **kw, stream=stream)
+
+
+def test_states_and_outputs_are_seen_by_autograd():
+    """What a step and a norm write counts as changed in place; what they do not, not."""
+    c = Call([(40,), (300,)], p=BF16, master=True, bits=8, missing=(1,))
+    out = torch.empty(2, device=DEV)
+    written = [c.params[0], c.m, c.v, c.scales, c.master]
+    others = [c.params[1], c.grads[0], c.step]
+    before = [t._version for t in written + others]
+    c.run()
+    assert [t._version for t in written + others] == [n + (i < len(written)) for i, n in enumerate(before)]
+    before = c.step._version, c.grads[0]._version, out._version
+    ob.wtconv_grad_norm(c.grads, 1.0, step=c.step, out=out)
+    assert (c.step._version, c.grads[0]._version, out._version) == (before[0] + 1, before[1], before[2] + 1)

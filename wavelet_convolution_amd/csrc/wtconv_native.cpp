@@ -166,6 +166,14 @@ at::Tensor output(const char* name, PyObject* given, const at::Tensor& like, at:
     return t;
 }
 
+// Autograd's own record of a change in place, as torch's operations keep it: a
+// graph that needs what a tensor of the caller's held before raises an error.
+void changed(PyObject* o) {
+    if (o == Py_None) return;
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // ------------------------------------------------------------- expert rows
 
 PyObject* tuple_of(std::initializer_list<const at::Tensor*> ts) {
@@ -205,6 +213,7 @@ PyObject* expert_sort(PyObject*, PyObject* const* a, Py_ssize_t) {
         check_status(wtconv_expert_sort(&d, e.const_data_ptr(), wide ? WTCONV_I64 : WTCONV_I32,
                                         order.mutable_data_ptr<int32_t>(), place.mutable_data_ptr<int32_t>(),
                                         offsets.mutable_data_ptr<int32_t>(), ws.p, ws.bytes, stream));
+        for (int i : {2, 3, 4}) changed(a[i]);
         return tuple_of({&order, &place, &offsets});
     });
 }
@@ -259,6 +268,7 @@ PyObject* expert_rows_fwd(PyObject*, PyObject* const* a, Py_ssize_t) {
         const at::Tensor xs = output("xs", a[3], x, x.scalar_type(), {r.place.numel(), x.size(-1)});
         check_status(wtconv_expert_rows_fwd(&r.d, x.const_data_ptr(), r.at, r.ends, xs.mutable_data_ptr(),
                                             stream));
+        changed(a[3]);
         return THPVariable_Wrap(xs);
     });
 }
@@ -273,6 +283,7 @@ PyObject* expert_rows_bwd(PyObject*, PyObject* const* a, Py_ssize_t) {
         const at::Tensor dx = output("dx", a[3], dxs, dxs.scalar_type(), token_shape(r.place, dxs.size(-1)));
         check_status(wtconv_expert_rows_bwd(&r.d, dxs.const_data_ptr(), r.at, r.ends, dx.mutable_data_ptr(),
                                             stream));
+        changed(a[3]);
         return THPVariable_Wrap(dx);
     });
 }
@@ -289,6 +300,7 @@ PyObject* expert_sum_fwd(PyObject*, PyObject* const* a, Py_ssize_t) {
         const at::Tensor y = output("y", a[4], ys, ys.scalar_type(), token_shape(r.place, ys.size(-1)));
         check_status(wtconv_expert_sum_fwd(&r.d, ys.const_data_ptr(), w.const_data_ptr<float>(), r.at, r.ends,
                                            y.mutable_data_ptr(), stream));
+        changed(a[4]);
         return THPVariable_Wrap(y);
     });
 }
@@ -319,6 +331,8 @@ PyObject* expert_sum_bwd(PyObject*, PyObject* const* a, Py_ssize_t) {
         check_status(wtconv_expert_sum_bwd(&r.d, dy.const_data_ptr(), ys_at, w_at, r.at, r.ends,
                                            dys.defined() ? dys.mutable_data_ptr() : nullptr,
                                            dw.defined() ? dw.mutable_data_ptr<float>() : nullptr, stream));
+        if (want_dys) changed(a[7]);
+        if (want_dw) changed(a[8]);
         return tuple_of({&dys, &dw});
     });
 }
@@ -482,11 +496,14 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t) {
         void* const stream = stream_of(*c.like);
         check_status(wtconv_adamw_step(&c.d, c.n, c.p.data(), c.g.data(), c.counts.data(), c.lr, c.wd, c.m, c.v,
                                        c.scales, c.master, c.step, c.factor, c.lr_factor, c.rng, stream));
-        // autograd's own record of changes in place, as torch's operations keep it
-        for (int32_t i = 0; i < c.n; ++i) {
-            const at::Tensor& t = THPVariable_Unpack(c.params.o[i]);
-            if (c.g[i] && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
-        }
+        bool any = false;
+        for (int32_t i = 0; i < c.n; ++i)
+            if (c.g[i]) {
+                changed(c.params.o[i]);
+                any = true;
+            }
+        if (any)
+            for (int i : {2, 3, 10, 11}) changed(a[i]);
         Py_RETURN_NONE;
     });
 }
@@ -519,6 +536,8 @@ PyObject* grad_norm(PyObject*, PyObject* const* a, Py_ssize_t) {
         const Workspace ws(a[4], need, *like);
         check_status(wtconv_grad_norm(n, g.data(), counts.data(), types.data(), most, (int64_t*)step,
                                       out.mutable_data_ptr<float>(), ws.p, ws.bytes, stream));
+        changed(a[2]);
+        changed(a[3]);
         return THPVariable_Wrap(out);
     });
 }
