@@ -850,3 +850,90 @@ def test_states_and_outputs_are_seen_by_autograd():
     before = c.step._version, c.grads[0]._version, out._version
     ob.wtconv_grad_norm(c.grads, 1.0, step=c.step, out=out)
     assert (c.step._version, c.grads[0]._version, out._version) == (before[0] + 1, before[1], before[2] + 1)
+
+
+# around a wavefront's blocks and a workgroup's piece, of 1,024 or 2,048 elements by types and states
+PIECES = [(1023,), (1024,), (1025,), (2047,), (2048,), (2049,), (4095,), (4096,), (1,), (3 * 2048 + 5,)]
+
+
+@pytest.mark.parametrize("bits,random", STATES)
+@pytest.mark.parametrize("p,g,master", KINDS)
+def test_sizes_around_a_workgroup_s_piece(p, g, master, bits, random):
+    Call(PIECES, p=p, g=g, master=master, bits=bits, random=random, seed=21).check()
+
+
+# the largest tensor of a call, and one beyond 2^32 elements whose states are in 32 bits: grids of more than one row
+@pytest.mark.parametrize("p,bits,n,gib", [(BF16, 8, 2 ** 34, 150), (F32, 32, 2 ** 32 + 5001, 110)])
+def test_the_largest_tensor(p, bits, n, gib, monkeypatch):
+    """All of it holds the same numbers, but for windows, which hold others: the windows are those of the 64-bit form,
+    and everything else is alike afterwards. A small tensor stands behind it."""
+    if torch.cuda.mem_get_info()[0] < gib * 2 ** 30:
+        pytest.skip(f"needs {gib} GiB")
+    import numpy as np
+
+    import tests._step_ref as ref
+    from tests._block_ref import philox
+
+    gen = torch.Generator(DEV).manual_seed(n % 1009)
+    kind = torch.float8_e4m3fn if bits == 8 else F32
+    whole = -(-n // BLOCK) * BLOCK
+    P, G = torch.full((n,), 0.5, dtype=p, device=DEV), torch.full((n,), 2.0 ** -16, dtype=p, device=DEV)
+    P2, G2 = torch.randn(300, generator=gen, device=DEV).to(p), torch.randn(300, generator=gen, device=DEV).to(p)
+    m, v = (torch.zeros(whole + 512, dtype=kind, device=DEV) for _ in range(2))
+    scales = torch.zeros((whole + 512) // BLOCK, 2, device=DEV) if bits == 8 else None
+    rng = dropout_rng(5) if bits == 8 else None
+    step = torch.ones(1, dtype=torch.int64, device=DEV)
+    kw = dict(lr=1e-2, weight_decay=0.1)
+    windows = [slice(a, min(n, a + 1024)) for a in (1024, 2 ** 30 - 512, 2 ** 31 - 512, 2 ** 32 - 512,
+                                                    n // BLOCK * BLOCK - 1024, n // BLOCK * BLOCK - 256)]
+    windows[-2] = slice(windows[-2].start, windows[-1].start)
+    real = ref.random_bits
+
+    def bits_from(first):
+        def window(count, tensor, site, rng):
+            seed, offset = (int(x) & (2 ** 64 - 1) for x in rng.tolist())
+            groups = np.arange(first // 4, first // 4 - (-count // 4))
+            words = philox(groups, site + tensor, offset, seed).reshape(-1)[:count].astype(np.int64)
+            return torch.from_numpy(np.stack([words & 0xFFFF, words >> 16], -1)).double()
+        return window
+
+    wants = []
+    for w in windows:
+        k = w.stop - w.start
+        P[w], G[w] = torch.randn(k, generator=gen, device=DEV).to(p), (1e-3 * torch.randn(k, generator=gen, device=DEV)).to(p)
+        states = slice(w.start, w.start + -(-k // BLOCK) * BLOCK)
+        wants.append(Step([P[w]], [G[w]], m[states], v[states], 1, **kw, rng=rng, site=9,
+                          scales=None if scales is None else scales[states.start // BLOCK:states.stop // BLOCK]))
+    wants.append(Step([P2], [G2], m[whole:], v[whole:], 1, **kw, rng=rng, site=10,
+                      scales=None if scales is None else scales[whole // BLOCK:]))
+    rest = n - sum(w.stop - w.start for w in windows)
+    squares = rest * 2.0 ** -32 + sum(float((G[w].double() ** 2).sum()) for w in windows) + float((G2.double() ** 2).sum())
+    norm = ob.wtconv_grad_norm([G, G2], math.inf)
+    ob.wtconv_adamw_step([P, P2], [G, G2], m, v, step, **kw, scales=scales, rng=rng, site=9)
+    torch.cuda.synchronize()
+    assert abs(float(norm[0]) - math.sqrt(squares)) <= 1.001 * U * math.sqrt(squares)
+    for w, want in zip(windows, wants):
+        monkeypatch.setattr(ref, "random_bits", bits_from(w.start))
+        want.check()
+    monkeypatch.setattr(ref, "random_bits", real)
+    wants[-1].check()
+    # everything else: the element before the first window's
+    alike = [P[0].clone(), m[0].clone().view(torch.uint8 if bits == 8 else F32), v[0].clone().view(torch.uint8 if bits == 8 else F32)]
+    assert float(P[0]) < 0.5 and float(m[0].float()) > 0 and float(v[0].float()) > 0
+    for at in range(0, n, 2 ** 30):
+        end = min(n, at + 2 ** 30)
+        other = torch.zeros(end - at, dtype=torch.bool, device=DEV)
+        for t, one in zip((P, m.view(alike[1].dtype), v.view(alike[2].dtype)), alike):
+            other |= t[at:end] != one
+        for w in windows:
+            a, b = max(w.start, at), min(w.stop, end)
+            if a < b:
+                other[a - at:b - at] = False
+        assert not other.any(), (at, other.nonzero()[:4])
+    if scales is not None:
+        blocks = torch.ones(n // BLOCK, dtype=torch.bool, device=DEV)
+        for w in windows:
+            blocks[w.start // BLOCK:-(-w.stop // BLOCK)] = False
+        assert (scales[:n // BLOCK][blocks] == scales[0]).all()
+    del P, G, m, v, scales, other, wants
+    torch.cuda.empty_cache()
