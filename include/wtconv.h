@@ -457,8 +457,11 @@ wtconv_status_t wtconv_expert_sum_bwd(const wtconv_expert_desc_t *desc, const vo
  * moments of a block whose largest is below 2^-100 are held as zero, and a
  * root that is not zero as 2^-9 units at least, so that no parameter is
  * divided by a root that was lost). The step itself uses m and v before
- * that rounding, which is to the nearest value, or, with rng (two 64-bit
- * integers {seed, offset} on the device, as for dropout), to the value below
+ * that rounding. What is rounded are the fp32 values: of a million numbers a
+ * few that stand next to a border between two of 8 bits become the other one
+ * than exact arithmetic gives, the same in every call. Rounding is to the
+ * nearest value, or, with rng (two 64-bit integers {seed, offset} on the
+ * device, as for dropout), to the value below
  * or above it with the probabilities that make the mean right: |q| becomes
  * floor(|q| / s + (u + 1/2) / 65536) s with s the distance of e4m3 numbers at
  * q and u the low (m) or high (v) 16 bits of word e % 4 of Philox4x32-10

@@ -1,9 +1,10 @@
 // AdamW and the gradients' norm over many tensors. Memory is the bound: every
 // element of a parameter, its gradient and its states is read once and
-// written once (copy rate of the card 5.2 TB/s). AdamW: 34.6 M bf16 parameters
-// in 330 tensors with fp32 master copies, 28 bytes an element, 190 us, 5.1 TB/s;
-// 76 M with states in 8 bits, 16 bytes an element, 233 us, 5.2 TB/s. Norm: 34.6 M
-// bf16 elements 18.8 us, of which 6 are the latency of its two launches.
+// written once (the card copies at 5.2 TB/s; a large tensor multiplied in place
+// reaches 6.0). AdamW: 34.6 M bf16 parameters in 330 tensors with fp32 master
+// copies, 28 bytes an element, 189 us, 5.1 TB/s; 76 M with states in 8 bits, 16
+// bytes an element, 212 us, 5.8 TB/s. Norm: 34.6 M bf16 elements 18.2 us, of which
+// 6 are the latency of its two launches.
 #include "wtconv_block_device.h"
 #include "wtconv_optim.h"
 
@@ -68,8 +69,9 @@ __device__ __forceinline__ void widen_e4m3(uint32_t w, float unit, float (&o)[4]
     o[3] = hi[1] * unit;
 }
 
-// 1 - e^x for x <= 0: the series of e^x - 1 down to -1 (its next term is 2^-25 of
-// the sum), so that no near numbers are subtracted; below, the power itself.
+// 1 - e^x for x <= 0: the series of e^x - 1 down to -1 (its next term, x^12 / 12!,
+// is 2^-28 of the sum there), so that no near numbers are subtracted; below, the
+// power itself.
 __device__ __forceinline__ float one_less_exp(float x) {
     constexpr float inv[] = {1.f, 1.f / 2, 1.f / 6, 1.f / 24, 1.f / 120, 1.f / 720, 1.f / 5040, 1.f / 40320, 1.f / 362880,
                              1.f / 3628800, 1.f / 39916800};
@@ -96,9 +98,9 @@ __device__ __forceinline__ void roots(const float (&v)[4], float (&root)[4]) {
 
 // A wavefront takes one block of 256 elements, a lane four of them, and ends:
 // the next one's loads are on their way while it computes, with more of them in
-// flight than a loop over blocks keeps (four blocks a wavefront, two at a time:
-// 219 us for 190, with states in 8 bits 250 for 233; streaming stores change
-// neither). It takes two where an element is only ten or twelve bytes and its
+// flight than a loop over blocks keeps (four blocks a wavefront, two at a time,
+// measured before the arithmetic below had its present form: 219 us for 190, with
+// states in 8 bits 250 for 233, now 212; streaming stores changed neither). It takes two where an element is only ten or twelve bytes and its
 // instructions are the bound, one after the other: 33 M bf16 parameters without
 // master copies, states in 8 bits, 67 us for 77, with random rounding 84 for 91;
 // fp32 parameters 107 for 99.
