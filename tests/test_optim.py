@@ -937,3 +937,23 @@ def test_the_largest_tensor(p, bits, n, gib, monkeypatch):
         assert (scales[:n // BLOCK][blocks] == scales[0]).all()
     del P, G, m, v, scales, other, wants
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("kind", [list, tuple, torch.tensor])
+def test_a_rate_for_each_parameter_of_a_group(kind):
+    """Rates and decays set as a sequence, or a tensor on the host, are those of groups of one parameter each."""
+    a, b = net(), net()
+    rates, decays = [1e-2, 3e-3, 5e-2, 0.0], [0.0, 0.1, 0.2, 0.3]
+    o = AdamW(a.parameters(), max_norm=1.0)
+    o.param_groups[0].update(lr=kind(rates), weight_decay=kind(decays))
+    p = AdamW([dict(params=[q], lr=r, weight_decay=d) for q, r, d in zip(b.parameters(), rates, decays)], max_norm=1.0)
+    for i in range(3):
+        for m, x in ((a, o), (b, p)):
+            gradients(m, i)
+            x.step()
+    assert all(torch.equal(x, y) for x, y in zip(a.parameters(), b.parameters()))
+    before = _state(a, o)
+    o.param_groups[0]["lr"] = kind(rates[:3])
+    with pytest.raises(ValueError):
+        o.step()
+    assert _same_state(before, _state(a, o))

@@ -100,10 +100,11 @@ __device__ __forceinline__ void roots(const float (&v)[4], float (&root)[4]) {
 // the next one's loads are on their way while it computes, with more of them in
 // flight than a loop over blocks keeps (four blocks a wavefront, two at a time,
 // measured before the arithmetic below had its present form: 219 us for 190, with
-// states in 8 bits 250 for 233, now 212; streaming stores changed neither). It takes two where an element is only ten or twelve bytes and its
-// instructions are the bound, one after the other: 33 M bf16 parameters without
-// master copies, states in 8 bits, 67 us for 77, with random rounding 84 for 91;
-// fp32 parameters 107 for 99.
+// states in 8 bits 250 for 233, now 212; streaming stores changed neither). It
+// takes two where an element is only ten or twelve bytes and its instructions are
+// the bound, one after the other: 33 M bf16 parameters without master copies,
+// states in 8 bits, 67 us for 77, with random rounding 84 for 91; fp32 parameters
+// 107 for 99.
 template <typename P, typename G, bool MASTER, int MODE, int TENSORS>
 __global__ __launch_bounds__(T) void k_adamw(AdamTable<TENSORS> a, uint32_t wgs) {
     const float f = a.factor ? *a.factor : 1.f;

@@ -194,12 +194,15 @@ class AdamW(torch.optim.Optimizer):
             mine.update({k: v for k, v in other.items() if k != "params"})
 
 
-def _number(name: str, v) -> float:
+def _number(name: str, v):
+    """A number on the host; several of them (one for each parameter) as they are."""
     if type(v) is float:
         return v
-    if isinstance(v, torch.Tensor) and v.device.type != "cpu":
-        raise ValueError(f"{name} must be a number on the host (lr_factor scales rates on the GPU)")
-    return float(v)
+    if isinstance(v, torch.Tensor):
+        if v.device.type != "cpu":
+            raise ValueError(f"{name} must be a number on the host (lr_factor scales rates on the GPU)")
+        return float(v) if v.numel() == 1 else v
+    return v if isinstance(v, (list, tuple)) else float(v)
 
 
 def _wrong_numbers(g):
